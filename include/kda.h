@@ -86,6 +86,9 @@ typedef enum {
 #define KDA_DEVERR_RANGE 0x10u      /* one-sequence bf16 d=128 prefill: a key-side chunk product
                                        (Q', M, T' below) beyond fp16's range (|x| > 65504), which
                                        needs keys far from unit norm; results invalid */
+#define KDA_DEVERR_PAGES 0x20u      /* a page number outside the pool, or a length the table cannot hold */
+#define KDA_DEVERR_EXHAUSTED 0x40u  /* kda_cache_fork: fewer free pages than the new rows need  */
+#define KDA_DEVERR_PARENT 0x80u     /* a parent outside [-1, rows)                              */
 
 /*
  * Bytes of device workspace kda_prefill needs for this problem (0 is a valid
@@ -363,6 +366,158 @@ KDA_API kda_status kda_prefill_host(const void* q, const void* k, const void* v,
                                     int64_t total_tokens, int32_t H, int32_t d_k, int32_t d_v, kda_dtype dt,
                                     float scale, const float* state_in, float* state_out, void* o,
                                     void* device_buffer, size_t device_buffer_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Decoding a hybrid stack.  The pages interleave KDA layers with full-attention layers ("Kimi K3 changed
+ * the memory math for agentic AI forever": recurrent states for the former, a paged key-value cache for
+ * the latter).  The functions below are what such a decode loop needs next to kda_decode_step: attention
+ * of the new token over the paged cache, a beam search's selection, and the bookkeeping that gives every
+ * chosen beam its states and its pages.  All of it stays on the device, so that a whole step can be
+ * captured in a CUDA graph.
+ *
+ * A page pool holds num_pages pages of page_size tokens; a page's keys (or values) are [H_kv][page_size][d],
+ * contiguous.  Row b of a block table, block_table[b][0 .. max_pages), names the pages that hold tokens
+ * 0 .. page_size - 1, page_size .. 2 page_size - 1, ... of sequence b; entries past its last page are -1.
+ * ------------------------------------------------------------------------------------------------ */
+
+/*
+ * Attention of one new token per sequence over a paged key-value cache:
+ *
+ *     s_t = scale * q . k_t,   o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m)
+ *
+ * over the visible tokens t of its row: t < seq_lens[b], and with window > 0 also t >= seq_lens[b] -
+ * window or t < sinks (a sliding window behind a few first tokens that stay visible).  Query head h reads
+ * key-value head h / (H_q / H_kv).  A row with no visible token gives o = 0 and lse = -inf.  What lies in
+ * the pools past a row's end is never used, whatever it holds.
+ *
+ *   q            [B, H_q, d]   dtype dt
+ *   k_pages      num_pages pages of [H_kv, page_size, d], dtype dt, page p at k_pages + p * k_page_stride
+ *   v_pages      likewise, at v_pages + p * v_page_stride (strides in elements)
+ *   block_table  [B, max_pages] int32;  seq_lens [B] int32, the new token included
+ *   k_new, v_new [B, H_kv, d] dtype dt, or both NULL: the new token's key and value, which the call
+ *                stores at position seq_lens[b] - 1 and attends to.  That position's page must belong
+ *                to row b alone.  NULL: the cache holds them already.
+ *   o            [B, H_q, d] dtype dt;  lse [B, H_q] float32 or NULL: m + log sum exp(s_t - m)
+ *   workspace    kda_attention_decode_workspace_size(...) bytes: partial results of rows whose length is
+ *                split over several CTAs, joined in a fixed order (two calls give the same bits)
+ * Sizes: d in {16, 64, 128}; H_q a multiple of H_kv; any page_size >= 1.  Alignment: q, k_new, v_new, o
+ * and the pools 16 bytes, page strides multiples of 16 bytes.  A length outside [0, max_pages * page_size]
+ * counts as 0, and a page outside [0, num_pages) as page 0; both set KDA_DEVERR_PAGES.
+ */
+KDA_API size_t kda_attention_decode_workspace_size(int32_t B, int32_t H_q, int32_t H_kv, int32_t d, kda_dtype dt);
+KDA_API kda_status kda_attention_decode(const void* q, void* k_pages, void* v_pages, const int32_t* block_table,
+                                        const int32_t* seq_lens, const void* k_new, const void* v_new, int32_t B,
+                                        int32_t H_q, int32_t H_kv, int32_t d, int32_t num_pages, int32_t page_size,
+                                        int32_t max_pages, int64_t k_page_stride, int64_t v_page_stride, kda_dtype dt,
+                                        float scale, int32_t window, int32_t sinks, void* o, float* lse,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A beam search's selection: for each of N groups, the K best of its K x V continuations
+ *
+ *     s(b, v) = beam_scores[b] + (x_bv - lse_b),   lse_b = m + log sum_v exp(x_bv - m),  m = max_v x_bv
+ *
+ * in float32, by score, the lowest b * V + v first among equal scores.  A score that is not a number
+ * (a logit row with a NaN or +inf, or with nothing above -inf) counts as -inf.  A finished beam offers one
+ * continuation, eos_token at its unchanged score; its other words count as -inf.
+ *
+ *   logits       [N * K, V] dtype dt, row r at logits + r * row_stride (elements, >= V)
+ *   beam_scores  [N, K] float32;  finished [N, K] bytes, nonzero = finished, or NULL
+ *   eos_token    in [0, V), or -1: none (then finished must be NULL)
+ *   scores       [N, K] float32, best first (may be beam_scores, in place)
+ *   parent       [N, K] int32: the row n * K + b that the new beam continues
+ *   token        [N, K] int32;  finished_out [N, K] bytes (token == eos_token or parent finished), or NULL
+ *                (may be finished, in place)
+ *   workspace    kda_beam_select_workspace_size(...) bytes
+ * K <= KDA_BEAM_MAX_K.
+ */
+#define KDA_BEAM_MAX_K 32
+KDA_API size_t kda_beam_select_workspace_size(int32_t N, int32_t K, int32_t V, kda_dtype dt);
+KDA_API kda_status kda_beam_select(const void* logits, int64_t row_stride, const float* beam_scores,
+                                   const uint8_t* finished, int32_t eos_token, int32_t N, int32_t K, int32_t V,
+                                   kda_dtype dt, float* scores, int32_t* parent, int32_t* token,
+                                   uint8_t* finished_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A pool of equal slots (resident KDA states, or pages of a cache) on one or several layers: slot s of
+ * layer l is the slot_bytes bytes at data + l * layer_stride + s * slot_stride.  Strides and slot_bytes
+ * in bytes, multiples of 16; data 16-byte aligned.  A call takes at most KDA_MAX_POOLS pools.
+ */
+typedef struct kda_pool {
+    void* data;
+    int64_t layer_stride;
+    int64_t slot_stride;
+    int64_t slot_bytes;
+    int32_t layers;
+    int32_t slots;
+} kda_pool;
+#define KDA_MAX_POOLS 8
+
+/*
+ * Copies slots within pools: for i < n, slot src[i] to slot dst[i], on every layer of every pool.
+ * src NULL means src[i] = i.  Entries with src or dst negative, or equal, are skipped; one outside a
+ * pool is skipped and sets KDA_DEVERR_PAGES.  No dst may occur twice or be another entry's src.
+ */
+KDA_API kda_status kda_copy_pages(const kda_pool* pools, int32_t num_pools, const int32_t* src, const int32_t* dst,
+                                  int32_t n, void* stream);
+
+/*
+ * Gives the B rows of a decode batch the KDA states of the rows that they continue: new row i continues
+ * row parent[i] (-1: none, a row that starts anew).  The lowest row with a given parent takes over its
+ * parent's slot in place; the r-th of the other continuing rows gets the r-th slot (by row) of the rows
+ * that nobody continues, and the state is copied there; rows without a parent get the slots that are then
+ * left, contents unchanged.  So state_idx_out is a permutation of state_idx, a copy's target is never
+ * read, and only states that have to move are moved.
+ *   state_idx [B] int32 (distinct slots);  parent [B] int32;  state_idx_out [B] int32, another array
+ * B <= KDA_FORK_MAX_ROWS (KDA_ERR_TOO_LARGE above).  A parent outside [-1, B) counts as -1 and sets
+ * KDA_DEVERR_PARENT; a copy from or to a slot outside a pool is skipped and sets KDA_DEVERR_STATE_IDX.
+ */
+#define KDA_FORK_MAX_ROWS 8192
+KDA_API kda_status kda_state_fork(const kda_pool* pools, int32_t num_pools, const int32_t* state_idx,
+                                  const int32_t* parent, int32_t B, int32_t* state_idx_out, void* stream);
+
+/*
+ * Replaces the rows of a block table: new row i continues old row parent[i] (-1: an empty row) and gets
+ * room for grow[i] more tokens.  This forks, reorders, frees, starts and extends rows in one call:
+ *  - Whole pages are shared: the new row names its parent's pages, and ref_count says how many rows name a
+ *    page.  Every old row gives up its pages; a page that nobody names any more is free (count 0).
+ *  - A partly filled last page stays with the lowest row that continues its parent; every other one gets a
+ *    page of its own, into which the page is copied on every layer of the pools.
+ *  - Pages of its own come from the free ones, the lowest first, handed out by new row and then by
+ *    position.
+ * seq_lens_out[i] = seq_lens[parent[i]] + grow[i].  When the free pages run out, the entries without a page
+ * are -1, the row ends before the first of them, and KDA_DEVERR_EXHAUSTED is set; a length outside
+ * [0, max_pages * page_size], a negative grow or one that the table cannot hold, or a page outside the pool
+ * is clamped (to an empty row, no growth, the table's end; no page) and sets KDA_DEVERR_PAGES.
+ *   block_table     [rows_in, max_pages];  seq_lens [rows_in];  parent, grow [rows_out], grow may be NULL (0)
+ *   ref_count       [num_pages];  ref_count_out [num_pages], may be ref_count (in place)
+ *   block_table_out [rows_out, max_pages] and seq_lens_out [rows_out]: other arrays than the input's
+ *   copy_src, copy_dst [rows_out] or NULL: the page copied for row i and where to, -1 for none (for pools
+ *                   that this call does not get: kda_copy_pages takes them)
+ *   pools           pools of num_pages slots; num_pools may be 0
+ * All tables int32 on the device.
+ */
+KDA_API size_t kda_cache_fork_workspace_size(int32_t rows_in, int32_t rows_out, int32_t max_pages, int32_t num_pages);
+KDA_API kda_status kda_cache_fork(const int32_t* block_table, const int32_t* seq_lens, int32_t rows_in,
+                                  const int32_t* parent, const int32_t* grow, int32_t rows_out, int32_t max_pages,
+                                  int32_t page_size, const int32_t* ref_count, int32_t num_pages,
+                                  int32_t* block_table_out, int32_t* seq_lens_out, int32_t* ref_count_out,
+                                  int32_t* copy_src, int32_t* copy_dst, const kda_pool* pools, int32_t num_pools,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Moves the live pages (ref_count > 0) of a cache together at the low end of its pools: with n live pages,
+ * the live ones at n and above go, in ascending order, to the free ones below n.  page_map [num_pages]
+ * receives each page's new number, -1 for a free page; block_table_out [rows, max_pages] is block_table
+ * with every entry replaced by its new number (entries outside [0, num_pages) become -1), ref_count_out the
+ * counts at the new numbers.  block_table_out may be block_table, ref_count_out may be ref_count.  Other
+ * tables and pools of the same pages follow with page_map (kda_copy_pages with src NULL and dst page_map).
+ */
+KDA_API size_t kda_cache_compact_workspace_size(int32_t num_pages);
+KDA_API kda_status kda_cache_compact(const int32_t* block_table, int32_t rows, int32_t max_pages,
+                                     const int32_t* ref_count, int32_t num_pages, int32_t* block_table_out,
+                                     int32_t* ref_count_out, int32_t* page_map, const kda_pool* pools,
+                                     int32_t num_pools, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's error

@@ -20,6 +20,8 @@ KDA_ERR_TOO_LARGE = 6
 KDA_NOALLOC_MAX_SEQS = 16384
 KDA_DTYPE_F32, KDA_DTYPE_BF16 = 0, 1
 KDA_DEVERR_CU_SEQLENS, KDA_DEVERR_STATE_IDX = 0x1, 0x2
+KDA_DEVERR_PAGES, KDA_DEVERR_EXHAUSTED, KDA_DEVERR_PARENT = 0x20, 0x40, 0x80
+KDA_BEAM_MAX_K, KDA_MAX_POOLS, KDA_FORK_MAX_ROWS = 32, 8, 8192
 
 class PrefillOptions(ctypes.Structure):
     """kda_prefill_options (include/kda.h)."""
@@ -31,6 +33,12 @@ class PrefillOptions(ctypes.Structure):
 class DecodeOptions(ctypes.Structure):
     """kda_decode_options (include/kda.h)."""
     _fields_ = [("alpha_mode", ctypes.c_int32), ("state_dtype", ctypes.c_int32)]
+
+
+class Pool(ctypes.Structure):
+    """kda_pool (include/kda.h)."""
+    _fields_ = [("data", ctypes.c_void_p), ("layer_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("slot_bytes", ctypes.c_int64), ("layers", ctypes.c_int32), ("slots", ctypes.c_int32)]
 
 
 KDA_ALPHA_PER_CHANNEL, KDA_ALPHA_PER_HEAD, KDA_ALPHA_NONE = 0, 1, 2
@@ -60,6 +68,20 @@ SIGNATURES = {
     "kda_prefill_host_buffer_size": (_sz, [_i32, _i64, _i32, _i32, _i32, ctypes.c_int]),
     "kda_prefill_host": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, ctypes.c_int,
                                         _f32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "kda_attention_decode_workspace_size": (_sz, [_i32, _i32, _i32, _i32, ctypes.c_int]),
+    "kda_attention_decode": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                            _i32, _i64, _i64, ctypes.c_int, _f32, _i32, _i32, _vp, _vp, _vp, _sz,
+                                            _vp]),
+    "kda_beam_select_workspace_size": (_sz, [_i32, _i32, _i32, ctypes.c_int]),
+    "kda_beam_select": (ctypes.c_int, [_vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, ctypes.c_int, _vp, _vp, _vp, _vp,
+                                       _vp, _sz, _vp]),
+    "kda_copy_pages": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i32, _vp]),
+    "kda_state_fork": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i32, _vp, _vp]),
+    "kda_cache_fork_workspace_size": (_sz, [_i32, _i32, _i32, _i32]),
+    "kda_cache_fork": (ctypes.c_int, [_vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _i32, _vp, _sz, _vp]),
+    "kda_cache_compact_workspace_size": (_sz, [_i32]),
+    "kda_cache_compact": (ctypes.c_int, [_vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
     "kda_get_device_error": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
@@ -342,6 +364,308 @@ def kda_prefill_backward(q, k, v, beta, alpha, cu_seqlens, grad_o, state_in=None
     if rc != KDA_OK:
         raise KdaError("kda_prefill_backward", rc)
     return gq, gk, gv, gb, ga, gs
+
+
+# ---- decoding a hybrid stack: one call of these takes microseconds, so the checks here stay light ----
+def _check_at(name, t, dtype, shape, dev):
+    """_check with the device as its index (-1: host memory)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+
+
+def _cuda_index(name, t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _raw_stream(stream, dev):
+    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+
+def _workspace(workspace, need, dev):
+    """The caller's workspace, or a new one: (tensor, bytes)."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=torch.device("cuda", dev))
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on device {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _pools(pools, dev):
+    """A ctypes array of kda_pool for tensors [layers, slots, ...] whose slots are contiguous."""
+    if isinstance(pools, torch.Tensor):
+        pools = (pools,)
+    out = (Pool * max(len(pools), 1))()
+    for d, t in zip(out, pools):
+        if t.dim() < 3:
+            raise ValueError(f"pool: shape {tuple(t.shape)}, expected [layers, slots, ...]")
+        if t.get_device() != dev:
+            raise ValueError(f"pool is on {t.device}, expected device {dev}")
+        e, n, shape, stride = t.element_size(), 1, t.shape, t.stride()
+        for size, step in zip(reversed(shape[2:]), reversed(stride[2:])):
+            if size != 1 and step != n:
+                raise ValueError("pool: a slot must be contiguous")
+            n *= size
+        d.data, d.layers, d.slots, d.slot_bytes = t.data_ptr(), shape[0], shape[1], n * e
+        d.layer_stride = stride[0] * e if shape[0] > 1 else 0
+        d.slot_stride = stride[1] * e if shape[1] > 1 else 0
+    return out, len(pools)
+
+
+def _page_stride(name, t, shape, dtype, dev):
+    """Elements from page to page of a pool [P, H_kv, page_size, d] whose pages are contiguous."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+    if not t.is_contiguous() and shape[0] and not t[0].is_contiguous():
+        raise ValueError(f"{name}: a page must be contiguous")
+    return t.stride(0)
+
+
+def kda_attention_decode_workspace_size(B: int, H_q: int, H_kv: int, d: int,
+                                        dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(load().kda_attention_decode_workspace_size(B, H_q, H_kv, d, _dt(dtype)))
+
+
+def kda_attention_decode(q, k_pages, v_pages, block_table, seq_lens, *, scale: float = 1.0, window: int = 0,
+                         sinks: int = 0, k_new=None, v_new=None, o=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token per sequence over a paged key-value cache; returns o [B, H_q, d].
+
+    q [B, H_q, d] (bf16 or f32); k_pages, v_pages [P, H_kv, page_size, d] of q's dtype (a view whose pages are
+    contiguous will do, e.g. one half of a [P, 2, H_kv, page_size, d] pool); block_table [B, M] int32 page
+    numbers, seq_lens [B] int32 with the new token.  k_new, v_new [B, H_kv, d]: the new token's key and value,
+    stored at position seq_lens - 1 by this call.  window > 0: only the last `window` tokens and the first
+    `sinks` are visible.  lse [B, H_q] f32, if given, receives the log of the softmax's sum.
+    """
+    L = load()
+    B, Hq, d = q.shape
+    P, Hkv, ps, _ = k_pages.shape
+    dt, dev = q.dtype, _cuda_index("q", q)
+    _check_at("q", q, dt, (B, Hq, d), dev)
+    ks = _page_stride("k_pages", k_pages, (P, Hkv, ps, d), dt, dev)
+    vs = _page_stride("v_pages", v_pages, (P, Hkv, ps, d), dt, dev)
+    M = block_table.shape[1]
+    _check_at("block_table", block_table, torch.int32, (B, M), dev)
+    _check_at("seq_lens", seq_lens, torch.int32, (B,), dev)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    kn = vn = None
+    if k_new is not None:
+        _check_at("k_new", k_new, dt, (B, Hkv, d), dev)
+        _check_at("v_new", v_new, dt, (B, Hkv, d), dev)
+        kn, vn = k_new.data_ptr(), v_new.data_ptr()
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _check_at("o", o, dt, (B, Hq, d), dev)
+    if lse is not None:
+        _check_at("lse", lse, torch.float32, (B, Hq), dev)
+    code = _dt(dt)
+    need = 0 if workspace is not None else L.kda_attention_decode_workspace_size(B, Hq, Hkv, d, code)
+    workspace, wbytes = _workspace(workspace, need, dev)
+    rc = L.kda_attention_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                                seq_lens.data_ptr(), kn, vn, B, Hq, Hkv, d, P, ps, M, ks, vs, code, scale, window,
+                                sinks, o.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                                wbytes, _raw_stream(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_attention_decode", rc)
+    return o
+
+
+def kda_beam_select_workspace_size(N: int, K: int, V: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(load().kda_beam_select_workspace_size(N, K, V, _dt(dtype)))
+
+
+def kda_beam_select(logits, beam_scores, *, finished=None, eos_token: int = -1, scores_out=None, parent=None,
+                    token=None, finished_out=None, workspace=None, stream=None):
+    """A beam search's selection; returns (scores, parent, token, finished or None), each [N, K], best first.
+
+    logits [N * K, V] (bf16 or f32; rows may lie further apart than V), beam_scores [N, K] f32.  A beam's
+    continuation v scores beam_scores + log_softmax(logits)[v]; the K best of a group's K * V, the lowest
+    place first among equal ones.  parent holds row numbers n * K + b, as kda_state_fork and kda_cache_fork take
+    them.  finished [N, K] uint8: such a beam goes on with eos_token alone, at its unchanged score.
+    """
+    L = load()
+    N, K = beam_scores.shape
+    V = logits.shape[1]
+    dev = _cuda_index("logits", logits)
+    if logits.shape != (N * K, V):
+        raise ValueError(f"logits: shape {tuple(logits.shape)}, expected {(N * K, V)}")
+    step, inner = logits.stride()
+    if inner != 1 and V > 1 or step < V and N * K > 1:
+        raise ValueError("logits: a row must be contiguous")
+    _check_at("beam_scores", beam_scores, torch.float32, (N, K), dev)
+    if finished is not None:
+        _check_at("finished", finished, torch.uint8, (N, K), dev)
+    if scores_out is None:
+        scores_out = torch.empty_like(beam_scores)
+    else:
+        _check_at("scores_out", scores_out, torch.float32, (N, K), dev)
+    if parent is None:
+        parent = torch.empty((N, K), dtype=torch.int32, device=logits.device)
+    else:
+        _check_at("parent", parent, torch.int32, (N, K), dev)
+    if token is None:
+        token = torch.empty((N, K), dtype=torch.int32, device=logits.device)
+    else:
+        _check_at("token", token, torch.int32, (N, K), dev)
+    if finished_out is None:
+        if finished is not None:
+            finished_out = torch.empty_like(finished)
+    else:
+        _check_at("finished_out", finished_out, torch.uint8, (N, K), dev)
+    code = _dt(logits.dtype)
+    need = 0 if workspace is not None else L.kda_beam_select_workspace_size(N, K, V, code)
+    workspace, wbytes = _workspace(workspace, need, dev)
+    rc = L.kda_beam_select(logits.data_ptr(), max(step, V), beam_scores.data_ptr(),
+                           None if finished is None else finished.data_ptr(), eos_token, N, K, V, code,
+                           scores_out.data_ptr(), parent.data_ptr(), token.data_ptr(),
+                           None if finished_out is None else finished_out.data_ptr(), workspace.data_ptr(), wbytes,
+                           _raw_stream(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_beam_select", rc)
+    return scores_out, parent, token, finished_out
+
+
+def kda_copy_pages(pools, src, dst, *, stream=None):
+    """Copies slot src[i] to slot dst[i] on every layer of every pool.  pools: tensors [layers, slots, ...]
+    (any dtype, contiguous slots); src, dst [n] int32 (src None: src[i] = i); negative entries are skipped."""
+    dev = _cuda_index("dst", dst)
+    n = dst.shape[0]
+    _check_at("dst", dst, torch.int32, (n,), dev)
+    if src is not None:
+        _check_at("src", src, torch.int32, (n,), dev)
+    arr, count = _pools(pools, dev)
+    rc = load().kda_copy_pages(arr, count, None if src is None else src.data_ptr(), dst.data_ptr(), n,
+                               _raw_stream(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_copy_pages", rc)
+
+
+def kda_state_fork(pools, state_idx, parent, *, state_idx_out=None, stream=None):
+    """Gives each row i of a decode batch the state of row parent[i] (-1: a row that starts anew); returns the
+    new state_idx [B], a permutation of the old one.  pools: one tensor or several [layers, slots, ...] of
+    states (kda_decode_step's pool is pool[layer]).  Copies only states that two rows continue."""
+    dev = _cuda_index("state_idx", state_idx)
+    parent = parent.reshape(-1) if parent.dim() != 1 else parent
+    B = state_idx.shape[0]
+    _check_at("state_idx", state_idx, torch.int32, (B,), dev)
+    _check_at("parent", parent, torch.int32, (B,), dev)
+    if state_idx_out is None:
+        state_idx_out = torch.empty_like(state_idx)
+    else:
+        _check_at("state_idx_out", state_idx_out, torch.int32, (B,), dev)
+    arr, count = _pools(pools, dev)
+    rc = load().kda_state_fork(arr, count, state_idx.data_ptr(), parent.data_ptr(), B, state_idx_out.data_ptr(),
+                               _raw_stream(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_state_fork", rc)
+    return state_idx_out
+
+
+def kda_cache_fork_workspace_size(rows_in: int, rows_out: int, max_pages: int, num_pages: int) -> int:
+    return int(load().kda_cache_fork_workspace_size(rows_in, rows_out, max_pages, num_pages))
+
+
+def kda_cache_fork(block_table, seq_lens, parent, ref_count, page_size: int, *, grow=None, pools=(),
+                   block_table_out=None, seq_lens_out=None, ref_count_out=None, copy_src=None, copy_dst=None,
+                   workspace=None, stream=None):
+    """Replaces the rows of a block table: row i continues old row parent[i] (-1: an empty row) and gets room
+    for grow[i] more tokens.  Returns (block_table, seq_lens, ref_count) of the new rows.
+
+    block_table [R, M], seq_lens [R], parent [R'], grow [R'] or None, ref_count [P], all int32.  Whole pages
+    are shared and counted, a partly filled last page stays with one row and is copied for the others (on every
+    layer of `pools`, tensors [layers, P, ...]), and pages come from the free ones, the lowest first.
+    ref_count is updated in place unless ref_count_out is given.  copy_src, copy_dst [R'] receive the pages
+    copied, for pools that are not passed here.
+    """
+    L = load()
+    dev = _cuda_index("block_table", block_table)
+    parent = parent.reshape(-1) if parent.dim() != 1 else parent
+    R, M = block_table.shape
+    P, R2 = ref_count.shape[0], parent.shape[0]
+    _check_at("block_table", block_table, torch.int32, (R, M), dev)
+    _check_at("seq_lens", seq_lens, torch.int32, (R,), dev)
+    _check_at("parent", parent, torch.int32, (R2,), dev)
+    _check_at("ref_count", ref_count, torch.int32, (P,), dev)
+    if grow is not None:
+        _check_at("grow", grow, torch.int32, (R2,), dev)
+    if block_table_out is None:
+        block_table_out = torch.empty((R2, M), dtype=torch.int32, device=block_table.device)
+    else:
+        _check_at("block_table_out", block_table_out, torch.int32, (R2, M), dev)
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty(R2, dtype=torch.int32, device=block_table.device)
+    else:
+        _check_at("seq_lens_out", seq_lens_out, torch.int32, (R2,), dev)
+    if ref_count_out is None:
+        ref_count_out = ref_count
+    else:
+        _check_at("ref_count_out", ref_count_out, torch.int32, (P,), dev)
+    cs = cd = None
+    if copy_src is not None or copy_dst is not None:
+        _check_at("copy_src", copy_src, torch.int32, (R2,), dev)
+        _check_at("copy_dst", copy_dst, torch.int32, (R2,), dev)
+        cs, cd = copy_src.data_ptr(), copy_dst.data_ptr()
+    arr, count = _pools(pools, dev)
+    need = 0 if workspace is not None else L.kda_cache_fork_workspace_size(R, R2, M, P)
+    workspace, wbytes = _workspace(workspace, need, dev)
+    rc = L.kda_cache_fork(block_table.data_ptr(), seq_lens.data_ptr(), R, parent.data_ptr(),
+                          None if grow is None else grow.data_ptr(), R2, M, page_size, ref_count.data_ptr(), P,
+                          block_table_out.data_ptr(), seq_lens_out.data_ptr(), ref_count_out.data_ptr(), cs, cd, arr,
+                          count, workspace.data_ptr(), wbytes, _raw_stream(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_cache_fork", rc)
+    return block_table_out, seq_lens_out, ref_count_out
+
+
+def kda_cache_compact_workspace_size(num_pages: int) -> int:
+    return int(load().kda_cache_compact_workspace_size(num_pages))
+
+
+def kda_cache_compact(block_table, ref_count, *, pools=(), block_table_out=None, ref_count_out=None, page_map=None,
+                      workspace=None, stream=None):
+    """Moves the live pages (ref_count > 0) together at the low end of the pools; returns (block_table,
+    ref_count, page_map) with the new numbers.  block_table and ref_count are updated in place unless outputs are
+    given; page_map [P] int32 holds each page's new number, -1 for a free one."""
+    L = load()
+    dev = _cuda_index("block_table", block_table)
+    R, M = block_table.shape
+    P = ref_count.shape[0]
+    _check_at("block_table", block_table, torch.int32, (R, M), dev)
+    _check_at("ref_count", ref_count, torch.int32, (P,), dev)
+    if block_table_out is None:
+        block_table_out = block_table
+    else:
+        _check_at("block_table_out", block_table_out, torch.int32, (R, M), dev)
+    if ref_count_out is None:
+        ref_count_out = ref_count
+    else:
+        _check_at("ref_count_out", ref_count_out, torch.int32, (P,), dev)
+    if page_map is None:
+        page_map = torch.empty_like(ref_count)
+    else:
+        _check_at("page_map", page_map, torch.int32, (P,), dev)
+    arr, count = _pools(pools, dev)
+    need = 0 if workspace is not None else L.kda_cache_compact_workspace_size(P)
+    workspace, wbytes = _workspace(workspace, need, dev)
+    rc = L.kda_cache_compact(block_table.data_ptr(), R, M, ref_count.data_ptr(), P, block_table_out.data_ptr(),
+                             ref_count_out.data_ptr(), page_map.data_ptr(), arr, count, workspace.data_ptr(), wbytes,
+                             _raw_stream(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_cache_compact", rc)
+    return block_table_out, ref_count_out, page_map
 
 
 def kda_get_device_error(stream=None) -> int:

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "kda_internal.cuh"
+#include "kda_serve.cuh"
 
 namespace {
 
@@ -72,6 +73,8 @@ int32_t g_test_stall = 0;   // test builds only: set by kda_test_stall_prefill
 #endif
 
 }  // namespace
+
+kda_status kda::device_error_word(unsigned** out) { return error_word(out); }
 
 #ifdef KDA_TEST_HOOKS
 // Test builds only (-DKDA_TEST_HOOKS; not in kda.h): while `on` is nonzero, the tcgen05 prefill kernels of

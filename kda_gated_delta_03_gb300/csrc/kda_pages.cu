@@ -1,0 +1,578 @@
+// Slots and pages: copies within pools, the fork of a batch's KDA states, and the fork and the compaction
+// of a paged cache.
+//
+// None of this computes anything; what it costs is the bytes that have to move and the latency of the
+// bookkeeping in front of them.  So the bookkeeping is one kernel on one thread-block cluster, whose CTAs
+// meet at the hardware's cluster barrier between the steps that depend on one another (a chain of small
+// launches would pay a launch each), and the copies are one kernel over the whole GPU that reads its work
+// list from the bookkeeping.  Every list is ranked by prefix sums, never by the order in which atomics
+// arrive: two calls give the same tables.
+
+#include <climits>
+
+#include "kda_serve.cuh"
+
+namespace kda {
+namespace {
+
+// ---- copies ----
+constexpr int CT = 256;                       // threads of a copying CTA
+constexpr int64_t PIECE = 16384;              // bytes of a slot that one group of threads moves at a time
+constexpr int CV = 4;                         // 16-byte vectors that a thread has in flight
+
+// The group of CTAs' threads moves all pieces of n slots within one pool; slot_pair(i, src, dst) names the
+// i-th copy (false: skip it).  A slot smaller than a piece is moved by fewer threads, so that small pages
+// still fill the CTA.
+template <typename Pair>
+__device__ __forceinline__ void copy_pool(const kda_pool& p, int64_t n, Pair slot_pair, unsigned* err, unsigned err_bit) {
+    const int64_t vecs = p.slot_bytes / 16, pieces = (p.slot_bytes + PIECE - 1) / PIECE;
+    const int64_t per = (vecs + pieces - 1) / pieces;                      // vectors of a piece
+    int lanes = 8;
+    while (lanes < CT && lanes * CV < per) lanes *= 2;
+    const int groups = CT / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    const int64_t units = n * p.layers * pieces;
+    for (int64_t u = (int64_t)blockIdx.x * groups + group; u < units; u += (int64_t)gridDim.x * groups) {
+        const int64_t piece = u % pieces, r = u / pieces;
+        const int64_t layer = r % p.layers, pair = r / p.layers;
+        int src, dst;
+        if (!slot_pair(pair, src, dst)) continue;
+        if (src < 0 || src >= p.slots || dst < 0 || dst >= p.slots) {
+            if (lane == 0) atomicOr(err, err_bit);
+            continue;
+        }
+        char* base = static_cast<char*>(p.data) + layer * p.layer_stride;
+        const uint4* from = reinterpret_cast<const uint4*>(base + src * p.slot_stride);
+        uint4* to = reinterpret_cast<uint4*>(base + dst * p.slot_stride);
+        const int64_t end = min(vecs, (piece + 1) * per);
+        for (int64_t v = piece * per + lane; v < end; v += (int64_t)lanes * CV) {
+            uint4 x[CV];
+#pragma unroll
+            for (int k = 0; k < CV; ++k)
+                if (v + k * lanes < end) x[k] = __ldcs(from + v + k * lanes);
+#pragma unroll
+            for (int k = 0; k < CV; ++k)
+                if (v + k * lanes < end) __stcs(to + v + k * lanes, x[k]);
+        }
+    }
+}
+
+// Copies the pairs of a list; its length is n, or *n_dev where an earlier kernel counts it.
+__global__ void __launch_bounds__(CT) kda_copy_kernel(const __grid_constant__ PoolSet set, const int32_t* src,
+                                                      const int32_t* dst, int32_t n, const int32_t* n_dev,
+                                                      unsigned* err) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t count = n_dev ? *n_dev : n;
+    for (int i = 0; i < set.n; ++i)
+        copy_pool(set.pool[i], count,
+                  [&](int64_t pair, int& s, int& d) {
+                      d = dst[pair];
+                      s = src ? src[pair] : (int)pair;
+                      return s >= 0 && d >= 0 && s != d;
+                  },
+                  err, KDA_DEVERR_PAGES);
+}
+
+// ---- block-wide exclusive prefix sums ----
+template <typename T, int NT>
+__device__ __forceinline__ T block_scan(T x, T& total, T* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const T y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    __syncthreads();                                   // warp_sums of an earlier scan is read no more
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    T before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        const T s = warp_sums[w];
+        if (w < warp) before += s;
+        sum += s;
+    }
+    total = sum;
+    return before + inc - x;
+}
+
+// ---- the fork of a batch's states ----
+// Every CTA works out the whole plan (a few thousand integers at most) and copies its share, so that the
+// call is one launch.  Shared memory: first[B], then the rows that need a copy and the free rows.
+__global__ void __launch_bounds__(CT) kda_state_fork_kernel(const __grid_constant__ PoolSet set,
+                                                            const int32_t* state_idx, const int32_t* parent, int32_t B,
+                                                            int32_t* out, unsigned* err) {
+    extern __shared__ int32_t fork_sm[];
+    __shared__ unsigned long long sums[CT / 32];
+    int32_t* first = fork_sm;
+    uint16_t* extra = reinterpret_cast<uint16_t*>(first + B);
+    uint16_t* freed = extra + B;
+    for (int i = threadIdx.x; i < B; i += CT) first[i] = INT_MAX;
+    __syncthreads();
+    for (int i = threadIdx.x; i < B; i += CT) {
+        const int p = parent[i];
+        if (p >= 0 && p < B) atomicMin(&first[p], i);
+        else if (p != -1 && blockIdx.x == 0) atomicOr(err, KDA_DEVERR_PARENT);
+    }
+    __syncthreads();
+    // ranks of the rows that need a copy (bits 0-19), of the free rows (20-39) and of the new rows (40-59)
+    unsigned long long base = 0;
+    for (int t = 0; t < B; t += CT) {
+        const int i = t + threadIdx.x;
+        const int p = i < B ? parent[i] : -1;
+        const bool goes_on = p >= 0 && p < B;
+        const bool is_extra = goes_on && first[p] != i, is_free = i < B && first[i] == INT_MAX;
+        const unsigned long long flags = (is_extra ? 1ull : 0) | (is_free ? 1ull << 20 : 0);
+        unsigned long long total;
+        const unsigned long long at = base + block_scan<unsigned long long, CT>(flags, total, sums);
+        if (is_extra) extra[at & 0xFFFFF] = (uint16_t)i;
+        if (is_free) freed[(at >> 20) & 0xFFFFF] = (uint16_t)i;
+        base += total;
+    }
+    __syncthreads();
+    const int copies = (int)(base & 0xFFFFF);
+    if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < copies; i += CT) out[extra[i]] = state_idx[freed[i]];
+        int started = 0;
+        for (int t = 0; t < B; t += CT) {
+            const int i = t + threadIdx.x;
+            const int p = i < B ? parent[i] : -1;
+            const bool goes_on = p >= 0 && p < B;
+            unsigned long long total;
+            const unsigned long long at = block_scan<unsigned long long, CT>(i < B && !goes_on ? 1 : 0, total, sums);
+            if (goes_on && first[p] == i) out[i] = state_idx[p];
+            if (i < B && !goes_on) out[i] = state_idx[freed[copies + started + (int)at]];
+            started += (int)total;
+        }
+    }
+    for (int i = 0; i < set.n; ++i)
+        copy_pool(set.pool[i], copies,
+                  [&](int64_t pair, int& s, int& d) {
+                      s = state_idx[parent[extra[pair]]];
+                      d = state_idx[freed[pair]];
+                      return true;
+                  },
+                  err, KDA_DEVERR_STATE_IDX);
+}
+
+// ---- one cluster's bookkeeping ----
+constexpr int NC = 8;                         // CTAs of the cluster
+constexpr int PT = 1024;                      // threads of each
+
+// Everything that the cluster's threads wrote before is seen by all of them after.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+struct ForkScratch {
+    int32_t* first;              // [rows_in] the lowest new row that continues an old one
+    int32_t* count;              // [rows_in] how many continue it
+    int32_t* fresh_at;           // [rows_out] pages of its own before row i, counted within its CTA's rows
+    int32_t* copy_at;            // [rows_out] likewise for copies
+    int32_t* fresh;              // [num_pages] the pages handed out, in order
+    int32_t* src;                // [rows_out] the copies
+    int32_t* dst;
+    int32_t* totals;             // [3][NC] pages of their own, copies, free pages per CTA; then the copies' number
+};
+constexpr int TOTALS = 3 * NC + 1;
+
+size_t pad(size_t ints) { return (ints + 63) / 64 * 64; }
+
+ForkScratch fork_scratch(int32_t* w, int32_t rows_in, int32_t rows_out, int32_t num_pages, size_t* ints) {
+    ForkScratch s;
+    size_t at = 0;
+    auto take = [&](size_t n) { int32_t* p = w ? w + at : nullptr; at += pad(n); return p; };
+    s.totals = take(TOTALS);
+    s.first = take(rows_in);
+    s.count = take(rows_in);
+    s.fresh_at = take(rows_out);
+    s.copy_at = take(rows_out);
+    s.src = take(rows_out);
+    s.dst = take(rows_out);
+    s.fresh = take(num_pages);
+    if (ints) *ints = at;
+    return s;
+}
+
+struct RowPlan {
+    int parent;                  // -1: none
+    int shared;                  // pages taken over from the parent
+    int need;                    // pages in all
+    int full;                    // whole pages of the parent
+    int len;                     // new length
+    bool copy;                   // page `full` is a copy of the parent's
+};
+
+__device__ __forceinline__ int old_length(const ForkParams& p, int row) {
+    const int len = p.lens[row];
+    return len < 0 || len > p.max_pages * p.page_size ? 0 : len;
+}
+
+__device__ __forceinline__ RowPlan row_plan(const ForkParams& p, const ForkScratch& s, int i) {
+    RowPlan r;
+    const int cap = p.max_pages * p.page_size;
+    r.parent = p.parent[i];
+    if (r.parent < 0 || r.parent >= p.rows_in) r.parent = -1;
+    const int len = r.parent < 0 ? 0 : old_length(p, r.parent);
+    int grow = p.grow ? p.grow[i] : 0;
+    if (grow < 0 || grow > cap - len) {
+        atomicOr(p.err, KDA_DEVERR_PAGES);
+        grow = grow < 0 ? 0 : cap - len;
+    }
+    r.len = len + grow;
+    r.full = len / p.page_size;
+    r.copy = len > r.full * p.page_size && s.first[r.parent] != i;
+    r.shared = r.copy ? r.full : (len + p.page_size - 1) / p.page_size;
+    r.need = (int)(((int64_t)r.len + p.page_size - 1) / p.page_size);
+    return r;
+}
+
+__global__ void __launch_bounds__(PT) kda_cache_fork_kernel(ForkParams p, ForkScratch s) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ unsigned long long sums[PT / 32];
+    const int cta = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    const int gt = cta * PT + tid, gw = gt >> 5;
+    constexpr int GT = NC * PT, GW = GT / 32;
+
+    // counts start from the old ones
+    for (int i = gt; i < p.rows_in; i += GT) {
+        s.first[i] = INT_MAX;
+        s.count[i] = 0;
+        const int len = p.lens[i];
+        if (len < 0 || len > p.max_pages * p.page_size) atomicOr(p.err, KDA_DEVERR_PAGES);
+    }
+    if (p.ref_out != p.ref)
+        for (int i = gt; i < p.num_pages; i += GT) p.ref_out[i] = p.ref[i];
+    cluster_sync();
+
+    // who continues whom
+    for (int i = gt; i < p.rows_out; i += GT) {
+        const int q = p.parent[i];
+        if (q >= 0 && q < p.rows_in) {
+            atomicMin(&s.first[q], i);
+            atomicAdd(&s.count[q], 1);
+        } else if (q != -1) {
+            atomicOr(p.err, KDA_DEVERR_PARENT);
+        }
+    }
+    cluster_sync();
+
+    // pages of its own and copies of every new row, ranked within this CTA's rows
+    const int rows = (p.rows_out + NC - 1) / NC, r0 = min(cta * rows, p.rows_out), r1 = min(r0 + rows, p.rows_out);
+    unsigned long long base = 0;                       // pages (bits 0-31) and copies (32-63) so far
+    for (int t = r0; t < r1; t += PT) {
+        const int i = t + tid;
+        unsigned long long mine = 0;
+        if (i < r1) {
+            const RowPlan r = row_plan(p, s, i);
+            mine = (unsigned)(r.need - r.shared) | (r.copy ? 1ull << 32 : 0ull);
+        }
+        unsigned long long total;
+        const unsigned long long at = base + block_scan<unsigned long long, PT>(mine, total, sums);
+        if (i < r1) {
+            s.fresh_at[i] = (int)(at & 0xFFFFFFFFu);
+            s.copy_at[i] = (int)(at >> 32);
+        }
+        base += total;
+    }
+    if (tid == 0) {
+        s.totals[cta] = (int)(base & 0xFFFFFFFFu);
+        s.totals[NC + cta] = (int)(base >> 32);
+    }
+    // pages that are taken over, and what the old rows' counts change by: a row continued c times names its
+    // whole pages c times instead of once, and its last, partly filled one once if anybody continues it
+    for (int i = gw; i < p.rows_out; i += GW) {
+        const RowPlan r = row_plan(p, s, i);
+        for (int j = lane; j < p.max_pages; j += 32) {
+            int page = -1;
+            if (j < r.shared) {
+                page = p.table[(int64_t)r.parent * p.max_pages + j];
+                if (page < 0 || page >= p.num_pages) {
+                    atomicOr(p.err, KDA_DEVERR_PAGES);
+                    page = -1;
+                }
+            }
+            p.table_out[(int64_t)i * p.max_pages + j] = page;
+        }
+    }
+    for (int i = gw; i < p.rows_in; i += GW) {
+        const int c = s.count[i];
+        if (c == 1) continue;
+        const int len = old_length(p, i), full = len / p.page_size, pages = full + (len % p.page_size != 0);
+        for (int j = lane; j < pages; j += 32) {
+            const int page = p.table[(int64_t)i * p.max_pages + j];
+            const int change = j < full ? c - 1 : c > 0 ? 0 : -1;
+            if (page >= 0 && page < p.num_pages) {
+                if (change) atomicAdd(&p.ref_out[page], change);
+            } else {
+                atomicOr(p.err, KDA_DEVERR_PAGES);
+            }
+        }
+    }
+    cluster_sync();
+
+    // the lowest free pages, in order
+    int wanted = 0;
+    for (int c = 0; c < NC; ++c) wanted += s.totals[c];
+    const int seg = (p.num_pages + NC - 1) / NC, p0 = min(cta * seg, p.num_pages), p1 = min(p0 + seg, p.num_pages);
+    int available = 0;
+    if (wanted > 0) {
+        int mine = 0;
+        for (int i = p0 + tid; i < p1; i += PT) mine += p.ref_out[i] == 0;
+        unsigned long long total;
+        block_scan<unsigned long long, PT>((unsigned long long)mine, total, sums);
+        if (tid == 0) s.totals[2 * NC + cta] = (int)total;
+        cluster_sync();
+        int at = 0;
+        for (int c = 0; c < NC; ++c) {
+            if (c < cta) at += s.totals[2 * NC + c];
+            available += s.totals[2 * NC + c];
+        }
+        for (int t = p0; t < p1 && at < wanted; t += PT) {
+            const int i = t + tid;
+            const bool is_free = i < p1 && p.ref_out[i] == 0;
+            unsigned long long found;
+            const int rank = at + (int)block_scan<unsigned long long, PT>(is_free ? 1 : 0, found, sums);
+            if (is_free && rank < wanted) {
+                s.fresh[rank] = i;
+                p.ref_out[i] = 1;
+            }
+            at += (int)found;
+        }
+        cluster_sync();
+    }
+
+    // the pages of their own into the new rows, the new lengths, and the copies
+    int copies = 0;
+    for (int c = 0; c < NC; ++c) copies += s.totals[NC + c];
+    if (gt == 0) s.totals[3 * NC] = copies;
+    for (int i = gw; i < p.rows_out; i += GW) {
+        const RowPlan r = row_plan(p, s, i);
+        int at = s.fresh_at[i], copy_at = s.copy_at[i];
+        for (int c = 0; c < i / rows; ++c) {
+            at += s.totals[c];
+            copy_at += s.totals[NC + c];
+        }
+        for (int j = r.shared + lane; j < r.need; j += 32) {
+            const int rank = at + j - r.shared;
+            if (rank < available) p.table_out[(int64_t)i * p.max_pages + j] = s.fresh[rank];
+        }
+        if (lane == 0) {
+            int len = r.len, src = -1, dst = -1;
+            if (at + r.need - r.shared > available && r.need > r.shared) {
+                atomicOr(p.err, KDA_DEVERR_EXHAUSTED);
+                const int have = max(0, min(available - at, r.need - r.shared));
+                len = min(len, (r.shared + have) * p.page_size);
+            }
+            p.lens_out[i] = len;
+            if (r.copy) {
+                src = p.table[(int64_t)r.parent * p.max_pages + r.full];
+                dst = at < available ? s.fresh[at] : -1;
+                if (src < 0 || src >= p.num_pages || dst < 0) {
+                    if (dst >= 0) atomicOr(p.err, KDA_DEVERR_PAGES);
+                    src = dst = -1;
+                }
+                s.src[copy_at] = src;
+                s.dst[copy_at] = dst;
+            }
+            if (p.copy_src) {
+                p.copy_src[i] = src;
+                p.copy_dst[i] = dst;
+            }
+        }
+    }
+}
+
+struct CompactScratch {
+    int32_t* movers;             // [num_pages] live pages at n_live and above, the last first
+    int32_t* holes;              // [num_pages] free pages below n_live
+    int32_t* src;                // [num_pages] the copies
+    int32_t* dst;
+    int32_t* totals;             // [2][NC] live pages, holes per CTA; then the copies' number
+};
+
+CompactScratch compact_scratch(int32_t* w, int32_t num_pages, size_t* ints) {
+    CompactScratch s;
+    size_t at = 0;
+    auto take = [&](size_t n) { int32_t* p = w ? w + at : nullptr; at += pad(n); return p; };
+    s.totals = take(2 * NC + 1);
+    s.movers = take(num_pages);
+    s.holes = take(num_pages);
+    s.src = take(num_pages);
+    s.dst = take(num_pages);
+    if (ints) *ints = at;
+    return s;
+}
+
+// With n live pages and `below` of them under n, the live page of rank r >= below (counted from 0) goes to
+// the hole of rank r - below.  `below` is known only once every CTA has counted, so the movers are listed
+// from the last live page backwards (rank n - 1 first) and paired with the holes a step later.
+__global__ void __launch_bounds__(PT) kda_cache_compact_kernel(CompactParams p, CompactScratch s) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ unsigned long long sums[PT / 32];
+    const int cta = blockIdx.x, tid = threadIdx.x, gt = cta * PT + tid;
+    constexpr int GT = NC * PT;
+    const int seg = (p.num_pages + NC - 1) / NC, p0 = min(cta * seg, p.num_pages), p1 = min(p0 + seg, p.num_pages);
+
+    int mine = 0;
+    for (int i = p0 + tid; i < p1; i += PT) mine += p.ref[i] > 0;
+    unsigned long long total;
+    block_scan<unsigned long long, PT>((unsigned long long)mine, total, sums);
+    if (tid == 0) s.totals[cta] = (int)total;
+    cluster_sync();
+    int live = 0, n = 0;                               // live pages before this CTA's, and in all
+    for (int c = 0; c < NC; ++c) {
+        if (c < cta) live += s.totals[c];
+        n += s.totals[c];
+    }
+    int my_holes = 0;
+    for (int t = p0; t < p1; t += PT) {
+        const int i = t + tid;
+        const int ref = i < p1 ? p.ref[i] : 0;
+        const bool is_live = ref > 0;
+        unsigned long long found;
+        const int rank = live + (int)block_scan<unsigned long long, PT>(is_live ? 1 : 0, found, sums);
+        live += (int)found;
+        if (i >= p1) continue;
+        if (is_live && i >= n) {
+            s.movers[n - 1 - rank] = i;
+        } else {
+            p.page_map[i] = is_live ? i : -1;
+            if (!is_live && i < n) {
+                s.holes[i - rank] = i;
+                ++my_holes;
+            } else {
+                p.ref_out[i] = is_live ? ref : 0;
+            }
+        }
+    }
+    block_scan<unsigned long long, PT>((unsigned long long)my_holes, total, sums);
+    if (tid == 0) s.totals[NC + cta] = (int)total;
+    cluster_sync();
+    int moves = 0;
+    for (int c = 0; c < NC; ++c) moves += s.totals[NC + c];
+    if (gt == 0) s.totals[2 * NC] = moves;
+    for (int i = gt; i < moves; i += GT) {
+        const int src = s.movers[moves - 1 - i], dst = s.holes[i], ref = p.ref[src];
+        s.src[i] = src;
+        s.dst[i] = dst;
+        p.page_map[src] = dst;
+        p.ref_out[dst] = ref;
+        p.ref_out[src] = 0;
+    }
+    cluster_sync();
+    for (int64_t e = gt; e < p.entries; e += GT) {
+        const int page = p.table[e];
+        p.table_out[e] = page >= 0 && page < p.num_pages ? p.page_map[page] : -1;
+    }
+}
+
+cudaError_t sm_count(int* sms) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+// CTAs that copy n slots (at most): one per piece, up to eight per SM.
+cudaError_t copy_grid(const PoolSet& set, int64_t n, int* grid) {
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    int64_t most = 1;
+    for (int i = 0; i < set.n; ++i) {
+        const int64_t units = n * set.pool[i].layers * ((set.pool[i].slot_bytes + PIECE - 1) / PIECE);
+        most = units > most ? units : most;
+    }
+    *grid = (int)(most < 8 * (int64_t)sms ? most : 8 * (int64_t)sms);
+    return cudaSuccess;
+}
+
+// `after`: the list comes from the kernel launched just before on this stream, whose end the copying kernel
+// waits for itself, so that its launch is already done by then.
+cudaError_t launch_copy(const PoolSet& set, const int32_t* src, const int32_t* dst, int32_t n, const int32_t* n_dev,
+                        unsigned* err, bool after, cudaStream_t s) {
+    int grid = 0;
+    const cudaError_t e = copy_grid(set, n, &grid);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(CT);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kda_copy_kernel, set, src, dst, n, n_dev, err);
+}
+
+template <typename... Args, typename... Given>
+cudaError_t launch_cluster(void (*kernel)(Args...), cudaStream_t s, Given... given) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(NC);
+    cfg.blockDim = dim3(PT);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = NC;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, given...);
+}
+
+}  // namespace
+
+cudaError_t launch_copy_pages(const PoolSet& pools, const int32_t* src, const int32_t* dst, int32_t n, unsigned* err,
+                              cudaStream_t s) {
+    return launch_copy(pools, src, dst, n, nullptr, err, false, s);
+}
+
+cudaError_t launch_state_fork(const PoolSet& pools, const int32_t* state_idx, const int32_t* parent, int32_t B,
+                              int32_t* state_idx_out, unsigned* err, cudaStream_t s) {
+    int grid = 0;
+    cudaError_t e = copy_grid(pools, B, &grid);
+    if (e != cudaSuccess) return e;
+    const size_t smem = (size_t)B * 8;
+    if (smem > 48 * 1024) {
+        e = cudaFuncSetAttribute(kda_state_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 KDA_FORK_MAX_ROWS * 8);
+        if (e != cudaSuccess) return e;
+    }
+    kda_state_fork_kernel<<<grid, CT, smem, s>>>(pools, state_idx, parent, B, state_idx_out, err);
+    return cudaGetLastError();
+}
+
+size_t cache_fork_workspace(int32_t rows_in, int32_t rows_out, int32_t max_pages, int32_t num_pages) {
+    size_t ints = 0;
+    fork_scratch(nullptr, rows_in, rows_out, num_pages, &ints);
+    return ints * 4;
+}
+
+cudaError_t launch_cache_fork(const ForkParams& p, const PoolSet& pools, void* workspace, cudaStream_t s) {
+    const ForkScratch sc = fork_scratch(static_cast<int32_t*>(workspace), p.rows_in, p.rows_out, p.num_pages, nullptr);
+    const cudaError_t e = launch_cluster(kda_cache_fork_kernel, s, p, sc);
+    if (e != cudaSuccess || pools.n == 0 || p.rows_out == 0) return e;
+    return launch_copy(pools, sc.src, sc.dst, p.rows_out, sc.totals + 3 * NC, p.err, true, s);
+}
+
+size_t cache_compact_workspace(int32_t num_pages) {
+    size_t ints = 0;
+    compact_scratch(nullptr, num_pages, &ints);
+    return ints * 4;
+}
+
+cudaError_t launch_cache_compact(const CompactParams& p, const PoolSet& pools, void* workspace, unsigned* err,
+                                 cudaStream_t s) {
+    if (p.num_pages == 0) {
+        if (p.entries == 0) return cudaSuccess;
+        return cudaMemsetAsync(p.table_out, 0xFF, p.entries * sizeof(int32_t), s);       // no page is live: all -1
+    }
+    const CompactScratch sc = compact_scratch(static_cast<int32_t*>(workspace), p.num_pages, nullptr);
+    const cudaError_t e = launch_cluster(kda_cache_compact_kernel, s, p, sc);
+    if (e != cudaSuccess || pools.n == 0) return e;
+    return launch_copy(pools, sc.src, sc.dst, p.num_pages / 2 + 1, sc.totals + 2 * NC, err, true, s);
+}
+
+}  // namespace kda
