@@ -3,108 +3,832 @@
 //   s_t = scale * q . k_t,   o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),   m = max_t s_t
 //
 // in one pass: the running maximum and sum of the softmax, the sum over the values rescaled whenever the
-// maximum grows.
+// maximum grows.  Exponents are taken in base 2 (scale * log2 e folded into the scores).  Every key and
+// value is read once and meets the g = H_q / H_kv query heads that share it, 4 g flop for 2 elements, so
+// with bf16 caches and g up to 32 the reads bound the kernel, not the products.
+//
+// The visible tokens of all rows and heads are numbered tile after tile and cut into equal contiguous
+// shares, one per CTA (two CTAs per SM), so that one long sequence, many short ones and anything between
+// fill the GPU alike.  The shares are worked out on the device from seq_lens; the host never sees them.
+// Inside a CTA each warp takes every fourth sub-tile of TS tokens through its own ring of asynchronous
+// copies (cp.async, no barrier with other warps) and keeps its own maximum, sum and accumulator; the four
+// are joined in shared memory where a (row, head) unit ends.  A unit that a share's border cuts leaves
+// partial results in the workspace, which a second kernel joins in the order of the CTAs: no atomics, the
+// same bits on every call.
+//
+// The products: with the tokens as the 16 rows of mma.m16n8k16 and the query heads as its 8 columns, both
+// products take the cache as the A operand straight from shared memory (K by ldmatrix, V by ldmatrix.trans)
+// and leave no padding at 8 heads; 2 CTAs x 4 warps need about a tenth of the SM's issue slots at the
+// memory's rate, so the larger tcgen05 tiles (64 rows at least, with the softmax between the two products
+// behind a round trip through tensor memory) would only add latency.  fp32 caches take the same path
+// with FFMA.
 
 #include <cmath>
+#include <type_traits>
 
 #include "kda_serve.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int AT = 128;                       // threads: four warps, each on every fourth token
+constexpr int NW = 4;                         // warps of a CTA
+constexpr int AT = NW * 32;
+constexpr int CTAS_PER_SM = 2;
+constexpr int MAX_CTAS = 512;                 // of the main kernel, whatever the GPU (bounds the workspace)
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
 
-__device__ __forceinline__ bool visible(const AttnParams& p, int t, int len) {
-    return t < len && (p.window == 0 || t >= len - p.window || t < p.sinks);
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 16 bytes from global to shared memory; zeros, and no read, where `read` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(AT) kda_attn_simple_kernel(AttnParams p) {
-    constexpr int W = AT / 32, E = (D + 31) / 32;
-    const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, kvh = h / (p.Hq / p.Hkv);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ float sm_m[W], sm_l[W], sm_o[W][D];
-    int len = p.lens[b];
-    if (len < 0 || len > p.max_pages * p.page_size) {
-        if (threadIdx.x == 0) atomicOr(p.err, KDA_DEVERR_PAGES);
-        len = 0;
+// ---- which tokens a row's tiles hold ----
+struct Row {
+    int len;
+    int tiles;                   // tiles with a visible token
+    int lead;                    // the first `lead` of them start at token 0,
+    int skip;                    // the others at tile lead + skip (between sinks and window)
+    int from;                    // first token of the window
+};
+
+template <int TILE>
+__device__ __forceinline__ Row row_of(const AttnParams& p, int len) {
+    Row r;
+    r.len = len < 0 || len > p.max_pages * p.page_size ? 0 : len;
+    const int all = (r.len + TILE - 1) / TILE;
+    r.from = p.window > 0 && r.len > p.window ? r.len - p.window : 0;
+    r.lead = r.skip = 0;
+    r.tiles = all;
+    const int sink_tiles = (min(p.sinks, r.from) + TILE - 1) / TILE, first = r.from / TILE;
+    if (first > sink_tiles) {
+        r.lead = sink_tiles;
+        r.skip = first - sink_tiles;
+        r.tiles = all - r.skip;
     }
-    const T* q = static_cast<const T*>(p.q) + ((int64_t)b * p.Hq + h) * D;
-    float qr[E], acc[E], m = -INFINITY, l = 0.f;
+    return r;
+}
+
+// A place in the CTA's share: tile `tile` of unit `unit` (key-value head and head block) of row `b`.
+struct Place {
+    int b, unit, tile;
+    Row row;
+};
+
+template <typename T, int D, int NH>
+struct Core;
+
+// bf16: tokens are the rows and heads the columns of the tensor core's tile.
+template <int D, int NH>
+struct Core<__nv_bfloat16, D, NH> {
+    static constexpr int TS = 16;                       // tokens of a warp's sub-tile
+    static constexpr int CPR = D / 8;                   // 16-byte chunks of a token
+    static constexpr int NT = NH / 8, KT = D / 16;
+    static constexpr int SLOTS = 2 * NT;                // heads that a lane has columns of
+    static constexpr int ACC = NT * KT * 4;
+    static constexpr int QP = D * 2 + 16;               // bytes from head to head of q (conflict-free fragments)
+    static constexpr int P_BYTES = 0;
+
+    uint32_t qf[NT][KT][2];
+    float acc[ACC], m[SLOTS], l[SLOTS];
+
+    __device__ static int swizzle(int row, int chunk) { return D >= 64 ? chunk ^ (row & 7) : chunk; }
+    __device__ static int head_of_slot(int s, int lane) { return (s >> 1) * 8 + 2 * (lane & 3) + (s & 1); }
+    __device__ static int slot_of(int i) { return i / (KT * 4) * 2 + (i & 1); }
+    __device__ static int dim_of(int i, int lane) { return (i / 4 % KT) * 16 + (lane >> 2) + 8 * ((i >> 1) & 1); }
+    __device__ static bool owns_output(int) { return true; }
+    __device__ static bool writes_stats(int lane) { return lane < 4; }
+
+    __device__ void begin(const unsigned char* q, int lane) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        qr[e] = lane + 32 * e < D ? to_float(q[lane + 32 * e]) * p.scale : 0.f;
-        acc[e] = 0.f;
-    }
-    for (int t = warp; t < len; t += W) {
-        if (!visible(p, t, len)) continue;
-        int page = p.table[(int64_t)b * p.max_pages + t / p.page_size];
-        if (page < 0 || page >= p.num_pages) {
-            if (lane == 0) atomicOr(p.err, KDA_DEVERR_PAGES);
-            page = 0;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    qf[n][k][h] = *reinterpret_cast<const uint32_t*>(q + (n * 8 + (lane >> 2)) * QP +
+                                                                     (k * 16 + 2 * (lane & 3) + 8 * h) * 2);
+#pragma unroll
+        for (int i = 0; i < ACC; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            m[s] = -INFINITY;
+            l[s] = 0.f;
         }
-        const int64_t at = ((int64_t)kvh * p.page_size + t % p.page_size) * D;
-        T* kc = static_cast<T*>(p.k_pages) + page * p.k_stride + at;
-        T* vc = static_cast<T*>(p.v_pages) + page * p.v_stride + at;
-        const bool is_new = p.k_new && t == len - 1;
-        const int64_t nat = ((int64_t)b * p.Hkv + kvh) * D;
-        const T* k = is_new ? static_cast<const T*>(p.k_new) + nat : kc;
-        const T* v = is_new ? static_cast<const T*>(p.v_new) + nat : vc;
-        float s = 0.f;
+    }
+
+    // One sub-tile; bit t of `seen`: token t is visible (a token that is not lies in shared memory as zeros).
+    __device__ void step(uint32_t ks, uint32_t vs, unsigned seen, float scale2, unsigned char*, int lane) {
+        float s[NT][4];
+        const int i8 = lane >> 3, r8 = lane & 7;
+        {
+            float s1[NT][4];                            // two chains of products
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (lane + 32 * e < D) s += qr[e] * to_float(k[lane + 32 * e]);
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-        const float c = expf(m - base), w = expf(s - base);
-        l = l * c + w;
-        m = mn;
+                for (int e = 0; e < 4; ++e) s[n][e] = s1[n][e] = 0.f;
+            const int row = (i8 & 1) * 8 + r8;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (lane + 32 * e < D) {
-                acc[e] = acc[e] * c + w * to_float(v[lane + 32 * e]);
-                if (is_new && h % (p.Hq / p.Hkv) == 0) {
-                    kc[lane + 32 * e] = k[lane + 32 * e];
-                    vc[lane + 32 * e] = v[lane + 32 * e];
+            for (int k = 0; k < KT; ++k) {
+                uint32_t a[4];
+                ldsm4(ks + row * (D * 2) + swizzle(row, 2 * k + (i8 >> 1)) * 16, a);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_bf16(k & 1 ? s1[n] : s[n], a, qf[n][k][0], qf[n][k][1]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + s1[n][e]) * scale2;
+        }
+        if (seen != 0xFFFFu) {
+            const bool lo = seen >> (lane >> 2) & 1, hi = seen >> ((lane >> 2) + 8) & 1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!(e < 2 ? lo : hi)) s[n][e] = -INFINITY;
+        }
+        uint32_t ph[NT][2], pl[NT][2];
+        bool grown = false;
+        float keep[SLOTS];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float x = fmaxf(s[n][c], s[n][c + 2]);
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+                const float mn = fmaxf(m[2 * n + c], x), base = mn == -INFINITY ? 0.f : mn;
+                keep[2 * n + c] = exp2_approx(m[2 * n + c] - base);
+                grown |= mn != m[2 * n + c];
+                m[2 * n + c] = mn;
+                s[n][c] = exp2_approx(s[n][c] - base);
+                s[n][c + 2] = exp2_approx(s[n][c + 2] - base);
+            }
+        if (__any_sync(0xFFFFFFFFu, grown)) {
+#pragma unroll
+            for (int i = 0; i < ACC; ++i) acc[i] *= keep[slot_of(i)];
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) l[i] *= keep[i];
+        }
+        // The weights go to the tensor core as bf16 pairs hi + lo (16 bits together): rounded to bf16 alone
+        // they would add 1.1e-3 of relative error to an output that is itself rounded to 1.7e-3.
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float x = s[n][2 * h], y = s[n][2 * h + 1];
+                l[2 * n] += x;
+                l[2 * n + 1] += y;
+                const uint32_t hi = pack_bf16(x, y);
+                const uint32_t lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+                ph[n][h] = transpose8x8(hi);
+                pl[n][h] = transpose8x8(lo);
+            }
+        const int row = (i8 >> 1) * 8 + r8;
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            uint32_t a[4];
+            ldsm4_trans(vs + row * (D * 2) + swizzle(row, 2 * k + (i8 & 1)) * 16, a);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float(&o)[4] = *reinterpret_cast<float(*)[4]>(&acc[(n * KT + k) * 4]);
+                mma_bf16(o, a, ph[n][0], ph[n][1]);
+                mma_bf16(o, a, pl[n][0], pl[n][1]);
+            }
+        }
+    }
+
+    __device__ void sum_lanes() {
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) l[s] += __shfl_xor_sync(0xFFFFFFFFu, l[s], o);
+    }
+};
+
+// fp32: four lanes per token for the scores, then D / 32 output columns per lane.
+template <int D, int NH>
+struct Core<float, D, NH> {
+    static constexpr int TS = 8;
+    static constexpr int CPR = D / 4;
+    static constexpr int E = D >= 32 ? D / 32 : 1;      // columns of a lane (d = 16: lanes 16-31 repeat 0-15)
+    static constexpr int SLOTS = NH;
+    static constexpr int ACC = NH * E;
+    static constexpr int QP = D * 4;
+    static constexpr int P_BYTES = TS * NH * 4;         // the weights, from the token's lanes to all of them
+
+    const unsigned char* q;
+    float acc[ACC], m[SLOTS], l[SLOTS];
+
+    __device__ static int swizzle(int row, int chunk) { return D >= 64 ? chunk ^ ((row & 1) << 2) : chunk; }
+    __device__ static int head_of_slot(int s, int) { return s; }
+    __device__ static int slot_of(int i) { return i / E; }
+    __device__ static int dim_of(int i, int lane) { return (lane * E + i % E) % D; }
+    __device__ static bool owns_output(int lane) { return lane * E < D; }
+    __device__ static bool writes_stats(int lane) { return lane == 0; }
+
+    __device__ void begin(const unsigned char* qbuf, int) {
+        q = qbuf;
+#pragma unroll
+        for (int i = 0; i < ACC; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            m[s] = -INFINITY;
+            l[s] = 0.f;
+        }
+    }
+
+    __device__ void step(uint32_t ks, uint32_t vs, unsigned seen, float scale2, unsigned char* pbuf, int lane) {
+        const int r = lane >> 2, c = lane & 3;
+        float s[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) s[h] = 0.f;
+#pragma unroll
+        for (int j = 0; j < CPR / 4; ++j) {
+            const int chunk = c + 4 * j;
+            float4 k;
+            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(k.x), "=f"(k.y), "=f"(k.z), "=f"(k.w)
+                         : "r"(ks + r * (D * 4) + swizzle(r, chunk) * 16) : "memory");
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                const float4 x = *reinterpret_cast<const float4*>(q + h * QP + chunk * 16);
+                s[h] += x.x * k.x + x.y * k.y + x.z * k.z + x.w * k.w;
+            }
+        }
+        float* pw = reinterpret_cast<float*>(pbuf);
+        bool grown = false;
+        float keep[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            s[h] += __shfl_xor_sync(0xFFFFFFFFu, s[h], 1);
+            s[h] += __shfl_xor_sync(0xFFFFFFFFu, s[h], 2);
+            s[h] = seen >> r & 1 ? s[h] * scale2 : -INFINITY;
+            float x = s[h];
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+            const float mn = fmaxf(m[h], x), base = mn == -INFINITY ? 0.f : mn;
+            keep[h] = exp2_approx(m[h] - base);
+            grown |= mn != m[h];
+            m[h] = mn;
+            s[h] = exp2_approx(s[h] - base);
+            if ((h & 3) == c) pw[r * NH + h] = s[h];
+        }
+        if (__any_sync(0xFFFFFFFFu, grown)) {
+#pragma unroll
+            for (int i = 0; i < ACC; ++i) acc[i] *= keep[slot_of(i)];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) l[h] *= keep[h];
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) l[h] += s[h];
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < TS; ++t) {
+            float v[E];
+            const int d0 = (lane * E) % D;
+            const uint32_t at = vs + t * (D * 4) + swizzle(t, d0 / 4) * 16 + (d0 & 3) * 4;
+#pragma unroll
+            for (int e = 0; e < E; ++e) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[e]) : "r"(at + 4 * e) : "memory");
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                const float w = pw[t * NH + h];
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[h * E + e] += w * v[e];
+            }
+        }
+        __syncwarp();
+    }
+
+    __device__ void sum_lanes() {
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) l[s] += __shfl_xor_sync(0xFFFFFFFFu, l[s], o);
+    }
+};
+
+__host__ __device__ constexpr int piece_floats(int heads, int d) { return (heads * (d + 2) + 3) / 4 * 4; }
+
+template <typename T, int D, int NH>
+struct Layout {
+    using C = Core<T, D, NH>;
+    static constexpr int TILE = NW * C::TS;
+    static constexpr int SUB = C::TS * D * (int)sizeof(T);        // bytes of a sub-tile's keys
+    static constexpr int STAGES = D == 128 ? 3 : D == 64 ? 6 : 8;
+    static constexpr int RING = STAGES * 2 * SUB;                 // of one warp
+    static constexpr int Q = NW * RING;
+    static constexpr int Q_BYTES = NH * C::QP;
+    static constexpr int MERGE = Q + Q_BYTES;                     // two warps' accumulators, one head tile at a time
+    static constexpr int MERGE_REGS = NH == 16 ? (C::ACC < 16 ? C::ACC : 16) : (C::ACC < 32 ? C::ACC : 32);
+    static constexpr int STATS = MERGE + 2 * MERGE_REGS * 32 * 4; // m, l [NW][NH]
+    static constexpr int PW = STATS + 2 * NW * NH * 4;
+    static constexpr int MISC = PW + NW * C::P_BYTES;
+    static constexpr int BYTES = MISC + 32;
+    static_assert(CTAS_PER_SM * (BYTES + 1024) <= 233472, "two CTAs per SM");
+    // workspace: a record per CTA, then its two partial results of o[NH][D], m[NH], l[NH]
+    static constexpr int PIECE = piece_floats(NH, D);
+};
+
+// Partial results of a unit that starts in this CTA's share and goes on in others'.
+struct Record {
+    int b, unit;                 // -1: none
+    int last;                    // the CTA with its end
+    int slot;                    // of the first piece; the others lie in slot 0
+};
+
+template <typename T, int D, int NH>
+__global__ void __launch_bounds__(AT, CTAS_PER_SM) kda_attn_kernel(AttnParams p, int head_blocks, int grid) {
+    using C = Core<T, D, NH>;
+    using L = Layout<T, D, NH>;
+    constexpr int TS = C::TS, TILE = L::TILE, CPR = C::CPR;
+    extern __shared__ __align__(128) unsigned char sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    const int group = p.Hq / p.Hkv, units = p.Hkv * head_blocks;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- this CTA's share ----
+    int* misc = reinterpret_cast<int*>(sm + L::MISC);
+    int64_t total = 0;
+    {
+        int mine = 0;
+        for (int b = tid; b < p.B; b += AT) mine += row_of<TILE>(p, p.lens[b]).tiles;
+        // tiles of all rows: below 2^31 each, the sum in 64 bits
+        int64_t sum = mine;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        int64_t* sums = reinterpret_cast<int64_t*>(sm + L::STATS);
+        if (lane == 0) sums[warp] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < NW; ++w) total += sums[w];
+        __syncthreads();
+    }
+    // no more shares than tiles: none of them is empty, so a unit's pieces lie in consecutive CTAs
+    const int64_t flat = total * units, shares = flat < grid ? flat : grid;
+    const int64_t begin = cta < shares ? cta * flat / shares : flat, end = cta < shares ? (cta + 1) * flat / shares : flat;
+    int left = (int)(end - begin);                      // tiles of this CTA's share
+    Place at{};
+    if (left > 0) {
+        int64_t base = 0;                               // tiles of the rows before
+        int64_t* sums = reinterpret_cast<int64_t*>(sm + L::STATS);
+        for (int b0 = 0; b0 < p.B; b0 += AT) {
+            const int b = b0 + tid;
+            const int mine = b < p.B ? row_of<TILE>(p, p.lens[b]).tiles : 0;
+            int64_t inc = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            if (lane == 31) sums[warp] = inc;
+            __syncthreads();
+            int64_t before = base, chunk = 0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                if (w < warp) before += sums[w];
+                chunk += sums[w];
+            }
+            const int64_t hi = (before + inc) * units, lo = hi - (int64_t)mine * units;
+            if (mine > 0 && begin >= lo && begin < hi) {
+                misc[0] = b;
+                misc[1] = (int)((begin - lo) / mine);
+                misc[2] = (int)((begin - lo) % mine);
+            }
+            base += chunk;
+            __syncthreads();
+            if (begin < base * units) break;
+        }
+        at.b = misc[0];
+        at.unit = misc[1];
+        at.tile = misc[2];
+        at.row = row_of<TILE>(p, p.lens[at.b]);
+    }
+
+    auto next = [&](Place& x) {                         // the tile after x; only called while the share goes on
+        if (++x.tile < x.row.tiles) return;
+        x.tile = 0;
+        if (++x.unit < units) return;
+        x.unit = 0;
+        while (x.b + 1 < p.B) {
+            x.row = row_of<TILE>(p, __ldg(p.lens + ++x.b));
+            if (x.row.tiles > 0) break;
+        }
+    };
+    // this warp's sub-tile of a tile: its first token, and which of its tokens are visible
+    auto sub_tile = [&](const Place& x, unsigned& seen) -> int {
+        const int t = x.tile < x.row.lead ? x.tile : x.tile + x.row.skip;
+        const int first = t * TILE + warp * TS;
+        constexpr unsigned ALL = (1u << TS) - 1;
+        seen = first >= x.row.len ? 0u : x.row.len - first >= TS ? ALL : (1u << (x.row.len - first)) - 1;
+        if (first < x.row.from) {
+            const unsigned win = x.row.from - first >= TS ? 0u : ALL << (x.row.from - first);
+            const unsigned sink = first >= p.sinks ? 0u : p.sinks - first >= TS ? ALL : (1u << (p.sinks - first)) - 1;
+            seen &= win | sink;
+        }
+        return first;
+    };
+    const T* kp = static_cast<const T*>(p.k_pages);
+    const T* vp = static_cast<const T*>(p.v_pages);
+    const uint32_t ring = smem_addr(sm) + warp * L::RING;
+
+    // ---- copies of this warp's next visible sub-tile into stage `stage` ----
+    Place ahead = at;
+    int ahead_left = left, stage_in = 0;
+    const bool whole_pages = p.page_size % TS == 0;     // a sub-tile never crosses a page
+    auto issue = [&]() {
+        unsigned seen = 0;
+        int first = 0;
+        while (ahead_left > 0) {
+            first = sub_tile(ahead, seen);
+            if (seen) break;
+            if (--ahead_left > 0) next(ahead);
+        }
+        if (ahead_left > 0) {
+            const uint32_t dst = ring + stage_in * (2 * L::SUB);
+            stage_in = stage_in + 1 == L::STAGES ? 0 : stage_in + 1;
+            const int kvh = ahead.unit / head_blocks;
+            const int32_t* table = p.table + (int64_t)ahead.b * p.max_pages;
+            const bool has_new = p.k_new && ahead.row.len - 1 - first < TS && ahead.row.len - 1 >= first;
+            if (whole_pages && seen == (1u << TS) - 1 && !has_new) {
+                const int slot = first / p.page_size, row = first - slot * p.page_size;
+                int page = __ldg(table + slot);
+                if (page < 0 || page >= p.num_pages) {
+                    if (lane == 0) atomicOr(p.err, KDA_DEVERR_PAGES);
+                    page = 0;
+                }
+                const int64_t off = ((int64_t)kvh * p.page_size + row) * D;
+                const char* k = reinterpret_cast<const char*>(kp + page * p.k_stride + off);
+                const char* v = reinterpret_cast<const char*>(vp + page * p.v_stride + off);
+#pragma unroll
+                for (int i = 0; i < TS * CPR / 32; ++i) {
+                    const int id = lane + 32 * i, r = id / CPR, c = id % CPR;
+                    const uint32_t to = dst + r * (CPR * 16) + C::swizzle(r, c) * 16;
+                    copy16(to, k + id * 16, true);
+                    copy16(to + L::SUB, v + id * 16, true);
+                }
+            } else {
+                // lane t looks token t's place up, every lane then copies its chunks of each token
+                int page = 0, row = 0;
+                const bool mine = lane < TS && seen >> lane & 1;
+                if (mine) {
+                    const int t = first + lane, slot = t / p.page_size;
+                    row = t - slot * p.page_size;
+                    page = __ldg(table + slot);
+                    if (page < 0 || page >= p.num_pages) {
+                        atomicOr(p.err, KDA_DEVERR_PAGES);
+                        page = 0;
+                    }
+                }
+                const int64_t new_at = ((int64_t)ahead.b * p.Hkv + kvh) * D;
+#pragma unroll
+                for (int i = 0; i < TS * CPR / 32; ++i) {
+                    const int id = lane + 32 * i, r = id / CPR, c = id % CPR;
+                    const int pg = __shfl_sync(0xFFFFFFFFu, page, r), rw = __shfl_sync(0xFFFFFFFFu, row, r);
+                    const int64_t off = ((int64_t)kvh * p.page_size + rw) * D;
+                    const T* k = kp + pg * p.k_stride + off;
+                    const T* v = vp + pg * p.v_stride + off;
+                    if (has_new && first + r == ahead.row.len - 1) {
+                        k = static_cast<const T*>(p.k_new) + new_at;
+                        v = static_cast<const T*>(p.v_new) + new_at;
+                    }
+                    const bool read = seen >> r & 1;
+                    const uint32_t to = dst + r * (CPR * 16) + C::swizzle(r, c) * 16;
+                    copy16(to, reinterpret_cast<const char*>(read ? k : kp) + (read ? c * 16 : 0), read);
+                    copy16(to + L::SUB, reinterpret_cast<const char*>(read ? v : vp) + (read ? c * 16 : 0), read);
                 }
             }
-    }
+            if (--ahead_left > 0) next(ahead);
+        }
+        copy_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < L::STAGES - 1; ++i) issue();
+
+    // ---- q of a unit: fetched to registers while the unit before it runs, then to shared memory ----
+    constexpr int QV = NH * D * (int)sizeof(T) / 16, QPT = (QV + AT - 1) / AT, QC = D * (int)sizeof(T) / 16;
+    uint4 qnext[QPT];
+    auto fetch_q = [&](int b, int unit) {
+        const int kvh = unit / head_blocks, h0 = unit % head_blocks * NH;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (lane + 32 * e < D) sm_o[warp][lane + 32 * e] = acc[e];
-    if (lane == 0) {
-        sm_m[warp] = m;
-        sm_l[warp] = l;
+        for (int i = 0; i < QPT; ++i) {
+            const int id = tid + i * AT, h = id / QC, c = id % QC;
+            qnext[i] = make_uint4(0, 0, 0, 0);
+            if (id < QV && h0 + h < group)
+                qnext[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
+                                                                ((int64_t)b * p.Hq + kvh * group + h0 + h) * D) + c);
+        }
+    };
+    auto store_q = [&]() {
+#pragma unroll
+        for (int i = 0; i < QPT; ++i) {
+            const int id = tid + i * AT, h = id / QC, c = id % QC;
+            if (id < QV) *reinterpret_cast<uint4*>(sm + L::Q + h * C::QP + c * 16) = qnext[i];
+        }
+    };
+
+    Record* record = reinterpret_cast<Record*>(p.workspace) + cta;
+    float* pieces = reinterpret_cast<float*>(p.workspace + MAX_CTAS * sizeof(Record)) + (int64_t)cta * 2 * L::PIECE;
+    float* sm_m = reinterpret_cast<float*>(sm + L::STATS);
+    float* sm_l = sm_m + NW * NH;
+    float* merge = reinterpret_cast<float*>(sm + L::MERGE);
+    const float scale2 = p.scale * LOG2E;
+    bool first_unit = true, recorded = false;
+    int stage = 0;
+    if (left > 0) {
+        fetch_q(at.b, at.unit);
+        store_q();
+        __syncthreads();
     }
-    __syncthreads();
-    float top = -INFINITY, sum = 0.f;
-    for (int w = 0; w < W; ++w) top = fmaxf(top, sm_m[w]);
-    const float base = top == -INFINITY ? 0.f : top;
-    for (int w = 0; w < W; ++w) sum += sm_l[w] * expf(sm_m[w] - base);
-    for (int i = threadIdx.x; i < D; i += AT) {
-        float o = 0.f;
-        for (int w = 0; w < W; ++w) o += sm_o[w][i] * expf(sm_m[w] - base);
-        store_from_float(static_cast<T*>(p.o), ((int64_t)b * p.Hq + h) * D + i, sum > 0.f ? o / sum : 0.f);
+    C core;
+    while (left > 0) {
+        // ---- one unit, or this share's part of it ----
+        const int b = at.b, unit = at.unit, t0 = at.tile, count = min(left, at.row.tiles - t0);
+        const bool starts = t0 == 0, ends = t0 + count == at.row.tiles;
+        const Row row = at.row;
+        core.begin(sm + L::Q, lane);
+        Place after = at;
+        after.tile = t0 + count - 1;
+        if (left > count) {
+            next(after);
+            fetch_q(after.b, after.unit);
+        }
+        for (int i = 0; i < count; ++i, ++at.tile) {
+            unsigned seen;
+            const int first = sub_tile(at, seen);
+            if (!seen) continue;
+            copy_wait<L::STAGES - 2>();
+            __syncwarp();
+            issue();
+            const uint32_t ks = ring + stage * (2 * L::SUB), vs = ks + L::SUB;
+            core.step(ks, vs, seen, scale2, sm + L::PW + warp * C::P_BYTES, lane);
+            if (p.k_new && unit % head_blocks == 0 && row.len - 1 - first < TS && row.len - 1 >= first) {
+                // the new token's key and value into the cache, from the copy in shared memory
+                const int t = row.len - 1, r = t - first, slot = t / p.page_size;
+                const int page = __ldg(p.table + (int64_t)b * p.max_pages + slot);
+                if (page >= 0 && page < p.num_pages) {
+                    const int64_t off = ((int64_t)(unit / head_blocks) * p.page_size + (t - slot * p.page_size)) * D;
+                    for (int c = lane; c < 2 * CPR; c += 32) {
+                        const bool is_k = c < CPR;
+                        const int chunk = is_k ? c : c - CPR;
+                        uint4 x;
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                     : "r"((is_k ? ks : vs) + r * (CPR * 16) + C::swizzle(r, chunk) * 16) : "memory");
+                        T* to = is_k ? static_cast<T*>(p.k_pages) + page * p.k_stride
+                                     : static_cast<T*>(p.v_pages) + page * p.v_stride;
+                        reinterpret_cast<uint4*>(to + off)[chunk] = x;
+                    }
+                }
+            }
+            stage = stage + 1 == L::STAGES ? 0 : stage + 1;
+        }
+
+        // ---- join the warps ----
+        core.sum_lanes();
+        if (C::writes_stats(lane)) {
+#pragma unroll
+            for (int s = 0; s < C::SLOTS; ++s) {
+                sm_m[warp * NH + C::head_of_slot(s, lane)] = core.m[s];
+                sm_l[warp * NH + C::head_of_slot(s, lane)] = core.l[s];
+            }
+        }
+        __syncthreads();
+        if (left > count) store_q();                    // every warp is done with this unit's
+        float top[C::SLOTS], sum[C::SLOTS], mult[C::SLOTS];
+#pragma unroll
+        for (int s = 0; s < C::SLOTS; ++s) {
+            const int h = C::head_of_slot(s, lane);
+            top[s] = -INFINITY;
+            sum[s] = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) top[s] = fmaxf(top[s], sm_m[w * NH + h]);
+            const float base = top[s] == -INFINITY ? 0.f : top[s];
+#pragma unroll
+            for (int w = 0; w < NW; ++w) sum[s] += sm_l[w * NH + h] * exp2_approx(sm_m[w * NH + h] - base);
+            mult[s] = exp2_approx(core.m[s] - base);
+        }
+#pragma unroll
+        for (int i = 0; i < C::ACC; ++i) core.acc[i] *= mult[C::slot_of(i)];
+#pragma unroll
+        for (int from = NW / 2; from >= 1; from /= 2)
+#pragma unroll
+            for (int r0 = 0; r0 < C::ACC; r0 += L::MERGE_REGS) {
+                if (warp >= from && warp < 2 * from) {
+#pragma unroll
+                    for (int i = 0; i < L::MERGE_REGS; ++i)
+                        merge[((warp - from) * L::MERGE_REGS + i) * 32 + lane] = core.acc[r0 + i];
+                }
+                __syncthreads();
+                if (warp < from) {
+#pragma unroll
+                    for (int i = 0; i < L::MERGE_REGS; ++i)
+                        core.acc[r0 + i] += merge[(warp * L::MERGE_REGS + i) * 32 + lane];
+                }
+                __syncthreads();
+            }
+        if (warp == 0) {
+            const int kvh = unit / head_blocks, h0 = unit % head_blocks * NH;
+            if (starts && ends) {
+#pragma unroll
+                for (int s = 0; s < C::SLOTS; ++s) mult[s] = sum[s] == 0.f ? 0.f : 1.f / sum[s];
+#pragma unroll
+                for (int i = 0; i < C::ACC; ++i) {
+                    const int s = C::slot_of(i), h = h0 + C::head_of_slot(s, lane);
+                    if (h < group && C::owns_output(lane))
+                        store_from_float(static_cast<T*>(p.o), ((int64_t)b * p.Hq + kvh * group + h) * D + C::dim_of(i, lane),
+                                         core.acc[i] * mult[s]);
+                }
+                if (p.lse && C::writes_stats(lane)) {
+#pragma unroll
+                    for (int s = 0; s < C::SLOTS; ++s) {
+                        const int h = h0 + C::head_of_slot(s, lane);
+                        if (h < group)
+                            p.lse[(int64_t)b * p.Hq + kvh * group + h] =
+                                sum[s] == 0.f ? -INFINITY : (top[s] + log2f(sum[s])) * LN2;
+                    }
+                }
+            } else {
+                float* piece = pieces + (first_unit ? 0 : L::PIECE);
+                if (C::writes_stats(lane)) {
+#pragma unroll
+                    for (int s = 0; s < C::SLOTS; ++s) {
+                        piece[NH * D + C::head_of_slot(s, lane)] = top[s];
+                        piece[NH * D + NH + C::head_of_slot(s, lane)] = sum[s];
+                    }
+                }
+                if (C::owns_output(lane)) {
+#pragma unroll
+                    for (int i = 0; i < C::ACC; ++i)
+                        piece[C::head_of_slot(C::slot_of(i), lane) * D + C::dim_of(i, lane)] = core.acc[i];
+                }
+                if (starts && lane == 0) {
+                    const int64_t x = end - left + row.tiles;           // flat tiles up to the unit's last
+                    *record = Record{b, unit, (int)((x * shares - 1) / flat), first_unit ? 0 : 1};
+                    recorded = true;
+                }
+            }
+        }
+        left -= count;
+        first_unit = false;
+        if (left > 0) at = after;
     }
-    if (p.lse && threadIdx.x == 0) p.lse[(int64_t)b * p.Hq + h] = sum > 0.f ? top + logf(sum) : -INFINITY;
+    if (tid == 0 && !recorded) record->b = -1;
+    // rows without a visible token
+    for (int b = cta; b < p.B; b += grid) {
+        const int len = p.lens[b];
+        if (tid == 0 && (len < 0 || len > p.max_pages * p.page_size)) atomicOr(p.err, KDA_DEVERR_PAGES);
+        if (row_of<TILE>(p, len).tiles) continue;
+        T* o = static_cast<T*>(p.o) + (int64_t)b * p.Hq * D;
+        for (int i = tid; i < p.Hq * D; i += AT) store_from_float(o, i, 0.f);
+        if (p.lse)
+            for (int h = tid; h < p.Hq; h += AT) p.lse[(int64_t)b * p.Hq + h] = -INFINITY;
+    }
 }
 
-template <typename T>
-cudaError_t launch_simple(const AttnParams& p, cudaStream_t s) {
-    const int grid = p.B * p.Hq;
-    if (p.d == 16) kda_attn_simple_kernel<T, 16><<<grid, AT, 0, s>>>(p);
-    else if (p.d == 64) kda_attn_simple_kernel<T, 64><<<grid, AT, 0, s>>>(p);
-    else kda_attn_simple_kernel<T, 128><<<grid, AT, 0, s>>>(p);
-    return cudaGetLastError();
+// Joins the pieces of the unit that starts in share blockIdx.x and goes on in others, one CTA per head.
+template <typename T, int D, int NH>
+__global__ void __launch_bounds__(AT) kda_attn_join_kernel(AttnParams p, int head_blocks) {
+    using L = Layout<T, D, NH>;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Record r = reinterpret_cast<const Record*>(p.workspace)[blockIdx.x];
+    const int group = p.Hq / p.Hkv, h = blockIdx.y;
+    if (r.b < 0 || r.unit % head_blocks * NH + h >= group) return;
+    const int first = blockIdx.x, n = r.last - first + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float* pieces = reinterpret_cast<const float*>(p.workspace + MAX_CTAS * sizeof(Record)) + (int64_t)first * 2 * L::PIECE;
+    __shared__ float weight[MAX_CTAS], red[NW], part[AT * 4];
+    auto piece = [&](int i) { return pieces + (int64_t)i * 2 * L::PIECE + (i == 0 ? r.slot * L::PIECE : 0); };
+    float top = -INFINITY;
+    for (int i = tid; i < n; i += AT) top = fmaxf(top, weight[i] = piece(i)[NH * D + h]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, red[w]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    for (int i = tid; i < n; i += AT) {
+        const float w = exp2_approx(weight[i] - base);
+        weight[i] = w;
+        sum += w * piece(i)[NH * D + NH + h];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    __syncthreads();
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) sum += red[w];
+    constexpr int V = D / 4, G = AT / V;                // lanes of a piece, pieces at a time
+    const int g = tid / V, c = tid % V;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = g; i < n; i += G) {
+        const float4 x = *reinterpret_cast<const float4*>(piece(i) + h * D + 4 * c);
+        const float w = weight[i];
+        o.x += w * x.x;
+        o.y += w * x.y;
+        o.z += w * x.z;
+        o.w += w * x.w;
+    }
+    reinterpret_cast<float4*>(part)[tid] = o;
+    __syncthreads();
+    const int64_t row = (int64_t)r.b * p.Hq + r.unit / head_blocks * group + r.unit % head_blocks * NH + h;
+    for (int d = tid; d < D; d += AT) {
+        float x = 0.f;
+#pragma unroll
+        for (int k = 0; k < G; ++k) x += part[k * D + d];
+        store_from_float(static_cast<T*>(p.o), row * D + d, sum == 0.f ? 0.f : x / sum);
+    }
+    if (p.lse && tid == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * LN2;
+}
+
+template <typename T, int D, int NH>
+cudaError_t launch_core(const AttnParams& p, cudaStream_t s) {
+    using L = Layout<T, D, NH>;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kda_attn_kernel<T, D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    if (e != cudaSuccess) return e;
+    const int group = p.Hq / p.Hkv, head_blocks = (group + NH - 1) / NH;
+    const int grid = sms * CTAS_PER_SM < MAX_CTAS ? sms * CTAS_PER_SM : MAX_CTAS;
+    kda_attn_kernel<T, D, NH><<<grid, AT, L::BYTES, s>>>(p, head_blocks, grid);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(grid, group < NH ? group : NH);
+    cfg.blockDim = dim3(AT);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<T, D, NH>, p, head_blocks);
+}
+
+template <typename T, int NH>
+cudaError_t launch_d(const AttnParams& p, cudaStream_t s) {
+    if (p.d == 16) return launch_core<T, 16, NH>(p, s);
+    if (p.d == 64) return launch_core<T, 64, NH>(p, s);
+    return launch_core<T, 128, NH>(p, s);
+}
+
+// Query heads that meet a key at once: the smallest variant that holds the group, else blocks of the largest.
+int block_heads(int group, kda_dtype dt) {
+    if (dt == KDA_DTYPE_BF16) return group <= 8 ? 8 : 16;
+    return group == 1 ? 1 : group <= 4 ? 4 : group <= 8 ? 8 : 16;
 }
 
 }  // namespace
 
-size_t attn_workspace(int32_t, int32_t, int32_t, int32_t, kda_dtype) { return 0; }
+size_t attn_workspace(int32_t, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype dt) {
+    return MAX_CTAS * (sizeof(Record) + 2 * (size_t)piece_floats(block_heads(Hq / Hkv, dt), d) * sizeof(float));
+}
 
 cudaError_t launch_attention_decode(const AttnParams& p, kda_dtype dt, cudaStream_t s) {
-    return dt == KDA_DTYPE_BF16 ? launch_simple<__nv_bfloat16>(p, s) : launch_simple<float>(p, s);
+    const int nh = block_heads(p.Hq / p.Hkv, dt);
+    if (dt == KDA_DTYPE_BF16) return nh == 8 ? launch_d<__nv_bfloat16, 8>(p, s) : launch_d<__nv_bfloat16, 16>(p, s);
+    if (nh == 1) return launch_d<float, 1>(p, s);
+    if (nh == 4) return launch_d<float, 4>(p, s);
+    if (nh == 8) return launch_d<float, 8>(p, s);
+    return launch_d<float, 16>(p, s);
 }
 
 }  // namespace kda
