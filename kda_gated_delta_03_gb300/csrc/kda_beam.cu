@@ -4,11 +4,11 @@
 //
 // and of the K * V continuations of a group the K best, the lowest b * V + v first among equal scores.
 //
-// The logits are read once.  s is a monotone function of x within a row, so a chunk of a row contributes
+// The logits are read once.  s is a monotone function of x within a row, so a part of a row contributes
 // its K + 1 largest logits, its maximum and its sum of exponentials without knowing lse; a second kernel
-// puts each row's lse together, scores what the chunks offer and takes the K best of the group.  Two logits
+// puts each row's lse together, scores what the parts offer and takes the K best of the group.  Two logits
 // that differ can round to one score, and then the lower place wins whatever its logit: the (K + 1)-th
-// entry shows whether that can concern anything that a chunk left out, and then (rarely: beside scores so
+// entry shows whether that can concern anything that a part left out, and then (rarely: beside scores so
 // large that neighbouring logits fall together) the group's logits are searched for the places with
 // exactly that score.  Rows that offer nothing (finished, no score) are not read.
 
@@ -19,11 +19,14 @@
 namespace kda {
 namespace {
 
+constexpr float LOG2E = 1.4426950408889634f;
 constexpr int BT = 256;                       // threads
 constexpr int BW = BT / 32;
-constexpr int GROUPS = BT / 4;                // groups of four threads whose maxima bound the K-th logit
-constexpr int CAP = 1024;                     // logits that a chunk compares with one another at the end
-constexpr int THREAD_BYTES = 128;             // of logits in a thread's registers
+constexpr int GROUPS = BT / 4;                // groups of threads whose maxima bound the K-th logit, at most
+constexpr int FEW = 15;                       // beams up to which half as many groups bound it as well
+constexpr int CAP = 1024;                     // logits kept until they are compared with one another
+constexpr int THREAD_BYTES = 64;              // of logits in a thread's registers, and as many on their way
+constexpr int CTAS_PER_SM = 4;
 static_assert(KDA_BEAM_MAX_K + 1 <= GROUPS, "the bound on the K-th logit");
 
 // A value and its place as one whole number: larger values first, then lower places; no two are equal.
@@ -45,13 +48,23 @@ __device__ __forceinline__ float beam_score(float bs, float x, float lse) {
     return s != s ? -INFINITY : s;
 }
 
-__device__ __forceinline__ float exp_of(float x) {
+__device__ __forceinline__ float exp2_approx(float x) {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// The next value below a finite x in the logits' type.
+__device__ __forceinline__ float exp_of(float x) { return exp2_approx(x * LOG2E); }
+
+// The next value above x (-inf included) or below a finite x in the logits' type.
+__device__ __forceinline__ float above(float x, float) {
+    const unsigned u = __float_as_uint(x + 0.f);
+    return __uint_as_float(u & 0x80000000u ? u - 1u : u + 1u);
+}
+__device__ __forceinline__ float above(float x, __nv_bfloat16) {
+    const unsigned u = __float_as_uint(x + 0.f) >> 16;
+    return __uint_as_float((u & 0x8000u ? u - 1u : u + 1u) << 16);
+}
 __device__ __forceinline__ float below(float x, float) {
     const unsigned u = __float_as_uint(x + 0.f);
     return __uint_as_float(u == 0u ? 0x80000001u : u & 0x80000000u ? u + 1u : u - 1u);
@@ -62,18 +75,18 @@ __device__ __forceinline__ float below(float x, __nv_bfloat16) {
 }
 
 template <typename T>
-constexpr int CHUNK = BT * THREAD_BYTES / (int)sizeof(T);        // logits of a CTA
+constexpr int CHUNK = BT * THREAD_BYTES / (int)sizeof(T);        // logits of a CTA at a time
 
 template <typename T>
 struct Workspace {
-    float2* stats;               // [N * K][chunks] maximum, sum of exp(x - maximum)
-    unsigned long long* list;    // [N * K][chunks][K + 1] largest logits, in order; 0: none
+    float2* stats;               // [N * K][parts] t, and the sum of exp(x - t)
+    unsigned long long* list;    // [N * K][parts][K + 1] largest logits, in order; 0: none
 };
 template <typename T>
-__host__ __device__ inline Workspace<T> workspace(const BeamParams& p, int chunks) {
+__host__ __device__ inline Workspace<T> workspace(const BeamParams& p, int parts) {
     Workspace<T> w;
     w.stats = reinterpret_cast<float2*>(p.workspace);
-    w.list = reinterpret_cast<unsigned long long*>(w.stats + (size_t)p.N * p.K * chunks);
+    w.list = reinterpret_cast<unsigned long long*>(w.stats + (size_t)p.N * p.K * parts);
     return w;
 }
 
@@ -83,48 +96,108 @@ __device__ __forceinline__ bool live(const BeamParams& p, int64_t row) {
     return !(p.finished && p.finished[row]) && bs == bs && bs != -INFINITY;
 }
 
-// A thread's logits in registers: vector j of thread t holds the elements (j * BT + t) * PER .. + PER - 1 of
-// the chunk, wherever the row starts, so that equal rows give equal sums.
+// A pair of floats as the packed arithmetic takes them (two lanes of one instruction).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t c;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(a), "l"(b));
+    return c;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t c;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(a), "l"(b));
+    return c;
+}
+__device__ __forceinline__ float lo_of(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+
+// A thread's logits in registers as they are stored: vector j of thread t holds the elements (j * BT + t) *
+// PER .. + PER - 1 of the chunk, wherever the row starts, so that equal rows give equal sums.
 template <typename T>
 struct Logits {
-    static constexpr int PER = 16 / (int)sizeof(T), NV = THREAD_BYTES / 16, COUNT = PER * NV;
-    uint32_t w[THREAD_BYTES / 4];
+    static constexpr int PER = 16 / (int)sizeof(T), NV = THREAD_BYTES / 16;
+    alignas(16) uint32_t w[4 * NV];
 
-    __device__ static int element(int i, int tid) { return (i / PER * BT + tid) * PER + i % PER; }
-    __device__ float get(int i) const {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-        else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-    }
-    __device__ void load(const T* x, int count, int tid) {
-        if (reinterpret_cast<uintptr_t>(x) % 16 == 0) {
+    // A row may start anywhere.  One that starts R elements past a 16-byte boundary is read by aligned vectors,
+    // two for each vector of its own (the second is the neighbour's first, in L1), and shifted into place.
+    // A vector is read only where it holds an element of the row.
+    template <int R>
+    __device__ void load_shifted(const T* x, int count, int rest, int tid) {
+        const uint4* v = reinterpret_cast<const uint4*>(x - R);
+        constexpr int WORDS = R * (int)sizeof(T) / 4;
+        constexpr bool HALF = R * (int)sizeof(T) % 4 != 0;
+        const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int at = (j * BT + tid) * PER;
-                if (at + PER <= count) {
-                    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(x + at));
-                    w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
-                } else {
-                    load_one_by_one(x, count, at, j);
+        for (int j = 0; j < NV; ++j) {
+            const int at = (j * BT + tid) * PER;
+            const uint4 a = at < rest ? __ldg(v + j * BT + tid) : none;
+            const uint4 b = R && at + PER - R < rest ? __ldg(v + j * BT + tid + 1) : none;
+            const uint32_t u[9] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0u};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[4 * j + e] = HALF ? __funnelshift_r(u[e + WORDS], u[e + WORDS + 1], 16) : u[e + WORDS];
+            if (at + PER > count) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t& y = w[4 * j + e];
+                    if constexpr (sizeof(T) == 4) {
+                        if (at + e >= count) y = 0xFF800000u;
+                    } else {
+                        if (at + 2 * e >= count) y = (y & 0xFFFF0000u) | 0xFF80u;
+                        if (at + 2 * e + 1 >= count) y = (y & 0xFFFFu) | 0xFF800000u;
+                    }
                 }
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) load_one_by_one(x, count, (j * BT + tid) * PER, j);
         }
     }
-
-private:
-    __device__ void load_one_by_one(const T* x, int count, int at, int j) {
+    // `count` elements of the chunk, `rest` of the row from its start
+    __device__ void load(const T* x, int count, int rest, int tid) {
+        const int r = (int)(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
+        if (r == 0 && count == CHUNK<T>) {
+            const uint4* v = reinterpret_cast<const uint4*>(x) + tid;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if constexpr (sizeof(T) == 4) {
-                w[4 * j + e] = at + e < count ? __float_as_uint(x[at + e]) : 0xFF800000u;
-            } else {
-                const unsigned short* u = reinterpret_cast<const unsigned short*>(x);
-                const int i = at + 2 * e;
-                w[4 * j + e] = (i < count ? u[i] : 0xFF80u) | (i + 1 < count ? (uint32_t)u[i + 1] << 16 : 0xFF800000u);
-            }
+            for (int j = 0; j < NV; ++j) *reinterpret_cast<uint4*>(w + 4 * j) = __ldg(v + j * BT);
+        } else if (r == 0) load_shifted<0>(x, count, rest, tid);
+        else if (r == 1) load_shifted<1>(x, count, rest, tid);
+        else if (r == 2) load_shifted<2>(x, count, rest, tid);
+        else if (r == 3) load_shifted<3>(x, count, rest, tid);
+        if constexpr (sizeof(T) == 2) {
+            if (r == 4) load_shifted<4>(x, count, rest, tid);
+            else if (r == 5) load_shifted<5>(x, count, rest, tid);
+            else if (r == 6) load_shifted<6>(x, count, rest, tid);
+            else if (r == 7) load_shifted<7>(x, count, rest, tid);
         }
+    }
+    // the largest of vectors j0 to j1 - 1
+    __device__ float vector_max(int j0, int j1) const {
+        if constexpr (sizeof(T) == 4) {
+            float m = __uint_as_float(w[4 * j0]);
+#pragma unroll
+            for (int i = 4 * j0 + 1; i < 4 * j1; ++i) m = fmaxf(m, __uint_as_float(w[i]));
+            return m;
+        } else {
+            const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
+            __nv_bfloat162 m = h[4 * j0];
+#pragma unroll
+            for (int i = 4 * j0 + 1; i < 4 * j1; ++i) m = __hmax2(m, h[i]);
+            return fmaxf(__low2float(m), __high2float(m));
+        }
+    }
+    // sum of exp(x - t): the difference first, so that neither large logits nor large masks lose anything
+    __device__ float sum_exp(float t) const {
+        const uint64_t scale = pair(LOG2E, LOG2E), off = pair(-t, -t);
+        uint64_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * NV / (sizeof(T) == 4 ? 2 : 1); ++i) {
+            uint64_t x;
+            if constexpr (sizeof(T) == 4) x = (uint64_t)w[2 * i + 1] << 32 | w[2 * i];
+            else x = (uint64_t)(w[i] & 0xFFFF0000u) << 32 | (w[i] << 16);
+            x = mul2(add2(x, off), scale);
+            sum = add2(sum, pair(exp2_approx(lo_of(x)), exp2_approx(hi_of(x))));
+        }
+        return lo_of(sum) + hi_of(sum);
     }
 };
 
@@ -137,182 +210,287 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long x) {
     return x;
 }
 
+// The L largest of n candidates, in order, to best[0 .. L); 0 where there are fewer.
+__device__ __forceinline__ void rank_candidates(const unsigned long long* cand, int n, int L, unsigned long long* best) {
+    for (int i = threadIdx.x; i < n; i += BT) {
+        const unsigned long long c = cand[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) rank += cand[j] > c;
+        if (rank < L) best[rank] = c;
+    }
+    for (int i = n + threadIdx.x; i < L; i += BT) best[i] = 0;
+}
+
+// One part of a row: chunks `first` to `last`, the next one on its way while one is worked on.  The first
+// gives a bound that at least L of its logits reach; from then on only logits above it are looked at one by
+// one (later ones lose to equal ones), a few in each chunk, and the warps need no barrier.  If more turn up
+// than are kept, the L-th best of those kept is a better bound and the part is searched again with it.
+//
+// The sum is that of exp(x - t), t the first chunk's maximum; a thread that meets a logit 64 above moves its own t
+// up.
 template <typename T>
-__global__ void __launch_bounds__(BT) kda_beam_chunk_kernel(BeamParams p, int chunks) {
+__global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamParams p, int parts) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ __align__(16) float group_max[GROUPS];
     __shared__ float warp_top[BW], warp_sum[BW], bound;
     __shared__ int found;
-    __shared__ unsigned long long cand[CAP];
+    __shared__ unsigned long long cand[CAP], best[KDA_BEAM_MAX_K + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / chunks;
-    const int chunk = blockIdx.x % chunks, L = p.K + 1;
+    const int64_t row = blockIdx.x / parts;
+    const int part = blockIdx.x % parts, L = p.K + 1;
     if (!live(p, row)) return;
-    const int base = chunk * CHUNK<T>, count = min(p.V - base, CHUNK<T>);
+    const int chunks = (p.V + CHUNK<T> - 1) / CHUNK<T>;
+    const int first = (int)((int64_t)part * chunks / parts), last = (int)((int64_t)(part + 1) * chunks / parts);
+    const T* logits = static_cast<const T*>(p.logits) + row * p.row_stride;
     using X = Logits<T>;
-    X x;
-    x.load(static_cast<const T*>(p.logits) + row * p.row_stride + base, count, tid);
-
-    float mine = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < X::COUNT; ++i) mine = fmaxf(mine, x.get(i));
-    float top = fmaxf(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    if ((lane & 3) == 0) group_max[tid / 4] = top;
-#pragma unroll
-    for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (lane == 0) warp_top[warp] = top;
+    auto load = [&](X& x, int chunk) {
+        const int base = chunk * CHUNK<T>, rest = p.V - base;
+        x.load(logits + base, min(rest, CHUNK<T>), rest, tid);
+    };
     if (tid == 0) found = 0;
+
+    float t = -INFINITY, limit = -INFINITY, sum = 0.f;   // limit: logits above it move t
+    float least = -INFINITY;                             // logits from it on are looked at
+    unsigned long long least_key = 0;                    // and those from this key on are kept
+    for (bool again = false;; again = true) {
+        X next;
+        load(next, first);
+#pragma unroll 1
+        for (int chunk = first; chunk < last; ++chunk) {
+            const X x = next;
+            if (chunk + 1 < last) load(next, chunk + 1);
+            const float mine = x.vector_max(0, X::NV);
+            if (chunk == first && !again) {
+                // groups of four threads, or of eight: with 32 groups the bound lets about as few through (an L
+                // of 16 at most), and one warp ranks them
+                const bool few = p.K <= FEW;
+                float g = fmaxf(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
+                g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 2));
+                if (!few && (lane & 3) == 0) group_max[tid / 4] = g;
+                g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 4));
+                if (few && (lane & 7) == 0) group_max[tid / 8] = g;
+#pragma unroll
+                for (int o = 8; o < 32; o *= 2) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
+                if (lane == 0) warp_top[warp] = g;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < BW; ++i) g = fmaxf(g, warp_top[i]);
+                t = g;
+                limit = g + 64.f;
+                const int groups = few ? GROUPS / 2 : GROUPS;
+                if (tid < groups) {
+                    g = group_max[tid];
+                    int rank = 0;
+#pragma unroll 4
+                    for (int j = 0; j < groups / 4; ++j) {
+                        const float4 y = reinterpret_cast<const float4*>(group_max)[j];
+                        rank += (y.x > g || (y.x == g && 4 * j < tid)) + (y.y > g || (y.y == g && 4 * j + 1 < tid)) +
+                                (y.z > g || (y.z == g && 4 * j + 2 < tid)) + (y.w > g || (y.w == g && 4 * j + 3 < tid));
+                    }
+                    if (rank == L - 1) bound = g;
+                }
+                __syncthreads();
+                least = bound == -INFINITY ? above(bound, T()) : bound;
+            }
+            if (__any_sync(0xFFFFFFFFu, mine >= least)) {
+                unsigned hits = 0;
+#pragma unroll
+                for (int j = 0; j < X::NV; ++j) hits |= (x.vector_max(j, j + 1) >= least ? 1u : 0u) << j;
+                // the few vectors with such a logit are read again, a lane per element
+                for (unsigned owners = __ballot_sync(0xFFFFFFFFu, hits != 0); owners; owners &= owners - 1) {
+                    const int owner = __ffs(owners) - 1;
+                    const unsigned theirs = __shfl_sync(0xFFFFFFFFu, hits, owner);
+                    int j = lane / X::PER;
+                    int place = chunk * CHUNK<T> + (j * BT + (tid - lane + owner)) * X::PER + lane % X::PER;
+#pragma unroll
+                    for (; j < X::NV; j += 32 / X::PER, place += 32 * BT)
+                        if (theirs >> j & 1 && place < p.V) {
+                            const float y = to_float(logits[place]);
+                            const unsigned long long c = candidate(y, (unsigned)place);
+                            if (y >= least && c >= least_key) {
+                                const int at = atomicAdd(&found, 1);
+                                if (at < CAP) cand[at] = c;
+                            }
+                        }
+                }
+                if (mine > limit) {                     // -inf until a thread meets its first logit
+                    if (sum != 0.f) sum *= exp_of(t - mine);
+                    t = mine;
+                    limit = mine + 64.f;
+                }
+            }
+            if (!again) sum += x.sum_exp(t == -INFINITY ? 0.f : t);
+            if (chunk == first && !again && bound != -INFINITY) least = above(bound, T());
+        }
+        __syncthreads();
+        const int n = found;
+        if (n <= CAP) break;
+        rank_candidates(cand, CAP, L, best);
+        __syncthreads();
+        if (tid == 0) found = 0;
+        least_key = best[L - 1];
+        least = candidate_value(least_key);
+        limit = INFINITY;
+        __syncthreads();
+    }
+
+    const Workspace<T> w = workspace<T>(p, parts);
+    rank_candidates(cand, found, L, w.list + (row * parts + part) * L);
+    float top = t;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (lane == 0) warp_top[warp] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < BW; ++w) top = fmaxf(top, warp_top[w]);
-    // the L-th largest of the groups' maxima: at least L logits are that large
-    if (tid < GROUPS) {
-        const float g = group_max[tid];
-        int rank = 0;
-#pragma unroll
-        for (int j = 0; j < GROUPS / 4; ++j) {
-            const float4 y = reinterpret_cast<const float4*>(group_max)[j];
-            rank += (y.x > g || (y.x == g && 4 * j < tid)) + (y.y > g || (y.y == g && 4 * j + 1 < tid)) +
-                    (y.z > g || (y.z == g && 4 * j + 2 < tid)) + (y.w > g || (y.w == g && 4 * j + 3 < tid));
-        }
-        if (rank == L - 1) bound = g;
-    }
-    // x - top first: the exponent of the largest logits, which make up the sum, is exact
-    const float zero = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < X::COUNT; ++i) sum += exp_of(x.get(i) - zero);
+    for (int i = 0; i < BW; ++i) top = fmaxf(top, warp_top[i]);
+    if (t != top) sum = sum == 0.f ? 0.f : sum * exp_of(t - top);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) warp_sum[warp] = sum;
     __syncthreads();
-    const float least = bound;
-    if (mine >= least && mine > -INFINITY) {
-#pragma unroll
-        for (int i = 0; i < X::COUNT; ++i) {
-            const float y = x.get(i);
-            if (y >= least && y > -INFINITY) {
-                const int at = atomicAdd(&found, 1);
-                if (at < CAP) cand[at] = candidate(y, (unsigned)(base + X::element(i, tid)));
-            }
-        }
-    }
-    __syncthreads();
-    const Workspace<T> w = workspace<T>(p, chunks);
-    unsigned long long* list = w.list + (row * chunks + chunk) * L;
     if (tid == 0) {
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < BW; ++i) sum += warp_sum[i];
-        w.stats[row * chunks + chunk] = make_float2(top, sum);
-    }
-    const int n = found;
-    if (n <= CAP) {
-        for (int i = tid; i < n; i += BT) {
-            const unsigned long long c = cand[i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += cand[j] > c;
-            if (rank < L) list[rank] = c;
-        }
-        for (int i = n + tid; i < L; i += BT) list[i] = 0;
-    } else {
-        // many equal logits: the largest left, L times
-        unsigned long long last = ~0ull;
-        for (int k = 0; k < L; ++k) {
-            unsigned long long best = 0;
-#pragma unroll
-            for (int i = 0; i < X::COUNT; ++i) {
-                const float y = x.get(i);
-                const unsigned long long c = candidate(y, (unsigned)(base + X::element(i, tid)));
-                if (y > -INFINITY && c < last && c > best) best = c;
-            }
-            best = warp_max(best);
-            if (lane == 0) cand[(k & 1) * BW + warp] = best;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < BW; ++i) best = cand[(k & 1) * BW + i] > best ? cand[(k & 1) * BW + i] : best;
-            if (tid == 0) list[k] = best;
-            last = best;
-        }
+        w.stats[row * parts + part] = make_float2(top, sum);
     }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int chunks) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ float bs[KDA_BEAM_MAX_K], lse[KDA_BEAM_MAX_K];
+__global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int parts) {
+    constexpr int KEPT = 2048;                         // scored entries in shared memory; more of them in their place
+    __shared__ float bs[KDA_BEAM_MAX_K], lse[KDA_BEAM_MAX_K], warp_left[BW];
     __shared__ unsigned char fin[KDA_BEAM_MAX_K], alive[KDA_BEAM_MAX_K];
-    __shared__ unsigned long long best[KDA_BEAM_MAX_K], red[2][BW];
-    __shared__ int doubt, counts[BW];
+    __shared__ unsigned long long kept[KEPT], best[KDA_BEAM_MAX_K], red[2][BW], group_max[GROUPS], cand[CAP], bound;
+    __shared__ int found, counts[BW];
     const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = p.K, L = K + 1;
-    const Workspace<T> w = workspace<T>(p, chunks);
-    const float2* stats = w.stats + (int64_t)n * K * chunks;
-    const unsigned long long* list = w.list + (int64_t)n * K * chunks * L;
+    const Workspace<T> w = workspace<T>(p, parts);
+    const float2* stats = w.stats + (int64_t)n * K * parts;
+    unsigned long long* list = w.list + (int64_t)n * K * parts * L;
+    const int per_row = parts * L, entries = K * per_row;
+    unsigned long long* scored = entries <= KEPT ? kept : list;
+    if (tid == 0) found = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    // a warp per row: its lse, and its entries as scores with their places in the group
+    unsigned long long mine = 0;
+    float left_out = -INFINITY;                        // no logit that a part left out scores more
     for (int b = warp; b < K; b += BW) {
         const int64_t row = (int64_t)n * K + b;
-        const bool reads = live(p, row);
-        float top = -INFINITY, sum = 0.f;
+        const float score = p.beam_scores[row];
+        const bool reads = live(p, row), done = p.finished && p.finished[row];
+        unsigned long long* to = scored + b * per_row;
+        bool is_alive = false;
+        float log_sum = 0.f;
         if (reads) {
-            for (int c = lane; c < chunks; c += 32) top = fmaxf(top, stats[b * chunks + c].x);
+            const unsigned long long* from = list + b * per_row;
+            constexpr int AHEAD = 4;                   // entries of a lane on their way
+            unsigned long long c[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) c[i] = lane + 32 * i < per_row ? from[lane + 32 * i] : 0;
+            // the row's largest logit stands first in one of the lists
+            float top = -INFINITY, sum = 0.f;
+            for (int i = lane; i < parts; i += 32)
+                if (from[i * L]) top = fmaxf(top, candidate_value(from[i * L]));
 #pragma unroll
             for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            for (int c = lane; c < chunks; c += 32) {
-                const float2 s = stats[b * chunks + c];
-                sum += s.y * (s.x == -INFINITY ? 0.f : exp_of(s.x - top));
+            for (int i = lane; i < parts; i += 32) {
+                const float2 s = stats[b * parts + i];
+                if (s.y != 0.f) sum += s.y * exp_of(s.x - top);
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            is_alive = top != -INFINITY && sum == sum;               // else every score of the row is -inf
+            log_sum = top + logf(sum);
+            for (int e0 = lane; e0 < per_row; e0 += 32 * AHEAD) {
+                unsigned long long after[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int e = e0 + 32 * (AHEAD + i);
+                    after[i] = e < per_row ? from[e] : 0;
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int e = e0 + 32 * i;
+                    unsigned long long d = 0;
+                    if (is_alive && c[i]) {
+                        const float x = candidate_value(c[i]), s = beam_score(score, x, log_sum);
+                        if (s != -INFINITY) d = candidate(s, (unsigned)b * p.V + candidate_place(c[i]));
+                        if (e % L == K) left_out = fmaxf(left_out, beam_score(score, below(x, T()), log_sum));
+                    }
+                    if (e < per_row) to[e] = d;
+                    mine = d > mine ? d : mine;
+                    c[i] = after[i];
+                }
+            }
+        } else {
+            for (int e = lane; e < per_row; e += 32) to[e] = 0;
+            __syncwarp();
+            if (lane == 0 && done && score == score && score != -INFINITY) {      // a finished beam's one word
+                const unsigned long long d = candidate(score, (unsigned)b * p.V + (unsigned)p.eos);
+                to[0] = d;
+                mine = d > mine ? d : mine;
+            }
         }
         if (lane == 0) {
-            bs[b] = p.beam_scores[row];
-            fin[b] = p.finished && p.finished[row];
-            lse[b] = top + logf(sum);
-            alive[b] = reads && top != -INFINITY && sum == sum;  // else every score of the row is -inf
+            bs[b] = score;
+            fin[b] = done;
+            lse[b] = log_sum;
+            alive[b] = is_alive;
         }
     }
-    if (tid == 0) doubt = 0;
-    __syncthreads();
-
-    // the entries as scores with their places in the group; a finished beam offers its one word
-    const int entries = K * chunks * L;
-    auto entry = [&](int e) -> unsigned long long {
-        const int b = e / (chunks * L);
-        float s = -INFINITY;
-        unsigned v = 0;
-        if (alive[b]) {
-            const unsigned long long c = list[e];
-            if (c == 0) return 0;
-            v = candidate_place(c);
-            s = beam_score(bs[b], candidate_value(c), lse[b]);
-        } else if (fin[b] && e == b * chunks * L) {
-            v = (unsigned)p.eos;
-            s = bs[b] != bs[b] ? -INFINITY : bs[b];
-        }
-        return s == -INFINITY ? 0 : candidate(s, (unsigned)b * p.V + v);
-    };
-    unsigned long long mine = 0;
-    for (int e = tid; e < entries; e += BT) {
-        const unsigned long long c = entry(e);
-        mine = c > mine ? c : mine;
-    }
-    int chosen = 0;                                    // continuations with a score
-    for (int k = 0; k < K; ++k) {
-        unsigned long long c = warp_max(mine);
-        if (lane == 0) red[k & 1][warp] = c;
-        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < BW; ++i) c = red[k & 1][i] > c ? red[k & 1][i] : c;
-        if (tid == 0) best[k] = c;
-        if (c == 0) break;
-        ++chosen;
-        if (c == mine) {                               // this thread's next one
-            mine = 0;
+    for (int o = 16; o; o >>= 1) left_out = fmaxf(left_out, __shfl_xor_sync(0xFFFFFFFFu, left_out, o));
+    if (lane == 0) warp_left[warp] = left_out;
+    // as in a part: the K-th largest of the groups' maxima bounds the K-th score from below
+    unsigned long long g = mine, other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+    g = other > g ? other : g;
+    other = __shfl_xor_sync(0xFFFFFFFFu, g, 2);
+    g = other > g ? other : g;
+    if ((lane & 3) == 0) group_max[tid / 4] = g;
+    __syncthreads();
+    if (tid < GROUPS) {
+        g = group_max[tid];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < GROUPS; ++j) rank += group_max[j] > g || (group_max[j] == g && j < tid);
+        if (rank == K - 1) bound = g;
+    }
+    __syncthreads();
+    const unsigned long long least = bound;
+#pragma unroll 4
+    for (int e = tid; e < entries; e += BT) {
+        const unsigned long long c = scored[e];
+        if (c && c >= least) {
+            const int at = atomicAdd(&found, 1);
+            if (at < CAP) cand[at] = c;
+        }
+    }
+    __syncthreads();
+    int chosen = min(found, K);                        // continuations with a score
+    if (found <= CAP) {
+        for (int i = tid; i < found; i += BT) {
+            const unsigned long long c = cand[i];
+            int rank = 0;
+            for (int j = 0; j < found; ++j) rank += cand[j] > c;
+            if (rank < K) best[rank] = c;
+        }
+    } else {
+        unsigned long long last = ~0ull;               // the best left, K times
+        for (int k = 0; k < K; ++k) {
+            unsigned long long c = 0;
             for (int e = tid; e < entries; e += BT) {
-                const unsigned long long d = entry(e);
-                if (d < c && d > mine) mine = d;
+                const unsigned long long d = scored[e];
+                if (d < last && d > c) c = d;
             }
+            c = warp_max(c);
+            if (lane == 0) red[k & 1][warp] = c;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < BW; ++i) c = red[k & 1][i] > c ? red[k & 1][i] : c;
+            if (tid == 0) best[k] = c;
+            last = c;
         }
     }
     __syncthreads();
@@ -323,14 +501,11 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int chu
         return beam_score(bs[b], to_float(static_cast<const T*>(p.logits)[((int64_t)n * K + b) * p.row_stride + v]), lse[b]);
     };
     if (chosen == K) {
-        // Could a logit that a chunk left out share the last score?  It lies below the chunk's last entry.
+        // could a logit that a part left out share the last score?
         const float worst = candidate_value(best[K - 1]);
-        for (int i = tid; i < K * chunks; i += BT) {
-            const int b = i / chunks;
-            const unsigned long long tail = alive[b] ? list[(int64_t)i * L + K] : 0;
-            if (tail && beam_score(bs[b], below(candidate_value(tail), T()), lse[b]) >= worst) doubt = 1;
-        }
-        __syncthreads();
+        bool doubt = false;
+#pragma unroll
+        for (int i = 0; i < BW; ++i) doubt |= warp_left[i] >= worst;
         if (doubt) {
             // everything above that score is chosen already; of those with exactly it, the lowest places
             int at = 0;
@@ -386,13 +561,19 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int chu
     }
 }
 
+// Parts of a row: enough for six CTAs per SM (of which four are resident; the rows that are not read end at
+// once), as far as a row has chunks.  The GPU's size is taken as 152 SMs, so that the workspace's size needs no
+// device.
 template <typename T>
-int chunk_count(int V) { return (V + CHUNK<T> - 1) / CHUNK<T>; }
+int part_count(const int64_t rows, int V) {
+    const int64_t chunks = (V + CHUNK<T> - 1) / CHUNK<T>, wanted = (6 * 152 + rows - 1) / rows;
+    return (int)(wanted < chunks ? wanted : chunks);
+}
 
 template <typename T>
 cudaError_t launch(const BeamParams& p, cudaStream_t s) {
-    const int chunks = chunk_count<T>(p.V);
-    kda_beam_chunk_kernel<T><<<(unsigned)p.N * p.K * chunks, BT, 0, s>>>(p, chunks);
+    const int parts = part_count<T>((int64_t)p.N * p.K, p.V);
+    kda_beam_part_kernel<T><<<(unsigned)p.N * p.K * parts, BT, 0, s>>>(p, parts);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -404,14 +585,15 @@ cudaError_t launch(const BeamParams& p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_beam_join_kernel<T>, p, chunks);
+    return cudaLaunchKernelEx(&cfg, kda_beam_join_kernel<T>, p, parts);
 }
 
 }  // namespace
 
 size_t beam_workspace(int32_t N, int32_t K, int32_t V, kda_dtype dt) {
-    const size_t chunks = dt == KDA_DTYPE_BF16 ? chunk_count<__nv_bfloat16>(V) : chunk_count<float>(V);
-    return (size_t)N * K * chunks * (sizeof(float2) + (K + 1) * sizeof(unsigned long long));
+    const int64_t rows = (int64_t)N * K;
+    const size_t parts = dt == KDA_DTYPE_BF16 ? part_count<__nv_bfloat16>(rows, V) : part_count<float>(rows, V);
+    return (size_t)rows * parts * (sizeof(float2) + (K + 1) * sizeof(unsigned long long));
 }
 
 cudaError_t launch_beam_select(const BeamParams& p, kda_dtype dt, cudaStream_t s) {

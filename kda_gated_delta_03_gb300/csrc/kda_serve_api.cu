@@ -99,8 +99,8 @@ kda_status kda_beam_select(const void* logits, int64_t row_stride, const float* 
         return KDA_ERR_INVALID_ARG;
     if (finished && eos_token < 0) return KDA_ERR_INVALID_ARG;
     if (K > KDA_BEAM_MAX_K) return KDA_ERR_UNSUPPORTED;
-    // a candidate's place b * V + v and the number of a row's part (at least 8,192 words) are 32-bit
-    if ((int64_t)K * V > INT32_MAX || (int64_t)N * K * ((V + 8191) / 8192) > INT32_MAX) return KDA_ERR_TOO_LARGE;
+    // a candidate's place b * V + v and a row's number n * K + b are 32-bit
+    if ((int64_t)K * V > INT32_MAX || (int64_t)N * K > INT32_MAX) return KDA_ERR_TOO_LARGE;
     if (N == 0) return KDA_OK;
     if (!logits || !aligned(logits, esize(dt)) || !beam_scores || !aligned(beam_scores, 4) || !scores ||
         !aligned(scores, 4) || !table_ok(parent) || !table_ok(token))

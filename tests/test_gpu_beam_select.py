@@ -16,13 +16,15 @@ NINF = -float("inf")
 
 
 def reference(logits, bs, finished=None, eos=-1):
-    """(scores, parent, token, finished) by the definition, float64 scores, lowest place first among equals."""
+    """(scores, parent, token, finished) by the definition, the sum in float64 and the score's three additions in
+    float32 as the definition has them, lowest place first among equals."""
     N, K = bs.shape
     x = logits.double().cpu().numpy().reshape(N, K, -1)
     V = x.shape[2]
     with np.errstate(all="ignore"):
         m = x.max(2, keepdims=True)
-        s = bs.double().cpu().numpy()[:, :, None] + (x - (m + np.log(np.exp(x - m).sum(2, keepdims=True))))
+        lse = m.astype(np.float32) + np.log(np.exp(x - m).sum(2, keepdims=True)).astype(np.float32)
+        s = (bs.cpu().numpy()[:, :, None] + (x.astype(np.float32) - lse)).astype(np.float64)
     if finished is not None:
         f = finished.cpu().numpy() != 0
         for n, b in zip(*np.nonzero(f)):
@@ -107,6 +109,32 @@ def test_rows_that_offer_nothing(dtype):
     bs[2] = NINF
     logits[12:16] = NINF
     check(logits, bs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fill", [-1e4, -1e10, -3e38, "lowest", NINF])
+def test_words_masked_by_a_large_negative_number(dtype, fill):
+    """A grammar leaves a few words, the others hold the mask's value: whole parts of the row, and whole rows."""
+    logits, bs = inputs(4, 4, 60000, dtype, 20)
+    fill = float(torch.finfo(DT[dtype]).min) if fill == "lowest" else fill
+    keep = torch.zeros(60000, dtype=torch.bool, device=DEV)
+    keep[[5, 31000, 31001, 45678, 59999]] = True
+    logits = torch.where(keep, logits, torch.full_like(logits, fill))
+    check(logits, bs)
+    logits[1:7] = fill                                 # rows without a word left
+    _, parent, token = check(logits, bs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logits_in_order(dtype):
+    """Rising and falling rows: every chunk of the one holds larger logits than all before it."""
+    ramp = torch.linspace(-20, 20, 100000, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    noise = 1e-3 * torch.rand((8, 100000), device=DEV, generator=g)
+    logits = (torch.stack([ramp, ramp.flip(0)] * 4) + noise).to(DT[dtype])
+    bs = -3.0 * torch.arange(8, device=DEV, dtype=torch.float32).view(2, 4) / 7
+    check(logits, bs)
+    check(100 * logits, bs)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
