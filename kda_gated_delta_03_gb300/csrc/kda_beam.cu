@@ -24,9 +24,10 @@ constexpr int BT = 256;                       // threads
 constexpr int BW = BT / 32;
 constexpr int GROUPS = BT / 4;                // groups of threads whose maxima bound the K-th logit, at most
 constexpr int FEW = 15;                       // beams up to which half as many groups bound it as well
-constexpr int CAP = 1024;                     // logits kept until they are compared with one another
-constexpr int THREAD_BYTES = 64;              // of logits in a thread's registers, and as many on their way
-constexpr int CTAS_PER_SM = 4;
+constexpr int CAP = 512;                      // logits kept until they are compared with one another
+constexpr int THREAD_BYTES = 64;              // of logits in a thread's registers
+constexpr int CTAS_PER_SM = 3;
+constexpr int STAGES = 4;                     // chunks of a warp in shared memory or on their way there
 static_assert(KDA_BEAM_MAX_K + 1 <= GROUPS, "the bound on the K-th logit");
 
 // A value and its place as one whole number: larger values first, then lower places; no two are equal.
@@ -113,75 +114,102 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float lo_of(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
 
-// A thread's logits in registers as they are stored: vector j of thread t holds the elements (j * BT + t) *
-// PER .. + PER - 1 of the chunk, wherever the row starts, so that equal rows give equal sums.
+// 16 bytes from global to shared memory; zeros, and no read, where `read` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// A thread's logits of a chunk: vector j of thread t holds the elements (j * BT + t) * PER .. + PER - 1, wherever
+// the row starts, so that equal rows give equal sums.
+//
+// A row may start `off` elements past a 16-byte boundary.  Its vectors are copied as they lie between
+// boundaries, 33 for the 32 of a warp, and put into place on the way to the registers; so a warp needs
+// nothing that another one copies.
 template <typename T>
 struct Logits {
     static constexpr int PER = 16 / (int)sizeof(T), NV = THREAD_BYTES / 16;
-    alignas(16) uint32_t w[4 * NV];
+    static constexpr int WARP_BYTES = NV * 33 * 16;    // of a chunk
+    uint32_t w[4 * NV];
 
-    // A row may start anywhere.  One that starts R elements past a 16-byte boundary is read by aligned vectors,
-    // two for each vector of its own (the second is the neighbour's first, in L1), and shifted into place.
-    // A vector is read only where it holds an element of the row.
-    template <int R>
-    __device__ void load_shifted(const T* x, int count, int rest, int tid) {
-        const uint4* v = reinterpret_cast<const uint4*>(x - R);
-        constexpr int WORDS = R * (int)sizeof(T) / 4;
-        constexpr bool HALF = R * (int)sizeof(T) % 4 != 0;
-        const uint4 none = make_uint4(0, 0, 0, 0);
+    // The copies of chunk `chunk` of a row of V logits at v (rounded down to the boundary).
+    __device__ static void copy(uint32_t ring, const uint4* v, int chunk, int off, int V, int tid) {
+        const int lane = tid & 31;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int at = (j * BT + tid) * PER;
-            const uint4 a = at < rest ? __ldg(v + j * BT + tid) : none;
-            const uint4 b = R && at + PER - R < rest ? __ldg(v + j * BT + tid + 1) : none;
-            const uint32_t u[9] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0u};
+            const int at = (chunk * NV + j) * BT + tid;
+            copy16(ring + (j * 33 + lane) * 16, v + at, at * PER - off < V);
+            if (off && lane == 0) copy16(ring + (j * 33 + 32) * 16, v + at + 32, (at + 32) * PER - off < V);
+        }
+    }
+    // ... and to the registers; `count` elements of the chunk exist
+    __device__ void take(uint32_t ring, int off, int count, int tid) {
+        const int lane = tid & 31, words = off * (int)sizeof(T) / 4;
+        const bool half = off * (int)sizeof(T) % 4 != 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[4 * j + e] = HALF ? __funnelshift_r(u[e + WORDS], u[e + WORDS + 1], 16) : u[e + WORDS];
-            if (at + PER > count) {
+        for (int j = 0; j < NV; ++j) {
+            const uint4 a = shared16(ring + (j * 33 + lane) * 16);
+            uint32_t u[9] = {a.x, a.y, a.z, a.w, 0, 0, 0, 0, 0};
+            if (off) {
+                const uint4 b = shared16(ring + (j * 33 + lane + 1) * 16);
+                u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
+                if (words & 1) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t& y = w[4 * j + e];
-                    if constexpr (sizeof(T) == 4) {
-                        if (at + e >= count) y = 0xFF800000u;
-                    } else {
-                        if (at + 2 * e >= count) y = (y & 0xFFFF0000u) | 0xFF80u;
-                        if (at + 2 * e + 1 >= count) y = (y & 0xFFFFu) | 0xFF800000u;
-                    }
+                    for (int e = 0; e < 7; ++e) u[e] = u[e + 1];
+                }
+                if (words & 2) {
+#pragma unroll
+                    for (int e = 0; e < 5; ++e) u[e] = u[e + 2];
+                }
+                if (half) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) u[e] = __funnelshift_r(u[e], u[e + 1], 16);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[4 * j + e] = u[e];
+        }
+        if (count < CHUNK<T>) {
+#pragma unroll
+            for (int i = 0; i < 4 * NV; ++i) {
+                const int at = (i / 4 * BT + tid) * PER + i % 4 * (4 / (int)sizeof(T));
+                if constexpr (sizeof(T) == 4) {
+                    if (at >= count) w[i] = 0xFF800000u;
+                } else {
+                    if (at >= count) w[i] = (w[i] & 0xFFFF0000u) | 0xFF80u;
+                    if (at + 1 >= count) w[i] = (w[i] & 0xFFFFu) | 0xFF800000u;
                 }
             }
         }
     }
-    // `count` elements of the chunk, `rest` of the row from its start
-    __device__ void load(const T* x, int count, int rest, int tid) {
-        const int r = (int)(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
-        if (r == 0 && count == CHUNK<T>) {
-            const uint4* v = reinterpret_cast<const uint4*>(x) + tid;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) *reinterpret_cast<uint4*>(w + 4 * j) = __ldg(v + j * BT);
-        } else if (r == 0) load_shifted<0>(x, count, rest, tid);
-        else if (r == 1) load_shifted<1>(x, count, rest, tid);
-        else if (r == 2) load_shifted<2>(x, count, rest, tid);
-        else if (r == 3) load_shifted<3>(x, count, rest, tid);
-        if constexpr (sizeof(T) == 2) {
-            if (r == 4) load_shifted<4>(x, count, rest, tid);
-            else if (r == 5) load_shifted<5>(x, count, rest, tid);
-            else if (r == 6) load_shifted<6>(x, count, rest, tid);
-            else if (r == 7) load_shifted<7>(x, count, rest, tid);
+    // element i of thread `owner` of this warp, from shared memory
+    __device__ static float element(uint32_t ring, int off, int owner, int i) {
+        const uint32_t at = ring + (i / PER * 33 + owner) * 16 + (i % PER + off) * (int)sizeof(T);
+        if constexpr (sizeof(T) == 4) {
+            float x;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+            return x;
+        } else {
+            unsigned short x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+            return __uint_as_float((uint32_t)x << 16);
         }
     }
-    // the largest of vectors j0 to j1 - 1
-    __device__ float vector_max(int j0, int j1) const {
+    __device__ float max() const {
         if constexpr (sizeof(T) == 4) {
-            float m = __uint_as_float(w[4 * j0]);
+            float m = __uint_as_float(w[0]);
 #pragma unroll
-            for (int i = 4 * j0 + 1; i < 4 * j1; ++i) m = fmaxf(m, __uint_as_float(w[i]));
+            for (int i = 1; i < 4 * NV; ++i) m = fmaxf(m, __uint_as_float(w[i]));
             return m;
         } else {
             const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
-            __nv_bfloat162 m = h[4 * j0];
+            __nv_bfloat162 m = h[0];
 #pragma unroll
-            for (int i = 4 * j0 + 1; i < 4 * j1; ++i) m = __hmax2(m, h[i]);
+            for (int i = 1; i < 4 * NV; ++i) m = __hmax2(m, h[i]);
             return fmaxf(__low2float(m), __high2float(m));
         }
     }
@@ -222,10 +250,11 @@ __device__ __forceinline__ void rank_candidates(const unsigned long long* cand, 
     for (int i = n + threadIdx.x; i < L; i += BT) best[i] = 0;
 }
 
-// One part of a row: chunks `first` to `last`, the next one on its way while one is worked on.  The first
-// gives a bound that at least L of its logits reach; from then on only logits above it are looked at one by
-// one (later ones lose to equal ones), a few in each chunk, and the warps need no barrier.  If more turn up
-// than are kept, the L-th best of those kept is a better bound and the part is searched again with it.
+// One part of a row, chunk by chunk.  The first chunk gives a bound that at least L of its logits reach; from
+// then on only logits above it are looked at one by one (later ones lose to equal ones), and the bound moves
+// up to the L-th best after the second chunk and the fourth, so that a few remain in each chunk and most
+// chunks need no barrier.  If more turn up than are kept, the L-th best of those kept is a better bound and the
+// part is searched again with it.
 //
 // The sum is that of exp(x - t), t the first chunk's maximum; a thread that meets a logit 64 above moves its own t
 // up.
@@ -237,30 +266,42 @@ __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamPara
     __shared__ int found;
     __shared__ unsigned long long cand[CAP], best[KDA_BEAM_MAX_K + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / parts;
-    const int part = blockIdx.x % parts, L = p.K + 1;
+    const int64_t row = blockIdx.x / (unsigned)parts;
+    const int part = blockIdx.x % (unsigned)parts, L = p.K + 1;
     if (!live(p, row)) return;
     const int chunks = (p.V + CHUNK<T> - 1) / CHUNK<T>;
     const int first = (int)((int64_t)part * chunks / parts), last = (int)((int64_t)(part + 1) * chunks / parts);
-    const T* logits = static_cast<const T*>(p.logits) + row * p.row_stride;
     using X = Logits<T>;
-    auto load = [&](X& x, int chunk) {
-        const int base = chunk * CHUNK<T>, rest = p.V - base;
-        x.load(logits + base, min(rest, CHUNK<T>), rest, tid);
-    };
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_bytes) + warp * (STAGES * X::WARP_BYTES);
+    const uintptr_t logits = reinterpret_cast<uintptr_t>(static_cast<const T*>(p.logits) + row * p.row_stride);
+    const int off = (int)(logits % 16 / sizeof(T));
+    const uint4* v = reinterpret_cast<const uint4*>(logits - logits % 16);
     if (tid == 0) found = 0;
 
     float t = -INFINITY, limit = -INFINITY, sum = 0.f;   // limit: logits above it move t
     float least = -INFINITY;                             // logits from it on are looked at
     unsigned long long least_key = 0;                    // and those from this key on are kept
     for (bool again = false;; again = true) {
-        X next;
-        load(next, first);
+        int ahead = first, in = 0, out = 0;              // the next chunk to copy, stages
+        auto copy_next = [&]() {
+            if (ahead < last) X::copy(ring + in * X::WARP_BYTES, v, ahead, off, p.V, tid);
+            ++ahead;
+            in = in + 1 == STAGES ? 0 : in + 1;
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
+        };
+#pragma unroll 1
+        for (int i = 0; i < STAGES - 1; ++i) copy_next();
 #pragma unroll 1
         for (int chunk = first; chunk < last; ++chunk) {
-            const X x = next;
-            if (chunk + 1 < last) load(next, chunk + 1);
-            const float mine = x.vector_max(0, X::NV);
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
+            __syncwarp();                                // the warp's copies are there, its reads of the next stage over
+            const uint32_t stage = ring + out * X::WARP_BYTES;
+            out = out + 1 == STAGES ? 0 : out + 1;
+            copy_next();
+            X x;
+            x.take(stage, off, min(p.V - chunk * CHUNK<T>, CHUNK<T>), tid);
+            const float mine = x.max();
             if (chunk == first && !again) {
                 // groups of four threads, or of eight: with 32 groups the bound lets about as few through (an L
                 // of 16 at most), and one warp ranks them
@@ -293,26 +334,24 @@ __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamPara
                 __syncthreads();
                 least = bound == -INFINITY ? above(bound, T()) : bound;
             }
-            if (__any_sync(0xFFFFFFFFu, mine >= least)) {
-                unsigned hits = 0;
+            const unsigned owners = __ballot_sync(0xFFFFFFFFu, mine >= least);
+            if (owners) {
+                // the few threads with such a logit: theirs are read again, a lane per element
+                for (unsigned rest = owners; rest; rest &= rest - 1) {
+                    const int owner = __ffs(rest) - 1;
 #pragma unroll
-                for (int j = 0; j < X::NV; ++j) hits |= (x.vector_max(j, j + 1) >= least ? 1u : 0u) << j;
-                // the few vectors with such a logit are read again, a lane per element
-                for (unsigned owners = __ballot_sync(0xFFFFFFFFu, hits != 0); owners; owners &= owners - 1) {
-                    const int owner = __ffs(owners) - 1;
-                    const unsigned theirs = __shfl_sync(0xFFFFFFFFu, hits, owner);
-                    int j = lane / X::PER;
-                    int place = chunk * CHUNK<T> + (j * BT + (tid - lane + owner)) * X::PER + lane % X::PER;
-#pragma unroll
-                    for (; j < X::NV; j += 32 / X::PER, place += 32 * BT)
-                        if (theirs >> j & 1 && place < p.V) {
-                            const float y = to_float(logits[place]);
+                    for (int e = 0; e < X::NV * X::PER; e += 32) {
+                        const int i = e + lane;
+                        const int place = chunk * CHUNK<T> + (i / X::PER * BT + tid - lane + owner) * X::PER + i % X::PER;
+                        if (i < X::NV * X::PER && place < p.V) {
+                            const float y = X::element(stage, off, owner, i);
                             const unsigned long long c = candidate(y, (unsigned)place);
                             if (y >= least && c >= least_key) {
                                 const int at = atomicAdd(&found, 1);
                                 if (at < CAP) cand[at] = c;
                             }
                         }
+                    }
                 }
                 if (mine > limit) {                     // -inf until a thread meets its first logit
                     if (sum != 0.f) sum *= exp_of(t - mine);
@@ -320,8 +359,21 @@ __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamPara
                     limit = mine + 64.f;
                 }
             }
-            if (!again) sum += x.sum_exp(t == -INFINITY ? 0.f : t);
-            if (chunk == first && !again && bound != -INFINITY) least = above(bound, T());
+            if (again) continue;
+            sum += x.sum_exp(t == -INFINITY ? 0.f : t);
+            if (chunk == first && bound != -INFINITY) least = above(bound, T());
+            if ((chunk == first + 1 || chunk == first + 3) && chunk + 1 < last) {
+                __syncthreads();
+                const int n = found;
+                if (n >= L && n <= CAP) {
+                    rank_candidates(cand, n, L, best);
+                    __syncthreads();
+                    if (tid < L) cand[tid] = best[tid];
+                    if (tid == 0) found = L;
+                    least = fmaxf(least, above(candidate_value(best[L - 1]), T()));
+                }
+                __syncthreads();
+            }
         }
         __syncthreads();
         const int n = found;
@@ -566,15 +618,19 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int par
 // device.
 template <typename T>
 int part_count(const int64_t rows, int V) {
-    const int64_t chunks = (V + CHUNK<T> - 1) / CHUNK<T>, wanted = (6 * 152 + rows - 1) / rows;
+    const int64_t chunks = (V + CHUNK<T> - 1) / CHUNK<T>, wanted = (3 * 152 + rows - 1) / rows;
     return (int)(wanted < chunks ? wanted : chunks);
 }
 
 template <typename T>
 cudaError_t launch(const BeamParams& p, cudaStream_t s) {
     const int parts = part_count<T>((int64_t)p.N * p.K, p.V);
-    kda_beam_part_kernel<T><<<(unsigned)p.N * p.K * parts, BT, 0, s>>>(p, parts);
-    const cudaError_t e = cudaGetLastError();
+    constexpr int ring = BW * STAGES * Logits<T>::WARP_BYTES;
+    static_assert(CTAS_PER_SM * (ring + 8 * 1024) <= 233472, "the rings, the kept logits and the system's 1 KB");
+    cudaError_t e = cudaFuncSetAttribute(kda_beam_part_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+    if (e != cudaSuccess) return e;
+    kda_beam_part_kernel<T><<<(unsigned)p.N * p.K * parts, BT, ring, s>>>(p, parts);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
