@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -36,7 +37,7 @@ class DecodeOptions(ctypes.Structure):
 
 
 class Pool(ctypes.Structure):
-    """kda_pool (include/kda.h)."""
+    """kda_pool (include/kda.h); _POOL packs the same fields."""
     _fields_ = [("data", ctypes.c_void_p), ("layer_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
                 ("slot_bytes", ctypes.c_int64), ("layers", ctypes.c_int32), ("slots", ctypes.c_int32)]
 
@@ -367,16 +368,24 @@ def kda_prefill_backward(q, k, v, beta, alpha, cu_seqlens, grad_o, state_in=None
 
 
 # ---- decoding a hybrid stack: one call of these takes microseconds, so the checks here stay light ----
+_POOL = struct.Struct("@Pqqqii")
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+_DTYPES = {torch.float32: KDA_DTYPE_F32, torch.bfloat16: KDA_DTYPE_BF16}
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _check_at(name, t, dtype, shape, dev):
-    """_check with the device as its index (-1: host memory)."""
+    """_check with the device as its index."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+    raise ValueError(f"{name} is on {t.device}, expected CUDA device {dev}")
 
 
 def _cuda_index(name, t):
@@ -387,37 +396,43 @@ def _cuda_index(name, t):
 
 
 def _raw_stream(stream, dev):
-    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _workspace(workspace, need, dev):
-    """The caller's workspace, or a new one: (tensor, bytes)."""
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=torch.device("cuda", dev))
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on device {dev}")
-    return workspace, workspace.numel() * workspace.element_size()
+def _workspace(workspace, dev):
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on CUDA device {dev}")
+    return workspace.numel() * workspace.element_size()
+
+
+def _new_workspace(need, dev):
+    return torch.empty(max(need, 1), dtype=_U8, device=torch.device("cuda", dev))
 
 
 def _pools(pools, dev):
-    """A ctypes array of kda_pool for tensors [layers, slots, ...] whose slots are contiguous."""
+    """kda_pool records of tensors [layers, slots, ...] whose slots are contiguous: (bytes, how many)."""
     if isinstance(pools, torch.Tensor):
         pools = (pools,)
-    out = (Pool * max(len(pools), 1))()
-    for d, t in zip(out, pools):
-        if t.dim() < 3:
-            raise ValueError(f"pool: shape {tuple(t.shape)}, expected [layers, slots, ...]")
+    packed = []
+    for t in pools:
+        shape, stride, e = t.shape, t.stride(), t.element_size()
+        if len(shape) < 3:
+            raise ValueError(f"pool: shape {tuple(shape)}, expected [layers, slots, ...]")
         if t.get_device() != dev:
-            raise ValueError(f"pool is on {t.device}, expected device {dev}")
-        e, n, shape, stride = t.element_size(), 1, t.shape, t.stride()
-        for size, step in zip(reversed(shape[2:]), reversed(stride[2:])):
-            if size != 1 and step != n:
-                raise ValueError("pool: a slot must be contiguous")
+            raise ValueError(f"pool is on {t.device}, expected CUDA device {dev}")
+        layers, slots = shape[0], shape[1]
+        n = 1
+        for size in shape[2:]:
             n *= size
-        d.data, d.layers, d.slots, d.slot_bytes = t.data_ptr(), shape[0], shape[1], n * e
-        d.layer_stride = stride[0] * e if shape[0] > 1 else 0
-        d.slot_stride = stride[1] * e if shape[1] > 1 else 0
-    return out, len(pools)
+        if not t.is_contiguous():
+            m = 1
+            for size, step in zip(reversed(shape[2:]), reversed(stride[2:])):
+                if size != 1 and step != m:
+                    raise ValueError("pool: a slot must be contiguous")
+                m *= size
+        packed.append(_POOL.pack(t.data_ptr(), stride[0] * e if layers > 1 else 0, stride[1] * e if slots > 1 else 0,
+                                 n * e, layers, slots))
+    return b"".join(packed), len(packed)
 
 
 def _page_stride(name, t, shape, dtype, dev):
@@ -427,7 +442,7 @@ def _page_stride(name, t, shape, dtype, dev):
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+        raise ValueError(f"{name} is on {t.device}, expected CUDA device {dev}")
     if not t.is_contiguous() and shape[0] and not t[0].is_contiguous():
         raise ValueError(f"{name}: a page must be contiguous")
     return t.stride(0)
@@ -448,20 +463,26 @@ def kda_attention_decode(q, k_pages, v_pages, block_table, seq_lens, *, scale: f
     stored at position seq_lens - 1 by this call.  window > 0: only the last `window` tokens and the first
     `sinks` are visible.  lse [B, H_q] f32, if given, receives the log of the softmax's sum.
     """
-    L = load()
+    L = _LIB or load()
     B, Hq, d = q.shape
-    P, Hkv, ps, _ = k_pages.shape
+    shape = P, Hkv, ps, _ = k_pages.shape
     dt, dev = q.dtype, _cuda_index("q", q)
-    _check_at("q", q, dt, (B, Hq, d), dev)
-    ks = _page_stride("k_pages", k_pages, (P, Hkv, ps, d), dt, dev)
-    vs = _page_stride("v_pages", v_pages, (P, Hkv, ps, d), dt, dev)
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    if d != shape[3]:
+        raise ValueError(f"k_pages: shape {tuple(shape)}, expected a last dimension of {d}")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    ks = _page_stride("k_pages", k_pages, shape, dt, dev)
+    vs = _page_stride("v_pages", v_pages, shape, dt, dev)
     M = block_table.shape[1]
-    _check_at("block_table", block_table, torch.int32, (B, M), dev)
-    _check_at("seq_lens", seq_lens, torch.int32, (B,), dev)
-    if (k_new is None) != (v_new is None):
-        raise ValueError("k_new and v_new go together")
-    kn = vn = None
-    if k_new is not None:
+    _check_at("block_table", block_table, _I32, (B, M), dev)
+    _check_at("seq_lens", seq_lens, _I32, (B,), dev)
+    kn = vn = out_lse = None
+    if k_new is not None or v_new is not None:
+        if k_new is None or v_new is None:
+            raise ValueError("k_new and v_new go together")
         _check_at("k_new", k_new, dt, (B, Hkv, d), dev)
         _check_at("v_new", v_new, dt, (B, Hkv, d), dev)
         kn, vn = k_new.data_ptr(), v_new.data_ptr()
@@ -470,14 +491,14 @@ def kda_attention_decode(q, k_pages, v_pages, block_table, seq_lens, *, scale: f
     else:
         _check_at("o", o, dt, (B, Hq, d), dev)
     if lse is not None:
-        _check_at("lse", lse, torch.float32, (B, Hq), dev)
-    code = _dt(dt)
-    need = 0 if workspace is not None else L.kda_attention_decode_workspace_size(B, Hq, Hkv, d, code)
-    workspace, wbytes = _workspace(workspace, need, dev)
+        _check_at("lse", lse, _F32, (B, Hq), dev)
+        out_lse = lse.data_ptr()
+    if workspace is None:
+        workspace = _new_workspace(L.kda_attention_decode_workspace_size(B, Hq, Hkv, d, code), dev)
+    wbytes = _workspace(workspace, dev)
     rc = L.kda_attention_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
                                 seq_lens.data_ptr(), kn, vn, B, Hq, Hkv, d, P, ps, M, ks, vs, code, scale, window,
-                                sinks, o.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                                wbytes, _raw_stream(stream, dev))
+                                sinks, o.data_ptr(), out_lse, workspace.data_ptr(), wbytes, _raw_stream(stream, dev))
     if rc != KDA_OK:
         raise KdaError("kda_attention_decode", rc)
     return o
@@ -496,7 +517,7 @@ def kda_beam_select(logits, beam_scores, *, finished=None, eos_token: int = -1, 
     place first among equal ones.  parent holds row numbers n * K + b, as kda_state_fork and kda_cache_fork take
     them.  finished [N, K] uint8: such a beam goes on with eos_token alone, at its unchanged score.
     """
-    L = load()
+    L = _LIB or load()
     N, K = beam_scores.shape
     V = logits.shape[1]
     dev = _cuda_index("logits", logits)
@@ -505,29 +526,32 @@ def kda_beam_select(logits, beam_scores, *, finished=None, eos_token: int = -1, 
     step, inner = logits.stride()
     if inner != 1 and V > 1 or step < V and N * K > 1:
         raise ValueError("logits: a row must be contiguous")
-    _check_at("beam_scores", beam_scores, torch.float32, (N, K), dev)
+    _check_at("beam_scores", beam_scores, _F32, (N, K), dev)
     if finished is not None:
-        _check_at("finished", finished, torch.uint8, (N, K), dev)
+        _check_at("finished", finished, _U8, (N, K), dev)
     if scores_out is None:
         scores_out = torch.empty_like(beam_scores)
     else:
-        _check_at("scores_out", scores_out, torch.float32, (N, K), dev)
+        _check_at("scores_out", scores_out, _F32, (N, K), dev)
     if parent is None:
         parent = torch.empty((N, K), dtype=torch.int32, device=logits.device)
     else:
-        _check_at("parent", parent, torch.int32, (N, K), dev)
+        _check_at("parent", parent, _I32, (N, K), dev)
     if token is None:
         token = torch.empty((N, K), dtype=torch.int32, device=logits.device)
     else:
-        _check_at("token", token, torch.int32, (N, K), dev)
+        _check_at("token", token, _I32, (N, K), dev)
     if finished_out is None:
         if finished is not None:
             finished_out = torch.empty_like(finished)
     else:
-        _check_at("finished_out", finished_out, torch.uint8, (N, K), dev)
-    code = _dt(logits.dtype)
-    need = 0 if workspace is not None else L.kda_beam_select_workspace_size(N, K, V, code)
-    workspace, wbytes = _workspace(workspace, need, dev)
+        _check_at("finished_out", finished_out, _U8, (N, K), dev)
+    code = _DTYPES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {logits.dtype}")
+    if workspace is None:
+        workspace = _new_workspace(L.kda_beam_select_workspace_size(N, K, V, code), dev)
+    wbytes = _workspace(workspace, dev)
     rc = L.kda_beam_select(logits.data_ptr(), max(step, V), beam_scores.data_ptr(),
                            None if finished is None else finished.data_ptr(), eos_token, N, K, V, code,
                            scores_out.data_ptr(), parent.data_ptr(), token.data_ptr(),
@@ -543,11 +567,11 @@ def kda_copy_pages(pools, src, dst, *, stream=None):
     (any dtype, contiguous slots); src, dst [n] int32 (src None: src[i] = i); negative entries are skipped."""
     dev = _cuda_index("dst", dst)
     n = dst.shape[0]
-    _check_at("dst", dst, torch.int32, (n,), dev)
+    _check_at("dst", dst, _I32, (n,), dev)
     if src is not None:
-        _check_at("src", src, torch.int32, (n,), dev)
+        _check_at("src", src, _I32, (n,), dev)
     arr, count = _pools(pools, dev)
-    rc = load().kda_copy_pages(arr, count, None if src is None else src.data_ptr(), dst.data_ptr(), n,
+    rc = (_LIB or load()).kda_copy_pages(arr, count, None if src is None else src.data_ptr(), dst.data_ptr(), n,
                                _raw_stream(stream, dev))
     if rc != KDA_OK:
         raise KdaError("kda_copy_pages", rc)
@@ -560,14 +584,14 @@ def kda_state_fork(pools, state_idx, parent, *, state_idx_out=None, stream=None)
     dev = _cuda_index("state_idx", state_idx)
     parent = parent.reshape(-1) if parent.dim() != 1 else parent
     B = state_idx.shape[0]
-    _check_at("state_idx", state_idx, torch.int32, (B,), dev)
-    _check_at("parent", parent, torch.int32, (B,), dev)
+    _check_at("state_idx", state_idx, _I32, (B,), dev)
+    _check_at("parent", parent, _I32, (B,), dev)
     if state_idx_out is None:
         state_idx_out = torch.empty_like(state_idx)
     else:
-        _check_at("state_idx_out", state_idx_out, torch.int32, (B,), dev)
+        _check_at("state_idx_out", state_idx_out, _I32, (B,), dev)
     arr, count = _pools(pools, dev)
-    rc = load().kda_state_fork(arr, count, state_idx.data_ptr(), parent.data_ptr(), B, state_idx_out.data_ptr(),
+    rc = (_LIB or load()).kda_state_fork(arr, count, state_idx.data_ptr(), parent.data_ptr(), B, state_idx_out.data_ptr(),
                                _raw_stream(stream, dev))
     if rc != KDA_OK:
         raise KdaError("kda_state_fork", rc)
@@ -590,37 +614,38 @@ def kda_cache_fork(block_table, seq_lens, parent, ref_count, page_size: int, *, 
     ref_count is updated in place unless ref_count_out is given.  copy_src, copy_dst [R'] receive the pages
     copied, for pools that are not passed here.
     """
-    L = load()
+    L = _LIB or load()
     dev = _cuda_index("block_table", block_table)
     parent = parent.reshape(-1) if parent.dim() != 1 else parent
     R, M = block_table.shape
     P, R2 = ref_count.shape[0], parent.shape[0]
-    _check_at("block_table", block_table, torch.int32, (R, M), dev)
-    _check_at("seq_lens", seq_lens, torch.int32, (R,), dev)
-    _check_at("parent", parent, torch.int32, (R2,), dev)
-    _check_at("ref_count", ref_count, torch.int32, (P,), dev)
+    _check_at("block_table", block_table, _I32, (R, M), dev)
+    _check_at("seq_lens", seq_lens, _I32, (R,), dev)
+    _check_at("parent", parent, _I32, (R2,), dev)
+    _check_at("ref_count", ref_count, _I32, (P,), dev)
     if grow is not None:
-        _check_at("grow", grow, torch.int32, (R2,), dev)
+        _check_at("grow", grow, _I32, (R2,), dev)
     if block_table_out is None:
         block_table_out = torch.empty((R2, M), dtype=torch.int32, device=block_table.device)
     else:
-        _check_at("block_table_out", block_table_out, torch.int32, (R2, M), dev)
+        _check_at("block_table_out", block_table_out, _I32, (R2, M), dev)
     if seq_lens_out is None:
         seq_lens_out = torch.empty(R2, dtype=torch.int32, device=block_table.device)
     else:
-        _check_at("seq_lens_out", seq_lens_out, torch.int32, (R2,), dev)
+        _check_at("seq_lens_out", seq_lens_out, _I32, (R2,), dev)
     if ref_count_out is None:
         ref_count_out = ref_count
     else:
-        _check_at("ref_count_out", ref_count_out, torch.int32, (P,), dev)
+        _check_at("ref_count_out", ref_count_out, _I32, (P,), dev)
     cs = cd = None
     if copy_src is not None or copy_dst is not None:
-        _check_at("copy_src", copy_src, torch.int32, (R2,), dev)
-        _check_at("copy_dst", copy_dst, torch.int32, (R2,), dev)
+        _check_at("copy_src", copy_src, _I32, (R2,), dev)
+        _check_at("copy_dst", copy_dst, _I32, (R2,), dev)
         cs, cd = copy_src.data_ptr(), copy_dst.data_ptr()
     arr, count = _pools(pools, dev)
-    need = 0 if workspace is not None else L.kda_cache_fork_workspace_size(R, R2, M, P)
-    workspace, wbytes = _workspace(workspace, need, dev)
+    if workspace is None:
+        workspace = _new_workspace(L.kda_cache_fork_workspace_size(R, R2, M, P), dev)
+    wbytes = _workspace(workspace, dev)
     rc = L.kda_cache_fork(block_table.data_ptr(), seq_lens.data_ptr(), R, parent.data_ptr(),
                           None if grow is None else grow.data_ptr(), R2, M, page_size, ref_count.data_ptr(), P,
                           block_table_out.data_ptr(), seq_lens_out.data_ptr(), ref_count_out.data_ptr(), cs, cd, arr,
@@ -639,27 +664,28 @@ def kda_cache_compact(block_table, ref_count, *, pools=(), block_table_out=None,
     """Moves the live pages (ref_count > 0) together at the low end of the pools; returns (block_table,
     ref_count, page_map) with the new numbers.  block_table and ref_count are updated in place unless outputs are
     given; page_map [P] int32 holds each page's new number, -1 for a free one."""
-    L = load()
+    L = _LIB or load()
     dev = _cuda_index("block_table", block_table)
     R, M = block_table.shape
     P = ref_count.shape[0]
-    _check_at("block_table", block_table, torch.int32, (R, M), dev)
-    _check_at("ref_count", ref_count, torch.int32, (P,), dev)
+    _check_at("block_table", block_table, _I32, (R, M), dev)
+    _check_at("ref_count", ref_count, _I32, (P,), dev)
     if block_table_out is None:
         block_table_out = block_table
     else:
-        _check_at("block_table_out", block_table_out, torch.int32, (R, M), dev)
+        _check_at("block_table_out", block_table_out, _I32, (R, M), dev)
     if ref_count_out is None:
         ref_count_out = ref_count
     else:
-        _check_at("ref_count_out", ref_count_out, torch.int32, (P,), dev)
+        _check_at("ref_count_out", ref_count_out, _I32, (P,), dev)
     if page_map is None:
         page_map = torch.empty_like(ref_count)
     else:
-        _check_at("page_map", page_map, torch.int32, (P,), dev)
+        _check_at("page_map", page_map, _I32, (P,), dev)
     arr, count = _pools(pools, dev)
-    need = 0 if workspace is not None else L.kda_cache_compact_workspace_size(P)
-    workspace, wbytes = _workspace(workspace, need, dev)
+    if workspace is None:
+        workspace = _new_workspace(L.kda_cache_compact_workspace_size(P), dev)
+    wbytes = _workspace(workspace, dev)
     rc = L.kda_cache_compact(block_table.data_ptr(), R, M, ref_count.data_ptr(), P, block_table_out.data_ptr(),
                              ref_count_out.data_ptr(), page_map.data_ptr(), arr, count, workspace.data_ptr(), wbytes,
                              _raw_stream(stream, dev))

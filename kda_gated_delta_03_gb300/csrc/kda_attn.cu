@@ -780,11 +780,9 @@ __global__ void __launch_bounds__(AT) kda_attn_join_kernel(AttnParams p, int hea
 template <typename T, int D, int NH>
 cudaError_t launch_core(const AttnParams& p, cudaStream_t s) {
     using L = Layout<T, D, NH>;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kda_attn_kernel<T, D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    static DeviceSetup done;
+    int sms = 0;
+    cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_attn_kernel<T, D, NH>), L::BYTES, &sms);
     if (e != cudaSuccess) return e;
     const int group = p.Hq / p.Hkv, head_blocks = (group + NH - 1) / NH;
     const int grid = sms * CTAS_PER_SM < MAX_CTAS ? sms * CTAS_PER_SM : MAX_CTAS;

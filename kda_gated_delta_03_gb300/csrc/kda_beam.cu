@@ -627,7 +627,9 @@ cudaError_t launch(const BeamParams& p, cudaStream_t s) {
     const int parts = part_count<T>((int64_t)p.N * p.K, p.V);
     constexpr int ring = BW * STAGES * Logits<T>::WARP_BYTES;
     static_assert(CTAS_PER_SM * (ring + 8 * 1024) <= 233472, "the rings, the kept logits and the system's 1 KB");
-    cudaError_t e = cudaFuncSetAttribute(kda_beam_part_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+    static DeviceSetup done;
+    int sms = 0;
+    cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_beam_part_kernel<T>), ring, &sms);
     if (e != cudaSuccess) return e;
     kda_beam_part_kernel<T><<<(unsigned)p.N * p.K * parts, BT, ring, s>>>(p, parts);
     e = cudaGetLastError();

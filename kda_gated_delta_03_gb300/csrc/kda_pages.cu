@@ -467,16 +467,12 @@ __global__ void __launch_bounds__(PT) kda_cache_compact_kernel(CompactParams p, 
     }
 }
 
-cudaError_t sm_count(int* sms) {
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-}
-
 // CTAs that copy n slots (at most): one per piece, up to eight per SM.
 cudaError_t copy_grid(const PoolSet& set, int64_t n, int* grid) {
+    static DeviceSetup done;
     int sms = 0;
-    const cudaError_t e = sm_count(&sms);
+    const cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_state_fork_kernel), KDA_FORK_MAX_ROWS * 8,
+                                       &sms);
     if (e != cudaSuccess) return e;
     int64_t most = 1;
     for (int i = 0; i < set.n; ++i) {
@@ -532,14 +528,9 @@ cudaError_t launch_copy_pages(const PoolSet& pools, const int32_t* src, const in
 cudaError_t launch_state_fork(const PoolSet& pools, const int32_t* state_idx, const int32_t* parent, int32_t B,
                               int32_t* state_idx_out, unsigned* err, cudaStream_t s) {
     int grid = 0;
-    cudaError_t e = copy_grid(pools, B, &grid);
+    const cudaError_t e = copy_grid(pools, B, &grid);
     if (e != cudaSuccess) return e;
     const size_t smem = (size_t)B * 8;
-    if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(kda_state_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 KDA_FORK_MAX_ROWS * 8);
-        if (e != cudaSuccess) return e;
-    }
     kda_state_fork_kernel<<<grid, CT, smem, s>>>(pools, state_idx, parent, B, state_idx_out, err);
     return cudaGetLastError();
 }

@@ -2,12 +2,36 @@
 // selection, forks of states and cache pages) between their C-ABI host code and their kernels.
 #pragma once
 
+#include <atomic>
+
 #include "kda_internal.cuh"
 
 namespace kda {
 
 // The current device's error word (defined with the other entry points' host code).
 kda_status device_error_word(unsigned** out);
+
+// The current device's SMs, and a kernel's right to `smem` bytes of dynamic shared memory there.  Both are asked for
+// once per device: these calls are made for every generated token.  `done` is the kernel's own.
+struct DeviceSetup {
+    std::atomic<int> sms[64] = {};               // 0: not asked yet
+};
+inline cudaError_t device_setup(DeviceSetup& done, const void* kernel, int smem, int* sms) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < 64;
+    int n = known ? done.sms[dev].load(std::memory_order_acquire) : 0;
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess && smem > 48 * 1024)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (known) done.sms[dev].store(n, std::memory_order_release);
+    }
+    *sms = n;
+    return cudaSuccess;
+}
 
 // Everything the paged attention kernels need, already validated on the host.
 struct AttnParams {
