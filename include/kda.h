@@ -495,7 +495,7 @@ KDA_API kda_status kda_state_fork(const kda_pool* pools, int32_t num_pools, cons
  *   copy_src, copy_dst [rows_out] or NULL: the page copied for row i and where to, -1 for none (for pools
  *                   that this call does not get: kda_copy_pages takes them)
  *   pools           pools of num_pages slots; num_pools may be 0
- * All tables int32 on the device.
+ * All tables int32 on the device.  rows_in and rows_out at most KDA_FORK_MAX_ROWS (KDA_ERR_TOO_LARGE above).
  */
 KDA_API size_t kda_cache_fork_workspace_size(int32_t rows_in, int32_t rows_out, int32_t max_pages, int32_t num_pages);
 KDA_API kda_status kda_cache_fork(const int32_t* block_table, const int32_t* seq_lens, int32_t rows_in,

@@ -164,141 +164,122 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
-struct ForkScratch {
-    int32_t* first;              // [rows_in] the lowest new row that continues an old one
-    int32_t* count;              // [rows_in] how many continue it
-    int32_t* fresh_at;           // [rows_out] pages of its own before row i, counted within its CTA's rows
-    int32_t* copy_at;            // [rows_out] likewise for copies
-    int32_t* fresh;              // [num_pages] the pages handed out, in order
-    int32_t* src;                // [rows_out] the copies
-    int32_t* dst;
-    int32_t* totals;             // [3][NC] pages of their own, copies, free pages per CTA; then the copies' number
-};
-constexpr int TOTALS = 3 * NC + 1;
-
-size_t pad(size_t ints) { return (ints + 63) / 64 * 64; }
-
-ForkScratch fork_scratch(int32_t* w, int32_t rows_in, int32_t rows_out, int32_t num_pages, size_t* ints) {
-    ForkScratch s;
-    size_t at = 0;
-    auto take = [&](size_t n) { int32_t* p = w ? w + at : nullptr; at += pad(n); return p; };
-    s.totals = take(TOTALS);
-    s.first = take(rows_in);
-    s.count = take(rows_in);
-    s.fresh_at = take(rows_out);
-    s.copy_at = take(rows_out);
-    s.src = take(rows_out);
-    s.dst = take(rows_out);
-    s.fresh = take(num_pages);
-    if (ints) *ints = at;
-    return s;
-}
-
+// What the bookkeeping of a fork leaves for the kernel that writes the tables and copies the pages.
 struct RowPlan {
     int parent;                  // -1: none
     int shared;                  // pages taken over from the parent
     int need;                    // pages in all
-    int full;                    // whole pages of the parent
-    int len;                     // new length
-    bool copy;                   // page `full` is a copy of the parent's
+    int fresh_at;                // rank of the first page of its own
 };
+struct ForkScratch {
+    RowPlan* plan;               // [rows_out]
+    int32_t* listed;             // [num_pages] each CTA's free pages, at its own part of the pages
+    int32_t* fresh;              // [num_pages] the pages handed out, in order
+    int32_t* src;                // [rows_out] the copies
+    int32_t* dst;
+    int32_t* totals;             // [NC] free pages listed per CTA; then pages handed out, copies
+};
+
+size_t pad(size_t ints) { return (ints + 63) / 64 * 64; }
+
+ForkScratch fork_scratch(int32_t* w, int32_t rows_out, int32_t num_pages, size_t* ints) {
+    ForkScratch s;
+    size_t at = 0;
+    auto take = [&](size_t n) { int32_t* p = w ? w + at : nullptr; at += pad(n); return p; };
+    s.totals = take(NC + 2);
+    s.plan = reinterpret_cast<RowPlan*>(take(4 * (size_t)rows_out));
+    s.src = take(rows_out);
+    s.dst = take(rows_out);
+    s.listed = take(num_pages);
+    s.fresh = take(num_pages);
+    if (ints) *ints = at;
+    return s;
+}
 
 __device__ __forceinline__ int old_length(const ForkParams& p, int row) {
     const int len = p.lens[row];
     return len < 0 || len > p.max_pages * p.page_size ? 0 : len;
 }
 
-__device__ __forceinline__ RowPlan row_plan(const ForkParams& p, const ForkScratch& s, int i) {
-    RowPlan r;
-    const int cap = p.max_pages * p.page_size;
-    r.parent = p.parent[i];
-    if (r.parent < 0 || r.parent >= p.rows_in) r.parent = -1;
-    const int len = r.parent < 0 ? 0 : old_length(p, r.parent);
-    int grow = p.grow ? p.grow[i] : 0;
-    if (grow < 0 || grow > cap - len) {
-        atomicOr(p.err, KDA_DEVERR_PAGES);
-        grow = grow < 0 ? 0 : cap - len;
-    }
-    r.len = len + grow;
-    r.full = len / p.page_size;
-    r.copy = len > r.full * p.page_size && s.first[r.parent] != i;
-    r.shared = r.copy ? r.full : (len + p.page_size - 1) / p.page_size;
-    r.need = (int)(((int64_t)r.len + p.page_size - 1) / p.page_size);
-    return r;
-}
-
+// The bookkeeping: which pages every new row takes over and how many it needs of its own, the counts, and the
+// lowest free pages, in order.  Every CTA works out all rows' plans in its own shared memory (first, count
+// [rows_in], fresh_at, copy_at [rows_out]), which costs less than one more meeting of the cluster; counts and
+// pages are divided among the CTAs.
 __global__ void __launch_bounds__(PT) kda_cache_fork_kernel(ForkParams p, ForkScratch s) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ int32_t fork_sm[];
     __shared__ unsigned long long sums[PT / 32];
     const int cta = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const int gt = cta * PT + tid, gw = gt >> 5;
     constexpr int GT = NC * PT, GW = GT / 32;
+    int32_t* first = fork_sm;
+    int32_t* count = first + p.rows_in;
+    int32_t* fresh_at = count + p.rows_in;
+    int32_t* copy_at = fresh_at + p.rows_out;                    // -1: no copy
+    const int cap = p.max_pages * p.page_size;
 
-    // counts start from the old ones
-    for (int i = gt; i < p.rows_in; i += GT) {
-        s.first[i] = INT_MAX;
-        s.count[i] = 0;
-        const int len = p.lens[i];
-        if (len < 0 || len > p.max_pages * p.page_size) atomicOr(p.err, KDA_DEVERR_PAGES);
-    }
-    if (p.ref_out != p.ref)
+    if (p.ref_out != p.ref) {
+#pragma unroll 4
         for (int i = gt; i < p.num_pages; i += GT) p.ref_out[i] = p.ref[i];
-    cluster_sync();
-
-    // who continues whom
-    for (int i = gt; i < p.rows_out; i += GT) {
+    }
+    for (int i = tid; i < p.rows_in; i += PT) {
+        first[i] = INT_MAX;
+        count[i] = 0;
+    }
+    __syncthreads();
+    for (int i = tid; i < p.rows_out; i += PT) {
         const int q = p.parent[i];
         if (q >= 0 && q < p.rows_in) {
-            atomicMin(&s.first[q], i);
-            atomicAdd(&s.count[q], 1);
-        } else if (q != -1) {
+            atomicMin(&first[q], i);
+            atomicAdd(&count[q], 1);
+        } else if (q != -1 && cta == 0) {
             atomicOr(p.err, KDA_DEVERR_PARENT);
         }
     }
-    cluster_sync();
-
-    // pages of its own and copies of every new row, ranked within this CTA's rows
-    const int rows = (p.rows_out + NC - 1) / NC, r0 = min(cta * rows, p.rows_out), r1 = min(r0 + rows, p.rows_out);
-    unsigned long long base = 0;                       // pages (bits 0-31) and copies (32-63) so far
-    for (int t = r0; t < r1; t += PT) {
+    __syncthreads();
+    unsigned long long base = 0;                       // pages of their own (bits 0-31) and copies (32-63) so far
+    for (int t = 0; t < p.rows_out; t += PT) {
         const int i = t + tid;
         unsigned long long mine = 0;
-        if (i < r1) {
-            const RowPlan r = row_plan(p, s, i);
-            mine = (unsigned)(r.need - r.shared) | (r.copy ? 1ull << 32 : 0ull);
+        RowPlan r;
+        int len = 0;
+        bool copy = false;
+        if (i < p.rows_out) {
+            r.parent = p.parent[i];
+            if (r.parent < 0 || r.parent >= p.rows_in) r.parent = -1;
+            len = r.parent < 0 ? 0 : old_length(p, r.parent);
+            const int full = len / p.page_size;
+            copy = len > full * p.page_size && first[r.parent] != i;
+            r.shared = copy ? full : (len + p.page_size - 1) / p.page_size;
+            int grow = p.grow ? p.grow[i] : 0;
+            if (grow < 0 || grow > cap - len) {
+                if (cta == 0) atomicOr(p.err, KDA_DEVERR_PAGES);
+                grow = grow < 0 ? 0 : cap - len;
+            }
+            len += grow;
+            r.need = (int)(((int64_t)len + p.page_size - 1) / p.page_size);
+            mine = (unsigned)(r.need - r.shared) | (copy ? 1ull << 32 : 0ull);
         }
         unsigned long long total;
         const unsigned long long at = base + block_scan<unsigned long long, PT>(mine, total, sums);
-        if (i < r1) {
-            s.fresh_at[i] = (int)(at & 0xFFFFFFFFu);
-            s.copy_at[i] = (int)(at >> 32);
+        if (i < p.rows_out) {
+            r.fresh_at = fresh_at[i] = (int)(at & 0xFFFFFFFFu);
+            copy_at[i] = copy ? (int)(at >> 32) : -1;
+            if (i % NC == cta) s.plan[i] = r;
         }
         base += total;
     }
-    if (tid == 0) {
-        s.totals[cta] = (int)(base & 0xFFFFFFFFu);
-        s.totals[NC + cta] = (int)(base >> 32);
-    }
-    // pages that are taken over, and what the old rows' counts change by: a row continued c times names its
-    // whole pages c times instead of once, and its last, partly filled one once if anybody continues it
-    for (int i = gw; i < p.rows_out; i += GW) {
-        const RowPlan r = row_plan(p, s, i);
-        for (int j = lane; j < p.max_pages; j += 32) {
-            int page = -1;
-            if (j < r.shared) {
-                page = p.table[(int64_t)r.parent * p.max_pages + j];
-                if (page < 0 || page >= p.num_pages) {
-                    atomicOr(p.err, KDA_DEVERR_PAGES);
-                    page = -1;
-                }
-            }
-            p.table_out[(int64_t)i * p.max_pages + j] = page;
-        }
-    }
+    const int wanted = (int)(base & 0xFFFFFFFFu), copies = (int)(base >> 32);
+    cluster_sync();                                    // the counts' copy is complete
+
+    // a row continued c times names its whole pages c times instead of once, and its last, partly filled one once
+    // if anybody continues it
     for (int i = gw; i < p.rows_in; i += GW) {
-        const int c = s.count[i];
+        const int c = count[i], length = p.lens[i];
+        if (lane == 0 && (length < 0 || length > cap)) atomicOr(p.err, KDA_DEVERR_PAGES);
         if (c == 1) continue;
         const int len = old_length(p, i), full = len / p.page_size, pages = full + (len % p.page_size != 0);
+#pragma unroll 4
         for (int j = lane; j < pages; j += 32) {
             const int page = p.table[(int64_t)i * p.max_pages + j];
             const int change = j < full ? c - 1 : c > 0 ? 0 : -1;
@@ -309,78 +290,118 @@ __global__ void __launch_bounds__(PT) kda_cache_fork_kernel(ForkParams p, ForkSc
             }
         }
     }
-    cluster_sync();
-
-    // the lowest free pages, in order
-    int wanted = 0;
-    for (int c = 0; c < NC; ++c) wanted += s.totals[c];
+    int available = 0, before = 0, mine = 0;           // free pages listed in all, before this CTA's, by it
     const int seg = (p.num_pages + NC - 1) / NC, p0 = min(cta * seg, p.num_pages), p1 = min(p0 + seg, p.num_pages);
-    int available = 0;
     if (wanted > 0) {
-        int mine = 0;
-        for (int i = p0 + tid; i < p1; i += PT) mine += p.ref_out[i] == 0;
-        unsigned long long total;
-        block_scan<unsigned long long, PT>((unsigned long long)mine, total, sums);
-        if (tid == 0) s.totals[2 * NC + cta] = (int)total;
-        cluster_sync();
-        int at = 0;
-        for (int c = 0; c < NC; ++c) {
-            if (c < cta) at += s.totals[2 * NC + c];
-            available += s.totals[2 * NC + c];
-        }
-        for (int t = p0; t < p1 && at < wanted; t += PT) {
-            const int i = t + tid;
-            const bool is_free = i < p1 && p.ref_out[i] == 0;
+        cluster_sync();                                // the counts are final
+        // this CTA's lowest free pages, as many as all rows want together
+        constexpr int BATCH = 4;
+        for (int t = p0; t < p1 && mine < wanted; t += BATCH * PT) {
+            int ref[BATCH], n = 0;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int i = t + tid * BATCH + k;
+                ref[k] = i < p1 ? p.ref_out[i] : 1;
+                n += ref[k] == 0;
+            }
             unsigned long long found;
-            const int rank = at + (int)block_scan<unsigned long long, PT>(is_free ? 1 : 0, found, sums);
-            if (is_free && rank < wanted) {
-                s.fresh[rank] = i;
-                p.ref_out[i] = 1;
-            }
-            at += (int)found;
+            int rank = mine + (int)block_scan<unsigned long long, PT>((unsigned long long)n, found, sums);
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+                if (ref[k] == 0) s.listed[p0 + rank++] = t + tid * BATCH + k;
+            mine += (int)found;
         }
+        if (tid == 0) s.totals[cta] = mine;
         cluster_sync();
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int n = s.totals[c];
+            if (c < cta) before += n;
+            available += n;
+        }
+        for (int r = tid; r < mine && before + r < wanted; r += PT) {
+            const int page = s.listed[p0 + r];
+            s.fresh[before + r] = page;
+            p.ref_out[page] = 1;
+        }
     }
+    if (gt == 0) {
+        s.totals[NC] = min(available, wanted);
+        s.totals[NC + 1] = copies;
+    }
+    for (int i = gt; i < p.rows_out; i += GT) {
+        int q = p.parent[i];
+        if (q < 0 || q >= p.rows_in) q = -1;
+        int len = q < 0 ? 0 : old_length(p, q);
+        const int full = len / p.page_size, at = fresh_at[i];
+        const int next = i + 1 < p.rows_out ? fresh_at[i + 1] : wanted;
+        const bool copy = copy_at[i] >= 0;
+        const int shared = copy ? full : (len + p.page_size - 1) / p.page_size;
+        len += p.grow ? max(0, min(p.grow[i], cap - len)) : 0;
+        if (next > at && next > available) {           // the row ends before its first page that is missing
+            atomicOr(p.err, KDA_DEVERR_EXHAUSTED);
+            len = min(len, (shared + max(0, available - at)) * p.page_size);
+        }
+        p.lens_out[i] = len;
+        int src = -1, dst = -1;
+        if (copy) {
+            src = p.table[(int64_t)q * p.max_pages + full];
+            if (at < available) {
+                int c = 0, r = at;
+                for (; c < NC - 1 && r >= s.totals[c]; ++c) r -= s.totals[c];
+                dst = s.listed[min(c * seg, p.num_pages) + r];
+            }
+            if (src < 0 || src >= p.num_pages || dst < 0) {
+                if (dst >= 0) atomicOr(p.err, KDA_DEVERR_PAGES);
+                src = dst = -1;
+            }
+            s.src[copy_at[i]] = src;
+            s.dst[copy_at[i]] = dst;
+        }
+        if (p.copy_src) {
+            p.copy_src[i] = src;
+            p.copy_dst[i] = dst;
+        }
+    }
+}
 
-    // the pages of their own into the new rows, the new lengths, and the copies
-    int copies = 0;
-    for (int c = 0; c < NC; ++c) copies += s.totals[NC + c];
-    if (gt == 0) s.totals[3 * NC] = copies;
-    for (int i = gw; i < p.rows_out; i += GW) {
-        const RowPlan r = row_plan(p, s, i);
-        int at = s.fresh_at[i], copy_at = s.copy_at[i];
-        for (int c = 0; c < i / rows; ++c) {
-            at += s.totals[c];
-            copy_at += s.totals[NC + c];
-        }
-        for (int j = r.shared + lane; j < r.need; j += 32) {
-            const int rank = at + j - r.shared;
-            if (rank < available) p.table_out[(int64_t)i * p.max_pages + j] = s.fresh[rank];
-        }
-        if (lane == 0) {
-            int len = r.len, src = -1, dst = -1;
-            if (at + r.need - r.shared > available && r.need > r.shared) {
-                atomicOr(p.err, KDA_DEVERR_EXHAUSTED);
-                const int have = max(0, min(available - at, r.need - r.shared));
-                len = min(len, (r.shared + have) * p.page_size);
+// The new rows' tables, a warp per row, and the copies of their pages.
+__global__ void __launch_bounds__(CT) kda_cache_fork_finish_kernel(ForkParams p, ForkScratch s,
+                                                                   const __grid_constant__ PoolSet set) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, handed = s.totals[NC], copies = s.totals[NC + 1];
+    for (int i = blockIdx.x * (CT / 32) + (threadIdx.x >> 5); i < p.rows_out; i += gridDim.x * (CT / 32)) {
+        const RowPlan r = s.plan[i];
+        const int32_t* from = p.table + (int64_t)r.parent * p.max_pages;
+        int32_t* to = p.table_out + (int64_t)i * p.max_pages;
+        constexpr int BATCH = 4;
+        for (int j0 = lane; j0 < p.max_pages; j0 += 32 * BATCH) {
+            int page[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int j = j0 + 32 * k, rank = r.fresh_at + j - r.shared;
+                page[k] = j < r.shared ? from[j] : j < r.need && rank < handed ? s.fresh[rank] : -1;
             }
-            p.lens_out[i] = len;
-            if (r.copy) {
-                src = p.table[(int64_t)r.parent * p.max_pages + r.full];
-                dst = at < available ? s.fresh[at] : -1;
-                if (src < 0 || src >= p.num_pages || dst < 0) {
-                    if (dst >= 0) atomicOr(p.err, KDA_DEVERR_PAGES);
-                    src = dst = -1;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int j = j0 + 32 * k;
+                if (j >= p.max_pages) break;
+                if (j < r.shared && (page[k] < 0 || page[k] >= p.num_pages)) {
+                    atomicOr(p.err, KDA_DEVERR_PAGES);
+                    page[k] = -1;
                 }
-                s.src[copy_at] = src;
-                s.dst[copy_at] = dst;
-            }
-            if (p.copy_src) {
-                p.copy_src[i] = src;
-                p.copy_dst[i] = dst;
+                to[j] = page[k];
             }
         }
     }
+    for (int i = 0; i < set.n; ++i)
+        copy_pool(set.pool[i], copies,
+                  [&](int64_t pair, int& from, int& to) {
+                      from = s.src[pair];
+                      to = s.dst[pair];
+                      return from >= 0;
+                  },
+                  p.err, KDA_DEVERR_PAGES);
 }
 
 struct CompactScratch {
@@ -468,28 +489,19 @@ __global__ void __launch_bounds__(PT) kda_cache_compact_kernel(CompactParams p, 
 }
 
 // CTAs that copy n slots (at most): one per piece, up to eight per SM.
-cudaError_t copy_grid(const PoolSet& set, int64_t n, int* grid) {
-    static DeviceSetup done;
-    int sms = 0;
-    const cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_state_fork_kernel), KDA_FORK_MAX_ROWS * 8,
-                                       &sms);
-    if (e != cudaSuccess) return e;
+int copy_grid(const PoolSet& set, int64_t n, int sms) {
     int64_t most = 1;
     for (int i = 0; i < set.n; ++i) {
         const int64_t units = n * set.pool[i].layers * ((set.pool[i].slot_bytes + PIECE - 1) / PIECE);
         most = units > most ? units : most;
     }
-    *grid = (int)(most < 8 * (int64_t)sms ? most : 8 * (int64_t)sms);
-    return cudaSuccess;
+    return (int)(most < 8 * (int64_t)sms ? most : 8 * (int64_t)sms);
 }
 
-// `after`: the list comes from the kernel launched just before on this stream, whose end the copying kernel
-// waits for itself, so that its launch is already done by then.
-cudaError_t launch_copy(const PoolSet& set, const int32_t* src, const int32_t* dst, int32_t n, const int32_t* n_dev,
-                        unsigned* err, bool after, cudaStream_t s) {
-    int grid = 0;
-    const cudaError_t e = copy_grid(set, n, &grid);
-    if (e != cudaSuccess) return e;
+// `after`: the kernel works on what the one launched just before on this stream leaves, and waits for its end
+// itself, so that its launch is already done by then.
+template <typename... Args, typename... Given>
+cudaError_t launch_wide(void (*kernel)(Args...), int grid, bool after, cudaStream_t s, const Given&... given) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(grid);
@@ -499,15 +511,16 @@ cudaError_t launch_copy(const PoolSet& set, const int32_t* src, const int32_t* d
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = after ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kda_copy_kernel, set, src, dst, n, n_dev, err);
+    return cudaLaunchKernelEx(&cfg, kernel, given...);
 }
 
 template <typename... Args, typename... Given>
-cudaError_t launch_cluster(void (*kernel)(Args...), cudaStream_t s, Given... given) {
+cudaError_t launch_cluster(void (*kernel)(Args...), size_t smem, cudaStream_t s, const Given&... given) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(NC);
     cfg.blockDim = dim3(PT);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = NC;
@@ -522,30 +535,41 @@ cudaError_t launch_cluster(void (*kernel)(Args...), cudaStream_t s, Given... giv
 
 cudaError_t launch_copy_pages(const PoolSet& pools, const int32_t* src, const int32_t* dst, int32_t n, unsigned* err,
                               cudaStream_t s) {
-    return launch_copy(pools, src, dst, n, nullptr, err, false, s);
+    static DeviceSetup done;
+    int sms = 0;
+    const cudaError_t e = device_setup(done, nullptr, 0, &sms);
+    if (e != cudaSuccess) return e;
+    const int32_t* none = nullptr;
+    return launch_wide(kda_copy_kernel, copy_grid(pools, n, sms), false, s, pools, src, dst, n, none, err);
 }
 
 cudaError_t launch_state_fork(const PoolSet& pools, const int32_t* state_idx, const int32_t* parent, int32_t B,
                               int32_t* state_idx_out, unsigned* err, cudaStream_t s) {
-    int grid = 0;
-    const cudaError_t e = copy_grid(pools, B, &grid);
+    static DeviceSetup done;
+    int sms = 0;
+    const cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_state_fork_kernel), KDA_FORK_MAX_ROWS * 8, &sms);
     if (e != cudaSuccess) return e;
-    const size_t smem = (size_t)B * 8;
-    kda_state_fork_kernel<<<grid, CT, smem, s>>>(pools, state_idx, parent, B, state_idx_out, err);
+    kda_state_fork_kernel<<<copy_grid(pools, B, sms), CT, (size_t)B * 8, s>>>(pools, state_idx, parent, B, state_idx_out, err);
     return cudaGetLastError();
 }
 
-size_t cache_fork_workspace(int32_t rows_in, int32_t rows_out, int32_t max_pages, int32_t num_pages) {
+size_t cache_fork_workspace(int32_t rows_out, int32_t num_pages) {
     size_t ints = 0;
-    fork_scratch(nullptr, rows_in, rows_out, num_pages, &ints);
+    fork_scratch(nullptr, rows_out, num_pages, &ints);
     return ints * 4;
 }
 
 cudaError_t launch_cache_fork(const ForkParams& p, const PoolSet& pools, void* workspace, cudaStream_t s) {
-    const ForkScratch sc = fork_scratch(static_cast<int32_t*>(workspace), p.rows_in, p.rows_out, p.num_pages, nullptr);
-    const cudaError_t e = launch_cluster(kda_cache_fork_kernel, s, p, sc);
-    if (e != cudaSuccess || pools.n == 0 || p.rows_out == 0) return e;
-    return launch_copy(pools, sc.src, sc.dst, p.rows_out, sc.totals + 3 * NC, p.err, true, s);
+    static DeviceSetup done;
+    int sms = 0;
+    cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_cache_fork_kernel), KDA_FORK_MAX_ROWS * 16, &sms);
+    if (e != cudaSuccess) return e;
+    const ForkScratch sc = fork_scratch(static_cast<int32_t*>(workspace), p.rows_out, p.num_pages, nullptr);
+    e = launch_cluster(kda_cache_fork_kernel, ((size_t)p.rows_in + p.rows_out) * 8, s, p, sc);
+    if (e != cudaSuccess || p.rows_out == 0) return e;
+    const int rows = (p.rows_out + CT / 32 - 1) / (CT / 32), copies = copy_grid(pools, p.rows_out, sms);
+    const int grid = rows > copies ? (rows < 8 * sms ? rows : 8 * sms) : copies;
+    return launch_wide(kda_cache_fork_finish_kernel, grid, true, s, p, sc, pools);
 }
 
 size_t cache_compact_workspace(int32_t num_pages) {
@@ -560,10 +584,16 @@ cudaError_t launch_cache_compact(const CompactParams& p, const PoolSet& pools, v
         if (p.entries == 0) return cudaSuccess;
         return cudaMemsetAsync(p.table_out, 0xFF, p.entries * sizeof(int32_t), s);       // no page is live: all -1
     }
+    static DeviceSetup done;
+    int sms = 0;
+    cudaError_t e = device_setup(done, nullptr, 0, &sms);
+    if (e != cudaSuccess) return e;
     const CompactScratch sc = compact_scratch(static_cast<int32_t*>(workspace), p.num_pages, nullptr);
-    const cudaError_t e = launch_cluster(kda_cache_compact_kernel, s, p, sc);
+    e = launch_cluster(kda_cache_compact_kernel, 0, s, p, sc);
     if (e != cudaSuccess || pools.n == 0) return e;
-    return launch_copy(pools, sc.src, sc.dst, p.num_pages / 2 + 1, sc.totals + 2 * NC, err, true, s);
+    const int32_t most = p.num_pages / 2 + 1;
+    return launch_wide(kda_copy_kernel, copy_grid(pools, most, sms), true, s, pools, (const int32_t*)sc.src,
+                       (const int32_t*)sc.dst, most, (const int32_t*)(sc.totals + 2 * NC), err);
 }
 
 }  // namespace kda

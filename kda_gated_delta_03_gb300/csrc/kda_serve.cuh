@@ -108,7 +108,7 @@ struct ForkParams {
     int32_t page_size;
     int32_t num_pages;
 };
-size_t cache_fork_workspace(int32_t rows_in, int32_t rows_out, int32_t max_pages, int32_t num_pages);
+size_t cache_fork_workspace(int32_t rows_out, int32_t num_pages);
 cudaError_t launch_cache_fork(const ForkParams& p, const PoolSet& pools, void* workspace, cudaStream_t s);
 
 struct CompactParams {

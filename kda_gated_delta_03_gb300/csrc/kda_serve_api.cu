@@ -147,7 +147,8 @@ kda_status kda_state_fork(const kda_pool* pools, int32_t num_pools, const int32_
 
 size_t kda_cache_fork_workspace_size(int32_t rows_in, int32_t rows_out, int32_t max_pages, int32_t num_pages) {
     if (rows_in < 0 || rows_out <= 0 || max_pages < 0 || num_pages < 0) return 0;
-    return align_up(kda::cache_fork_workspace(rows_in, rows_out, max_pages, num_pages), 256);
+    if (rows_in > KDA_FORK_MAX_ROWS || rows_out > KDA_FORK_MAX_ROWS) return 0;
+    return align_up(kda::cache_fork_workspace(rows_out, num_pages), 256);
 }
 
 kda_status kda_cache_fork(const int32_t* block_table, const int32_t* seq_lens, int32_t rows_in, const int32_t* parent,
@@ -162,6 +163,7 @@ kda_status kda_cache_fork(const int32_t* block_table, const int32_t* seq_lens, i
     kda::PoolSet set{};
     const kda_status st = take_pools(pools, num_pools, num_pages, &set);
     if (st != KDA_OK) return st;
+    if (rows_in > KDA_FORK_MAX_ROWS || rows_out > KDA_FORK_MAX_ROWS) return KDA_ERR_TOO_LARGE;
     if (rows_in == 0 && rows_out == 0) return KDA_OK;
     if (rows_out > 0 && (!table_ok(parent) || !table_ok(seq_lens_out) || (grow && !aligned(grow, 4))))
         return KDA_ERR_INVALID_ARG;
@@ -173,7 +175,7 @@ kda_status kda_cache_fork(const int32_t* block_table, const int32_t* seq_lens, i
     if ((block_table_out && block_table_out == block_table) || (seq_lens_out && seq_lens_out == seq_lens))
         return KDA_ERR_INVALID_ARG;
     if (take_workspace(workspace, workspace_bytes,
-                       align_up(kda::cache_fork_workspace(rows_in, rows_out, max_pages, num_pages), 256)) != KDA_OK)
+                       align_up(kda::cache_fork_workspace(rows_out, num_pages), 256)) != KDA_OK)
         return KDA_ERR_WORKSPACE;
     unsigned* err = nullptr;
     if (kda::device_error_word(&err) != KDA_OK) return KDA_ERR_CUDA;

@@ -125,6 +125,7 @@ def fork(lib, **over):
     (dict(lout=None), INV), (dict(tout=None), INV), (dict(table=None), INV), (dict(lens=None), INV), (dict(ref=None), INV),
     (dict(rout=None), INV), (dict(cs=P), INV), (dict(cs=P, cd=ODD2), INV), (dict(tout=P), INV), (dict(lout=P), INV),
     (dict(n=-1), INV), (dict(ws=None), WS), (dict(wsb=100), WS), (dict(ws=0x10010), WS), (dict(R=0, R2=0), OK),
+    (dict(R=8193), TOO_LARGE), (dict(R2=8193), TOO_LARGE),
 ])
 def test_cache_fork_refuses(lib, over, code):
     assert fork(lib, **over) == code
