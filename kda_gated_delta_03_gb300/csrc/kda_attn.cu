@@ -33,8 +33,7 @@ namespace {
 
 constexpr int NW = 4;                         // warps of a CTA
 constexpr int AT = NW * 32;
-constexpr int CTAS_PER_SM = 2;
-constexpr int MAX_CTAS = 512;                 // of the main kernel, whatever the GPU (bounds the workspace)
+constexpr int MAX_CTAS = 640;                 // of the main kernel, whatever the GPU (bounds the workspace)
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -348,17 +347,18 @@ struct Layout {
     using C = Core<T, D, NH>;
     static constexpr int TILE = NW * C::TS;
     static constexpr int SUB = C::TS * D * (int)sizeof(T);        // bytes of a sub-tile's keys
-    static constexpr int STAGES = D == 128 ? 3 : D == 64 ? 6 : 8;
+    static constexpr int CTAS_PER_SM = D < 128 && NH <= 8 ? 4 : D == 128 && NH <= 8 ? 3 : 2;
+    static constexpr int STAGES = D == 128 ? (CTAS_PER_SM == 2 ? 3 : 2) : D == 64 ? (CTAS_PER_SM == 4 ? 3 : 6) : 8;
     static constexpr int RING = STAGES * 2 * SUB;                 // of one warp
     static constexpr int Q = NW * RING;
     static constexpr int Q_BYTES = NH * C::QP;
     static constexpr int MERGE = Q + Q_BYTES;                     // two warps' accumulators, one head tile at a time
-    static constexpr int MERGE_REGS = NH == 16 ? (C::ACC < 16 ? C::ACC : 16) : (C::ACC < 32 ? C::ACC : 32);
+    static constexpr int MERGE_REGS = C::ACC < 16 ? C::ACC : 16;
     static constexpr int STATS = MERGE + 2 * MERGE_REGS * 32 * 4; // m, l [NW][NH]
     static constexpr int PW = STATS + 2 * NW * NH * 4;
     static constexpr int MISC = PW + NW * C::P_BYTES;
     static constexpr int BYTES = MISC + 32;
-    static_assert(CTAS_PER_SM * (BYTES + 1024) <= 233472, "two CTAs per SM");
+    static_assert(CTAS_PER_SM * (BYTES + 1024) <= 233472, "shared memory of the CTAs of an SM");
     // workspace: a record per CTA, then its two partial results of o[NH][D], m[NH], l[NH]
     static constexpr int PIECE = piece_floats(NH, D);
 };
@@ -371,7 +371,7 @@ struct Record {
 };
 
 template <typename T, int D, int NH>
-__global__ void __launch_bounds__(AT, CTAS_PER_SM) kda_attn_kernel(AttnParams p, int head_blocks, int grid) {
+__global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_kernel(AttnParams p, int head_blocks, int grid) {
     using C = Core<T, D, NH>;
     using L = Layout<T, D, NH>;
     constexpr int TS = C::TS, TILE = L::TILE, CPR = C::CPR;
@@ -785,7 +785,7 @@ cudaError_t launch_core(const AttnParams& p, cudaStream_t s) {
     cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_attn_kernel<T, D, NH>), L::BYTES, &sms);
     if (e != cudaSuccess) return e;
     const int group = p.Hq / p.Hkv, head_blocks = (group + NH - 1) / NH;
-    const int grid = sms * CTAS_PER_SM < MAX_CTAS ? sms * CTAS_PER_SM : MAX_CTAS;
+    const int grid = sms * L::CTAS_PER_SM < MAX_CTAS ? sms * L::CTAS_PER_SM : MAX_CTAS;
     kda_attn_kernel<T, D, NH><<<grid, AT, L::BYTES, s>>>(p, head_blocks, grid);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
