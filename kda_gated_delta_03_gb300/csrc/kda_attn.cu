@@ -82,6 +82,7 @@ struct Row {
     int lead;                    // the first `lead` of them start at token 0,
     int skip;                    // the others at tile lead + skip (between sinks and window)
     int from;                    // first token of the window
+    int solid;                   // tokens below it come from the cache (the new one does not)
 };
 
 template <int TILE>
@@ -92,6 +93,7 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, int len) {
     r.from = p.window > 0 && r.len > p.window ? r.len - p.window : 0;
     r.lead = r.skip = 0;
     r.tiles = all;
+    r.solid = p.k_new ? r.len - 1 : r.len;
     const int sink_tiles = (min(p.sinks, r.from) + TILE - 1) / TILE, first = r.from / TILE;
     if (first > sink_tiles) {
         r.lead = sink_tiles;
@@ -101,9 +103,9 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, int len) {
     return r;
 }
 
-// A place in the CTA's share: tile `tile` of unit `unit` (key-value head and head block) of row `b`.
+// A place in the CTA's share: tile `tile` of key-value head kvh and head block hb of row b.
 struct Place {
-    int b, unit, tile;
+    int b, kvh, hb, tile;
     Row row;
 };
 
@@ -150,27 +152,29 @@ struct Core<__nv_bfloat16, D, NH> {
     }
 
     // One sub-tile; bit t of `seen`: token t is visible (a token that is not lies in shared memory as zeros).
+    // Rows of shared memory: chunk c of row r at c ^ (r & 7), so that a fragment's address is one XOR away from the
+    // lane's own (the sub-tiles start on 2 KB boundaries).
     __device__ void step(uint32_t ks, uint32_t vs, unsigned seen, float scale2, unsigned char*, int lane) {
-        float s[NT][4];
+        constexpr int SW = D >= 64 ? 7 : 0;
         const int i8 = lane >> 3, r8 = lane & 7;
-        {
-            float s1[NT][4];                            // two chains of products
+        float s[NT][4], s1[NT][4];                      // two chains of products
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = s1[n][e] = 0.f;
+        const uint32_t ka = ks + ((i8 & 1) * 8 + r8) * (D * 2) + (((i8 >> 1) ^ (r8 & SW)) << 4);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            uint32_t a[4];
+            ldsm4(ka ^ (k << 5), a);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_bf16(k & 1 ? s1[n] : s[n], a, qf[n][k][0], qf[n][k][1]);
+        }
+        if (KT > 1) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = s1[n][e] = 0.f;
-            const int row = (i8 & 1) * 8 + r8;
-#pragma unroll
-            for (int k = 0; k < KT; ++k) {
-                uint32_t a[4];
-                ldsm4(ks + row * (D * 2) + swizzle(row, 2 * k + (i8 >> 1)) * 16, a);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16(k & 1 ? s1[n] : s[n], a, qf[n][k][0], qf[n][k][1]);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + s1[n][e]) * scale2;
+                for (int e = 0; e < 4; ++e) s[n][e] += s1[n][e];
         }
         if (seen != 0xFFFFu) {
             const bool lo = seen >> (lane >> 2) & 1, hi = seen >> ((lane >> 2) + 8) & 1;
@@ -180,36 +184,39 @@ struct Core<__nv_bfloat16, D, NH> {
                 for (int e = 0; e < 4; ++e)
                     if (!(e < 2 ? lo : hi)) s[n][e] = -INFINITY;
         }
-        uint32_t ph[NT][2], pl[NT][2];
+        float base[SLOTS];
         bool grown = false;
-        float keep[SLOTS];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int c = 0; c < SLOTS; ++c) {
+            float x = fmaxf(s[c / 2][c & 1], s[c / 2][(c & 1) + 2]);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float x = fmaxf(s[n][c], s[n][c + 2]);
+            for (int o = 4; o < 32; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+            x = fmaxf(m[c], x * scale2);
+            grown |= x != m[c];
+            base[c] = x;
+        }
+        if (__any_sync(0xFFFFFFFFu, grown)) {           // the maximum of some head: rescale to it
+            float keep[SLOTS];
 #pragma unroll
-                for (int o = 4; o < 32; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-                const float mn = fmaxf(m[2 * n + c], x), base = mn == -INFINITY ? 0.f : mn;
-                keep[2 * n + c] = exp2_approx(m[2 * n + c] - base);
-                grown |= mn != m[2 * n + c];
-                m[2 * n + c] = mn;
-                s[n][c] = exp2_approx(s[n][c] - base);
-                s[n][c + 2] = exp2_approx(s[n][c + 2] - base);
+            for (int c = 0; c < SLOTS; ++c) {
+                keep[c] = exp2_approx(m[c] - (base[c] == -INFINITY ? 0.f : base[c]));
+                m[c] = base[c];
+                l[c] *= keep[c];
             }
-        if (__any_sync(0xFFFFFFFFu, grown)) {
 #pragma unroll
             for (int i = 0; i < ACC; ++i) acc[i] *= keep[slot_of(i)];
-#pragma unroll
-            for (int i = 0; i < SLOTS; ++i) l[i] *= keep[i];
         }
         // The weights go to the tensor core as bf16 pairs hi + lo (16 bits together): rounded to bf16 alone
         // they would add 1.1e-3 of relative error to an output that is itself rounded to 1.7e-3.
+        uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            const float b0 = base[2 * n] == -INFINITY ? 0.f : base[2 * n];
+            const float b1 = base[2 * n + 1] == -INFINITY ? 0.f : base[2 * n + 1];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float x = s[n][2 * h], y = s[n][2 * h + 1];
+                const float x = exp2_approx(fmaf(s[n][2 * h], scale2, -b0));
+                const float y = exp2_approx(fmaf(s[n][2 * h + 1], scale2, -b1));
                 l[2 * n] += x;
                 l[2 * n + 1] += y;
                 const uint32_t hi = pack_bf16(x, y);
@@ -217,11 +224,12 @@ struct Core<__nv_bfloat16, D, NH> {
                 ph[n][h] = transpose8x8(hi);
                 pl[n][h] = transpose8x8(lo);
             }
-        const int row = (i8 >> 1) * 8 + r8;
+        }
+        const uint32_t va = vs + ((i8 >> 1) * 8 + r8) * (D * 2) + (((i8 & 1) ^ (r8 & SW)) << 4);
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
             uint32_t a[4];
-            ldsm4_trans(vs + row * (D * 2) + swizzle(row, 2 * k + (i8 & 1)) * 16, a);
+            ldsm4_trans(va ^ (k << 5), a);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float(&o)[4] = *reinterpret_cast<float(*)[4]>(&acc[(n * KT + k) * 4]);
@@ -290,30 +298,36 @@ struct Core<float, D, NH> {
         }
         float* pw = reinterpret_cast<float*>(pbuf);
         bool grown = false;
-        float keep[NH];
+        float base[NH];
+        const bool sees = seen >> r & 1;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
             s[h] += __shfl_xor_sync(0xFFFFFFFFu, s[h], 1);
             s[h] += __shfl_xor_sync(0xFFFFFFFFu, s[h], 2);
-            s[h] = seen >> r & 1 ? s[h] * scale2 : -INFINITY;
+            if (!sees) s[h] = -INFINITY;
             float x = s[h];
 #pragma unroll
             for (int o = 4; o < 32; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-            const float mn = fmaxf(m[h], x), base = mn == -INFINITY ? 0.f : mn;
-            keep[h] = exp2_approx(m[h] - base);
-            grown |= mn != m[h];
-            m[h] = mn;
-            s[h] = exp2_approx(s[h] - base);
-            if ((h & 3) == c) pw[r * NH + h] = s[h];
+            base[h] = fmaxf(m[h], x * scale2);
+            grown |= base[h] != m[h];
         }
-        if (__any_sync(0xFFFFFFFFu, grown)) {
+        if (__any_sync(0xFFFFFFFFu, grown)) {           // the maximum of some head: rescale to it
+            float keep[NH];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                keep[h] = exp2_approx(m[h] - (base[h] == -INFINITY ? 0.f : base[h]));
+                m[h] = base[h];
+                l[h] *= keep[h];
+            }
 #pragma unroll
             for (int i = 0; i < ACC; ++i) acc[i] *= keep[slot_of(i)];
-#pragma unroll
-            for (int h = 0; h < NH; ++h) l[h] *= keep[h];
         }
 #pragma unroll
-        for (int h = 0; h < NH; ++h) l[h] += s[h];
+        for (int h = 0; h < NH; ++h) {
+            const float x = exp2_approx(fmaf(s[h], scale2, -(base[h] == -INFINITY ? 0.f : base[h])));
+            l[h] += x;
+            if ((h & 3) == c) pw[r * NH + h] = x;
+        }
         __syncwarp();
 #pragma unroll
         for (int t = 0; t < TS; ++t) {
@@ -375,7 +389,7 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
     using C = Core<T, D, NH>;
     using L = Layout<T, D, NH>;
     constexpr int TS = C::TS, TILE = L::TILE, CPR = C::CPR;
-    extern __shared__ __align__(128) unsigned char sm[];
+    extern __shared__ __align__(1024) unsigned char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
     const int group = p.Hq / p.Hkv, units = p.Hkv * head_blocks;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -433,29 +447,32 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
             if (begin < base * units) break;
         }
         at.b = misc[0];
-        at.unit = misc[1];
+        at.kvh = misc[1] / head_blocks;
+        at.hb = misc[1] - at.kvh * head_blocks;
         at.tile = misc[2];
         at.row = row_of<TILE>(p, p.lens[at.b]);
     }
 
-    auto next = [&](Place& x) {                         // the tile after x; only called while the share goes on
-        if (++x.tile < x.row.tiles) return;
+    auto next_unit = [&](Place& x) {                    // only called while the share goes on
         x.tile = 0;
-        if (++x.unit < units) return;
-        x.unit = 0;
+        if (++x.hb < head_blocks) return;
+        x.hb = 0;
+        if (++x.kvh < p.Hkv) return;
+        x.kvh = 0;
         while (x.b + 1 < p.B) {
             x.row = row_of<TILE>(p, __ldg(p.lens + ++x.b));
             if (x.row.tiles > 0) break;
         }
     };
     // this warp's sub-tile of a tile: its first token, and which of its tokens are visible
-    auto sub_tile = [&](const Place& x, unsigned& seen) -> int {
-        const int t = x.tile < x.row.lead ? x.tile : x.tile + x.row.skip;
-        const int first = t * TILE + warp * TS;
-        constexpr unsigned ALL = (1u << TS) - 1;
-        seen = first >= x.row.len ? 0u : x.row.len - first >= TS ? ALL : (1u << (x.row.len - first)) - 1;
-        if (first < x.row.from) {
-            const unsigned win = x.row.from - first >= TS ? 0u : ALL << (x.row.from - first);
+    constexpr unsigned ALL = (1u << TS) - 1;
+    auto sub_tile = [&](const Row& row, int tile, unsigned& seen) -> int {
+        const int first = (tile + (tile < row.lead ? 0 : row.skip)) * TILE + warp * TS;
+        seen = ALL;
+        if (first >= row.from && first + TS <= row.len) return first;
+        seen = first >= row.len ? 0u : row.len - first >= TS ? ALL : (1u << (row.len - first)) - 1;
+        if (first < row.from) {
+            const unsigned win = row.from - first >= TS ? 0u : ALL << (row.from - first);
             const unsigned sink = first >= p.sinks ? 0u : p.sinks - first >= TS ? ALL : (1u << (p.sinks - first)) - 1;
             seen &= win | sink;
         }
@@ -464,8 +481,14 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
     const T* kp = static_cast<const T*>(p.k_pages);
     const T* vp = static_cast<const T*>(p.v_pages);
     const uint32_t ring = smem_addr(sm) + warp * L::RING;
+    auto page_of = [&](int t) -> int { return p.page_magic ? (int)(__umulhi(t, p.page_magic) >> p.page_shift) : t; };
+    auto checked = [&](int page) -> int {
+        if ((unsigned)page < (unsigned)p.num_pages) return page;
+        atomicOr(p.err, KDA_DEVERR_PAGES);
+        return 0;
+    };
 
-    // ---- copies of this warp's next visible sub-tile into stage `stage` ----
+    // ---- copies of this warp's next visible sub-tile into the ring ----
     Place ahead = at;
     int ahead_left = left, stage_in = 0;
     const bool whole_pages = p.page_size % TS == 0;     // a sub-tile never crosses a page
@@ -473,65 +496,53 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
         unsigned seen = 0;
         int first = 0;
         while (ahead_left > 0) {
-            first = sub_tile(ahead, seen);
+            first = sub_tile(ahead.row, ahead.tile, seen);
             if (seen) break;
-            if (--ahead_left > 0) next(ahead);
+            if (--ahead_left > 0 && ++ahead.tile == ahead.row.tiles) next_unit(ahead);
         }
         if (ahead_left > 0) {
             const uint32_t dst = ring + stage_in * (2 * L::SUB);
             stage_in = stage_in + 1 == L::STAGES ? 0 : stage_in + 1;
-            const int kvh = ahead.unit / head_blocks;
             const int32_t* table = p.table + (int64_t)ahead.b * p.max_pages;
-            const bool has_new = p.k_new && ahead.row.len - 1 - first < TS && ahead.row.len - 1 >= first;
-            if (whole_pages && seen == (1u << TS) - 1 && !has_new) {
-                const int slot = first / p.page_size, row = first - slot * p.page_size;
-                int page = __ldg(table + slot);
-                if (page < 0 || page >= p.num_pages) {
-                    if (lane == 0) atomicOr(p.err, KDA_DEVERR_PAGES);
-                    page = 0;
-                }
-                const int64_t off = ((int64_t)kvh * p.page_size + row) * D;
-                const char* k = reinterpret_cast<const char*>(kp + page * p.k_stride + off);
-                const char* v = reinterpret_cast<const char*>(vp + page * p.v_stride + off);
+            if (whole_pages && seen == ALL && first + TS <= ahead.row.solid) {
+                // one run of memory, copied as it lies
+                const int slot = page_of(first), page = checked(__ldg(table + slot));
+                const int64_t off = ((int64_t)ahead.kvh * p.page_size + first - slot * p.page_size) * D;
+                const char* k = reinterpret_cast<const char*>(kp + page * p.k_stride + off) + lane * 16;
+                const char* v = reinterpret_cast<const char*>(vp + page * p.v_stride + off) + lane * 16;
 #pragma unroll
                 for (int i = 0; i < TS * CPR / 32; ++i) {
                     const int id = lane + 32 * i, r = id / CPR, c = id % CPR;
                     const uint32_t to = dst + r * (CPR * 16) + C::swizzle(r, c) * 16;
-                    copy16(to, k + id * 16, true);
-                    copy16(to + L::SUB, v + id * 16, true);
+                    copy16(to, k + i * 512, true);
+                    copy16(to + L::SUB, v + i * 512, true);
                 }
             } else {
-                // lane t looks token t's place up, every lane then copies its chunks of each token
-                int page = 0, row = 0;
-                const bool mine = lane < TS && seen >> lane & 1;
-                if (mine) {
-                    const int t = first + lane, slot = t / p.page_size;
-                    row = t - slot * p.page_size;
-                    page = __ldg(table + slot);
-                    if (page < 0 || page >= p.num_pages) {
-                        atomicOr(p.err, KDA_DEVERR_PAGES);
-                        page = 0;
-                    }
+                // 32 / TS lanes a token, each with its token's own place
+                constexpr int LPT = 32 / TS;
+                const int r = lane / LPT, t = first + r;
+                const bool read = seen >> r & 1;
+                const T* k = kp;
+                const T* v = vp;
+                if (read && t >= ahead.row.solid) {
+                    const int64_t off = ((int64_t)ahead.b * p.Hkv + ahead.kvh) * D;
+                    k = static_cast<const T*>(p.k_new) + off;
+                    v = static_cast<const T*>(p.v_new) + off;
+                } else if (read) {
+                    const int slot = page_of(t), page = checked(__ldg(table + slot));
+                    const int64_t off = ((int64_t)ahead.kvh * p.page_size + t - slot * p.page_size) * D;
+                    k += page * p.k_stride + off;
+                    v += page * p.v_stride + off;
                 }
-                const int64_t new_at = ((int64_t)ahead.b * p.Hkv + kvh) * D;
 #pragma unroll
-                for (int i = 0; i < TS * CPR / 32; ++i) {
-                    const int id = lane + 32 * i, r = id / CPR, c = id % CPR;
-                    const int pg = __shfl_sync(0xFFFFFFFFu, page, r), rw = __shfl_sync(0xFFFFFFFFu, row, r);
-                    const int64_t off = ((int64_t)kvh * p.page_size + rw) * D;
-                    const T* k = kp + pg * p.k_stride + off;
-                    const T* v = vp + pg * p.v_stride + off;
-                    if (has_new && first + r == ahead.row.len - 1) {
-                        k = static_cast<const T*>(p.k_new) + new_at;
-                        v = static_cast<const T*>(p.v_new) + new_at;
-                    }
-                    const bool read = seen >> r & 1;
+                for (int i = 0; i < CPR / LPT; ++i) {
+                    const int c = i * LPT + lane % LPT;
                     const uint32_t to = dst + r * (CPR * 16) + C::swizzle(r, c) * 16;
-                    copy16(to, reinterpret_cast<const char*>(read ? k : kp) + (read ? c * 16 : 0), read);
-                    copy16(to + L::SUB, reinterpret_cast<const char*>(read ? v : vp) + (read ? c * 16 : 0), read);
+                    copy16(to, reinterpret_cast<const char*>(k) + c * 16, read);
+                    copy16(to + L::SUB, reinterpret_cast<const char*>(v) + c * 16, read);
                 }
             }
-            if (--ahead_left > 0) next(ahead);
+            if (--ahead_left > 0 && ++ahead.tile == ahead.row.tiles) next_unit(ahead);
         }
         copy_commit();
     };
@@ -541,8 +552,9 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
     // ---- q of a unit: fetched to registers while the unit before it runs, then to shared memory ----
     constexpr int QV = NH * D * (int)sizeof(T) / 16, QPT = (QV + AT - 1) / AT, QC = D * (int)sizeof(T) / 16;
     uint4 qnext[QPT];
-    auto fetch_q = [&](int b, int unit) {
-        const int kvh = unit / head_blocks, h0 = unit % head_blocks * NH;
+    const uint32_t flip = p.scale < 0.f ? (sizeof(T) == 2 ? 0x80008000u : 0x80000000u) : 0u;   // q carries the scale's sign
+    auto fetch_q = [&](int b, int kvh, int hb) {
+        const int h0 = hb * NH;
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
             const int id = tid + i * AT, h = id / QC, c = id % QC;
@@ -556,7 +568,10 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
             const int id = tid + i * AT, h = id / QC, c = id % QC;
-            if (id < QV) *reinterpret_cast<uint4*>(sm + L::Q + h * C::QP + c * 16) = qnext[i];
+            const uint4 x = qnext[i];
+            if (id < QV)
+                *reinterpret_cast<uint4*>(sm + L::Q + h * C::QP + c * 16) =
+                    make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
         }
     };
 
@@ -565,42 +580,41 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
     float* sm_m = reinterpret_cast<float*>(sm + L::STATS);
     float* sm_l = sm_m + NW * NH;
     float* merge = reinterpret_cast<float*>(sm + L::MERGE);
-    const float scale2 = p.scale * LOG2E;
+    const float scale2 = fmaxf(fabsf(p.scale) * LOG2E, 1e-38f);      // above 0: a masked score stays at -inf
     bool first_unit = true, recorded = false;
     int stage = 0;
     if (left > 0) {
-        fetch_q(at.b, at.unit);
+        fetch_q(at.b, at.kvh, at.hb);
         store_q();
         __syncthreads();
     }
     C core;
     while (left > 0) {
         // ---- one unit, or this share's part of it ----
-        const int b = at.b, unit = at.unit, t0 = at.tile, count = min(left, at.row.tiles - t0);
+        const int b = at.b, t0 = at.tile, count = min(left, at.row.tiles - t0);
         const bool starts = t0 == 0, ends = t0 + count == at.row.tiles;
         const Row row = at.row;
         core.begin(sm + L::Q, lane);
         Place after = at;
-        after.tile = t0 + count - 1;
         if (left > count) {
-            next(after);
-            fetch_q(after.b, after.unit);
+            next_unit(after);
+            fetch_q(after.b, after.kvh, after.hb);
         }
-        for (int i = 0; i < count; ++i, ++at.tile) {
+        for (int tile = t0; tile < t0 + count; ++tile) {
             unsigned seen;
-            const int first = sub_tile(at, seen);
+            const int first = sub_tile(row, tile, seen);
             if (!seen) continue;
             copy_wait<L::STAGES - 2>();
             __syncwarp();
             issue();
             const uint32_t ks = ring + stage * (2 * L::SUB), vs = ks + L::SUB;
             core.step(ks, vs, seen, scale2, sm + L::PW + warp * C::P_BYTES, lane);
-            if (p.k_new && unit % head_blocks == 0 && row.len - 1 - first < TS && row.len - 1 >= first) {
+            if (first + TS > row.solid && p.k_new && at.hb == 0 && row.solid >= first) {
                 // the new token's key and value into the cache, from the copy in shared memory
-                const int t = row.len - 1, r = t - first, slot = t / p.page_size;
+                const int t = row.solid, r = t - first, slot = page_of(t);
                 const int page = __ldg(p.table + (int64_t)b * p.max_pages + slot);
                 if (page >= 0 && page < p.num_pages) {
-                    const int64_t off = ((int64_t)(unit / head_blocks) * p.page_size + (t - slot * p.page_size)) * D;
+                    const int64_t off = ((int64_t)at.kvh * p.page_size + (t - slot * p.page_size)) * D;
                     for (int c = lane; c < 2 * CPR; c += 32) {
                         const bool is_k = c < CPR;
                         const int chunk = is_k ? c : c - CPR;
@@ -660,7 +674,7 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
                 __syncthreads();
             }
         if (warp == 0) {
-            const int kvh = unit / head_blocks, h0 = unit % head_blocks * NH;
+            const int kvh = at.kvh, h0 = at.hb * NH;
             if (starts && ends) {
 #pragma unroll
                 for (int s = 0; s < C::SLOTS; ++s) mult[s] = sum[s] == 0.f ? 0.f : 1.f / sum[s];
@@ -696,7 +710,7 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
                 }
                 if (starts && lane == 0) {
                     const int64_t x = end - left + row.tiles;           // flat tiles up to the unit's last
-                    *record = Record{b, unit, (int)((x * shares - 1) / flat), first_unit ? 0 : 1};
+                    *record = Record{b, kvh * head_blocks + at.hb, (int)((x * shares - 1) / flat), first_unit ? 0 : 1};
                     recorded = true;
                 }
             }
@@ -778,12 +792,16 @@ __global__ void __launch_bounds__(AT) kda_attn_join_kernel(AttnParams p, int hea
 }
 
 template <typename T, int D, int NH>
-cudaError_t launch_core(const AttnParams& p, cudaStream_t s) {
+cudaError_t launch_core(AttnParams p, cudaStream_t s) {
     using L = Layout<T, D, NH>;
     static DeviceSetup done;
     int sms = 0;
     cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_attn_kernel<T, D, NH>), L::BYTES, &sms);
     if (e != cudaSuccess) return e;
+    // floor(2^(32 + shift) / page_size) + 1 with 2^shift < page_size <= 2^(shift + 1): exact for 31-bit tokens
+    p.page_shift = 0;
+    while ((2ll << p.page_shift) < p.page_size) ++p.page_shift;
+    p.page_magic = p.page_size == 1 ? 0u : (uint32_t)((1ull << (32 + p.page_shift)) / p.page_size + 1);
     const int group = p.Hq / p.Hkv, head_blocks = (group + NH - 1) / NH;
     const int grid = sms * L::CTAS_PER_SM < MAX_CTAS ? sms * L::CTAS_PER_SM : MAX_CTAS;
     kda_attn_kernel<T, D, NH><<<grid, AT, L::BYTES, s>>>(p, head_blocks, grid);

@@ -58,6 +58,9 @@ struct AttnParams {
     int32_t window;              // 0: every token below the length
     int32_t sinks;
     float scale;
+    // set by the launcher: t / page_size = umulhi(t, page_magic) >> page_shift for t < 2^31 (page_magic 0: t itself)
+    uint32_t page_magic;
+    int32_t page_shift;
 };
 size_t attn_workspace(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype dt);
 cudaError_t launch_attention_decode(const AttnParams& p, kda_dtype dt, cudaStream_t s);

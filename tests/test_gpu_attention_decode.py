@@ -158,6 +158,18 @@ def test_flat_and_peaked_softmax(dtype, qstd):
     check([1, 333, 2000], 8, 2, 64, 32, dtype, seed=9, qstd=qstd)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [-0.25, 0.0, 1e-30, -3.0])
+def test_scales_of_either_sign_and_zero(dtype, scale):
+    lens = [1, 77, 300, 5000]
+    t, _ = make(lens, 8, 2, 64, 16, dtype, 31)
+    for window in (0, 50):
+        ref, ref_lse = reference(t, lens, 16, scale, window, 3)
+        lse = torch.empty((4, 8), device=DEV)
+        o = kda.kda_attention_decode(**t, scale=scale, window=window, sinks=3, lse=lse)
+        assert rel(o, ref) <= TOL[dtype] and float((lse.double() - ref_lse).abs().max()) <= 1e-4
+
+
 def test_values_keep_their_precision_under_many_equal_weights():
     """A bf16 row whose values nearly cancel: the weights must not be rounded to bf16 before the sum.  With flat
     weights w rounded at random, the error against the exact mean would be 2^-9 / sqrt(3) of |v| / sqrt(n) per
