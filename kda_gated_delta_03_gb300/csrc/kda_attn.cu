@@ -331,17 +331,28 @@ struct Core<float, D, NH> {
         __syncwarp();
 #pragma unroll
         for (int t = 0; t < TS; ++t) {
-            float v[E];
+            float v[E], w[NH];
             const int d0 = (lane * E) % D;
             const uint32_t at = vs + t * (D * 4) + swizzle(t, d0 / 4) * 16 + (d0 & 3) * 4;
+            if constexpr (E == 4)
+                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                             : "r"(at) : "memory");
+            else if constexpr (E == 2)
+                asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at) : "memory");
+            else
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(at) : "memory");
+            if constexpr (NH % 4 == 0) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[e]) : "r"(at + 4 * e) : "memory");
+                for (int h = 0; h < NH; h += 4)
+                    *reinterpret_cast<float4*>(w + h) = *reinterpret_cast<const float4*>(pw + t * NH + h);
+            } else {
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                const float w = pw[t * NH + h];
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[h * E + e] += w * v[e];
+                for (int h = 0; h < NH; ++h) w[h] = pw[t * NH + h];
             }
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[h * E + e] += w[h] * v[e];
         }
         __syncwarp();
     }
@@ -366,10 +377,10 @@ struct Layout {
     static constexpr int RING = STAGES * 2 * SUB;                 // of one warp
     static constexpr int Q = NW * RING;
     static constexpr int Q_BYTES = NH * C::QP;
-    static constexpr int MERGE = Q + Q_BYTES;                     // two warps' accumulators, one head tile at a time
-    static constexpr int MERGE_REGS = C::ACC < 16 ? C::ACC : 16;
-    static constexpr int STATS = MERGE + 2 * MERGE_REGS * 32 * 4; // m, l [NW][NH]
-    static constexpr int PW = STATS + 2 * NW * NH * 4;
+    static constexpr int MERGE = Q + Q_BYTES;                     // part of the warps' accumulators
+    static constexpr int MERGE_REGS = C::ACC < 8 ? C::ACC : D == 128 && sizeof(T) == 2 ? 16 : 8;
+    static constexpr int STATS = MERGE + NW * MERGE_REGS * 32 * 4;   // m, l [NW][NH], then multipliers [NW][NH], m, 1 / l [NH]
+    static constexpr int PW = STATS + (3 * NW + 2) * NH * 4;
     static constexpr int MISC = PW + NW * C::P_BYTES;
     static constexpr int BYTES = MISC + 32;
     static_assert(CTAS_PER_SM * (BYTES + 1024) <= 233472, "shared memory of the CTAs of an SM");
@@ -396,20 +407,35 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
 
     // ---- this CTA's share ----
     int* misc = reinterpret_cast<int*>(sm + L::MISC);
-    int64_t total = 0;
-    {
-        int mine = 0;
-        for (int b = tid; b < p.B; b += AT) mine += row_of<TILE>(p, p.lens[b]).tiles;
-        // tiles of all rows: below 2^31 each, the sum in 64 bits
-        int64_t sum = mine;
+    int64_t* sums = reinterpret_cast<int64_t*>(sm + L::MERGE);
+    // tiles of the rows b0 .. b0 + AT - 1: this thread's row's, those before it, and in all
+    auto scan_rows = [&](int b0, int& mine, int64_t& before, int64_t& all) {
+        mine = b0 + tid < p.B ? row_of<TILE>(p, __ldg(p.lens + b0 + tid)).tiles : 0;
+        int64_t inc = mine;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        int64_t* sums = reinterpret_cast<int64_t*>(sm + L::STATS);
-        if (lane == 0) sums[warp] = sum;
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) sums[warp] = inc;
         __syncthreads();
+        before = inc - mine;
+        all = 0;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) total += sums[w];
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += sums[w];
+            all += sums[w];
+        }
+    };
+    int mine;
+    int64_t before, total;                              // of the first AT rows, then of all
+    scan_rows(0, mine, before, total);
+    for (int b0 = AT; b0 < p.B; b0 += AT) {
+        int m;
+        int64_t unused, all;
         __syncthreads();
+        scan_rows(b0, m, unused, all);
+        total += all;
     }
     // no more shares than tiles: none of them is empty, so a unit's pieces lie in consecutive CTAs
     const int64_t flat = total * units, shares = flat < grid ? flat : grid;
@@ -417,40 +443,29 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
     int left = (int)(end - begin);                      // tiles of this CTA's share
     Place at{};
     if (left > 0) {
-        int64_t base = 0;                               // tiles of the rows before
-        int64_t* sums = reinterpret_cast<int64_t*>(sm + L::STATS);
+        int64_t base = 0;                               // tiles of the rows before b0
         for (int b0 = 0; b0 < p.B; b0 += AT) {
-            const int b = b0 + tid;
-            const int mine = b < p.B ? row_of<TILE>(p, p.lens[b]).tiles : 0;
-            int64_t inc = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-                if (lane >= o) inc += y;
+            int64_t all = total;
+            if (p.B > AT) {
+                __syncthreads();
+                scan_rows(b0, mine, before, all);
             }
-            if (lane == 31) sums[warp] = inc;
-            __syncthreads();
-            int64_t before = base, chunk = 0;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                if (w < warp) before += sums[w];
-                chunk += sums[w];
-            }
-            const int64_t hi = (before + inc) * units, lo = hi - (int64_t)mine * units;
+            const int64_t lo = (base + before) * units, hi = lo + (int64_t)mine * units;
             if (mine > 0 && begin >= lo && begin < hi) {
-                misc[0] = b;
-                misc[1] = (int)((begin - lo) / mine);
-                misc[2] = (int)((begin - lo) % mine);
+                const int64_t in = begin - lo;
+                misc[0] = b0 + tid;
+                misc[1] = (int)(in / mine);
+                misc[2] = (int)(in % mine);
             }
-            base += chunk;
-            __syncthreads();
+            base += all;
             if (begin < base * units) break;
         }
+        __syncthreads();
         at.b = misc[0];
         at.kvh = misc[1] / head_blocks;
         at.hb = misc[1] - at.kvh * head_blocks;
         at.tile = misc[2];
-        at.row = row_of<TILE>(p, p.lens[at.b]);
+        at.row = row_of<TILE>(p, __ldg(p.lens + at.b));
     }
 
     auto next_unit = [&](Place& x) {                    // only called while the share goes on
@@ -579,6 +594,8 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
     float* pieces = reinterpret_cast<float*>(p.workspace + MAX_CTAS * sizeof(Record)) + (int64_t)cta * 2 * L::PIECE;
     float* sm_m = reinterpret_cast<float*>(sm + L::STATS);
     float* sm_l = sm_m + NW * NH;
+    float* sm_mult = sm_l + NW * NH;
+    float* sm_inv = sm_mult + NW * NH;
     float* merge = reinterpret_cast<float*>(sm + L::MERGE);
     const float scale2 = fmaxf(fabsf(p.scale) * LOG2E, 1e-38f);      // above 0: a masked score stays at -inf
     bool first_unit = true, recorded = false;
@@ -630,90 +647,68 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
             stage = stage + 1 == L::STAGES ? 0 : stage + 1;
         }
 
-        // ---- join the warps ----
+        // ---- join the warps: their accumulators through shared memory, a few registers at a time ----
         core.sum_lanes();
         if (C::writes_stats(lane)) {
 #pragma unroll
-            for (int s = 0; s < C::SLOTS; ++s) {
-                sm_m[warp * NH + C::head_of_slot(s, lane)] = core.m[s];
-                sm_l[warp * NH + C::head_of_slot(s, lane)] = core.l[s];
+            for (int i = 0; i < C::SLOTS; ++i) {
+                sm_m[warp * NH + C::head_of_slot(i, lane)] = core.m[i];
+                sm_l[warp * NH + C::head_of_slot(i, lane)] = core.l[i];
             }
         }
-        __syncthreads();
-        if (left > count) store_q();                    // every warp is done with this unit's
-        float top[C::SLOTS], sum[C::SLOTS], mult[C::SLOTS];
+        const int kvh = at.kvh, h0 = at.hb * NH;
+        const bool complete = starts && ends;
+        float* piece = pieces + (first_unit ? 0 : L::PIECE);
 #pragma unroll
-        for (int s = 0; s < C::SLOTS; ++s) {
-            const int h = C::head_of_slot(s, lane);
-            top[s] = -INFINITY;
-            sum[s] = 0.f;
+        for (int r0 = 0; r0 < C::ACC; r0 += L::MERGE_REGS) {
 #pragma unroll
-            for (int w = 0; w < NW; ++w) top[s] = fmaxf(top[s], sm_m[w * NH + h]);
-            const float base = top[s] == -INFINITY ? 0.f : top[s];
+            for (int i = 0; i < L::MERGE_REGS; ++i)
+                if (r0 + i < C::ACC) merge[(warp * L::MERGE_REGS + i) * 32 + lane] = core.acc[r0 + i];
+            __syncthreads();
+            if (r0 == 0) {
+                if (left > count) store_q();            // every warp is done with this unit's
+                if (tid < NH) {
+                    float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) sum[s] += sm_l[w * NH + h] * exp2_approx(sm_m[w * NH + h] - base);
-            mult[s] = exp2_approx(core.m[s] - base);
+                    for (int w = 0; w < NW; ++w) top = fmaxf(top, sm_m[w * NH + tid]);
+                    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        const float x = exp2_approx(sm_m[w * NH + tid] - base);
+                        sm_mult[w * NH + tid] = x;
+                        sum += sm_l[w * NH + tid] * x;
+                    }
+                    sm_inv[tid] = sum == 0.f ? 0.f : 1.f / sum;
+                    if (!complete) {
+                        piece[NH * D + tid] = top;
+                        piece[NH * D + NH + tid] = sum;
+                    } else if (p.lse && h0 + tid < group) {
+                        p.lse[(int64_t)b * p.Hq + kvh * group + h0 + tid] =
+                            sum == 0.f ? -INFINITY : (top + log2f(sum)) * LN2;
+                    }
+                }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int k = 0; k < (L::MERGE_REGS + NW - 1) / NW; ++k) {
+                const int j = warp + NW * k, i = r0 + j;                 // register i of every warp
+                if (j >= L::MERGE_REGS || i >= C::ACC) break;
+                const int h = C::head_of_slot(C::slot_of(i), lane), d = C::dim_of(i, lane);
+                float o = 0.f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) o += merge[(w * L::MERGE_REGS + j) * 32 + lane] * sm_mult[w * NH + h];
+                if (!C::owns_output(lane)) continue;
+                if (!complete)
+                    piece[h * D + d] = o;
+                else if (h0 + h < group)
+                    store_from_float(static_cast<T*>(p.o), ((int64_t)b * p.Hq + kvh * group + h0 + h) * D + d, o * sm_inv[h]);
+            }
+            __syncthreads();
         }
-#pragma unroll
-        for (int i = 0; i < C::ACC; ++i) core.acc[i] *= mult[C::slot_of(i)];
-#pragma unroll
-        for (int from = NW / 2; from >= 1; from /= 2)
-#pragma unroll
-            for (int r0 = 0; r0 < C::ACC; r0 += L::MERGE_REGS) {
-                if (warp >= from && warp < 2 * from) {
-#pragma unroll
-                    for (int i = 0; i < L::MERGE_REGS; ++i)
-                        merge[((warp - from) * L::MERGE_REGS + i) * 32 + lane] = core.acc[r0 + i];
-                }
-                __syncthreads();
-                if (warp < from) {
-#pragma unroll
-                    for (int i = 0; i < L::MERGE_REGS; ++i)
-                        core.acc[r0 + i] += merge[(warp * L::MERGE_REGS + i) * 32 + lane];
-                }
-                __syncthreads();
-            }
-        if (warp == 0) {
-            const int kvh = at.kvh, h0 = at.hb * NH;
-            if (starts && ends) {
-#pragma unroll
-                for (int s = 0; s < C::SLOTS; ++s) mult[s] = sum[s] == 0.f ? 0.f : 1.f / sum[s];
-#pragma unroll
-                for (int i = 0; i < C::ACC; ++i) {
-                    const int s = C::slot_of(i), h = h0 + C::head_of_slot(s, lane);
-                    if (h < group && C::owns_output(lane))
-                        store_from_float(static_cast<T*>(p.o), ((int64_t)b * p.Hq + kvh * group + h) * D + C::dim_of(i, lane),
-                                         core.acc[i] * mult[s]);
-                }
-                if (p.lse && C::writes_stats(lane)) {
-#pragma unroll
-                    for (int s = 0; s < C::SLOTS; ++s) {
-                        const int h = h0 + C::head_of_slot(s, lane);
-                        if (h < group)
-                            p.lse[(int64_t)b * p.Hq + kvh * group + h] =
-                                sum[s] == 0.f ? -INFINITY : (top[s] + log2f(sum[s])) * LN2;
-                    }
-                }
-            } else {
-                float* piece = pieces + (first_unit ? 0 : L::PIECE);
-                if (C::writes_stats(lane)) {
-#pragma unroll
-                    for (int s = 0; s < C::SLOTS; ++s) {
-                        piece[NH * D + C::head_of_slot(s, lane)] = top[s];
-                        piece[NH * D + NH + C::head_of_slot(s, lane)] = sum[s];
-                    }
-                }
-                if (C::owns_output(lane)) {
-#pragma unroll
-                    for (int i = 0; i < C::ACC; ++i)
-                        piece[C::head_of_slot(C::slot_of(i), lane) * D + C::dim_of(i, lane)] = core.acc[i];
-                }
-                if (starts && lane == 0) {
-                    const int64_t x = end - left + row.tiles;           // flat tiles up to the unit's last
-                    *record = Record{b, kvh * head_blocks + at.hb, (int)((x * shares - 1) / flat), first_unit ? 0 : 1};
-                    recorded = true;
-                }
-            }
+        if (tid == 0 && starts && !ends) {
+            const int64_t x = end - left + row.tiles;                   // flat tiles up to the unit's last
+            *record = Record{b, kvh * head_blocks + at.hb, (int)((x * shares - 1) / flat), first_unit ? 0 : 1};
+            recorded = true;
         }
         left -= count;
         first_unit = false;
