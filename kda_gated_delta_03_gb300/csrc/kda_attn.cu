@@ -388,11 +388,13 @@ struct Layout {
     static constexpr int PIECE = piece_floats(NH, D);
 };
 
-// Partial results of a unit that starts in this CTA's share and goes on in others'.
+// Partial results of a unit that starts in one CTA's share and goes on in others'.  Records lie at the unit's
+// place where the units are no more than the CTAs, else at its first CTA's (which has one at most).
 struct Record {
     int b, unit;                 // -1: none
-    int last;                    // the CTA with its end
+    int first, last;             // the CTAs with its pieces
     int slot;                    // of the first piece; the others lie in slot 0
+    int pad[3];
 };
 
 template <typename T, int D, int NH>
@@ -590,7 +592,8 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
         }
     };
 
-    Record* record = reinterpret_cast<Record*>(p.workspace) + cta;
+    Record* records = reinterpret_cast<Record*>(p.workspace);
+    const bool by_unit = (int64_t)p.B * units <= grid;
     float* pieces = reinterpret_cast<float*>(p.workspace + MAX_CTAS * sizeof(Record)) + (int64_t)cta * 2 * L::PIECE;
     float* sm_m = reinterpret_cast<float*>(sm + L::STATS);
     float* sm_l = sm_m + NW * NH;
@@ -705,21 +708,29 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
             }
             __syncthreads();
         }
-        if (tid == 0 && starts && !ends) {
-            const int64_t x = end - left + row.tiles;                   // flat tiles up to the unit's last
-            *record = Record{b, kvh * head_blocks + at.hb, (int)((x * shares - 1) / flat), first_unit ? 0 : 1};
-            recorded = true;
+        if (tid == 0 && starts) {
+            const int unit = kvh * head_blocks + at.hb;
+            if (!ends) {
+                const int64_t x = end - left + row.tiles;               // flat tiles up to the unit's last
+                records[by_unit ? b * units + unit : cta] =
+                    Record{b, unit, cta, (int)((x * shares - 1) / flat), first_unit ? 0 : 1, {0, 0, 0}};
+                recorded = true;
+            } else if (by_unit) {
+                records[b * units + unit].b = -1;
+            }
         }
         left -= count;
         first_unit = false;
         if (left > 0) at = after;
     }
-    if (tid == 0 && !recorded) record->b = -1;
+    if (tid == 0 && !recorded && !by_unit) records[cta].b = -1;
     // rows without a visible token
     for (int b = cta; b < p.B; b += grid) {
         const int len = p.lens[b];
         if (tid == 0 && (len < 0 || len > p.max_pages * p.page_size)) atomicOr(p.err, KDA_DEVERR_PAGES);
         if (row_of<TILE>(p, len).tiles) continue;
+        if (by_unit)
+            for (int u = tid; u < units; u += AT) records[b * units + u].b = -1;
         T* o = static_cast<T*>(p.o) + (int64_t)b * p.Hq * D;
         for (int i = tid; i < p.Hq * D; i += AT) store_from_float(o, i, 0.f);
         if (p.lse)
@@ -727,7 +738,7 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
     }
 }
 
-// Joins the pieces of the unit that starts in share blockIdx.x and goes on in others, one CTA per head.
+// Joins the pieces of a unit, one CTA per record and head.
 template <typename T, int D, int NH>
 __global__ void __launch_bounds__(AT) kda_attn_join_kernel(AttnParams p, int head_blocks) {
     using L = Layout<T, D, NH>;
@@ -735,7 +746,7 @@ __global__ void __launch_bounds__(AT) kda_attn_join_kernel(AttnParams p, int hea
     const Record r = reinterpret_cast<const Record*>(p.workspace)[blockIdx.x];
     const int group = p.Hq / p.Hkv, h = blockIdx.y;
     if (r.b < 0 || r.unit % head_blocks * NH + h >= group) return;
-    const int first = blockIdx.x, n = r.last - first + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int first = r.first, n = r.last - first + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float* pieces = reinterpret_cast<const float*>(p.workspace + MAX_CTAS * sizeof(Record)) + (int64_t)first * 2 * L::PIECE;
     __shared__ float weight[MAX_CTAS], red[NW], part[AT * 4];
     auto piece = [&](int i) { return pieces + (int64_t)i * 2 * L::PIECE + (i == 0 ? r.slot * L::PIECE : 0); };
@@ -804,7 +815,8 @@ cudaError_t launch_core(AttnParams p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(grid, group < NH ? group : NH);
+    const int64_t all_units = (int64_t)p.B * p.Hkv * head_blocks;
+    cfg.gridDim = dim3(all_units < grid ? (unsigned)all_units : grid, group < NH ? group : NH);
     cfg.blockDim = dim3(AT);
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
