@@ -11,12 +11,13 @@ namespace kda {
 // The current device's error word (defined with the other entry points' host code).
 kda_status device_error_word(unsigned** out);
 
-// The current device's SMs, and a kernel's right to `smem` bytes of dynamic shared memory there.  Both are asked for
-// once per device: these calls are made for every generated token.  `done` is the kernel's own.
+// The current device's SMs, and a kernel's right to `smem` bytes of dynamic shared memory and to clusters of 16
+// CTAs there.  All is asked for once per device: these calls are made for every generated token.  `done` is the
+// kernel's own.
 struct DeviceSetup {
     std::atomic<int> sms[64] = {};               // 0: not asked yet
 };
-inline cudaError_t device_setup(DeviceSetup& done, const void* kernel, int smem, int* sms) {
+inline cudaError_t device_setup(DeviceSetup& done, const void* kernel, int smem, int* sms, bool cluster16 = false) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -26,6 +27,8 @@ inline cudaError_t device_setup(DeviceSetup& done, const void* kernel, int smem,
         e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess && smem > 48 * 1024)
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess && cluster16)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         if (known) done.sms[dev].store(n, std::memory_order_release);
     }
