@@ -423,31 +423,34 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int par
     const int per_row = parts * L, entries = K * per_row;
     unsigned long long* scored = entries <= KEPT ? kept : list;
     if (tid == 0) found = 0;
+    // the inputs are there since before the parts' kernel began
+    float score = warp < K ? p.beam_scores[n * K + warp] : 0.f;
+    bool done = warp < K && p.finished && p.finished[n * K + warp];
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // a warp per row: its lse, and its entries as scores with their places in the group
     unsigned long long mine = 0;
     float left_out = -INFINITY;                        // no logit that a part left out scores more
     for (int b = warp; b < K; b += BW) {
-        const int64_t row = (int64_t)n * K + b;
-        const float score = p.beam_scores[row];
-        const bool reads = live(p, row), done = p.finished && p.finished[row];
+        const unsigned long long* from = list + b * per_row;
         unsigned long long* to = scored + b * per_row;
+        constexpr int AHEAD = 4;                       // entries of a lane on their way (of a row that is not read: unused)
+        unsigned long long c[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) c[i] = lane + 32 * i < per_row ? from[lane + 32 * i] : 0;
+        const unsigned long long head = lane < parts ? from[lane * L] : 0;
+        const float2 stat = lane < parts ? stats[b * parts + lane] : make_float2(0.f, 0.f);
         bool is_alive = false;
         float log_sum = 0.f;
-        if (reads) {
-            const unsigned long long* from = list + b * per_row;
-            constexpr int AHEAD = 4;                   // entries of a lane on their way
-            unsigned long long c[AHEAD];
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) c[i] = lane + 32 * i < per_row ? from[lane + 32 * i] : 0;
+        if (!done && score == score && score != -INFINITY) {
             // the row's largest logit stands first in one of the lists
-            float top = -INFINITY, sum = 0.f;
-            for (int i = lane; i < parts; i += 32)
+            float top = head ? candidate_value(head) : -INFINITY, sum = 0.f;
+            for (int i = lane + 32; i < parts; i += 32)
                 if (from[i * L]) top = fmaxf(top, candidate_value(from[i * L]));
 #pragma unroll
             for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            for (int i = lane; i < parts; i += 32) {
+            if (lane < parts && stat.y != 0.f) sum = stat.y * exp_of(stat.x - top);
+            for (int i = lane + 32; i < parts; i += 32) {
                 const float2 s = stats[b * parts + i];
                 if (s.y != 0.f) sum += s.y * exp_of(s.x - top);
             }
@@ -455,6 +458,8 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int par
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
             is_alive = top != -INFINITY && sum == sum;               // else every score of the row is -inf
             log_sum = top + logf(sum);
+            int in_list = lane % L;                                  // of entry e0 + 32 * i
+            const int step = 32 % L;
             for (int e0 = lane; e0 < per_row; e0 += 32 * AHEAD) {
                 unsigned long long after[AHEAD];
 #pragma unroll
@@ -469,11 +474,13 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int par
                     if (is_alive && c[i]) {
                         const float x = candidate_value(c[i]), s = beam_score(score, x, log_sum);
                         if (s != -INFINITY) d = candidate(s, (unsigned)b * p.V + candidate_place(c[i]));
-                        if (e % L == K) left_out = fmaxf(left_out, beam_score(score, below(x, T()), log_sum));
+                        if (in_list == K) left_out = fmaxf(left_out, beam_score(score, below(x, T()), log_sum));
                     }
                     if (e < per_row) to[e] = d;
                     mine = d > mine ? d : mine;
                     c[i] = after[i];
+                    in_list += step;
+                    if (in_list >= L) in_list -= L;
                 }
             }
         } else {
@@ -491,22 +498,31 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int par
             lse[b] = log_sum;
             alive[b] = is_alive;
         }
+        if (b + BW < K) {
+            score = p.beam_scores[n * K + b + BW];
+            done = p.finished && p.finished[n * K + b + BW];
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) left_out = fmaxf(left_out, __shfl_xor_sync(0xFFFFFFFFu, left_out, o));
     if (lane == 0) warp_left[warp] = left_out;
     // as in a part: the K-th largest of the groups' maxima bounds the K-th score from below
-    unsigned long long g = mine, other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
-    g = other > g ? other : g;
-    other = __shfl_xor_sync(0xFFFFFFFFu, g, 2);
-    g = other > g ? other : g;
-    if ((lane & 3) == 0) group_max[tid / 4] = g;
+    const bool few = K <= FEW;
+    unsigned long long g = mine;
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2) {
+        if (o == 4 && !few) break;
+        const unsigned long long other = __shfl_xor_sync(0xFFFFFFFFu, g, o);
+        g = other > g ? other : g;
+    }
+    const int members = few ? 8 : 4, groups = BT / members;
+    if (lane % members == 0) group_max[tid / members] = g;
     __syncthreads();
-    if (tid < GROUPS) {
+    if (tid < groups) {
         g = group_max[tid];
         int rank = 0;
 #pragma unroll 8
-        for (int j = 0; j < GROUPS; ++j) rank += group_max[j] > g || (group_max[j] == g && j < tid);
+        for (int j = 0; j < groups; ++j) rank += group_max[j] > g || (group_max[j] == g && j < tid);
         if (rank == K - 1) bound = g;
     }
     __syncthreads();
