@@ -24,10 +24,12 @@ constexpr int BT = 256;                       // threads
 constexpr int BW = BT / 32;
 constexpr int GROUPS = BT / 4;                // groups of threads whose maxima bound the K-th logit, at most
 constexpr int FEW = 15;                       // beams up to which half as many groups bound it as well
-constexpr int CAP = 512;                      // logits kept until they are compared with one another
+constexpr int CAP = 512;                      // logits kept until they are compared with one another,
+constexpr int WARP_CAP = CAP / BW;            // so many by each warp
 constexpr int THREAD_BYTES = 64;              // of logits in a thread's registers
 constexpr int CTAS_PER_SM = 3;
 constexpr int STAGES = 4;                     // chunks of a warp in shared memory or on their way there
+static_assert(KDA_BEAM_MAX_K + 1 <= WARP_CAP, "the best of all warps' go on in the first one's place");
 static_assert(KDA_BEAM_MAX_K + 1 <= GROUPS, "the bound on the K-th logit");
 
 // A value and its place as one whole number: larger values first, then lower places; no two are equal.
@@ -139,6 +141,17 @@ struct Logits {
     // The copies of chunk `chunk` of a row of V logits at v (rounded down to the boundary).
     __device__ static void copy(uint32_t ring, const uint4* v, int chunk, int off, int V, int tid) {
         const int lane = tid & 31;
+        if ((int64_t)(chunk + 1) * CHUNK<T> + PER <= V) {              // not the row's end
+            const uint4* from = v + chunk * (NV * BT) + tid;
+            const uint32_t to = ring + lane * 16;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) copy16(to + j * (33 * 16), from + j * BT, true);
+            if (off && lane == 0) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) copy16(to + j * (33 * 16) + 32 * 16, from + j * BT + 32, true);
+            }
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int at = (chunk * NV + j) * BT + tid;
@@ -153,10 +166,13 @@ struct Logits {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const uint4 a = shared16(ring + (j * 33 + lane) * 16);
-            uint32_t u[9] = {a.x, a.y, a.z, a.w, 0, 0, 0, 0, 0};
-            if (off) {
+            w[4 * j] = a.x; w[4 * j + 1] = a.y; w[4 * j + 2] = a.z; w[4 * j + 3] = a.w;
+        }
+        if (off) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
                 const uint4 b = shared16(ring + (j * 33 + lane + 1) * 16);
-                u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
+                uint32_t u[9] = {w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3], b.x, b.y, b.z, b.w, 0};
                 if (words & 1) {
 #pragma unroll
                     for (int e = 0; e < 7; ++e) u[e] = u[e + 1];
@@ -169,9 +185,9 @@ struct Logits {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) u[e] = __funnelshift_r(u[e], u[e + 1], 16);
                 }
-            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[4 * j + e] = u[e];
+                for (int e = 0; e < 4; ++e) w[4 * j + e] = u[e];
+            }
         }
         if (count < CHUNK<T>) {
 #pragma unroll
@@ -251,10 +267,11 @@ __device__ __forceinline__ void rank_candidates(const unsigned long long* cand, 
 }
 
 // One part of a row, chunk by chunk.  The first chunk gives a bound that at least L of its logits reach; from
-// then on only logits above it are looked at one by one (later ones lose to equal ones), and the bound moves
-// up to the L-th best after the second chunk and the fourth, so that a few remain in each chunk and most
-// chunks need no barrier.  If more turn up than are kept, the L-th best of those kept is a better bound and the
-// part is searched again with it.
+// then on only logits above it are looked at one by one (later ones lose to equal ones), each warp with a list of
+// its own, and the bound moves up to the L-th best after the second chunk, the fourth, the eighth and so on.
+// So about L logits are looked at between two such steps (without them about L in every chunk: 38 us instead of 28
+// for 512 rows of 131,072), and the other chunks need no barrier.  If a warp's list runs over, the L-th best of
+// those kept is a better bound, and the part is searched again with it.
 //
 // The sum is that of exp(x - t), t the first chunk's maximum; a thread that meets a logit 64 above moves its own t
 // up.
@@ -263,8 +280,8 @@ __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamPara
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ __align__(16) float group_max[GROUPS];
     __shared__ float warp_top[BW], warp_sum[BW], bound;
-    __shared__ int found;
-    __shared__ unsigned long long cand[CAP], best[KDA_BEAM_MAX_K + 1];
+    __shared__ int found, kept[BW];
+    __shared__ unsigned long long cand[CAP], all[CAP], best[KDA_BEAM_MAX_K + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / (unsigned)parts;
     const int part = blockIdx.x % (unsigned)parts, L = p.K + 1;
@@ -274,121 +291,143 @@ __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamPara
     using X = Logits<T>;
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_bytes) + warp * (STAGES * X::WARP_BYTES);
-    const uintptr_t logits = reinterpret_cast<uintptr_t>(static_cast<const T*>(p.logits) + row * p.row_stride);
-    const int off = (int)(logits % 16 / sizeof(T));
-    const uint4* v = reinterpret_cast<const uint4*>(logits - logits % 16);
-    if (tid == 0) found = 0;
+    const uintptr_t start = reinterpret_cast<uintptr_t>(static_cast<const T*>(p.logits) + row * p.row_stride);
+    const int off = (int)(start % 16 / sizeof(T));
+    const uint4* v = reinterpret_cast<const uint4*>(start - start % 16);
 
     float t = -INFINITY, limit = -INFINITY, sum = 0.f;   // limit: logits above it move t
     float least = -INFINITY;                             // logits from it on are looked at
-    unsigned long long least_key = 0;                    // and those from this key on are kept
-    for (bool again = false;; again = true) {
-        int ahead = first, in = 0, out = 0;              // the next chunk to copy, stages
-        auto copy_next = [&]() {
-            if (ahead < last) X::copy(ring + in * X::WARP_BYTES, v, ahead, off, p.V, tid);
-            ++ahead;
-            in = in + 1 == STAGES ? 0 : in + 1;
-            asm volatile("cp.async.commit_group;\n" ::: "memory");
-        };
-#pragma unroll 1
-        for (int i = 0; i < STAGES - 1; ++i) copy_next();
-#pragma unroll 1
-        for (int chunk = first; chunk < last; ++chunk) {
-            asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
-            __syncwarp();                                // the warp's copies are there, its reads of the next stage over
-            const uint32_t stage = ring + out * X::WARP_BYTES;
-            out = out + 1 == STAGES ? 0 : out + 1;
-            copy_next();
-            X x;
-            x.take(stage, off, min(p.V - chunk * CHUNK<T>, CHUNK<T>), tid);
-            const float mine = x.max();
-            if (chunk == first && !again) {
-                // groups of four threads, or of eight: with 32 groups the bound lets about as few through (an L
-                // of 16 at most), and one warp ranks them
-                const bool few = p.K <= FEW;
-                float g = fmaxf(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
-                g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 2));
-                if (!few && (lane & 3) == 0) group_max[tid / 4] = g;
-                g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 4));
-                if (few && (lane & 7) == 0) group_max[tid / 8] = g;
+    int mine_kept = 0;                                   // in this warp's list (more than WARP_CAP: some are lost)
+    // All warps' lists as one, all[0 .. n); a barrier before and one inside.
+    auto gather = [&](bool& lost) -> int {
+        if (lane == 0) kept[warp] = mine_kept;
+        __syncthreads();
+        int before = 0, n = 0;
 #pragma unroll
-                for (int o = 8; o < 32; o *= 2) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
-                if (lane == 0) warp_top[warp] = g;
-                __syncthreads();
+        for (int w = 0; w < BW; ++w) {
+            const int c = kept[w];
+            lost |= c > WARP_CAP;
+            if (w < warp) before += min(c, WARP_CAP);
+            n += min(c, WARP_CAP);
+        }
+        for (int i = lane; i < min(mine_kept, WARP_CAP); i += 32) all[before + i] = cand[warp * WARP_CAP + i];
+        __syncthreads();
+        return n;
+    };
+    int ahead = first, in = 0, out = 0;                  // the next chunk to copy, stages
+    auto copy_next = [&]() {
+        if (ahead < last) X::copy(ring + in * X::WARP_BYTES, v, ahead, off, p.V, tid);
+        ++ahead;
+        in = in + 1 == STAGES ? 0 : in + 1;
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < STAGES - 1; ++i) copy_next();
+    bool lost = false;
+#pragma unroll 1
+    for (int chunk = first; chunk < last; ++chunk) {
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
+        __syncwarp();                                    // the warp's copies are there, its reads of the next stage over
+        const uint32_t stage = ring + out * X::WARP_BYTES;
+        out = out + 1 == STAGES ? 0 : out + 1;
+        copy_next();
+        X x;
+        x.take(stage, off, min(p.V - chunk * CHUNK<T>, CHUNK<T>), tid);
+        const float mine = x.max();
+        if (chunk == first) {
+            // groups of four threads, or of eight: with 32 groups the bound lets about as few through (an L of 16 at
+            // most), and one warp ranks them
+            const bool few = p.K <= FEW;
+            float g = fmaxf(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
+            g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 2));
+            if (!few && (lane & 3) == 0) group_max[tid / 4] = g;
+            g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 4));
+            if (few && (lane & 7) == 0) group_max[tid / 8] = g;
 #pragma unroll
-                for (int i = 0; i < BW; ++i) g = fmaxf(g, warp_top[i]);
-                t = g;
-                limit = g + 64.f;
-                const int groups = few ? GROUPS / 2 : GROUPS;
-                if (tid < groups) {
-                    g = group_max[tid];
-                    int rank = 0;
+            for (int o = 8; o < 32; o *= 2) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
+            if (lane == 0) warp_top[warp] = g;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < BW; ++i) g = fmaxf(g, warp_top[i]);
+            t = g;
+            limit = g + 64.f;
+            const int groups = few ? GROUPS / 2 : GROUPS;
+            if (tid < groups) {
+                g = group_max[tid];
+                int rank = 0;
 #pragma unroll 4
-                    for (int j = 0; j < groups / 4; ++j) {
-                        const float4 y = reinterpret_cast<const float4*>(group_max)[j];
-                        rank += (y.x > g || (y.x == g && 4 * j < tid)) + (y.y > g || (y.y == g && 4 * j + 1 < tid)) +
-                                (y.z > g || (y.z == g && 4 * j + 2 < tid)) + (y.w > g || (y.w == g && 4 * j + 3 < tid));
-                    }
-                    if (rank == L - 1) bound = g;
+                for (int j = 0; j < groups / 4; ++j) {
+                    const float4 y = reinterpret_cast<const float4*>(group_max)[j];
+                    rank += (y.x > g || (y.x == g && 4 * j < tid)) + (y.y > g || (y.y == g && 4 * j + 1 < tid)) +
+                            (y.z > g || (y.z == g && 4 * j + 2 < tid)) + (y.w > g || (y.w == g && 4 * j + 3 < tid));
                 }
-                __syncthreads();
-                least = bound == -INFINITY ? above(bound, T()) : bound;
+                if (rank == L - 1) bound = g;
             }
-            const unsigned owners = __ballot_sync(0xFFFFFFFFu, mine >= least);
-            if (owners) {
-                // the few threads with such a logit: theirs are read again, a lane per element
-                for (unsigned rest = owners; rest; rest &= rest - 1) {
-                    const int owner = __ffs(rest) - 1;
+            __syncthreads();
+            least = bound == -INFINITY ? above(bound, T()) : bound;
+        }
+        const unsigned owners = __ballot_sync(0xFFFFFFFFu, mine >= least);
+        if (owners) {
+            // the few threads with such a logit: theirs are read again, a lane per element
+            for (unsigned rest = owners; rest; rest &= rest - 1) {
+                const int owner = __ffs(rest) - 1;
 #pragma unroll
-                    for (int e = 0; e < X::NV * X::PER; e += 32) {
-                        const int i = e + lane;
-                        const int place = chunk * CHUNK<T> + (i / X::PER * BT + tid - lane + owner) * X::PER + i % X::PER;
-                        if (i < X::NV * X::PER && place < p.V) {
-                            const float y = X::element(stage, off, owner, i);
-                            const unsigned long long c = candidate(y, (unsigned)place);
-                            if (y >= least && c >= least_key) {
-                                const int at = atomicAdd(&found, 1);
-                                if (at < CAP) cand[at] = c;
-                            }
-                        }
-                    }
-                }
-                if (mine > limit) {                     // -inf until a thread meets its first logit
-                    if (sum != 0.f) sum *= exp_of(t - mine);
-                    t = mine;
-                    limit = mine + 64.f;
+                for (int e = 0; e < X::NV * X::PER; e += 32) {
+                    const int i = e + lane;
+                    const int place = chunk * CHUNK<T> + (i / X::PER * BT + tid - lane + owner) * X::PER + i % X::PER;
+                    const bool there = i < X::NV * X::PER && place < p.V;
+                    const float y = there ? X::element(stage, off, owner, i) : -INFINITY;
+                    const unsigned hits = __ballot_sync(0xFFFFFFFFu, there && y >= least);
+                    const int at = mine_kept + __popc(hits & ((1u << lane) - 1));
+                    if (hits >> lane & 1 && at < WARP_CAP) cand[warp * WARP_CAP + at] = candidate(y, (unsigned)place);
+                    mine_kept += __popc(hits);
                 }
             }
-            if (again) continue;
-            sum += x.sum_exp(t == -INFINITY ? 0.f : t);
-            if (chunk == first && bound != -INFINITY) least = above(bound, T());
-            if ((chunk == first + 1 || chunk == first + 3) && chunk + 1 < last) {
+            if (mine > limit) {                         // -inf until a thread meets its first logit
+                if (sum != 0.f) sum *= exp_of(t - mine);
+                t = mine;
+                limit = mine + 64.f;
+            }
+        }
+        sum += x.sum_exp(t == -INFINITY ? 0.f : t);
+        if (chunk == first && bound != -INFINITY) least = above(bound, T());
+        const int done = chunk - first + 1;
+        if (done >= 2 && (done & (done - 1)) == 0 && chunk + 1 < last && !lost) {
+            const int n = gather(lost);
+            if (n >= L && !lost) {
+                rank_candidates(all, n, L, best);
                 __syncthreads();
-                const int n = found;
-                if (n >= L && n <= CAP) {
-                    rank_candidates(cand, n, L, best);
-                    __syncthreads();
-                    if (tid < L) cand[tid] = best[tid];
-                    if (tid == 0) found = L;
-                    least = fmaxf(least, above(candidate_value(best[L - 1]), T()));
-                }
-                __syncthreads();
+                if (tid < L) cand[tid] = best[tid];
+                mine_kept = warp == 0 ? L : 0;
+                least = fmaxf(least, above(candidate_value(best[L - 1]), T()));
+            }
+        }
+    }
+    int n = gather(lost);
+    while (lost) {
+        // again, from the L-th best of those kept on; each time fewer remain
+        rank_candidates(all, min(n, CAP), L, best);
+        if (tid == 0) found = 0;
+        __syncthreads();
+        const unsigned long long from = best[L - 1];
+        const T* logits = static_cast<const T*>(p.logits) + row * p.row_stride;
+        const int stop = min(p.V, last * CHUNK<T>);
+        for (int i = first * CHUNK<T> + tid; i < stop; i += BT) {
+            const float y = to_float(logits[i]);
+            const unsigned long long c = candidate(y, (unsigned)i);
+            if (y > -INFINITY && c >= from) {
+                const int at = atomicAdd(&found, 1);
+                if (at < CAP) all[at] = c;
             }
         }
         __syncthreads();
-        const int n = found;
-        if (n <= CAP) break;
-        rank_candidates(cand, CAP, L, best);
-        __syncthreads();
-        if (tid == 0) found = 0;
-        least_key = best[L - 1];
-        least = candidate_value(least_key);
-        limit = INFINITY;
+        n = found;
+        lost = n > CAP;
         __syncthreads();
     }
 
     const Workspace<T> w = workspace<T>(p, parts);
-    rank_candidates(cand, found, L, w.list + (row * parts + part) * L);
+    rank_candidates(all, n, L, w.list + (row * parts + part) * L);
     float top = t;
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -642,7 +681,7 @@ template <typename T>
 cudaError_t launch(const BeamParams& p, cudaStream_t s) {
     const int parts = part_count<T>((int64_t)p.N * p.K, p.V);
     constexpr int ring = BW * STAGES * Logits<T>::WARP_BYTES;
-    static_assert(CTAS_PER_SM * (ring + 8 * 1024) <= 233472, "the rings, the kept logits and the system's 1 KB");
+    static_assert(CTAS_PER_SM * (ring + 9728) <= 233472, "the rings, the kept logits and the system's 1 KB");
     static DeviceSetup done;
     int sms = 0;
     cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_beam_part_kernel<T>), ring, &sms);
