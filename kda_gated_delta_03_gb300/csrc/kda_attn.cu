@@ -115,7 +115,8 @@ struct Core;
 // bf16: tokens are the rows and heads the columns of the tensor core's tile.
 template <int D, int NH>
 struct Core<__nv_bfloat16, D, NH> {
-    static constexpr int TS = 16;                       // tokens of a warp's sub-tile
+    static constexpr int MT = D == 128 ? 1 : D == 64 ? 2 : 4;        // blocks of 16 tokens that share a maximum's update
+    static constexpr int TS = 16 * MT;                  // tokens of a warp's sub-tile
     static constexpr int CPR = D / 8;                   // 16-byte chunks of a token
     static constexpr int NT = NH / 8, KT = D / 16;
     static constexpr int SLOTS = 2 * NT;                // heads that a lane has columns of
@@ -151,44 +152,51 @@ struct Core<__nv_bfloat16, D, NH> {
         }
     }
 
-    // One sub-tile; bit t of `seen`: token t is visible (a token that is not lies in shared memory as zeros).
-    // Rows of shared memory: chunk c of row r at c ^ (r & 7), so that a fragment's address is one XOR away from the
-    // lane's own (the sub-tiles start on 2 KB boundaries).
-    __device__ void step(uint32_t ks, uint32_t vs, unsigned seen, float scale2, unsigned char*, int lane) {
+    // One sub-tile; sees(t): token t of it is visible (a token that is not lies in shared memory as zeros), `all`: every
+    // one is.  Rows of shared memory: chunk c of row r at c ^ (r & 7), so that a fragment's address is one XOR away
+    // from the lane's own (the sub-tiles start on 2 KB boundaries).
+    template <typename Sees>
+    __device__ void step(uint32_t ks, uint32_t vs, bool all, Sees sees, float scale2, unsigned char*, int lane) {
         constexpr int SW = D >= 64 ? 7 : 0;
         const int i8 = lane >> 3, r8 = lane & 7;
-        float s[NT][4], s1[NT][4];                      // two chains of products
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = s1[n][e] = 0.f;
+        float s[MT][NT][4];
         const uint32_t ka = ks + ((i8 & 1) * 8 + r8) * (D * 2) + (((i8 >> 1) ^ (r8 & SW)) << 4);
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
-            uint32_t a[4];
-            ldsm4(ka ^ (k << 5), a);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_bf16(k & 1 ? s1[n] : s[n], a, qf[n][k][0], qf[n][k][1]);
-        }
-        if (KT > 1) {
+        for (int mt = 0; mt < MT; ++mt) {
+            float s1[NT][4];                            // two chains of products
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] += s1[n][e];
-        }
-        if (seen != 0xFFFFu) {
-            const bool lo = seen >> (lane >> 2) & 1, hi = seen >> ((lane >> 2) + 8) & 1;
+                for (int e = 0; e < 4; ++e) s[mt][n][e] = s1[n][e] = 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int k = 0; k < KT; ++k) {
+                uint32_t a[4];
+                ldsm4((ka ^ (k << 5)) + mt * (16 * D * 2), a);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (!(e < 2 ? lo : hi)) s[n][e] = -INFINITY;
+                for (int n = 0; n < NT; ++n) mma_bf16(k & 1 ? s1[n] : s[mt][n], a, qf[n][k][0], qf[n][k][1]);
+            }
+            if (KT > 1) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[mt][n][e] += s1[n][e];
+            }
+            if (!all) {
+                const bool lo = sees(mt * 16 + (lane >> 2)), hi = sees(mt * 16 + (lane >> 2) + 8);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!(e < 2 ? lo : hi)) s[mt][n][e] = -INFINITY;
+            }
         }
         float base[SLOTS];
         bool grown = false;
 #pragma unroll
         for (int c = 0; c < SLOTS; ++c) {
-            float x = fmaxf(s[c / 2][c & 1], s[c / 2][(c & 1) + 2]);
+            float x = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) x = fmaxf(x, fmaxf(s[mt][c / 2][c & 1], s[mt][c / 2][(c & 1) + 2]));
 #pragma unroll
             for (int o = 4; o < 32; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
             x = fmaxf(m[c], x * scale2);
@@ -208,33 +216,35 @@ struct Core<__nv_bfloat16, D, NH> {
         }
         // The weights go to the tensor core as bf16 pairs hi + lo (16 bits together): rounded to bf16 alone
         // they would add 1.1e-3 of relative error to an output that is itself rounded to 1.7e-3.
-        uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float b0 = base[2 * n] == -INFINITY ? 0.f : base[2 * n];
-            const float b1 = base[2 * n + 1] == -INFINITY ? 0.f : base[2 * n + 1];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float x = exp2_approx(fmaf(s[n][2 * h], scale2, -b0));
-                const float y = exp2_approx(fmaf(s[n][2 * h + 1], scale2, -b1));
-                l[2 * n] += x;
-                l[2 * n + 1] += y;
-                const uint32_t hi = pack_bf16(x, y);
-                const uint32_t lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
-                ph[n][h] = transpose8x8(hi);
-                pl[n][h] = transpose8x8(lo);
-            }
-        }
         const uint32_t va = vs + ((i8 >> 1) * 8 + r8) * (D * 2) + (((i8 & 1) ^ (r8 & SW)) << 4);
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
-            uint32_t a[4];
-            ldsm4_trans(va ^ (k << 5), a);
+        for (int c = 0; c < SLOTS; ++c) base[c] = base[c] == -INFINITY ? 0.f : base[c];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float(&o)[4] = *reinterpret_cast<float(*)[4]>(&acc[(n * KT + k) * 4]);
-                mma_bf16(o, a, ph[n][0], ph[n][1]);
-                mma_bf16(o, a, pl[n][0], pl[n][1]);
+        for (int mt = 0; mt < MT; ++mt) {
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float x = exp2_approx(fmaf(s[mt][n][2 * h], scale2, -base[2 * n]));
+                    const float y = exp2_approx(fmaf(s[mt][n][2 * h + 1], scale2, -base[2 * n + 1]));
+                    l[2 * n] += x;
+                    l[2 * n + 1] += y;
+                    const uint32_t hi = pack_bf16(x, y);
+                    const uint32_t lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+                    ph[n][h] = transpose8x8(hi);
+                    pl[n][h] = transpose8x8(lo);
+                }
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                uint32_t a[4];
+                ldsm4_trans((va ^ (k << 5)) + mt * (16 * D * 2), a);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float(&o)[4] = *reinterpret_cast<float(*)[4]>(&acc[(n * KT + k) * 4]);
+                    mma_bf16(o, a, ph[n][0], ph[n][1]);
+                    mma_bf16(o, a, pl[n][0], pl[n][1]);
+                }
             }
         }
     }
@@ -250,7 +260,8 @@ struct Core<__nv_bfloat16, D, NH> {
 // fp32: four lanes per token for the scores, then D / 32 output columns per lane.
 template <int D, int NH>
 struct Core<float, D, NH> {
-    static constexpr int TS = 8;
+    static constexpr int MT = D == 128 ? 1 : D == 64 ? 2 : 4;        // tokens of a lane
+    static constexpr int TS = 8 * MT;
     static constexpr int CPR = D / 4;
     static constexpr int E = D >= 32 ? D / 32 : 1;      // columns of a lane (d = 16: lanes 16-31 repeat 0-15)
     static constexpr int SLOTS = NH;
@@ -279,33 +290,45 @@ struct Core<float, D, NH> {
         }
     }
 
-    __device__ void step(uint32_t ks, uint32_t vs, unsigned seen, float scale2, unsigned char* pbuf, int lane) {
-        const int r = lane >> 2, c = lane & 3;
-        float s[NH];
+    template <typename Sees>
+    __device__ void step(uint32_t ks, uint32_t vs, bool all, Sees sees, float scale2, unsigned char* pbuf, int lane) {
+        const int r = lane >> 2, c = lane & 3;          // tokens r, r + 8, ...
+        float s[MT][NH];
 #pragma unroll
-        for (int h = 0; h < NH; ++h) s[h] = 0.f;
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < NH; ++h) s[mt][h] = 0.f;
 #pragma unroll
         for (int j = 0; j < CPR / 4; ++j) {
             const int chunk = c + 4 * j;
-            float4 k;
-            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(k.x), "=f"(k.y), "=f"(k.z), "=f"(k.w)
-                         : "r"(ks + r * (D * 4) + swizzle(r, chunk) * 16) : "memory");
+            float4 k[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(k[mt].x), "=f"(k[mt].y), "=f"(k[mt].z), "=f"(k[mt].w)
+                             : "r"(ks + (r + 8 * mt) * (D * 4) + swizzle(r, chunk) * 16) : "memory");
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 const float4 x = *reinterpret_cast<const float4*>(q + h * QP + chunk * 16);
-                s[h] += x.x * k.x + x.y * k.y + x.z * k.z + x.w * k.w;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    s[mt][h] += x.x * k[mt].x + x.y * k[mt].y + x.z * k[mt].z + x.w * k[mt].w;
             }
         }
         float* pw = reinterpret_cast<float*>(pbuf);
-        bool grown = false;
+        bool grown = false, seen[MT];
         float base[NH];
-        const bool sees = seen >> r & 1;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) seen[mt] = all || sees(r + 8 * mt);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            s[h] += __shfl_xor_sync(0xFFFFFFFFu, s[h], 1);
-            s[h] += __shfl_xor_sync(0xFFFFFFFFu, s[h], 2);
-            if (!sees) s[h] = -INFINITY;
-            float x = s[h];
+            float x = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                s[mt][h] += __shfl_xor_sync(0xFFFFFFFFu, s[mt][h], 1);
+                s[mt][h] += __shfl_xor_sync(0xFFFFFFFFu, s[mt][h], 2);
+                if (!seen[mt]) s[mt][h] = -INFINITY;
+                x = fmaxf(x, s[mt][h]);
+            }
 #pragma unroll
             for (int o = 4; o < 32; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
             base[h] = fmaxf(m[h], x * scale2);
@@ -324,9 +347,13 @@ struct Core<float, D, NH> {
         }
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            const float x = exp2_approx(fmaf(s[h], scale2, -(base[h] == -INFINITY ? 0.f : base[h])));
-            l[h] += x;
-            if ((h & 3) == c) pw[r * NH + h] = x;
+            const float from = base[h] == -INFINITY ? 0.f : base[h];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const float x = exp2_approx(fmaf(s[mt][h], scale2, -from));
+                l[h] += x;
+                if ((h & 3) == c) pw[(r + 8 * mt) * NH + h] = x;
+            }
         }
         __syncwarp();
 #pragma unroll
@@ -372,8 +399,8 @@ struct Layout {
     using C = Core<T, D, NH>;
     static constexpr int TILE = NW * C::TS;
     static constexpr int SUB = C::TS * D * (int)sizeof(T);        // bytes of a sub-tile's keys
-    static constexpr int CTAS_PER_SM = D < 128 && NH <= 8 ? 4 : D == 128 && NH <= 8 ? 3 : 2;
-    static constexpr int STAGES = D == 128 ? (CTAS_PER_SM == 2 ? 3 : 2) : D == 64 ? (CTAS_PER_SM == 4 ? 3 : 6) : 8;
+    static constexpr int CTAS_PER_SM = NH > 8 ? 2 : D == 16 ? 4 : 3;
+    static constexpr int STAGES = D > 16 && CTAS_PER_SM == 2 ? 3 : 2;
     static constexpr int RING = STAGES * 2 * SUB;                 // of one warp
     static constexpr int Q = NW * RING;
     static constexpr int Q_BYTES = NH * C::QP;
@@ -481,20 +508,15 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
             if (x.row.tiles > 0) break;
         }
     };
-    // this warp's sub-tile of a tile: its first token, and which of its tokens are visible
-    constexpr unsigned ALL = (1u << TS) - 1;
-    auto sub_tile = [&](const Row& row, int tile, unsigned& seen) -> int {
-        const int first = (tile + (tile < row.lead ? 0 : row.skip)) * TILE + warp * TS;
-        seen = ALL;
-        if (first >= row.from && first + TS <= row.len) return first;
-        seen = first >= row.len ? 0u : row.len - first >= TS ? ALL : (1u << (row.len - first)) - 1;
-        if (first < row.from) {
-            const unsigned win = row.from - first >= TS ? 0u : ALL << (row.from - first);
-            const unsigned sink = first >= p.sinks ? 0u : p.sinks - first >= TS ? ALL : (1u << (p.sinks - first)) - 1;
-            seen &= win | sink;
-        }
-        return first;
+    // this warp's sub-tile of a tile: its first token
+    auto sub_tile = [&](const Row& row, int tile) -> int {
+        return (tile + (tile < row.lead ? 0 : row.skip)) * TILE + warp * TS;
     };
+    auto any_seen = [&](const Row& row, int first) {
+        return first < row.len && (first + TS > row.from || first < p.sinks);
+    };
+    auto all_seen = [&](const Row& row, int first) { return first >= row.from && first + TS <= row.len; };
+    auto is_seen = [&](const Row& row, int t) { return t < row.len && (t >= row.from || t < p.sinks); };
     const T* kp = static_cast<const T*>(p.k_pages);
     const T* vp = static_cast<const T*>(p.v_pages);
     const uint32_t ring = smem_addr(sm) + warp * L::RING;
@@ -508,55 +530,65 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
     // ---- copies of this warp's next visible sub-tile into the ring ----
     Place ahead = at;
     int ahead_left = left, stage_in = 0;
-    const bool whole_pages = p.page_size % TS == 0;     // a sub-tile never crosses a page
+    constexpr int RUN = TS / C::MT;                     // tokens copied as one run of memory,
+    const bool whole_runs = p.page_size % RUN == 0;     // which then never crosses a page
     auto issue = [&]() {
-        unsigned seen = 0;
         int first = 0;
         while (ahead_left > 0) {
-            first = sub_tile(ahead.row, ahead.tile, seen);
-            if (seen) break;
+            first = sub_tile(ahead.row, ahead.tile);
+            if (any_seen(ahead.row, first)) break;
             if (--ahead_left > 0 && ++ahead.tile == ahead.row.tiles) next_unit(ahead);
         }
         if (ahead_left > 0) {
             const uint32_t dst = ring + stage_in * (2 * L::SUB);
             stage_in = stage_in + 1 == L::STAGES ? 0 : stage_in + 1;
             const int32_t* table = p.table + (int64_t)ahead.b * p.max_pages;
-            if (whole_pages && seen == ALL && first + TS <= ahead.row.solid) {
-                // one run of memory, copied as it lies
-                const int slot = page_of(first), page = checked(__ldg(table + slot));
-                const int64_t off = ((int64_t)ahead.kvh * p.page_size + first - slot * p.page_size) * D;
-                const char* k = reinterpret_cast<const char*>(kp + page * p.k_stride + off) + lane * 16;
-                const char* v = reinterpret_cast<const char*>(vp + page * p.v_stride + off) + lane * 16;
+            if (whole_runs && first >= ahead.row.from && first + TS <= ahead.row.solid) {
+                int page[C::MT];
 #pragma unroll
-                for (int i = 0; i < TS * CPR / 32; ++i) {
-                    const int id = lane + 32 * i, r = id / CPR, c = id % CPR;
-                    const uint32_t to = dst + r * (CPR * 16) + C::swizzle(r, c) * 16;
-                    copy16(to, k + i * 512, true);
-                    copy16(to + L::SUB, v + i * 512, true);
+                for (int m = 0; m < C::MT; ++m) page[m] = __ldg(table + page_of(first + m * RUN));
+#pragma unroll
+                for (int m = 0; m < C::MT; ++m) {
+                    const int t = first + m * RUN, in_page = t - page_of(t) * p.page_size, pg = checked(page[m]);
+                    const int64_t off = ((int64_t)ahead.kvh * p.page_size + in_page) * D;
+                    const char* k = reinterpret_cast<const char*>(kp + pg * p.k_stride + off) + lane * 16;
+                    const char* v = reinterpret_cast<const char*>(vp + pg * p.v_stride + off) + lane * 16;
+#pragma unroll
+                    for (int i = 0; i < (RUN * CPR + 31) / 32; ++i) {
+                        const int id = lane + 32 * i, r = m * RUN + id / CPR, c = id % CPR;
+                        const uint32_t to = dst + r * (CPR * 16) + C::swizzle(r, c) * 16;
+                        if (RUN * CPR % 32 == 0 || id < RUN * CPR) {
+                            copy16(to, k + i * 512, true);
+                            copy16(to + L::SUB, v + i * 512, true);
+                        }
+                    }
                 }
             } else {
-                // 32 / TS lanes a token, each with its token's own place
-                constexpr int LPT = 32 / TS;
-                const int r = lane / LPT, t = first + r;
-                const bool read = seen >> r & 1;
-                const T* k = kp;
-                const T* v = vp;
-                if (read && t >= ahead.row.solid) {
-                    const int64_t off = ((int64_t)ahead.b * p.Hkv + ahead.kvh) * D;
-                    k = static_cast<const T*>(p.k_new) + off;
-                    v = static_cast<const T*>(p.v_new) + off;
-                } else if (read) {
-                    const int slot = page_of(t), page = checked(__ldg(table + slot));
-                    const int64_t off = ((int64_t)ahead.kvh * p.page_size + t - slot * p.page_size) * D;
-                    k += page * p.k_stride + off;
-                    v += page * p.v_stride + off;
-                }
+                // each lane with its token's own place: several lanes a token, or several tokens a lane
+                constexpr int LPT = TS < 32 ? 32 / TS : 1, TPL = TS < 32 ? 1 : TS / 32;
 #pragma unroll
-                for (int i = 0; i < CPR / LPT; ++i) {
-                    const int c = i * LPT + lane % LPT;
-                    const uint32_t to = dst + r * (CPR * 16) + C::swizzle(r, c) * 16;
-                    copy16(to, reinterpret_cast<const char*>(k) + c * 16, read);
-                    copy16(to + L::SUB, reinterpret_cast<const char*>(v) + c * 16, read);
+                for (int j = 0; j < TPL; ++j) {
+                    const int r = lane / LPT + 32 * j, t = first + r;
+                    const bool read = is_seen(ahead.row, t);
+                    const T* k = kp;
+                    const T* v = vp;
+                    if (read && t >= ahead.row.solid) {
+                        const int64_t off = ((int64_t)ahead.b * p.Hkv + ahead.kvh) * D;
+                        k = static_cast<const T*>(p.k_new) + off;
+                        v = static_cast<const T*>(p.v_new) + off;
+                    } else if (read) {
+                        const int slot = page_of(t), page = checked(__ldg(table + slot));
+                        const int64_t off = ((int64_t)ahead.kvh * p.page_size + t - slot * p.page_size) * D;
+                        k += page * p.k_stride + off;
+                        v += page * p.v_stride + off;
+                    }
+#pragma unroll
+                    for (int i = 0; i < CPR / LPT; ++i) {
+                        const int c = i * LPT + lane % LPT;
+                        const uint32_t to = dst + r * (CPR * 16) + C::swizzle(r, c) * 16;
+                        copy16(to, reinterpret_cast<const char*>(k) + c * 16, read);
+                        copy16(to + L::SUB, reinterpret_cast<const char*>(v) + c * 16, read);
+                    }
                 }
             }
             if (--ahead_left > 0 && ++ahead.tile == ahead.row.tiles) next_unit(ahead);
@@ -621,14 +653,14 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
             fetch_q(after.b, after.kvh, after.hb);
         }
         for (int tile = t0; tile < t0 + count; ++tile) {
-            unsigned seen;
-            const int first = sub_tile(row, tile, seen);
-            if (!seen) continue;
+            const int first = sub_tile(row, tile);
+            if (!any_seen(row, first)) continue;
             copy_wait<L::STAGES - 2>();
             __syncwarp();
             issue();
             const uint32_t ks = ring + stage * (2 * L::SUB), vs = ks + L::SUB;
-            core.step(ks, vs, seen, scale2, sm + L::PW + warp * C::P_BYTES, lane);
+            core.step(ks, vs, all_seen(row, first), [&](int t) { return is_seen(row, first + t); }, scale2,
+                      sm + L::PW + warp * C::P_BYTES, lane);
             if (first + TS > row.solid && p.k_new && at.hb == 0 && row.solid >= first) {
                 // the new token's key and value into the cache, from the copy in shared memory
                 const int t = row.solid, r = t - first, slot = page_of(t);
