@@ -70,6 +70,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Two fp32 products and sums in one instruction.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 d, {%0, %1};\n"
+        "fma.rn.f32x2 d, a, b, d;\nmov.b64 {%0, %1}, d;\n}\n"
+        : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -293,11 +299,11 @@ struct Core<float, D, NH> {
     template <typename Sees>
     __device__ void step(uint32_t ks, uint32_t vs, bool all, Sees sees, float scale2, unsigned char* pbuf, int lane) {
         const int r = lane >> 2, c = lane & 3;          // tokens r, r + 8, ...
-        float s[MT][NH];
+        float s[MT][NH], s1[MT][NH];                    // even and odd columns
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int h = 0; h < NH; ++h) s[mt][h] = 0.f;
+            for (int h = 0; h < NH; ++h) s[mt][h] = s1[mt][h] = 0.f;
 #pragma unroll
         for (int j = 0; j < CPR / 4; ++j) {
             const int chunk = c + 4 * j;
@@ -310,8 +316,10 @@ struct Core<float, D, NH> {
             for (int h = 0; h < NH; ++h) {
                 const float4 x = *reinterpret_cast<const float4*>(q + h * QP + chunk * 16);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    s[mt][h] += x.x * k[mt].x + x.y * k[mt].y + x.z * k[mt].z + x.w * k[mt].w;
+                for (int mt = 0; mt < MT; ++mt) {
+                    fma2(s[mt][h], s1[mt][h], x.x, x.y, k[mt].x, k[mt].y);
+                    fma2(s[mt][h], s1[mt][h], x.z, x.w, k[mt].z, k[mt].w);
+                }
             }
         }
         float* pw = reinterpret_cast<float*>(pbuf);
@@ -324,6 +332,7 @@ struct Core<float, D, NH> {
             float x = -INFINITY;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
+                s[mt][h] += s1[mt][h];
                 s[mt][h] += __shfl_xor_sync(0xFFFFFFFFu, s[mt][h], 1);
                 s[mt][h] += __shfl_xor_sync(0xFFFFFFFFu, s[mt][h], 2);
                 if (!seen[mt]) s[mt][h] = -INFINITY;
@@ -377,9 +386,14 @@ struct Core<float, D, NH> {
                 for (int h = 0; h < NH; ++h) w[h] = pw[t * NH + h];
             }
 #pragma unroll
-            for (int h = 0; h < NH; ++h)
+            for (int h = 0; h < NH; ++h) {
+                if constexpr (E == 1) {
+                    acc[h] += w[h] * v[0];
+                } else {
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[h * E + e] += w[h] * v[e];
+                    for (int e = 0; e < E; e += 2) fma2(acc[h * E + e], acc[h * E + e + 1], w[h], w[h], v[e], v[e + 1]);
+                }
+            }
         }
         __syncwarp();
     }
