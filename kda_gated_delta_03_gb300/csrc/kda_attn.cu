@@ -130,7 +130,9 @@ struct Core<__nv_bfloat16, D, NH> {
     static constexpr int QP = D * 2 + 16;               // bytes from head to head of q (conflict-free fragments)
     static constexpr int P_BYTES = 0;
 
-    uint32_t qf[NT][KT][2];
+    static constexpr bool Q_KEPT = NT == 1;             // q's fragments in registers; else fetched each time
+    uint32_t qf[Q_KEPT ? KT : 1][2];
+    uint32_t qa;
     float acc[ACC], m[SLOTS], l[SLOTS];
 
     __device__ static int swizzle(int row, int chunk) { return D >= 64 ? chunk ^ (row & 7) : chunk; }
@@ -141,14 +143,15 @@ struct Core<__nv_bfloat16, D, NH> {
     __device__ static bool writes_stats(int lane) { return lane < 4; }
 
     __device__ void begin(const unsigned char* q, int lane) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
+        // as the B operand: heads 0-7, columns 0-7 and 8-15, then heads 8-15
+        qa = smem_addr(q) + ((lane >> 4) * 8 + (lane & 7)) * QP + ((lane >> 3) & 1) * 16;
+        if constexpr (Q_KEPT) {
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    qf[n][k][h] = *reinterpret_cast<const uint32_t*>(q + (n * 8 + (lane >> 2)) * QP +
-                                                                     (k * 16 + 2 * (lane & 3) + 8 * h) * 2);
+                    qf[k][h] = *reinterpret_cast<const uint32_t*>(q + (lane >> 2) * QP + (k * 16 + 2 * (lane & 3) + 8 * h) * 2);
+        }
 #pragma unroll
         for (int i = 0; i < ACC; ++i) acc[i] = 0.f;
 #pragma unroll
@@ -178,8 +181,14 @@ struct Core<__nv_bfloat16, D, NH> {
             for (int k = 0; k < KT; ++k) {
                 uint32_t a[4];
                 ldsm4((ka ^ (k << 5)) + mt * (16 * D * 2), a);
+                if constexpr (Q_KEPT) {
+                    mma_bf16(k & 1 ? s1[0] : s[mt][0], a, qf[k][0], qf[k][1]);
+                } else {
+                    uint32_t b[4];
+                    ldsm4(qa + k * 32, b);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16(k & 1 ? s1[n] : s[mt][n], a, qf[n][k][0], qf[n][k][1]);
+                    for (int n = 0; n < NT; ++n) mma_bf16(k & 1 ? s1[n] : s[mt][n], a, b[2 * n], b[2 * n + 1]);
+                }
             }
             if (KT > 1) {
 #pragma unroll
@@ -413,13 +422,13 @@ struct Layout {
     using C = Core<T, D, NH>;
     static constexpr int TILE = NW * C::TS;
     static constexpr int SUB = C::TS * D * (int)sizeof(T);        // bytes of a sub-tile's keys
-    static constexpr int CTAS_PER_SM = NH > 8 ? 2 : D == 16 ? 4 : 3;
+    static constexpr int CTAS_PER_SM = NH > 8 ? (sizeof(T) == 2 ? 3 : 2) : D == 16 ? 4 : 3;
     static constexpr int STAGES = D > 16 && CTAS_PER_SM == 2 ? 3 : 2;
     static constexpr int RING = STAGES * 2 * SUB;                 // of one warp
     static constexpr int Q = NW * RING;
     static constexpr int Q_BYTES = NH * C::QP;
     static constexpr int MERGE = Q + Q_BYTES;                     // part of the warps' accumulators
-    static constexpr int MERGE_REGS = C::ACC < 8 ? C::ACC : D == 128 && sizeof(T) == 2 ? 16 : 8;
+    static constexpr int MERGE_REGS = C::ACC < 8 ? C::ACC : D == 128 && NH == 8 && sizeof(T) == 2 ? 16 : 8;
     static constexpr int STATS = MERGE + NW * MERGE_REGS * 32 * 4;   // m, l [NW][NH], then multipliers [NW][NH], m, 1 / l [NH]
     static constexpr int PW = STATS + (3 * NW + 2) * NH * 4;
     static constexpr int MISC = PW + NW * C::P_BYTES;
