@@ -184,10 +184,13 @@ struct Core<__nv_bfloat16, D, NH> {
                 if constexpr (Q_KEPT) {
                     mma_bf16(k & 1 ? s1[0] : s[mt][0], a, qf[k][0], qf[k][1]);
                 } else {
-                    uint32_t b[4];
-                    ldsm4(qa + k * 32, b);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_bf16(k & 1 ? s1[n] : s[mt][n], a, b[2 * n], b[2 * n + 1]);
+                    for (int n = 0; n < NT; n += 2) {
+                        uint32_t b[4];
+                        ldsm4(qa + n * 8 * QP + k * 32, b);
+                        mma_bf16(k & 1 ? s1[n] : s[mt][n], a, b[0], b[1]);
+                        mma_bf16(k & 1 ? s1[n + 1] : s[mt][n + 1], a, b[2], b[3]);
+                    }
                 }
             }
             if (KT > 1) {
@@ -422,7 +425,7 @@ struct Layout {
     using C = Core<T, D, NH>;
     static constexpr int TILE = NW * C::TS;
     static constexpr int SUB = C::TS * D * (int)sizeof(T);        // bytes of a sub-tile's keys
-    static constexpr int CTAS_PER_SM = NH > 8 ? (sizeof(T) == 2 ? 3 : 2) : D == 16 ? 4 : 3;
+    static constexpr int CTAS_PER_SM = NH == 32 || (NH == 16 && sizeof(T) == 4) ? 2 : NH == 16 || D > 16 ? 3 : 4;
     static constexpr int STAGES = D > 16 && CTAS_PER_SM == 2 ? 3 : 2;
     static constexpr int RING = STAGES * 2 * SUB;                 // of one warp
     static constexpr int Q = NW * RING;
@@ -890,7 +893,7 @@ cudaError_t launch_d(const AttnParams& p, cudaStream_t s) {
 
 // Query heads that meet a key at once: the smallest variant that holds the group, else blocks of the largest.
 int block_heads(int group, kda_dtype dt) {
-    if (dt == KDA_DTYPE_BF16) return group <= 8 ? 8 : 16;
+    if (dt == KDA_DTYPE_BF16) return group <= 8 ? 8 : group <= 16 ? 16 : 32;
     return group == 1 ? 1 : group <= 4 ? 4 : group <= 8 ? 8 : 16;
 }
 
@@ -902,7 +905,9 @@ size_t attn_workspace(int32_t, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype dt)
 
 cudaError_t launch_attention_decode(const AttnParams& p, kda_dtype dt, cudaStream_t s) {
     const int nh = block_heads(p.Hq / p.Hkv, dt);
-    if (dt == KDA_DTYPE_BF16) return nh == 8 ? launch_d<__nv_bfloat16, 8>(p, s) : launch_d<__nv_bfloat16, 16>(p, s);
+    if (dt == KDA_DTYPE_BF16)
+        return nh == 8 ? launch_d<__nv_bfloat16, 8>(p, s) : nh == 16 ? launch_d<__nv_bfloat16, 16>(p, s)
+                                                                      : launch_d<__nv_bfloat16, 32>(p, s);
     if (nh == 1) return launch_d<float, 1>(p, s);
     if (nh == 4) return launch_d<float, 4>(p, s);
     if (nh == 8) return launch_d<float, 8>(p, s);
