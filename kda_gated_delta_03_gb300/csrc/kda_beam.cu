@@ -278,10 +278,10 @@ __device__ __forceinline__ void rank_candidates(const unsigned long long* cand, 
 template <typename T>
 __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamParams p, int parts) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ __align__(16) float group_max[GROUPS];
-    __shared__ float warp_top[BW], warp_sum[BW], bound;
+    __shared__ float warp_top[BW], warp_sum[BW], chunk_top, bound;
     __shared__ int found, kept[BW];
-    __shared__ unsigned long long cand[CAP], all[CAP], best[KDA_BEAM_MAX_K + 1];
+    __shared__ __align__(16) unsigned long long cand[CAP], all[CAP], best[KDA_BEAM_MAX_K + 1];
+    float* thread_max = reinterpret_cast<float*>(all);   // until the lists are put together
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / (unsigned)parts;
     const int part = blockIdx.x % (unsigned)parts, L = p.K + 1;
@@ -323,6 +323,57 @@ __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamPara
     };
 #pragma unroll 1
     for (int i = 0; i < STAGES - 1; ++i) copy_next();
+    // ---- the first chunk's maximum, and a bound that L of its logits reach ----
+    {
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
+        __syncwarp();
+        X x;
+        x.take(ring, off, min(p.V - first * CHUNK<T>, CHUNK<T>), tid);
+        const float mine = x.max();
+        // 64 groups of threads, or 32: for an L of 16 at most they let about as few through.  A group's threads lie
+        // 64 or 32 apart, so that a row of few words still has some in most groups.
+        thread_max[tid] = mine;
+        __syncthreads();
+        if (warp == 0) {
+            const bool few = p.K <= FEW;
+            float g = -INFINITY, h = -INFINITY;     // of groups `lane` and `lane` + 32
+#pragma unroll
+            for (int i = 0; i < BW; ++i) {
+                const float y = thread_max[i * 32 + lane];
+                if (few || i % 2 == 0) g = fmaxf(g, y);
+                else h = fmaxf(h, y);
+            }
+            int rank_g = 0, rank_h = 0;
+            if (few) {
+                thread_max[lane] = g;               // read above by this warp alone
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(thread_max + j);
+                    rank_g += (y.x > g || (y.x == g && j < lane)) + (y.y > g || (y.y == g && j + 1 < lane)) +
+                              (y.z > g || (y.z == g && j + 2 < lane)) + (y.w > g || (y.w == g && j + 3 < lane));
+                }
+                rank_h = L;
+            } else {
+#pragma unroll 8
+                for (int j = 0; j < 32; ++j) {
+                    const float y = __shfl_sync(0xFFFFFFFFu, g, j), z = __shfl_sync(0xFFFFFFFFu, h, j);
+                    rank_g += (y > g || (y == g && j < lane)) + (z > g);
+                    rank_h += (y >= h) + (z > h || (z == h && j < lane));
+                }
+            }
+            if (rank_g == L - 1) bound = g;
+            else if (rank_h == L - 1) bound = h;
+            g = fmaxf(g, h);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
+            if (lane == 0) chunk_top = g;
+        }
+        __syncthreads();
+        t = chunk_top;
+        limit = t + 64.f;
+        least = bound == -INFINITY ? above(bound, T()) : bound;
+    }
     bool lost = false;
 #pragma unroll 1
     for (int chunk = first; chunk < last; ++chunk) {
@@ -334,38 +385,6 @@ __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamPara
         X x;
         x.take(stage, off, min(p.V - chunk * CHUNK<T>, CHUNK<T>), tid);
         const float mine = x.max();
-        if (chunk == first) {
-            // groups of four threads, or of eight: with 32 groups the bound lets about as few through (an L of 16 at
-            // most), and one warp ranks them
-            const bool few = p.K <= FEW;
-            float g = fmaxf(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
-            g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 2));
-            if (!few && (lane & 3) == 0) group_max[tid / 4] = g;
-            g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, 4));
-            if (few && (lane & 7) == 0) group_max[tid / 8] = g;
-#pragma unroll
-            for (int o = 8; o < 32; o *= 2) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
-            if (lane == 0) warp_top[warp] = g;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < BW; ++i) g = fmaxf(g, warp_top[i]);
-            t = g;
-            limit = g + 64.f;
-            const int groups = few ? GROUPS / 2 : GROUPS;
-            if (tid < groups) {
-                g = group_max[tid];
-                int rank = 0;
-#pragma unroll 4
-                for (int j = 0; j < groups / 4; ++j) {
-                    const float4 y = reinterpret_cast<const float4*>(group_max)[j];
-                    rank += (y.x > g || (y.x == g && 4 * j < tid)) + (y.y > g || (y.y == g && 4 * j + 1 < tid)) +
-                            (y.z > g || (y.z == g && 4 * j + 2 < tid)) + (y.w > g || (y.w == g && 4 * j + 3 < tid));
-                }
-                if (rank == L - 1) bound = g;
-            }
-            __syncthreads();
-            least = bound == -INFINITY ? above(bound, T()) : bound;
-        }
         const unsigned owners = __ballot_sync(0xFFFFFFFFu, mine >= least);
         if (owners) {
             // the few threads with such a logit: theirs are read again, a lane per element
