@@ -4,24 +4,29 @@
 //
 // in one pass: the running maximum and sum of the softmax, the sum over the values rescaled whenever the
 // maximum grows.  Exponents are taken in base 2 (scale * log2 e folded into the scores).  Every key and
-// value is read once and meets the g = H_q / H_kv query heads that share it, 4 g flop for 2 elements, so
-// with bf16 caches and g up to 32 the reads bound the kernel, not the products.
+// value is read once and meets the g = H_q / H_kv query heads that share it, 4 g flop for 2 elements.
 //
 // The visible tokens of all rows and heads are numbered tile after tile and cut into equal contiguous
-// shares, one per CTA (two CTAs per SM), so that one long sequence, many short ones and anything between
-// fill the GPU alike.  The shares are worked out on the device from seq_lens; the host never sees them.
-// Inside a CTA each warp takes every fourth sub-tile of TS tokens through its own ring of asynchronous
-// copies (cp.async, no barrier with other warps) and keeps its own maximum, sum and accumulator; the four
-// are joined in shared memory where a (row, head) unit ends.  A unit that a share's border cuts leaves
-// partial results in the workspace, which a second kernel joins in the order of the CTAs: no atomics, the
-// same bits on every call.
+// shares, one per CTA (two to four CTAs per SM), so that one long sequence, many short ones and anything
+// between fill the GPU alike.  The shares are worked out on the device from seq_lens; the host never sees
+// them.  Inside a CTA each warp takes every fourth sub-tile of TS tokens through its own ring of asynchronous
+// copies (cp.async, no barrier with other warps) and keeps its own maximum, sum and accumulator; the four are
+// joined in shared memory where a (row, head) unit ends.  A unit that a share's border cuts leaves partial
+// results in the workspace, which a second kernel joins in the order of the CTAs: no atomics, the same bits on
+// every call.
+//
+// What bounds it is DRAM, once there is enough to read: one row of 1,048,573 tokens with 8 heads of 128 takes
+// 588 us (7.3 TB/s of reads), 64 rows of 310,000 tokens in all with 8 key-value heads 135 us (6.45 TB/s, the rest
+// is the first loads' latency, the joins and the second kernel, together about 12 us whatever the size).  With few
+// bytes that latency is all: 5.9 us for a row of 37 tokens.  With 16 and 32 query heads a key the products of
+// mma.sync begin to show (4.6 and 3.6 TB/s at 250 MB).
 //
 // The products: with the tokens as the 16 rows of mma.m16n8k16 and the query heads as its 8 columns, both
 // products take the cache as the A operand straight from shared memory (K by ldmatrix, V by ldmatrix.trans)
-// and leave no padding at 8 heads; 2 CTAs x 4 warps need about a tenth of the SM's issue slots at the
-// memory's rate, so the larger tcgen05 tiles (64 rows at least, with the softmax between the two products
-// behind a round trip through tensor memory) would only add latency.  fp32 caches take the same path
-// with FFMA.
+// and leave no padding at 8 heads.  A tcgen05 tile has 64 rows at least, its softmax sits behind a round trip
+// through tensor memory, and its operands want a layout that pages of any size do not have; at the reads' rate
+// the mma.sync form leaves the tensor pipe mostly idle up to 16 heads a key.  fp32 caches take the same path
+// with FFMA (two products in one instruction), since TF32's 11 bits would not keep fp32's precision.
 
 #include <cmath>
 #include <type_traits>

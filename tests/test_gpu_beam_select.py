@@ -189,6 +189,14 @@ def test_scores_that_round_together_in_part():
             assert got[n, a] > got[n, b] or (got[n, a] == got[n, b] and place[a] < place[b])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_zeros_of_both_signs_are_one_value(dtype):
+    logits = torch.full((2, 5000), -5.0, device=DEV)
+    logits[:, 4000], logits[:, 70], logits[:, 71] = 0.0, -0.0, 0.0
+    s, parent, token, _ = kda.kda_beam_select(logits.to(DT[dtype]), torch.tensor([[-1.0, -1.0]], device=DEV))
+    assert parent.tolist() == [[0, 0]] and token.tolist() == [[70, 71]]
+
+
 def test_in_place_and_reproducible():
     logits, bs = inputs(9, 6, 33333, "bf16", 12)
     fin = (torch.rand((9, 6), device=DEV) < 0.3).to(torch.uint8)
