@@ -17,12 +17,14 @@ namespace {
 
 // ---- copies ----
 // What bounds a copy is DRAM, which likes long runs of reads and of writes: three CTAs per SM, each with 32 KB
-// on its way, move 192 states of 2 MiB at 7.0 TB/s (read and written, 115 us); pieces of 16 KB with four vectors a
-// thread reach 6.5 TB/s, with eight CTAs per SM 5.2.
+// on its way, and a few pieces per CTA, so that what is moved at a time lies together, move 192 states of 2 MiB
+// at 7.2 TB/s (read and written, 112 us).  Pieces of 16 KB with four vectors a thread reach 6.5 TB/s and with eight
+// CTAs per SM 5.2; a resident CTA that strides over all pieces 6.4; one CTA a piece 5.1 (each works its list out).
 constexpr int CT = 256;                       // threads of a copying CTA
 constexpr int COPY_CTAS = 3;                  // of them per SM
 constexpr int CV = 8;                         // 16-byte vectors that a thread has in flight
 constexpr int PIECE = 32768;                  // bytes of a slot that one group of threads moves at a time
+constexpr int MOST_CTAS = 32;                 // copying CTAs launched per SM, at most
 
 // The grid's threads move all pieces of n slots within one pool; slot_pair(i, src, dst) names the i-th copy (false:
 // skip it).  A slot smaller than a piece is moved by fewer threads, so that small pages still fill the CTA.  A
@@ -38,6 +40,7 @@ __device__ __forceinline__ void copy_pool(const kda_pool& p, int64_t n, Pair slo
     const int groups = CT / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
     // unit = (pair * layers + layer) * pieces + piece; the grid's stride in the same three digits
     const unsigned first = blockIdx.x * groups + group, stride = gridDim.x * groups;
+    if (first >= n * p.layers * pieces) return;
     int piece = first % pieces, layer = first / pieces % p.layers;
     int64_t pair = first / pieces / p.layers;
     const int piece_step = stride % pieces, layer_step = stride / pieces % p.layers, pair_step = stride / pieces / p.layers;
@@ -548,14 +551,14 @@ __global__ void __launch_bounds__(PT) kda_cache_compact_kernel(CompactParams p, 
     }
 }
 
-// CTAs that copy n slots (at most): one per piece, up to eight per SM, three of them at a time.
+// CTAs that copy n slots (at most): one per piece as far as they go.
 int copy_grid(const PoolSet& set, int64_t n, int sms) {
     int64_t most = 1;
     for (int i = 0; i < set.n; ++i) {
         const int64_t units = n * set.pool[i].layers * ((set.pool[i].slot_bytes + PIECE - 1) / PIECE);
         most = units > most ? units : most;
     }
-    return (int)(most < 8 * (int64_t)sms ? most : 8 * (int64_t)sms);
+    return (int)(most < MOST_CTAS * (int64_t)sms ? most : MOST_CTAS * (int64_t)sms);
 }
 
 // `after`: the kernel works on what the one launched just before on this stream leaves, and waits for its end
@@ -630,7 +633,7 @@ cudaError_t launch_cache_fork(const ForkParams& p, const PoolSet& pools, void* w
     e = launch_cluster(kda_cache_fork_kernel, ((size_t)p.rows_in + p.rows_out) * 8, s, p, sc);
     if (e != cudaSuccess || p.rows_out == 0) return e;
     const int rows = (p.rows_out + CT / 32 - 1) / (CT / 32), copies = copy_grid(pools, p.rows_out, sms);
-    const int grid = rows > copies ? (rows < 8 * sms ? rows : 8 * sms) : copies;
+    const int grid = rows > copies ? (rows < MOST_CTAS * sms ? rows : MOST_CTAS * sms) : copies;
     return launch_wide(kda_cache_fork_finish_kernel, grid, true, s, p, sc, pools);
 }
 
