@@ -16,7 +16,7 @@
 // every call.
 //
 // What bounds it is DRAM, once there is enough to read: one row of 1,048,573 tokens with 8 heads of 128 takes
-// 588 us (7.3 TB/s of reads), 64 rows of 310,000 tokens in all with 8 key-value heads 135 us (6.45 TB/s, the rest
+// 588 us (7.3 TB/s of reads), 64 rows of 213,000 tokens in all with 8 key-value heads 135 us (6.45 TB/s, the rest
 // is the first loads' latency, the joins and the second kernel, together about 12 us whatever the size).  With few
 // bytes that latency is all: 5.9 us for a row of 37 tokens.  With 16 and 32 query heads a key the products of
 // mma.sync begin to show (4.6 and 3.6 TB/s at 250 MB).

@@ -13,9 +13,8 @@
 // exactly that score.  Rows that offer nothing (finished, no score) are not read.
 //
 // What it costs: 410 of 512 rows of 131,072 bf16 words (107 MB) take 28 us, of which the read at DRAM's rate
-// would be 16.  Issue slots are the rest (about 7 instructions a logit: unpacking, one exponential, the sum, the
-// maximum; a plain stream of them runs at DRAM's rate, so it is the barriers at a part's ends and its bound that
-// leave slots empty), and 5 us of the second kernel, a chain of loads and small steps for each group.
+// would be 16.  Issue slots are the rest (8 instructions a logit; a plain stream of loads, exponentials and
+// sums needs 4 and runs at DRAM's rate: the bound, the lists and the barriers around them are the rest), and 5 us of the second kernel, a chain of loads and small steps for each group.
 
 #include <cmath>
 

@@ -18,8 +18,8 @@ namespace {
 // ---- copies ----
 // What bounds a copy is DRAM, which likes long runs of reads and of writes: three CTAs per SM, each with 32 KB
 // on its way, and a few pieces per CTA, so that what is moved at a time lies together, move 192 states of 2 MiB
-// at 7.2 TB/s (read and written, 112 us).  Pieces of 16 KB with four vectors a thread reach 6.5 TB/s and with eight
-// CTAs per SM 5.2; a resident CTA that strides over all pieces 6.4; one CTA a piece 5.1 (each works its list out).
+// at 7.3 TB/s (read and written, 110 us).  Pieces of 16 KB with four vectors a thread reach 6.5 TB/s and with eight
+// resident CTAs per SM 5.2; a resident CTA that strides over all pieces 6.4; one CTA a piece 5.1 (each works its list out).
 constexpr int CT = 256;                       // threads of a copying CTA
 constexpr int COPY_CTAS = 3;                  // of them per SM
 constexpr int CV = 8;                         // 16-byte vectors that a thread has in flight
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(CT, COPY_CTAS) kda_state_fork_kernel(const __g
 
 // ---- one cluster's bookkeeping ----
 // 16 CTAs of 256 threads: fewer threads meet sooner at a barrier, more CTAs read the tables faster.  256 rows of up
-// to 377 pages, 96,632 pages (copies included): 32.5 us; 8 x 256: 34.1, 8 x 512: 34.8, 8 x 1024: 36.9, 16 x 512: 33.6.
+// to 377 pages, 96,632 pages (copies included), measured together: 32.5 us; 8 x 256: 34.1, 8 x 512: 34.8, 8 x 1024: 36.9, 16 x 512: 33.6.
 constexpr int NC = 16;                        // CTAs of the cluster
 constexpr int PT = 256;                       // threads of each
 
