@@ -6,19 +6,19 @@
 // maximum grows.  Exponents are taken in base 2 (scale * log2 e folded into the scores).  Every key and
 // value is read once and meets the g = H_q / H_kv query heads that share it, 4 g flop for 2 elements.
 //
-// The visible tokens of all rows and heads are numbered tile after tile and cut into equal contiguous
-// shares, one per CTA (two to four CTAs per SM), so that one long sequence, many short ones and anything
-// between fill the GPU alike.  The shares are worked out on the device from seq_lens; the host never sees
-// them.  Inside a CTA each warp takes every fourth sub-tile of TS tokens through its own ring of asynchronous
-// copies (cp.async, no barrier with other warps) and keeps its own maximum, sum and accumulator; the four are
-// joined in shared memory where a (row, head) unit ends.  A unit that a share's border cuts leaves partial
-// results in the workspace, which a second kernel joins in the order of the CTAs: no atomics, the same bits on
-// every call.
+// The visible tokens of all rows and heads are numbered tile after tile and cut into equal contiguous shares,
+// one per CTA (two to four CTAs per SM), so that one long sequence, many short ones and anything between fill
+// the GPU alike.  The shares are worked out on the device from seq_lens; the host never sees them (but it
+// sees when every row must be short, and then a CTA does a unit whole).  Inside a CTA each warp takes every
+// fourth sub-tile of TS tokens through its own ring of asynchronous copies (cp.async, no barrier with other
+// warps) and keeps its own maximum, sum and accumulator; the four are joined in shared memory where a (row,
+// head) unit ends.  A unit that a share's border cuts leaves partial results in the workspace, which a second
+// kernel joins in the order of the CTAs: no atomics, the same bits on every call.
 //
 // What bounds it is DRAM, once there is enough to read: one row of 1,048,573 tokens with 8 heads of 128 takes
 // 588 us (7.3 TB/s of reads), 64 rows of 213,000 tokens in all with 8 key-value heads 135 us (6.45 TB/s, the rest
 // is the first loads' latency, the joins and the second kernel, together about 12 us whatever the size).  With few
-// bytes that latency is all: 5.9 us for a row of 37 tokens.  With 16 and 32 query heads a key the products of
+// bytes that latency is all: 4.4 us for a row of 37 tokens.  With 16 and 32 query heads a key the products of
 // mma.sync begin to show (4.6 and 3.6 TB/s at 250 MB).
 //
 // The products: with the tokens as the 16 rows of mma.m16n8k16 and the query heads as its 8 columns, both
@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
 
     // ---- this CTA's share ----
     int* misc = reinterpret_cast<int*>(sm + L::MISC);
+    int64_t* split = reinterpret_cast<int64_t*>(sm + L::MISC + 16);
     int64_t* sums = reinterpret_cast<int64_t*>(sm + L::MERGE);
     // tiles of the rows b0 .. b0 + AT - 1: this thread's row's, those before it, and in all
     auto scan_rows = [&](int b0, int& mine, int64_t& before, int64_t& all) {
@@ -487,45 +488,60 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
             all += sums[w];
         }
     };
-    int mine;
-    int64_t before, total;                              // of the first AT rows, then of all
-    scan_rows(0, mine, before, total);
-    for (int b0 = AT; b0 < p.B; b0 += AT) {
-        int m;
-        int64_t unused, all;
-        __syncthreads();
-        scan_rows(b0, m, unused, all);
-        total += all;
-    }
-    // no more shares than tiles: none of them is empty, so a unit's pieces lie in consecutive CTAs
-    const int64_t flat = total * units, shares = flat < grid ? flat : grid;
-    const int64_t begin = cta < shares ? cta * flat / shares : flat, end = cta < shares ? (cta + 1) * flat / shares : flat;
-    int left = (int)(end - begin);                      // tiles of this CTA's share
+    int left = 0;                                       // tiles of this CTA's share
     Place at{};
-    if (left > 0) {
-        int64_t base = 0;                               // tiles of the rows before b0
-        for (int b0 = 0; b0 < p.B; b0 += AT) {
-            int64_t all = total;
-            if (p.B > AT) {
-                __syncthreads();
-                scan_rows(b0, mine, before, all);
-            }
-            const int64_t lo = (base + before) * units, hi = lo + (int64_t)mine * units;
-            if (mine > 0 && begin >= lo && begin < hi) {
-                const int64_t in = begin - lo;
-                misc[0] = b0 + tid;
-                misc[1] = (int)(in / mine);
-                misc[2] = (int)(in % mine);
-            }
-            base += all;
-            if (begin < base * units) break;
-        }
-        __syncthreads();
-        at.b = misc[0];
-        at.kvh = misc[1] / head_blocks;
-        at.hb = misc[1] - at.kvh * head_blocks;
-        at.tile = misc[2];
+    if (p.whole) {                                      // one unit, uncut
+        at.b = cta / units;
+        at.kvh = (cta - at.b * units) / head_blocks;
+        at.hb = cta % head_blocks;
         at.row = row_of<TILE>(p, __ldg(p.lens + at.b));
+        left = at.row.tiles;
+    } else {
+        int mine;
+        int64_t before, total;                              // of the first AT rows, then of all
+        scan_rows(0, mine, before, total);
+        for (int b0 = AT; b0 < p.B; b0 += AT) {
+            int m;
+            int64_t unused, all;
+            __syncthreads();
+            scan_rows(b0, m, unused, all);
+            total += all;
+        }
+        // no more shares than tiles: none of them is empty, so a unit's pieces lie in consecutive CTAs
+        const int64_t flat = total * units, shares = flat < grid ? flat : grid;
+        const int64_t begin = cta < shares ? cta * flat / shares : flat;
+        const int64_t end = cta < shares ? (cta + 1) * flat / shares : flat;
+        left = (int)(end - begin);
+        if (tid == 0) {                                 // for its records, later
+            split[0] = flat;
+            split[1] = end;
+            misc[3] = (int)shares;
+        }
+        if (left > 0) {
+            int64_t base = 0;                               // tiles of the rows before b0
+            for (int b0 = 0; b0 < p.B; b0 += AT) {
+                int64_t all = total;
+                if (p.B > AT) {
+                    __syncthreads();
+                    scan_rows(b0, mine, before, all);
+                }
+                const int64_t lo = (base + before) * units, hi = lo + (int64_t)mine * units;
+                if (mine > 0 && begin >= lo && begin < hi) {
+                    const int64_t in = begin - lo;
+                    misc[0] = b0 + tid;
+                    misc[1] = (int)(in / mine);
+                    misc[2] = (int)(in % mine);
+                }
+                base += all;
+                if (begin < base * units) break;
+            }
+            __syncthreads();
+            at.b = misc[0];
+            at.kvh = misc[1] / head_blocks;
+            at.hb = misc[1] - at.kvh * head_blocks;
+            at.tile = misc[2];
+            at.row = row_of<TILE>(p, __ldg(p.lens + at.b));
+        }
     }
 
     auto next_unit = [&](Place& x) {                    // only called while the share goes on
@@ -656,7 +672,7 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
     };
 
     Record* records = reinterpret_cast<Record*>(p.workspace);
-    const bool by_unit = (int64_t)p.B * units <= grid;
+    const bool by_unit = !p.whole && (int64_t)p.B * units <= grid;
     float* pieces = reinterpret_cast<float*>(p.workspace + MAX_CTAS * sizeof(Record)) + (int64_t)cta * 2 * L::PIECE;
     float* sm_m = reinterpret_cast<float*>(sm + L::STATS);
     float* sm_l = sm_m + NW * NH;
@@ -774,9 +790,9 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
         if (tid == 0 && starts) {
             const int unit = kvh * head_blocks + at.hb;
             if (!ends) {
-                const int64_t x = end - left + row.tiles;               // flat tiles up to the unit's last
+                const int64_t x = split[1] - left + row.tiles;          // flat tiles up to the unit's last
                 records[by_unit ? b * units + unit : cta] =
-                    Record{b, unit, cta, (int)((x * shares - 1) / flat), first_unit ? 0 : 1, {0, 0, 0}};
+                    Record{b, unit, cta, (int)((x * misc[3] - 1) / split[0]), first_unit ? 0 : 1, {0, 0, 0}};
                 recorded = true;
             } else if (by_unit) {
                 records[b * units + unit].b = -1;
@@ -786,7 +802,7 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
         first_unit = false;
         if (left > 0) at = after;
     }
-    if (tid == 0 && !recorded && !by_unit) records[cta].b = -1;
+    if (tid == 0 && !recorded && !by_unit && !p.whole) records[cta].b = -1;
     // rows without a visible token
     for (int b = cta; b < p.B; b += grid) {
         const int len = p.lens[b];
@@ -860,6 +876,26 @@ __global__ void __launch_bounds__(AT) kda_attn_join_kernel(AttnParams p, int hea
     if (p.lse && tid == 0) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * LN2;
 }
 
+
+// No row has more tiles with a visible token, whatever its length: as many as its table's pages hold, or as the
+// window and the first tokens touch.
+int64_t most_tiles(const AttnParams& p, int tile) {
+    const int64_t all = ((int64_t)p.max_pages * p.page_size + tile - 1) / tile;
+    if (p.window == 0) return all;
+    const int64_t seen = (p.sinks + (int64_t)tile - 1) / tile + (p.window + (int64_t)tile - 1) / tile + 1;
+    return seen < all ? seen : all;
+}
+
+// Whether each unit is done by one CTA, however long: no search for the shares, no pieces, no second kernel.  That
+// pays where rows are short beside those: always up to four tiles (a row of 64 tokens 4.2 us instead of 6.0, of 256
+// 6.9 instead of 7.4, 48 rows of 256 with 8 heads 12.9 instead of 18.0), and up to eight where the units fill a
+// quarter of the GPU (48 rows of 512: 19.9 instead of 24.9, of 1 to 512: 10.3 instead of 12.0; but one row of 512: 9.7
+// instead of 7.7).  With many units for each CTA that could be resident, each one's start shows instead: 1,024 units
+// of 64 tokens 14.0 us instead of 14.3, 4,096 of them 42.8 instead of 35.8.
+bool done_whole(int64_t units, int64_t tiles, int grid) {
+    return units <= 3 * (int64_t)grid && (tiles <= 4 || (tiles <= 8 && 4 * units >= grid));
+}
+
 template <typename T, int D, int NH>
 cudaError_t launch_core(AttnParams p, cudaStream_t s) {
     using L = Layout<T, D, NH>;
@@ -872,13 +908,15 @@ cudaError_t launch_core(AttnParams p, cudaStream_t s) {
     while ((2ll << p.page_shift) < p.page_size) ++p.page_shift;
     p.page_magic = p.page_size == 1 ? 0u : (uint32_t)((1ull << (32 + p.page_shift)) / p.page_size + 1);
     const int group = p.Hq / p.Hkv, head_blocks = (group + NH - 1) / NH;
-    const int grid = sms * L::CTAS_PER_SM < MAX_CTAS ? sms * L::CTAS_PER_SM : MAX_CTAS;
+    const int64_t all_units = (int64_t)p.B * p.Hkv * head_blocks;
+    int grid = sms * L::CTAS_PER_SM < MAX_CTAS ? sms * L::CTAS_PER_SM : MAX_CTAS;
+    p.whole = done_whole(all_units, most_tiles(p, L::TILE), grid);
+    if (p.whole) grid = (int)all_units;
     kda_attn_kernel<T, D, NH><<<grid, AT, L::BYTES, s>>>(p, head_blocks, grid);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.whole) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
-    const int64_t all_units = (int64_t)p.B * p.Hkv * head_blocks;
     cfg.gridDim = dim3(all_units < grid ? (unsigned)all_units : grid, group < NH ? group : NH);
     cfg.blockDim = dim3(AT);
     cfg.stream = s;

@@ -64,6 +64,7 @@ struct AttnParams {
     // set by the launcher: t / page_size = umulhi(t, page_magic) >> page_shift for t < 2^31 (page_magic 0: t itself)
     uint32_t page_magic;
     int32_t page_shift;
+    int32_t whole;               // set by the launcher: CTA i does all of unit i, and nothing is left to join
 };
 size_t attn_workspace(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype dt);
 cudaError_t launch_attention_decode(const AttnParams& p, kda_dtype dt, cudaStream_t s);

@@ -141,6 +141,29 @@ def test_lengths_split_over_the_gpu(dtype, case):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("tiles", [1, 4, 5, 8, 9])
+def test_rows_that_the_table_keeps_short(dtype, d, tiles):
+    """Units done whole and in shares: tables that hold up to 4, 8 and more tiles, few rows and many."""
+    most = tiles * {128: 64, 64: 128, 16: 256}[d] // (1 if dtype == "bf16" else 2)
+    check([most], 8, 2, d, 16, dtype, seed=tiles)
+    check([0, most, 1, most - 1], 4, 4, d, 32, dtype, seed=tiles + 1)
+    check([most if b % 3 == 0 else b % 5 for b in range(70)], 2, 2, d, 16, dtype, seed=tiles + 2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [450, 700, 1500])
+def test_more_rows_than_the_gpu_holds_ctas(dtype, B):
+    check([(b * 7) % 41 for b in range(B)], 2, 1, 64, 8, dtype, seed=B, max_pages=6)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window,sinks", [(40, 0), (20, 5), (1, 100)])
+def test_rows_that_the_window_keeps_short(dtype, window, sinks):
+    check([5000, 30, 0, 1000, 41, 1], 8, 2, 128, 16, dtype, window=window, sinks=sinks, seed=window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_without_a_new_token_and_with_a_wider_table(dtype):
     check([37, 0, 250], 8, 2, 128, 16, dtype, append=False, max_pages=40, extra_pages=0)
 
