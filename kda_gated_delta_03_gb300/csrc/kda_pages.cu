@@ -191,6 +191,11 @@ __global__ void __launch_bounds__(CT, COPY_CTAS) kda_state_fork_kernel(const __g
 // to 377 pages, 96,632 pages (copies included), measured together: 32.5 us; 8 x 256: 34.1, 8 x 512: 34.8, 8 x 1024: 36.9, 16 x 512: 33.6.
 constexpr int NC = 16;                        // CTAs of the cluster
 constexpr int PT = 256;                       // threads of each
+// Tables and copies up to so many bytes are left to the cluster's CTAs, which saves a launch (2 us of the host's time).
+// 4 rows of 32 KB pages, two pools: 4 layers (1 MB at most) 10.8 us against 11.0 in two launches, 16 layers 12.9
+// against 11.6, 32 layers 16.9 against 12.0.
+constexpr int64_t WHOLE_BYTES = 1 << 20;
+static_assert(PT == CT, "the cluster's threads move pages as the copying kernels' do");
 
 // Everything that the cluster's threads wrote before is seen by all of them after.
 __device__ __forceinline__ void cluster_sync() {
@@ -234,11 +239,50 @@ __device__ __forceinline__ int old_length(const ForkParams& p, int row) {
     return len < 0 || len > p.max_pages * p.page_size ? 0 : len;
 }
 
+// The new rows' tables, a warp per row, and the copies of their pages.
+__device__ __forceinline__ void fork_finish(const ForkParams p, const ForkScratch s, const PoolSet& set) {
+    const int lane = threadIdx.x & 31, handed = s.totals[NC], copies = s.totals[NC + 1];
+    for (int i = blockIdx.x * (CT / 32) + (threadIdx.x >> 5); i < p.rows_out; i += gridDim.x * (CT / 32)) {
+        const RowPlan r = s.plan[i];
+        const int32_t* from = p.table + (int64_t)r.parent * p.max_pages;
+        int32_t* to = p.table_out + (int64_t)i * p.max_pages;
+        constexpr int BATCH = 4;
+        for (int j0 = lane; j0 < p.max_pages; j0 += 32 * BATCH) {
+            int page[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int j = j0 + 32 * k, rank = r.fresh_at + j - r.shared;
+                page[k] = j < r.shared ? from[j] : j < r.need && rank < handed ? s.fresh[rank] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int j = j0 + 32 * k;
+                if (j >= p.max_pages) break;
+                if (j < r.shared && (page[k] < 0 || page[k] >= p.num_pages)) {
+                    atomicOr(p.err, KDA_DEVERR_PAGES);
+                    page[k] = -1;
+                }
+                to[j] = page[k];
+            }
+        }
+    }
+    for (int i = 0; i < set.n; ++i)
+        copy_pool(set.pool[i], copies,
+                  [&](int64_t pair, int& from, int& to) {
+                      from = s.src[pair];
+                      to = s.dst[pair];
+                      return from >= 0;
+                  },
+                  p.err, KDA_DEVERR_PAGES);
+}
+
 // The bookkeeping: which pages every new row takes over and how many it needs of its own, the counts, and the
 // lowest free pages, in order.  Every CTA works out all rows' plans in its own shared memory (first, count
 // [rows_in], fresh_at, copy_at [rows_out]), which costs less than one more meeting of the cluster; counts and
-// pages are divided among the CTAs.
-__global__ void __launch_bounds__(PT) kda_cache_fork_kernel(ForkParams p, ForkScratch s) {
+// pages are divided among the CTAs.  WHOLE: the cluster also writes the tables and moves the pages.
+template <bool WHOLE>
+__global__ void __launch_bounds__(PT) kda_cache_fork_kernel(ForkParams p, ForkScratch s,
+                                                            const __grid_constant__ PoolSet set) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ int32_t fork_sm[];
     __shared__ unsigned long long sums[PT / 32];
@@ -408,45 +452,17 @@ __global__ void __launch_bounds__(PT) kda_cache_fork_kernel(ForkParams p, ForkSc
             p.copy_dst[i] = dst;
         }
     }
+    if (WHOLE) {
+        cluster_sync();
+        fork_finish(p, s, set);
+    }
 }
 
-// The new rows' tables, a warp per row, and the copies of their pages.
+// What is more than the cluster should move by itself.
 __global__ void __launch_bounds__(CT, COPY_CTAS) kda_cache_fork_finish_kernel(ForkParams p, ForkScratch s,
                                                                    const __grid_constant__ PoolSet set) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, handed = s.totals[NC], copies = s.totals[NC + 1];
-    for (int i = blockIdx.x * (CT / 32) + (threadIdx.x >> 5); i < p.rows_out; i += gridDim.x * (CT / 32)) {
-        const RowPlan r = s.plan[i];
-        const int32_t* from = p.table + (int64_t)r.parent * p.max_pages;
-        int32_t* to = p.table_out + (int64_t)i * p.max_pages;
-        constexpr int BATCH = 4;
-        for (int j0 = lane; j0 < p.max_pages; j0 += 32 * BATCH) {
-            int page[BATCH];
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int j = j0 + 32 * k, rank = r.fresh_at + j - r.shared;
-                page[k] = j < r.shared ? from[j] : j < r.need && rank < handed ? s.fresh[rank] : -1;
-            }
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int j = j0 + 32 * k;
-                if (j >= p.max_pages) break;
-                if (j < r.shared && (page[k] < 0 || page[k] >= p.num_pages)) {
-                    atomicOr(p.err, KDA_DEVERR_PAGES);
-                    page[k] = -1;
-                }
-                to[j] = page[k];
-            }
-        }
-    }
-    for (int i = 0; i < set.n; ++i)
-        copy_pool(set.pool[i], copies,
-                  [&](int64_t pair, int& from, int& to) {
-                      from = s.src[pair];
-                      to = s.dst[pair];
-                      return from >= 0;
-                  },
-                  p.err, KDA_DEVERR_PAGES);
+    fork_finish(p, s, set);
 }
 
 struct CompactScratch {
@@ -625,13 +641,17 @@ size_t cache_fork_workspace(int32_t rows_out, int32_t num_pages) {
 }
 
 cudaError_t launch_cache_fork(const ForkParams& p, const PoolSet& pools, void* workspace, cudaStream_t s) {
-    static DeviceSetup done;
+    static DeviceSetup done[2];
+    int64_t bytes = (int64_t)p.rows_out * p.max_pages * 4;
+    for (int i = 0; i < pools.n; ++i) bytes += p.rows_out * pools.pool[i].layers * pools.pool[i].slot_bytes;
+    const bool whole = bytes <= WHOLE_BYTES;
+    auto* kernel = whole ? kda_cache_fork_kernel<true> : kda_cache_fork_kernel<false>;
     int sms = 0;
-    cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_cache_fork_kernel), KDA_FORK_MAX_ROWS * 16, &sms, true);
+    cudaError_t e = device_setup(done[whole], reinterpret_cast<const void*>(kernel), KDA_FORK_MAX_ROWS * 16, &sms, true);
     if (e != cudaSuccess) return e;
     const ForkScratch sc = fork_scratch(static_cast<int32_t*>(workspace), p.rows_out, p.num_pages, nullptr);
-    e = launch_cluster(kda_cache_fork_kernel, ((size_t)p.rows_in + p.rows_out) * 8, s, p, sc);
-    if (e != cudaSuccess || p.rows_out == 0) return e;
+    e = launch_cluster(kernel, ((size_t)p.rows_in + p.rows_out) * 8, s, p, sc, pools);
+    if (e != cudaSuccess || whole || p.rows_out == 0) return e;
     const int rows = (p.rows_out + CT / 32 - 1) / (CT / 32), copies = copy_grid(pools, p.rows_out, sms);
     const int grid = rows > copies ? (rows < MOST_CTAS * sms ? rows : MOST_CTAS * sms) : copies;
     return launch_wide(kda_cache_fork_finish_kernel, grid, true, s, p, sc, pools);

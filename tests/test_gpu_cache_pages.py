@@ -182,6 +182,20 @@ def test_cache_fork(R, M, ps, kind):
     run_fork(table, lens, parent, ref, ps, grow, pools, in_place=kind in ("one", "free"))
 
 
+@pytest.mark.parametrize("R,M,ps,slot", [(4, 9, 16, 1 << 19), (6, 40, 7, 1 << 17), (64, 12, 16, 8192), (300, 5, 3, 2048),
+                                         (2100, 3, 4, 512), (4, 9, 16, 65536), (4, 9, 16, 65536 + 64)])
+@pytest.mark.parametrize("kind", ["one", "random"])
+def test_cache_fork_of_large_pages(R, M, ps, slot, kind):
+    """More bytes than the bookkeeping's own CTAs move, and either side of that limit."""
+    rng = np.random.default_rng(R + M + slot)
+    P = 2 * R * M + 5
+    table, lens, ref = random_cache(R, M - 1, ps, P, rng)
+    table = np.concatenate([table, np.full((R, 1), -1, np.int32)], 1)
+    parent = np.full(R, R // 2) if kind == "one" else rng.integers(-1, R, R)
+    grow = rng.integers(0, ps + 1, R)
+    run_fork(table, lens, parent, ref, ps, grow, [pool_of((2, P, slot), R)])
+
+
 def test_cache_fork_more_and_fewer_rows():
     rng = np.random.default_rng(3)
     table, lens, ref = random_cache(5, 6, 4, 200, rng)
