@@ -406,11 +406,11 @@ __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamPara
                     mine_kept += __popc(hits);
                 }
             }
-            if (mine > limit) {                         // -inf until a thread meets its first logit
-                if (sum != 0.f) sum *= exp_of(t - mine);
-                t = mine;
-                limit = mine + 64.f;
-            }
+        }
+        if (mine > limit) {                             // whatever the bound: behind masks it may be far above t
+            if (sum != 0.f) sum *= exp_of(t - mine);
+            t = mine;
+            limit = mine + 64.f;
         }
         sum += x.sum_exp(t == -INFINITY ? 0.f : t);
         if (chunk == first && bound != -INFINITY) least = above(bound, T());

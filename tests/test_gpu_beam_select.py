@@ -126,6 +126,27 @@ def test_words_masked_by_a_large_negative_number(dtype, fill):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fill", [-200.0, -1e4, -1e10, "lowest"])
+@pytest.mark.parametrize("N,K", [(320, 1), (40, 8), (2, 4)])
+def test_weak_words_behind_masked_ones_and_strong_ones(dtype, fill, N, K):
+    """What a thread has met so far may be masks alone when others have already met the best words: the weak words
+    that it meets then are no candidates, but belong to the sum as they are."""
+    V, chunk = 40000, 8192 if dtype == "bf16" else 4096
+    logits, bs = inputs(N, K, V, dtype, 30)
+    fill = float(torch.finfo(DT[dtype]).min) if fill == "lowest" else fill
+    g = torch.Generator(device=DEV).manual_seed(31)
+    few = torch.rand(V, device=DEV, generator=g) < 0.002
+    check(torch.where(few, logits, torch.full_like(logits, fill)), bs)
+    strong, weak = torch.zeros(V, dtype=torch.bool, device=DEV), torch.zeros(V, dtype=torch.bool, device=DEV)
+    strong[torch.arange(chunk + 5, 2 * chunk - 60, 150, device=DEV)] = True
+    weak[torch.arange(2 * chunk + 70, V, 331, device=DEV)] = True
+    high, low = logits.abs() + 9, -logits.abs() - 1
+    check(torch.where(strong, high, torch.where(weak, low, torch.full_like(logits, fill))), bs)
+    if fill != float(torch.finfo(DT[dtype]).min):      # a mask that is added leaves the masked words different
+        check(torch.where(strong, high, torch.where(weak, low, logits + fill)), bs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_logits_in_order(dtype):
     """Rising and falling rows: every chunk of the one holds larger logits than all before it."""
     ramp = torch.linspace(-20, 20, 100000, device=DEV)
