@@ -146,7 +146,7 @@ kda_status kda_state_fork(const kda_pool* pools, int32_t num_pools, const int32_
 }
 
 size_t kda_cache_fork_workspace_size(int32_t rows_in, int32_t rows_out, int32_t max_pages, int32_t num_pages) {
-    if (rows_in < 0 || rows_out <= 0 || max_pages < 0 || num_pages < 0) return 0;
+    if (rows_in < 0 || rows_out < 0 || max_pages < 0 || num_pages < 0 || (rows_in == 0 && rows_out == 0)) return 0;
     if (rows_in > KDA_FORK_MAX_ROWS || rows_out > KDA_FORK_MAX_ROWS) return 0;
     return align_up(kda::cache_fork_workspace(rows_out, num_pages), 256);
 }

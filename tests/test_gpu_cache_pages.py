@@ -196,6 +196,14 @@ def test_cache_fork_of_large_pages(R, M, ps, slot, kind):
     run_fork(table, lens, parent, ref, ps, grow, [pool_of((2, P, slot), R)])
 
 
+def test_cache_fork_frees_every_row():
+    rng = np.random.default_rng(8)
+    table, lens, ref = random_cache(9, 6, 4, 300, rng, groups=3)
+    for pools in ([], [pool_of((1, 300, 8), 1)]):
+        _, _, left = run_fork(table, lens, np.zeros(0, np.int32), ref, 4, np.zeros(0, int), pools)
+        assert not left.any()
+
+
 def test_cache_fork_more_and_fewer_rows():
     rng = np.random.default_rng(3)
     table, lens, ref = random_cache(5, 6, 4, 200, rng)
