@@ -234,6 +234,8 @@ ForkScratch fork_scratch(int32_t* w, int32_t rows_out, int32_t num_pages, size_t
     return s;
 }
 
+__device__ __forceinline__ int pages_of(int len, int page_size) { return len / page_size + (len % page_size != 0); }
+
 __device__ __forceinline__ int old_length(const ForkParams& p, int row) {
     const int len = p.lens[row];
     return len < 0 || len > p.max_pages * p.page_size ? 0 : len;
@@ -335,14 +337,14 @@ __global__ void __launch_bounds__(PT) kda_cache_fork_kernel(ForkParams p, ForkSc
             len = r.parent < 0 ? 0 : old_length(p, r.parent);
             const int full = len / p.page_size;
             copy = len > full * p.page_size && first[r.parent] != i;
-            r.shared = copy ? full : (len + p.page_size - 1) / p.page_size;
+            r.shared = copy ? full : pages_of(len, p.page_size);
             int grow = p.grow ? p.grow[i] : 0;
             if (grow < 0 || grow > cap - len) {
                 if (cta == 0) atomicOr(p.err, KDA_DEVERR_PAGES);
                 grow = grow < 0 ? 0 : cap - len;
             }
             len += grow;
-            r.need = (int)(((int64_t)len + p.page_size - 1) / p.page_size);
+            r.need = pages_of(len, p.page_size);
             mine = (unsigned)(r.need - r.shared) | (copy ? 1ull << 32 : 0ull);
         }
         unsigned long long total;
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(PT) kda_cache_fork_kernel(ForkParams p, ForkSc
         const int full = len / p.page_size, at = fresh_at[i];
         const int next = i + 1 < p.rows_out ? fresh_at[i + 1] : wanted;
         const bool copy = copy_at[i] >= 0;
-        const int shared = copy ? full : (len + p.page_size - 1) / p.page_size;
+        const int shared = copy ? full : pages_of(len, p.page_size);
         len += p.grow ? max(0, min(p.grow[i], cap - len)) : 0;
         if (next > at && next > available) {           // the row ends before its first page that is missing
             atomicOr(p.err, KDA_DEVERR_EXHAUSTED);
@@ -643,7 +645,7 @@ size_t cache_fork_workspace(int32_t rows_out, int32_t num_pages) {
 cudaError_t launch_cache_fork(const ForkParams& p, const PoolSet& pools, void* workspace, cudaStream_t s) {
     static DeviceSetup done[2];
     int64_t bytes = (int64_t)p.rows_out * p.max_pages * 4;
-    for (int i = 0; i < pools.n; ++i) bytes += p.rows_out * pools.pool[i].layers * pools.pool[i].slot_bytes;
+    for (int i = 0; i < pools.n; ++i) bytes += (int64_t)p.rows_out * pools.pool[i].layers * pools.pool[i].slot_bytes;
     const bool whole = bytes <= WHOLE_BYTES;
     auto* kernel = whole ? kda_cache_fork_kernel<true> : kda_cache_fork_kernel<false>;
     int sms = 0;

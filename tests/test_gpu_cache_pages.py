@@ -196,6 +196,13 @@ def test_cache_fork_of_large_pages(R, M, ps, slot, kind):
     run_fork(table, lens, parent, ref, ps, grow, [pool_of((2, P, slot), R)])
 
 
+def test_cache_fork_of_pages_as_long_as_lengths_go():
+    """A length and a page together pass 2^31 here."""
+    ps = (1 << 30) + 5
+    table, ref = np.array([[2], [0]], np.int32), np.array([1, 0, 1, 0], np.int32)
+    run_fork(table, np.array([ps, ps - 1], np.int32), [0, 0, 1, 1, -1], ref, ps, [0, 0, 1, 0, 0], [pool_of((1, 4, 8), 1)])
+
+
 def test_cache_fork_frees_every_row():
     rng = np.random.default_rng(8)
     table, lens, ref = random_cache(9, 6, 4, 300, rng, groups=3)

@@ -44,6 +44,13 @@ def test_attention_refuses(lib, over, code):
     assert attention(lib, **over) == code
 
 
+def test_attention_longest_table(lib):
+    """A tile past the longest length still has to be a 32-bit number."""
+    last = 2 ** 31 - 1024
+    assert attention(lib, M=1, pages=1, ps=last, ws=None) == WS            # every other argument is accepted
+    assert attention(lib, M=1, pages=1, ps=last + 1, ws=None) == INV
+
+
 def test_attention_workspace(lib):
     assert lib.kda_attention_decode_workspace_size(0, 8, 2, 64, 1) == 0
     assert lib.kda_attention_decode_workspace_size(2, 9, 2, 64, 1) == 0
