@@ -399,6 +399,13 @@ def _raw_stream(stream, dev):
     return _current_raw_stream(dev) if stream is None else stream.cuda_stream
 
 
+def _in_stream(stream, call, *args, **kwargs):
+    """The call with `stream` as the current one, so that what it allocates itself belongs to that stream: a block of
+    another stream's may still be in use there, or be handed out again before this stream is done with it."""
+    with torch.cuda.stream(stream):
+        return call(*args, **kwargs)
+
+
 def _workspace(workspace, dev):
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on CUDA device {dev}")
@@ -463,6 +470,9 @@ def kda_attention_decode(q, k_pages, v_pages, block_table, seq_lens, *, scale: f
     stored at position seq_lens - 1 by this call.  window > 0: only the last `window` tokens and the first
     `sinks` are visible.  lse [B, H_q] f32, if given, receives the log of the softmax's sum.
     """
+    if stream is not None and (o is None or workspace is None):
+        return _in_stream(stream, kda_attention_decode, q, k_pages, v_pages, block_table, seq_lens, scale=scale,
+                          window=window, sinks=sinks, k_new=k_new, v_new=v_new, o=o, lse=lse, workspace=workspace)
     L = _LIB or load()
     B, Hq, d = q.shape
     shape = P, Hkv, ps, _ = k_pages.shape
@@ -517,6 +527,10 @@ def kda_beam_select(logits, beam_scores, *, finished=None, eos_token: int = -1, 
     place first among equal ones.  parent holds row numbers n * K + b, as kda_state_fork and kda_cache_fork take
     them.  finished [N, K] uint8: such a beam goes on with eos_token alone, at its unchanged score.
     """
+    if stream is not None and (workspace is None or scores_out is None or parent is None or token is None or finished_out is None):
+        return _in_stream(stream, kda_beam_select, logits, beam_scores, finished=finished, eos_token=eos_token,
+                          scores_out=scores_out, parent=parent, token=token, finished_out=finished_out,
+                          workspace=workspace)
     L = _LIB or load()
     N, K = beam_scores.shape
     V = logits.shape[1]
@@ -581,6 +595,8 @@ def kda_state_fork(pools, state_idx, parent, *, state_idx_out=None, stream=None)
     """Gives each row i of a decode batch the state of row parent[i] (-1: a row that starts anew); returns the
     new state_idx [B], a permutation of the old one.  pools: one tensor or several [layers, slots, ...] of
     states (kda_decode_step's pool is pool[layer]).  Copies only states that two rows continue."""
+    if stream is not None and (state_idx_out is None or not parent.is_contiguous()):
+        return _in_stream(stream, kda_state_fork, pools, state_idx, parent, state_idx_out=state_idx_out)
     dev = _cuda_index("state_idx", state_idx)
     parent = parent.reshape(-1) if parent.dim() != 1 else parent
     B = state_idx.shape[0]
@@ -614,6 +630,10 @@ def kda_cache_fork(block_table, seq_lens, parent, ref_count, page_size: int, *, 
     ref_count is updated in place unless ref_count_out is given.  copy_src, copy_dst [R'] receive the pages
     copied, for pools that are not passed here.
     """
+    if stream is not None and (block_table_out is None or seq_lens_out is None or workspace is None or not parent.is_contiguous()):
+        return _in_stream(stream, kda_cache_fork, block_table, seq_lens, parent, ref_count, page_size, grow=grow,
+                          pools=pools, block_table_out=block_table_out, seq_lens_out=seq_lens_out,
+                          ref_count_out=ref_count_out, copy_src=copy_src, copy_dst=copy_dst, workspace=workspace)
     L = _LIB or load()
     dev = _cuda_index("block_table", block_table)
     parent = parent.reshape(-1) if parent.dim() != 1 else parent
@@ -664,6 +684,10 @@ def kda_cache_compact(block_table, ref_count, *, pools=(), block_table_out=None,
     """Moves the live pages (ref_count > 0) together at the low end of the pools; returns (block_table,
     ref_count, page_map) with the new numbers.  block_table and ref_count are updated in place unless outputs are
     given; page_map [P] int32 holds each page's new number, -1 for a free one."""
+    if stream is not None and (page_map is None or workspace is None):
+        return _in_stream(stream, kda_cache_compact, block_table, ref_count, pools=pools,
+                          block_table_out=block_table_out, ref_count_out=ref_count_out, page_map=page_map,
+                          workspace=workspace)
     L = _LIB or load()
     dev = _cuda_index("block_table", block_table)
     R, M = block_table.shape
