@@ -16,9 +16,9 @@
 // kernel joins in the order of the CTAs: no atomics, the same bits on every call.
 //
 // What bounds it is DRAM, once there is enough to read: one row of 1,048,573 tokens with 8 heads of 128 takes
-// 588 us (7.3 TB/s of reads), 64 rows of 213,000 tokens in all with 8 key-value heads 135 us (6.45 TB/s, the rest
+// 580 us (7.4 TB/s of reads), 64 rows of 213,000 tokens in all with 8 key-value heads 134 us (6.5 TB/s, the rest
 // is the first loads' latency, the joins and the second kernel, together about 12 us whatever the size).  With few
-// bytes that latency is all: 4.4 us for a row of 37 tokens.  With 16 and 32 query heads a key the products of
+// bytes that latency is all: 4.2 us for a row of 37 tokens.  With 16 and 32 query heads a key the products of
 // mma.sync begin to show (4.6 and 3.6 TB/s at 250 MB).
 //
 // The products: with the tokens as the 16 rows of mma.m16n8k16 and the query heads as its 8 columns, both
