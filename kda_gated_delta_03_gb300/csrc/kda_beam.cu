@@ -7,10 +7,10 @@
 // The logits are read once.  s is a monotone function of x within a row, so a part of a row contributes
 // its K + 1 largest logits, its maximum and its sum of exponentials without knowing lse; a second kernel
 // puts each row's lse together, scores what the parts offer and takes the K best of the group.  Two logits
-// that differ can round to one score, and then the lower place wins whatever its logit: the (K + 1)-th
-// entry shows whether that can concern anything that a part left out, and then (rarely: beside scores so
-// large that neighbouring logits fall together) the group's logits are searched for the places with
-// exactly that score.  Rows that offer nothing (finished, no score) are not read.
+// that differ can round to one score, and then the lower place wins whatever its logit.  Whether that can concern
+// anything that a part left out is seen from its list (best_left_out), and then (rarely: where neighbouring logits
+// fall together at the last score that is chosen) the group's logits are searched for the places with exactly that
+// score.  Rows that offer nothing (finished, no score) are not read.
 //
 // What it costs: 410 of 512 rows of 131,072 bf16 words (107 MB) take 28 us, of which the read at DRAM's rate
 // would be 16.  Issue slots are the rest (8 instructions a logit; a plain stream of loads, exponentials and
@@ -258,6 +258,21 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long x) {
     return x;
 }
 
+// The best score (or more) among the logits that a part left out of its list and that may have to be chosen all the same.
+// Such a logit has at most K - 1 others before it, so two at least of the K + 1 listed ones come after it: with its
+// score, at higher places, and listed only since they are larger.  It is below the list's last logit x, or equals it;
+// the latter only where two listed logits above x share x's score.  (Equal logits alone are no such case.)
+template <typename T>
+__device__ float best_left_out(const unsigned long long* list, int K, unsigned long long last, float bs, float lse) {
+    const float x = candidate_value(last), s = beam_score(bs, x, lse), under = beam_score(bs, below(x, T()), lse);
+    if (under < s && beam_score(bs, above(x, T()), lse) == s) {
+        int i = K - 1;
+        while (i >= 0 && candidate_value(list[i]) == x) --i;
+        if (i >= 1 && beam_score(bs, candidate_value(list[i - 1]), lse) == s) return s;
+    }
+    return under;
+}
+
 // The L largest of n candidates, in order, to best[0 .. L); 0 where there are fewer.
 __device__ __forceinline__ void rank_candidates(const unsigned long long* cand, int n, int L, unsigned long long* best) {
     for (int i = threadIdx.x; i < n; i += BT) {
@@ -492,7 +507,7 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int par
 
     // a warp per row: its lse, and its entries as scores with their places in the group
     unsigned long long mine = 0;
-    float left_out = -INFINITY;                        // no logit that a part left out scores more
+    float left_out = -INFINITY;                        // the best of what the parts' lists left out, or more
     for (int b = warp; b < K; b += BW) {
         const unsigned long long* from = list + b * per_row;
         unsigned long long* to = scored + b * per_row;
@@ -500,7 +515,7 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int par
         unsigned long long c[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) c[i] = lane + 32 * i < per_row ? from[lane + 32 * i] : 0;
-        const unsigned long long head = lane < parts ? from[lane * L] : 0;
+        const unsigned long long head = lane < parts ? from[lane * L] : 0, tail = lane < parts ? from[lane * L + K] : 0;
         const float2 stat = lane < parts ? stats[b * parts + lane] : make_float2(0.f, 0.f);
         bool is_alive = false;
         float log_sum = 0.f;
@@ -520,8 +535,14 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int par
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
             is_alive = top != -INFINITY && sum == sum;               // else every score of the row is -inf
             log_sum = top + logf(sum);
-            int in_list = lane % L;                                  // of entry e0 + 32 * i
-            const int step = 32 % L;
+            if (is_alive) {
+                if (tail) left_out = fmaxf(left_out, best_left_out<T>(from + lane * L, K, tail, score, log_sum));
+                for (int i = lane + 32; i < parts; i += 32) {
+                    const unsigned long long last = from[i * L + K];
+                    if (last) left_out = fmaxf(left_out, best_left_out<T>(from + i * L, K, last, score, log_sum));
+                }
+            }
+            __syncwarp();                                            // scores may take the lists' place
             for (int e0 = lane; e0 < per_row; e0 += 32 * AHEAD) {
                 unsigned long long after[AHEAD];
 #pragma unroll
@@ -536,13 +557,10 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int par
                     if (is_alive && c[i]) {
                         const float x = candidate_value(c[i]), s = beam_score(score, x, log_sum);
                         if (s != -INFINITY) d = candidate(s, (unsigned)b * p.V + candidate_place(c[i]));
-                        if (in_list == K) left_out = fmaxf(left_out, beam_score(score, below(x, T()), log_sum));
                     }
                     if (e < per_row) to[e] = d;
                     mine = d > mine ? d : mine;
                     c[i] = after[i];
-                    in_list += step;
-                    if (in_list >= L) in_list -= L;
                 }
             }
         } else {

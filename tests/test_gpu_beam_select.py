@@ -210,6 +210,65 @@ def test_scores_that_round_together_in_part():
             assert got[n, a] > got[n, b] or (got[n, a] == got[n, b] and place[a] < place[b])
 
 
+def known_sums(N, K, V, dtype):
+    """Logits of -20 behind one of 50 in the third place, beside which no sum of V others up to 9 shows in float32 (V e^-41
+    is below 2^-26): a row's log-sum is 50, and every score is known to the bit."""
+    logits = torch.full((N * K, V), -20.0, dtype=DT[dtype], device=DEV)
+    logits[:, 2] = 50.0
+    return logits
+
+
+def check_exactly(logits, bs):
+    """Scores, parents and tokens of rows whose log-sum is 50, the lowest place first among equal scores."""
+    N, K = bs.shape
+    V = logits.shape[1]
+    s = (bs.view(N * K, 1) + (logits.float() - 50.0)).view(N, K * V)
+    best = torch.sort(s, dim=1, descending=True, stable=True)
+    score, parent, token, _ = kda.kda_beam_select(logits, bs)
+    rows = torch.arange(N, device=DEV)[:, None] * K
+    assert torch.equal(score, best.values[:, :K])
+    wrong = ((parent - rows) * V + token != best.indices[:, :K]).any(1).nonzero()[:, 0].tolist()
+    assert not wrong, (len(wrong), N)
+
+
+# float32 logits from 7.25 up, 2^-21 apart, bf16 ones from 4 up, 2^-5 apart; the beam scores' neighbours lie further apart
+NEIGHBOURS = {"f32": (7.25, 2.0 ** -21, (-30.0, -300.0)), "bf16": (4.0, 2.0 ** -5, (-2.0 ** 18, -2.0 ** 19, -1.3e5))}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_equal_logits_beside_their_upper_neighbour(dtype):
+    """Two words at some logit x, and later two at the next larger one.  Where the four score the same, the two lower
+    places win, although a list of the largest logits names but one of them."""
+    start, step, scores = NEIGHBOURS[dtype]
+    for beam in scores:
+        logits, bs = known_sums(64, 3, 2048, dtype), torch.full((64, 3), NINF, device=DEV)
+        bs[:, 0] = beam
+        x = start + step * torch.arange(64, device=DEV)
+        logits[::3, 5] = logits[::3, 6] = x.to(DT[dtype])
+        logits[::3, 1000] = logits[::3, 1001] = (x + step).to(DT[dtype])
+        check_exactly(logits, bs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [2, 4, 16, 32])
+@pytest.mark.parametrize("V", [300, 9000, 70001])
+def test_neighbouring_logits_that_round_together(dtype, K, V):
+    """Few values, many words of each, a few of which share a score: places and scores to the bit."""
+    rng = np.random.default_rng(V + K)
+    start, step, scores = NEIGHBOURS[dtype]
+    for beam in scores:
+        N = 24
+        logits, bs = known_sums(N, K, V, dtype), torch.full((N, K), NINF, device=DEV)
+        bs[:, 0] = beam * torch.from_numpy(rng.uniform(1, 2, N)).float().to(DEV)
+        if K > 2:
+            bs[:, 1] = bs[:, 0]
+        for r in range(N * K):
+            words = torch.from_numpy(3 + rng.permutation(V - 3)[:3 * K]).to(DEV)
+            values = start + step * torch.from_numpy(rng.integers(0, 32, 3 * K)).to(DEV)
+            logits[r, words] = values.to(DT[dtype])
+        check_exactly(logits, bs)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_zeros_of_both_signs_are_one_value(dtype):
     logits = torch.full((2, 5000), -5.0, device=DEV)
