@@ -290,7 +290,10 @@ __device__ __forceinline__ void rank_candidates(const unsigned long long* cand, 
 // its own, and the bound moves up to the L-th best after the second chunk, the fourth, the eighth and so on.
 // So about L logits are looked at between two such steps (without them about L in every chunk: 38 us instead of 28
 // for 512 rows of 131,072), and the other chunks need no barrier.  If a warp's list runs over, the L-th best of
-// those kept is a better bound, and the part is searched again with it.
+// those kept is a better bound, and the part is searched again with it.  Where too many reach that as well (a row in
+// rising order, or behind a masked stretch), the bound is found digit by digit, eight bits of a candidate at a time: ten
+// more reads of the part at most, whatever the row (320 rising rows of 400,000 bf16 words 2.5 ms; with
+// one bound after another from the lists 91).
 //
 // The sum is that of exp(x - t), t the first chunk's maximum; a thread that meets a logit 64 above moves its own t
 // up.
@@ -430,9 +433,9 @@ __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamPara
         sum += x.sum_exp(t == -INFINITY ? 0.f : t);
         if (chunk == first && bound != -INFINITY) least = above(bound, T());
         const int done = chunk - first + 1;
-        if (done >= 2 && (done & (done - 1)) == 0 && chunk + 1 < last && !lost) {
-            const int n = gather(lost);
-            if (n >= L && !lost) {
+        if (done >= 2 && (done & (done - 1)) == 0 && chunk + 1 < last) {
+            const int n = gather(lost);                  // the L-th best of those kept is a bound even if some were lost
+            if (n >= L) {
                 rank_candidates(all, n, L, best);
                 __syncthreads();
                 if (tid < L) cand[tid] = best[tid];
@@ -442,26 +445,63 @@ __global__ void __launch_bounds__(BT, CTAS_PER_SM) kda_beam_part_kernel(BeamPara
         }
     }
     int n = gather(lost);
-    while (lost) {
-        // again, from the L-th best of those kept on; each time fewer remain
-        rank_candidates(all, min(n, CAP), L, best);
-        if (tid == 0) found = 0;
-        __syncthreads();
-        const unsigned long long from = best[L - 1];
+    if (lost) {
         const T* logits = static_cast<const T*>(p.logits) + row * p.row_stride;
         const int stop = min(p.V, last * CHUNK<T>);
-        for (int i = first * CHUNK<T> + tid; i < stop; i += BT) {
-            const float y = to_float(logits[i]);
-            const unsigned long long c = candidate(y, (unsigned)i);
-            if (y > -INFINITY && c >= from) {
+        // every candidate of the part, eight of a thread on their way at a time
+        auto each = [&](auto use) {
+            constexpr int BATCH = 8;
+            for (int i0 = first * CHUNK<T> + tid; i0 < stop; i0 += BATCH * BT) {
+                float y[BATCH];
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) y[k] = i0 + k * BT < stop ? to_float(logits[i0 + k * BT]) : -INFINITY;
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k)
+                    if (y[k] > -INFINITY) use(candidate(y[k], (unsigned)(i0 + k * BT)));
+            }
+        };
+        // those from `from` on to the list, the first CAP that come
+        auto search = [&](unsigned long long from) {
+            if (tid == 0) found = 0;
+            __syncthreads();
+            each([&](unsigned long long c) {
+                if (c < from) return;
                 const int at = atomicAdd(&found, 1);
                 if (at < CAP) all[at] = c;
+            });
+            __syncthreads();
+            n = found;
+        };
+        rank_candidates(all, n, L, best);
+        __syncthreads();
+        search(best[L - 1]);
+        if (n > CAP) {
+            // the L-th best of the part, its highest digits first, until CAP at most share them or are better
+            unsigned long long from = 0;
+            int over = 0;                                // better than all that share the digits found
+            int* digits = reinterpret_cast<int*>(cand);  // how many have each
+            static_assert(BT == 256 && sizeof(cand) >= 256 * sizeof(int), "a thread per digit");
+            for (int shift = 56; n > CAP; shift -= 8) {
+                digits[tid] = 0;
+                __syncthreads();
+                each([&](unsigned long long c) {
+                    if (c >> shift >> 8 == from >> shift >> 8) atomicAdd(&digits[c >> shift & 255], 1);
+                });
+                __syncthreads();
+                int better = over;
+                for (int d = tid + 1; d < 256; ++d) better += digits[d];
+                if (better < L && better + digits[tid] >= L) {           // in one thread
+                    kept[0] = tid;
+                    kept[1] = better;
+                    kept[2] = better + digits[tid];
+                }
+                __syncthreads();
+                from |= (unsigned long long)kept[0] << shift;
+                over = kept[1];
+                n = kept[2];                             // L in the end: no two candidates are equal
             }
+            search(from);
         }
-        __syncthreads();
-        n = found;
-        lost = n > CAP;
-        __syncthreads();
     }
 
     const Workspace<T> w = workspace<T>(p, parts);

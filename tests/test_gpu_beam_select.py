@@ -159,6 +159,35 @@ def test_logits_in_order(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("first", [-20.0, -1e4])
+def test_rising_rows_cost_a_few_reads_more(dtype, first):
+    """Rows whose every word is larger than those before it (behind a masked first stretch, too) overflow the lists that
+    a part keeps.  A search with a bound on its passes (ten, each some ten reads of the row at most) stays within a
+    hundred times the same rows in random order; one that drops a list's length of words a pass does not."""
+    N, K, V = 40, 8, 400000
+    row = torch.linspace(-20, 20, V, device=DEV)
+    row[:V // 40] = first
+    order = torch.randperm(V, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    bs = -50.0 * torch.arange(K, device=DEV, dtype=torch.float32).repeat(N, 1)
+    times = []
+    for r in (row, row[order]):
+        r = r.to(DT[dtype])
+        logits = r.repeat(N * K, 1)
+        best = torch.sort(r.float(), descending=True, stable=True).indices[:K].tolist()
+        took = []
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            _, parent, token, _ = kda.kda_beam_select(logits, bs)
+            b.record()
+            torch.cuda.synchronize()
+            took.append(a.elapsed_time(b))
+        assert token.tolist() == [best] * N and parent.tolist() == [[n * K] * K for n in range(N)]
+        times.append(min(took))
+    assert times[0] <= 100 * times[1], times
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("V", [2, 2500, 40001])
 def test_ties_go_to_the_lowest_place(dtype, V):
     """Equal logits within a row and equal rows: the same arithmetic gives the same score wherever it stands."""
