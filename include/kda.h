@@ -430,7 +430,7 @@ KDA_API kda_status kda_attention_decode(const void* q, void* k_pages, void* v_pa
  *   token        [N, K] int32;  finished_out [N, K] bytes (token == eos_token or parent finished), or NULL
  *                (may be finished, in place)
  *   workspace    kda_beam_select_workspace_size(...) bytes
- * K <= KDA_BEAM_MAX_K.
+ * K <= KDA_BEAM_MAX_K; V at most 2^31 - 2^14, K * V and N * K below 2^31 (KDA_ERR_TOO_LARGE above).
  */
 #define KDA_BEAM_MAX_K 32
 KDA_API size_t kda_beam_select_workspace_size(int32_t N, int32_t K, int32_t V, kda_dtype dt);

@@ -12,6 +12,8 @@ bool table_ok(const void* p) { return p && aligned(p, 4); }
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 size_t esize(kda_dtype dt) { return dt == KDA_DTYPE_BF16 ? 2 : 4; }
 bool known(kda_dtype dt) { return dt == KDA_DTYPE_F32 || dt == KDA_DTYPE_BF16; }
+// Words of a row: places up to a chunk past its end are 32-bit numbers.
+constexpr int32_t MOST_WORDS = INT32_MAX - (1 << 14) + 1;
 bool head_ok(int32_t d) { return d == 16 || d == 64 || d == 128; }
 
 kda_status take_pools(const kda_pool* pools, int32_t n, int32_t slots, kda::PoolSet* out) {
@@ -87,7 +89,7 @@ kda_status kda_attention_decode(const void* q, void* k_pages, void* v_pages, con
 }
 
 size_t kda_beam_select_workspace_size(int32_t N, int32_t K, int32_t V, kda_dtype dt) {
-    if (N <= 0 || K <= 0 || K > KDA_BEAM_MAX_K || V <= 0 || !known(dt)) return 0;
+    if (N <= 0 || K <= 0 || K > KDA_BEAM_MAX_K || V <= 0 || V > MOST_WORDS || !known(dt)) return 0;
     return align_up(kda::beam_workspace(N, K, V, dt), 256);
 }
 
@@ -100,7 +102,7 @@ kda_status kda_beam_select(const void* logits, int64_t row_stride, const float* 
     if (finished && eos_token < 0) return KDA_ERR_INVALID_ARG;
     if (K > KDA_BEAM_MAX_K) return KDA_ERR_UNSUPPORTED;
     // a candidate's place b * V + v and a row's number n * K + b are 32-bit
-    if ((int64_t)K * V > INT32_MAX || (int64_t)N * K > INT32_MAX) return KDA_ERR_TOO_LARGE;
+    if (V > MOST_WORDS || (int64_t)K * V > INT32_MAX || (int64_t)N * K > INT32_MAX) return KDA_ERR_TOO_LARGE;
     if (N == 0) return KDA_OK;
     if (!logits || !aligned(logits, esize(dt)) || !beam_scores || !aligned(beam_scores, 4) || !scores ||
         !aligned(scores, 4) || !table_ok(parent) || !table_ok(token))

@@ -84,6 +84,18 @@ def test_select_workspace(lib):
         assert select(lib, V=100000, stride=100000, wsb=need - 1) == WS
 
 
+def test_select_longest_row(lib):
+    """A chunk past a row's end still has to be a 32-bit number."""
+    last = 2 ** 31 - 2 ** 14
+    for dt in (0, 1):
+        assert 0 < lib.kda_beam_select_workspace_size(1, 1, last, dt) <= 1 << 14
+        assert lib.kda_beam_select_workspace_size(1, 1, last + 1, dt) == 0
+        assert lib.kda_beam_select_workspace_size(1, 1, 2 ** 31 - 1, dt) == 0
+        assert select(lib, N=1, K=1, V=last, stride=last, dt=dt, ws=None) == WS       # every other argument is accepted
+        assert select(lib, N=1, K=1, V=last + 1, stride=last + 1, dt=dt) == TOO_LARGE
+        assert select(lib, N=1, K=1, V=2 ** 31 - 1, stride=2 ** 31 - 1, dt=dt) == TOO_LARGE
+
+
 def pool(**over):
     p = dict(data=P, layer_stride=0, slot_stride=64, slot_bytes=64, layers=1, slots=10)
     p.update(over)
