@@ -402,8 +402,8 @@ KDA_API kda_status kda_prefill_host(const void* q, const void* k, const void* v,
  *                split over several CTAs, joined in a fixed order (two calls give the same bits)
  * Sizes: d in {16, 64, 128}; H_q a multiple of H_kv; any page_size >= 1; max_pages * page_size at most
  * 2^31 - 1024.  Alignment: q, k_new, v_new, o and the pools 16 bytes, page strides multiples of 16 bytes.
- * A length outside [0, max_pages * page_size] counts as 0, and a page outside [0, num_pages) as page 0;
- * both set KDA_DEVERR_PAGES.
+ * A length outside [0, max_pages * page_size] counts as 0, and a page outside [0, num_pages) as page 0 where it
+ * is read; a new token whose page is outside is attended to, but not stored.  All set KDA_DEVERR_PAGES.
  */
 KDA_API size_t kda_attention_decode_workspace_size(int32_t B, int32_t H_q, int32_t H_kv, int32_t d, kda_dtype dt);
 KDA_API kda_status kda_attention_decode(const void* q, void* k_pages, void* v_pages, const int32_t* block_table,

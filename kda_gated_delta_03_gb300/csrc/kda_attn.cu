@@ -724,6 +724,8 @@ __global__ void __launch_bounds__(AT, Layout<T, D, NH>::CTAS_PER_SM) kda_attn_ke
                                      : static_cast<T*>(p.v_pages) + page * p.v_stride;
                         reinterpret_cast<uint4*>(to + off)[chunk] = x;
                     }
+                } else if (lane == 0) {
+                    atomicOr(p.err, KDA_DEVERR_PAGES);  // nobody may have read that page: not stored, and told
                 }
             }
             stage = stage + 1 == L::STAGES ? 0 : stage + 1;

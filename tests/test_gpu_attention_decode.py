@@ -270,6 +270,26 @@ def test_bad_tables_are_reported_not_faulted(dtype):
         assert rel(o[0], ref[0]) <= TOL[dtype] and rel(o[2], ref[2]) <= 2 * TOL[dtype]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [-1, 9, 1 << 30])
+def test_a_new_token_without_a_page_is_reported(dtype, page):
+    """A new token that begins a page which the table does not name: nobody reads that page, but what is not stored has
+    to be told.  The outputs are right, the pools unchanged but for the other row's token."""
+    lens = [33, 48]
+    t, new = make(lens, 4, 2, 64, 16, dtype, 41)
+    ref, _ = reference(t, lens, 16, 0.1, 0, 0, new)
+    want = t["k_pages"].clone(), t["v_pages"].clone()
+    p = int(t["block_table"][1, 2])
+    want[0][p, :, 15], want[1][p, :, 15] = new[0][1], new[1][1]
+    t["block_table"][0, 2] = page
+    assert t["k_pages"].shape[0] == 9
+    o = kda.kda_attention_decode(**t, scale=0.1, k_new=new[0], v_new=new[1])
+    assert kda.kda_get_device_error() == 0x20 and kda.kda_get_device_error() == 0
+    assert rel(o, ref) <= TOL[dtype]
+    i = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(t["k_pages"].view(i), want[0].view(i)) and torch.equal(t["v_pages"].view(i), want[1].view(i))
+
+
 def test_a_row_whose_scores_are_all_minus_infinity():
     """Keys of -inf against a positive query: every weight is exp(-inf), the row counts as empty."""
     t, _ = make([40], 2, 1, 64, 16, "f32", 11)
