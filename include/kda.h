@@ -400,8 +400,8 @@ KDA_API kda_status kda_prefill_host(const void* q, const void* k, const void* v,
  *   o            [B, H_q, d] dtype dt;  lse [B, H_q] float32 or NULL: m + log sum exp(s_t - m)
  *   workspace    kda_attention_decode_workspace_size(...) bytes: partial results of rows whose length is
  *                split over several CTAs, joined in a fixed order (two calls give the same bits)
- * Sizes: d in {16, 64, 128}; H_q a multiple of H_kv; any page_size >= 1; max_pages * page_size at most
- * 2^31 - 1024.  Alignment: q, k_new, v_new, o and the pools 16 bytes, page strides multiples of 16 bytes.
+ * Sizes: d in {16, 64, 128}; H_q a multiple of H_kv; any page_size >= 1; max_pages * page_size and B at most
+ * 2^31 - 1024, H_q * d below 2^31.  Alignment: q, k_new, v_new, o and the pools 16 bytes, page strides multiples of 16 bytes.
  * A length outside [0, max_pages * page_size] counts as 0, and a page outside [0, num_pages) as page 0 where it
  * is read; a new token whose page is outside is attended to, but not stored.  All set KDA_DEVERR_PAGES.
  */

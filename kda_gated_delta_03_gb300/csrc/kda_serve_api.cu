@@ -58,6 +58,7 @@ kda_status kda_attention_decode(const void* q, void* k_pages, void* v_pages, con
         return KDA_ERR_INVALID_ARG;
     if (H_q % H_kv != 0) return KDA_ERR_INVALID_ARG;
     if ((int64_t)max_pages * page_size > INT32_MAX - 1023) return KDA_ERR_INVALID_ARG;    // a tile past the end counts, too
+    if (B > INT32_MAX - 1023 || (int64_t)H_q * d > INT32_MAX) return KDA_ERR_INVALID_ARG;     // as does a step past the rows
     if (!head_ok(d)) return KDA_ERR_UNSUPPORTED;
     if (B == 0) return KDA_OK;
     if (!q || !o || !table_ok(seq_lens) || !aligned(q, 16) || !aligned(o, 16) || (lse && !aligned(lse, 4)))

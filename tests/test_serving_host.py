@@ -51,6 +51,16 @@ def test_attention_longest_table(lib):
     assert attention(lib, M=1, pages=1, ps=last + 1, ws=None) == INV
 
 
+def test_attention_most_rows_and_heads(lib):
+    """Rows past the last one, as a thread steps over them, and a row's outputs still have to be 32-bit numbers."""
+    last = 2 ** 31 - 1024
+    assert attention(lib, B=last, ws=None) == WS                           # every other argument is accepted
+    assert attention(lib, B=last + 1, ws=None) == INV
+    assert attention(lib, B=2 ** 31 - 1, ws=None) == INV
+    assert attention(lib, Hq=2 ** 25 - 2, ws=None) == WS
+    assert attention(lib, Hq=2 ** 25, ws=None) == INV
+
+
 def test_attention_workspace(lib):
     assert lib.kda_attention_decode_workspace_size(0, 8, 2, 64, 1) == 0
     assert lib.kda_attention_decode_workspace_size(2, 9, 2, 64, 1) == 0
