@@ -496,7 +496,9 @@ KDA_API kda_status kda_state_fork(const kda_pool* pools, int32_t num_pools, cons
  *   copy_src, copy_dst [rows_out] or NULL: the page copied for row i and where to, -1 for none (for pools
  *                   that this call does not get: kda_copy_pages takes them)
  *   pools           pools of num_pages slots; num_pools may be 0
- * All tables int32 on the device.  rows_in and rows_out at most KDA_FORK_MAX_ROWS (KDA_ERR_TOO_LARGE above).
+ * All tables int32 on the device.  rows_in and rows_out at most KDA_FORK_MAX_ROWS (KDA_ERR_TOO_LARGE above);
+ * max_pages * page_size and a table's entries below 2^31, max_pages at most 2^31 - 1024, num_pages at most
+ * 2^31 - 2^18.
  */
 KDA_API size_t kda_cache_fork_workspace_size(int32_t rows_in, int32_t rows_out, int32_t max_pages, int32_t num_pages);
 KDA_API kda_status kda_cache_fork(const int32_t* block_table, const int32_t* seq_lens, int32_t rows_in,
@@ -513,6 +515,7 @@ KDA_API kda_status kda_cache_fork(const int32_t* block_table, const int32_t* seq
  * with every entry replaced by its new number (entries outside [0, num_pages) become -1), ref_count_out the
  * counts at the new numbers.  block_table_out may be block_table, ref_count_out may be ref_count.  Other
  * tables and pools of the same pages follow with page_map (kda_copy_pages with src NULL and dst page_map).
+ * num_pages at most 2^31 - 2^18, rows * max_pages below 2^31.
  */
 KDA_API size_t kda_cache_compact_workspace_size(int32_t num_pages);
 KDA_API kda_status kda_cache_compact(const int32_t* block_table, int32_t rows, int32_t max_pages,

@@ -14,6 +14,8 @@ size_t esize(kda_dtype dt) { return dt == KDA_DTYPE_BF16 ? 2 : 4; }
 bool known(kda_dtype dt) { return dt == KDA_DTYPE_F32 || dt == KDA_DTYPE_BF16; }
 // Words of a row: places up to a chunk past its end are 32-bit numbers.
 constexpr int32_t MOST_WORDS = INT32_MAX - (1 << 14) + 1;
+// Pages of a pool and of a row's table: those that a grid or a warp steps over past the end are 32-bit numbers, too.
+constexpr int32_t MOST_PAGES = INT32_MAX - (1 << 18) + 1, MOST_ROW_PAGES = INT32_MAX - 1023;
 bool head_ok(int32_t d) { return d == 16 || d == 64 || d == 128; }
 
 kda_status take_pools(const kda_pool* pools, int32_t n, int32_t slots, kda::PoolSet* out) {
@@ -151,6 +153,7 @@ kda_status kda_state_fork(const kda_pool* pools, int32_t num_pools, const int32_
 size_t kda_cache_fork_workspace_size(int32_t rows_in, int32_t rows_out, int32_t max_pages, int32_t num_pages) {
     if (rows_in < 0 || rows_out < 0 || max_pages < 0 || num_pages < 0 || (rows_in == 0 && rows_out == 0)) return 0;
     if (rows_in > KDA_FORK_MAX_ROWS || rows_out > KDA_FORK_MAX_ROWS) return 0;
+    if (max_pages > MOST_ROW_PAGES || num_pages > MOST_PAGES) return 0;
     return align_up(kda::cache_fork_workspace(rows_out, num_pages), 256);
 }
 
@@ -161,7 +164,7 @@ kda_status kda_cache_fork(const int32_t* block_table, const int32_t* seq_lens, i
                           int32_t num_pools, void* workspace, size_t workspace_bytes, void* stream) {
     if (rows_in < 0 || rows_out < 0 || max_pages < 0 || page_size <= 0 || num_pages < 0) return KDA_ERR_INVALID_ARG;
     if ((int64_t)max_pages * page_size > INT32_MAX || (int64_t)rows_out * max_pages > INT32_MAX ||
-        (int64_t)rows_in * max_pages > INT32_MAX)
+        (int64_t)rows_in * max_pages > INT32_MAX || max_pages > MOST_ROW_PAGES || num_pages > MOST_PAGES)
         return KDA_ERR_INVALID_ARG;
     kda::PoolSet set{};
     const kda_status st = take_pools(pools, num_pools, num_pages, &set);
@@ -192,7 +195,7 @@ kda_status kda_cache_fork(const int32_t* block_table, const int32_t* seq_lens, i
 }
 
 size_t kda_cache_compact_workspace_size(int32_t num_pages) {
-    if (num_pages <= 0) return 0;
+    if (num_pages <= 0 || num_pages > MOST_PAGES) return 0;
     return align_up(kda::cache_compact_workspace(num_pages), 256);
 }
 
@@ -200,7 +203,8 @@ kda_status kda_cache_compact(const int32_t* block_table, int32_t rows, int32_t m
                              int32_t num_pages, int32_t* block_table_out, int32_t* ref_count_out, int32_t* page_map,
                              const kda_pool* pools, int32_t num_pools, void* workspace, size_t workspace_bytes,
                              void* stream) {
-    if (rows < 0 || max_pages < 0 || num_pages < 0 || (int64_t)rows * max_pages > INT32_MAX) return KDA_ERR_INVALID_ARG;
+    if (rows < 0 || max_pages < 0 || num_pages < 0 || num_pages > MOST_PAGES || (int64_t)rows * max_pages > INT32_MAX)
+        return KDA_ERR_INVALID_ARG;
     kda::PoolSet set{};
     const kda_status st = take_pools(pools, num_pools, num_pages, &set);
     if (st != KDA_OK) return st;

@@ -180,6 +180,21 @@ def test_cache_compact_refuses(lib, over, code):
     assert compact(lib, **over) == code
 
 
+def test_most_pages(lib):
+    """Pages past the last one, as a thread steps over them, still have to be 32-bit numbers."""
+    pages, row = 2 ** 31 - 2 ** 18, 2 ** 31 - 1024
+    assert fork(lib, pages=pages, ws=None) == WS                           # every other argument is accepted
+    assert fork(lib, pages=pages + 1, ws=None) == INV
+    assert fork(lib, R=1, R2=1, M=row, ps=1, ws=None) == WS
+    assert fork(lib, R=1, R2=1, M=row + 1, ps=1, ws=None) == INV
+    assert lib.kda_cache_fork_workspace_size(2, 2, 4, pages) > 0
+    assert lib.kda_cache_fork_workspace_size(2, 2, 4, pages + 1) == 0
+    assert lib.kda_cache_fork_workspace_size(2, 2, row + 1, 10) == 0
+    assert compact(lib, pages=pages, ws=None) == WS and compact(lib, pages=pages + 1, ws=None) == INV
+    assert lib.kda_cache_compact_workspace_size(pages) > 0
+    assert lib.kda_cache_compact_workspace_size(pages + 1) == 0
+
+
 def test_binding_wants_cuda_tensors():
     i = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
