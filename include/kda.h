@@ -62,7 +62,8 @@ typedef enum {
     KDA_ERR_WORKSPACE = 3,    /* workspace missing or smaller than the required size       */
     KDA_ERR_CUDA = 4,         /* a CUDA runtime call or launch failed                      */
     KDA_ERR_DEVICE = 5,       /* kda_get_device_error found device-detected errors         */
-    KDA_ERR_TOO_LARGE = 6     /* problem exceeds the fixed scratch of kda_prefill_noalloc  */
+    KDA_ERR_TOO_LARGE = 6     /* problem exceeds the fixed scratch of kda_prefill_noalloc, or a
+                                 limit on rows or words stated with the function            */
 } kda_status;
 
 typedef enum { KDA_DTYPE_F32 = 0, KDA_DTYPE_BF16 = 1 } kda_dtype;
@@ -388,7 +389,8 @@ KDA_API kda_status kda_prefill_host(const void* q, const void* k, const void* v,
  * over the visible tokens t of its row: t < seq_lens[b], and with window > 0 also t >= seq_lens[b] -
  * window or t < sinks (a sliding window behind a few first tokens that stay visible).  Query head h reads
  * key-value head h / (H_q / H_kv).  A row with no visible token gives o = 0 and lse = -inf.  What lies in
- * the pools past a row's end is never used, whatever it holds.
+ * the pools past a row's end is never used, whatever it holds; a visible value that is not finite makes its
+ * column of o not finite (in bf16 a NaN, also where the sum would be an infinity).
  *
  *   q            [B, H_q, d]   dtype dt
  *   k_pages      num_pages pages of [H_kv, page_size, d], dtype dt, page p at k_pages + p * k_page_stride
@@ -487,7 +489,8 @@ KDA_API kda_status kda_state_fork(const kda_pool* pools, int32_t num_pools, cons
  *  - Pages of its own come from the free ones, the lowest first, handed out by new row and then by
  *    position.
  * seq_lens_out[i] = seq_lens[parent[i]] + grow[i].  When the free pages run out, the entries without a page
- * are -1, the row ends before the first of them, and KDA_DEVERR_EXHAUSTED is set; a length outside
+ * are -1, the row ends before the first of them, and KDA_DEVERR_EXHAUSTED is set (such a row has no place for
+ * the tokens that it lacks: a new one is not to be stored at its last place); a length outside
  * [0, max_pages * page_size], a negative grow or one that the table cannot hold, or a page outside the pool
  * is clamped (to an empty row, no growth, the table's end; no page) and sets KDA_DEVERR_PAGES.
  *   block_table     [rows_in, max_pages];  seq_lens [rows_in];  parent, grow [rows_out], grow may be NULL (0)

@@ -18,15 +18,19 @@
 // What bounds it is DRAM, once there is enough to read: one row of 1,048,573 tokens with 8 heads of 128 takes
 // 580 us (7.4 TB/s of reads), 64 rows of 213,000 tokens in all with 8 key-value heads 134 us (6.5 TB/s, the rest
 // is the first loads' latency, the joins and the second kernel, together about 12 us whatever the size).  With few
-// bytes that latency is all: 4.2 us for a row of 37 tokens.  With 16 and 32 query heads a key the products of
-// mma.sync begin to show (4.6 and 3.6 TB/s at 250 MB).
+// bytes that latency is all: 4.2 us for a row of 37 tokens whose table holds no more pages, 6.0 in a table of 1,024
+// pages, where the shares are searched and the second kernel is launched all the same.  With more query heads a key
+// the products begin to show: 32 rows of 8,192 tokens and two key-value heads (260 MB) take 47.9 us with 8 heads a key,
+// 50.5 with 16 and 68.1 with 32 (3.8 TB/s); above 32 the cache is read once for each block of 32.
 //
 // The products: with the tokens as the 16 rows of mma.m16n8k16 and the query heads as its 8 columns, both
 // products take the cache as the A operand straight from shared memory (K by ldmatrix, V by ldmatrix.trans)
-// and leave no padding at 8 heads.  A tcgen05 tile has 64 rows at least, its softmax sits behind a round trip
-// through tensor memory, and its operands want a layout that pages of any size do not have; at the reads' rate
-// the mma.sync form leaves the tensor pipe mostly idle up to 16 heads a key.  fp32 caches take the same path
-// with FFMA (two products in one instruction), since TF32's 11 bits would not keep fp32's precision.
+// and leave no padding at 8 heads.  tcgen05 could take 128 tokens as its rows and the heads as its columns just as
+// well, with the scores and weights on a round trip through tensor memory.  There is little to gain up to 16 heads a key
+// (the tensor pipe is busy for 14 % of the time at 4 heads, 25 % at 16, and the kernel waits for loads); at 32 and more
+// (36 %, with the second product done twice for the weights' two halves) it would be the way on, and is not built.  fp32
+// caches take the same path with FFMA (two products in one instruction), since TF32's 11 bits would not keep fp32's
+// precision; at 4 heads a key they are read at 6.5 TB/s, 16 heads a key on one key-value head run at 2.0.
 
 #include <cmath>
 #include <type_traits>
@@ -888,7 +892,9 @@ int64_t most_tiles(const AttnParams& p, int tile) {
     return seen < all ? seen : all;
 }
 
-// Whether each unit is done by one CTA, however long: no search for the shares, no pieces, no second kernel.  That
+// Whether each unit is done by one CTA, however long: no search for the shares, no pieces, no second kernel.  It is
+// decided from what the table and the window can hold, which the host knows, not from the lengths, which it does not: a
+// table allocated for longer rows takes the other way (64 rows of 128 tokens 15.9 us instead of 12.4).  That
 // pays where rows are short beside those: always up to four tiles (a row of 64 tokens 4.2 us instead of 6.0, of 256
 // 6.9 instead of 7.4, 48 rows of 256 with 8 heads 12.9 instead of 18.0), and up to eight where the units fill a
 // quarter of the GPU (48 rows of 512: 19.9 instead of 24.9, of 1 to 512: 10.3 instead of 12.0; but one row of 512: 9.7

@@ -12,9 +12,12 @@
 // fall together at the last score that is chosen) the group's logits are searched for the places with exactly that
 // score.  Rows that offer nothing (finished, no score) are not read.
 //
-// What it costs: 410 of 512 rows of 131,072 bf16 words (107 MB) take 28 us, of which the read at DRAM's rate
+// What it costs: 410 of 512 rows of 131,072 bf16 words (107 MB) take 27.5 us, of which the read at DRAM's rate
 // would be 16.  Issue slots are the rest (8 instructions a logit; a plain stream of loads, exponentials and
-// sums needs 4 and runs at DRAM's rate: the bound, the lists and the barriers around them are the rest), and 5 us of the second kernel, a chain of loads and small steps for each group.
+// sums needs 4 and runs at DRAM's rate: the bound, the lists and the barriers around them make up the others), and 5 us
+// of the second kernel, a chain of loads and small steps for each group.  As many fp32 rows (215 MB) take 42 us.  What
+// costs more: rows in which more words reach the first chunk's bound than the lists hold (behind a finite mask that
+// leaves a few words in all, 180 us), and the search for places, one CTA per group, up to 0.15 ms for each row of 131,072.
 
 #include <cmath>
 
@@ -749,9 +752,9 @@ __global__ void __launch_bounds__(BT) kda_beam_join_kernel(BeamParams p, int par
     }
 }
 
-// Parts of a row: so many that there are two CTAs per SM, as far as a row has chunks.  A part costs about as much as
-// three chunks on top of its own (its bound, its list, its joining), so more of them pay only where the GPU would
-// stay empty: 64 rows of 200,000 fp32 words take 23 us in 5 parts a row, 28 in 8 and 36 in 15.  The GPU's size is
+// Parts of a row: so many that there are two CTAs per SM, as far as a row has chunks.  Each has its bound, its list and
+// its joining on top of its chunks, so more of them pay only where the GPU would stay empty: 64 rows of 200,000 fp32
+// words (16 groups of 4) take 17.7 us in 5 parts a row, 19.4 in 8 and 20.8 in 15.  The GPU's size is
 // taken as 152 SMs, so that the workspace's size needs no device.
 template <typename T>
 int part_count(const int64_t rows, int V) {
