@@ -90,6 +90,7 @@ typedef enum {
 #define KDA_DEVERR_PAGES 0x20u      /* a page number outside the pool, or a length the table cannot hold */
 #define KDA_DEVERR_EXHAUSTED 0x40u  /* kda_cache_fork: fewer free pages than the new rows need  */
 #define KDA_DEVERR_PARENT 0x80u     /* a parent outside [-1, rows)                              */
+#define KDA_DEVERR_TOKEN 0x100u     /* a token outside [-1, V)                                  */
 
 /*
  * Bytes of device workspace kda_prefill needs for this problem (0 is a valid
@@ -525,6 +526,112 @@ KDA_API kda_status kda_cache_compact(const int32_t* block_table, int32_t rows, i
                                      const int32_t* ref_count, int32_t num_pages, int32_t* block_table_out,
                                      int32_t* ref_count_out, int32_t* page_map, const kda_pool* pools,
                                      int32_t num_pools, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * A prompt's way through a hybrid stack's full-attention layers, and the scores of its tokens.  New tokens of
+ * several sequences lie packed one after the other, as kda_prefill takes them: sequence b has tokens
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1, at positions seq_lens[b] - n_b .. seq_lens[b] - 1 of its cache (n_b of
+ * them, seq_lens[b] with the new ones, as kda_cache_fork returns it for grow = n_b).  A chunk may be a whole
+ * prompt, a part of one behind what the cache holds already, or one token.  cu_seqlens[0] = 0; cu_seqlens[B] may be
+ * less than T, and outputs of the tokens behind it are left as they were.  A sequence whose borders are not
+ * 0 <= cu_seqlens[b] <= cu_seqlens[b + 1] <= T counts as empty and sets KDA_DEVERR_CU_SEQLENS.
+ * ------------------------------------------------------------------------------------------------ */
+
+#define KDA_ROTARY_HALF 0         /* pairs (x_i, x_{i + rotary_dim / 2}) */
+#define KDA_ROTARY_INTERLEAVED 1  /* pairs (x_2i, x_{2i + 1})            */
+
+/*
+ * Rotary positions: in the first rotary_dim places of every head of q and k, pair i of token t becomes
+ *
+ *     rotary_scale * (a cos - b sin, b cos + a sin),   angle = positions[t] * inv_freq[i]
+ *
+ * and the rest of the head is copied.  inverse != 0 turns by minus the angle, with the same scale: the gradient
+ * of the outputs becomes that of the inputs.  Angles are exact to 2^-32 of a turn for every 32-bit position.
+ *
+ *   q, q_out   [T, H_q, d] dtype dt, token t at q + t * q_stride (elements); likewise k, k_out with H_kv heads.
+ *              k NULL: only q.  q_out may be q and k_out may be k, with the same strides; no other overlap.
+ *   positions  [T] int32;  inv_freq [rotary_dim / 2] float64, finite, radians a position (how long contexts
+ *              stretch them is the caller's choice), NULL with rotary_dim = 0
+ * Sizes: d in {16, 64, 128}; rotary_dim even, 0 .. d; H_q * d and H_kv * d at most a token's stride, all of a
+ * token's elements below 2^30.  Alignment: an element; 16 bytes, with strides to match, is the fast way.
+ */
+KDA_API kda_status kda_rotary(const void* q, const void* k, const int32_t* positions, const double* inv_freq,
+                              int32_t T, int32_t H_q, int32_t H_kv, int32_t d, int32_t rotary_dim, int64_t q_stride,
+                              int64_t k_stride, kda_dtype dt, int32_t layout, float rotary_scale, int32_t inverse,
+                              void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * Stores a packed batch's new keys and values into their pages, keys rotated by their positions in the cache on
+ * the way (rotary_dim = 0: as they are).  Queries, if given, are rotated likewise into q_out.
+ *   q        NULL, or [T, H_q, d] at q + t * q_stride, and q_out [T, H_q, d] (may be q, with the same stride)
+ *   k, v     [T, H_kv, d] dtype dt at k + t * k_stride, v + t * v_stride
+ *   k_pages, v_pages, block_table [B, max_pages], seq_lens [B]  as for kda_attention_decode
+ *   cu_seqlens [B + 1] int32;  inv_freq, layout, rotary_scale  as for kda_rotary
+ * No two new tokens may have the same place, and k, v may not overlap the pools.  A token without a place (a length
+ * outside [0, max_pages * page_size] or less than n_b, a page outside [0, num_pages)) is not stored and sets
+ * KDA_DEVERR_PAGES.  Limits as for kda_rotary and kda_attention_decode.
+ */
+KDA_API kda_status kda_cache_append(const void* q, const void* k, const void* v, void* k_pages, void* v_pages,
+                                    const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_seqlens,
+                                    const double* inv_freq, int32_t B, int32_t T, int32_t H_q, int32_t H_kv, int32_t d,
+                                    int32_t rotary_dim, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                    int32_t num_pages, int32_t page_size, int32_t max_pages, int64_t k_page_stride,
+                                    int64_t v_page_stride, kda_dtype dt, int32_t layout, float rotary_scale,
+                                    void* q_out, int64_t q_out_stride, void* stream);
+
+/*
+ * Attention of a packed batch's new tokens over a paged cache that holds their keys and values already
+ * (kda_cache_append): as kda_attention_decode with the token's own position in the place of the last one.  The token
+ * at position i sees the tokens j <= i, and with window > 0 of those only j > i - window and j < sinks.  A token that
+ * sees nothing gives o = 0 and lse = -inf.  What a token does not see is not used for it, whatever it holds.
+ *   q          [T, H_q, d] dtype dt;  o likewise;  lse [T, H_q] float32 or NULL
+ *   cu_seqlens [B + 1] int32;  the other arguments as for kda_attention_decode
+ *   workspace  kda_attention_prefill_workspace_size(...) bytes: partial results of units whose keys are split over
+ *              several CTAs, joined in a fixed order (two calls give the same bits)
+ * bf16: scores, sums and outputs are float32 until the end; weights are rounded to bf16 for the second product, and
+ * their sum is that of the rounded ones.  Limits as for kda_attention_decode; T * H_q * d / d below 2^31.
+ * A length outside [0, max_pages * page_size] counts as 0, new tokens before position 0 see nothing, and a page outside
+ * [0, num_pages) reads as zeros; all set KDA_DEVERR_PAGES.
+ */
+KDA_API size_t kda_attention_prefill_workspace_size(int32_t B, int32_t T, int32_t H_q, int32_t H_kv, int32_t d,
+                                                    kda_dtype dt);
+KDA_API kda_status kda_attention_prefill(const void* q, const void* k_pages, const void* v_pages,
+                                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_seqlens,
+                                         int32_t B, int32_t T, int32_t H_q, int32_t H_kv, int32_t d, int32_t num_pages,
+                                         int32_t page_size, int32_t max_pages, int64_t k_page_stride,
+                                         int64_t v_page_stride, kda_dtype dt, float scale, int32_t window,
+                                         int32_t sinks, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/*
+ * Log probabilities of given tokens under rows of logits, in float32:
+ *
+ *     lse_t = m + log sum_v exp(x_tv - m),   logp_t = x_ty - lse_t,   entropy_t = -sum_v p_tv log p_tv
+ *
+ * and the `top` likeliest words of each row, the lowest word first among equal logits (a NaN counts as -inf there).
+ * A small -logp or entropy keeps its relative precision.  A row with nothing above -inf gives lse and every log
+ * probability -inf and entropy 0; a row with a NaN or +inf gives NaNs.
+ *   logits    [T, V] dtype dt, row t at logits + t * row_stride (elements, >= V)
+ *   tokens    [T] int32, -1: none (logp_t = 0); one outside [-1, V) counts as -1 and sets KDA_DEVERR_TOKEN
+ *   logp [T];  lse [T] or NULL;  entropy [T] or NULL
+ *   top_logp, top_token [T, top] float32 and int32, best first; NULL with top = 0
+ * top <= KDA_LOGPROBS_MAX_TOP and <= V; V at most 2^31 - 2^14, T at most 2^28 - 1 (KDA_ERR_TOO_LARGE above).
+ */
+#define KDA_LOGPROBS_MAX_TOP 32
+KDA_API kda_status kda_token_logprobs(const void* logits, int64_t row_stride, const int32_t* tokens, int32_t T,
+                                      int32_t V, kda_dtype dt, int32_t top, float* logp, float* lse, float* entropy,
+                                      float* top_logp, int32_t* top_token, void* stream);
+
+/*
+ * Their gradient: grad_tv = grad_logp_t (1[v = y_t] - p_tv) - grad_entropy_t p_tv (log p_tv + entropy_t), with p from
+ * the lse that kda_token_logprobs gave.  A token outside [0, V) has no grad_logp; a row whose lse is -inf no gradient.
+ *   grad  [T, V] dtype dt, row t at grad + t * grad_stride; may be logits, with the same stride
+ *   entropy and grad_entropy [T] float32, or both NULL
+ */
+KDA_API kda_status kda_token_logprobs_backward(const void* logits, int64_t row_stride, const int32_t* tokens,
+                                               const float* lse, const float* entropy, const float* grad_logp,
+                                               const float* grad_entropy, int32_t T, int32_t V, kda_dtype dt,
+                                               void* grad, int64_t grad_stride, void* stream);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's error

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -22,7 +23,10 @@ KDA_NOALLOC_MAX_SEQS = 16384
 KDA_DTYPE_F32, KDA_DTYPE_BF16 = 0, 1
 KDA_DEVERR_CU_SEQLENS, KDA_DEVERR_STATE_IDX = 0x1, 0x2
 KDA_DEVERR_PAGES, KDA_DEVERR_EXHAUSTED, KDA_DEVERR_PARENT = 0x20, 0x40, 0x80
+KDA_DEVERR_TOKEN = 0x100
 KDA_BEAM_MAX_K, KDA_MAX_POOLS, KDA_FORK_MAX_ROWS = 32, 8, 8192
+KDA_ROTARY_HALF, KDA_ROTARY_INTERLEAVED = 0, 1
+KDA_LOGPROBS_MAX_TOP = 32
 
 class PrefillOptions(ctypes.Structure):
     """kda_prefill_options (include/kda.h)."""
@@ -83,6 +87,17 @@ SIGNATURES = {
                                       _vp, _i32, _vp, _sz, _vp]),
     "kda_cache_compact_workspace_size": (_sz, [_i32]),
     "kda_cache_compact": (ctypes.c_int, [_vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "kda_rotary": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i64, _i64, ctypes.c_int, _i32, _f32,
+                                  _i32, _vp, _i64, _vp, _i64, _vp]),
+    "kda_cache_append": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                        _i64, _i64, _i64, _i32, _i32, _i32, _i64, _i64, ctypes.c_int, _i32, _f32, _vp,
+                                        _i64, _vp]),
+    "kda_attention_prefill_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
+    "kda_attention_prefill": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                             _i32, _i64, _i64, ctypes.c_int, _f32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "kda_token_logprobs": (ctypes.c_int, [_vp, _i64, _vp, _i32, _i32, ctypes.c_int, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "kda_token_logprobs_backward": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, ctypes.c_int, _vp,
+                                                   _i64, _vp]),
     "kda_get_device_error": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
@@ -716,6 +731,308 @@ def kda_cache_compact(block_table, ref_count, *, pools=(), block_table_out=None,
     if rc != KDA_OK:
         raise KdaError("kda_cache_compact", rc)
     return block_table_out, ref_count_out, page_map
+
+
+# ---- a prompt's way through the full-attention layers, and the scores of its tokens ----
+_F64 = torch.float64
+_LAYOUTS = {"half": KDA_ROTARY_HALF, "interleaved": KDA_ROTARY_INTERLEAVED}
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _elsewhere(dev, stream):
+    """Whether a call has to change the current device or stream before it allocates and launches."""
+    return stream is not None or dev != _current_device()
+
+
+def _there(dev, stream, call, *args, **kwargs):
+    """The call on its tensors' device and with `stream` as the current one (see _in_stream)."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(*args, **kwargs)
+        return _in_stream(stream, call, *args, **kwargs)
+
+
+def _heads(name, t, T, d, dtype, dev):
+    """A tensor [T, H, d] whose tokens are contiguous, as a slice of a fused projection is: (H, elements a token)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, 'heads', d)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected CUDA device {dev}")
+    H = t.shape[1]
+    step, head, inner = t.stride()
+    if inner != 1 and d > 1 or head != d and H > 1 or step < H * d and T > 1:
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return H, max(step, H * d)
+
+
+def _frequencies(inv_freq, dev):
+    if inv_freq is None:
+        return 0, None
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq: shape {tuple(inv_freq.shape)}, expected [rotary_dim / 2]")
+    _check_at("inv_freq", inv_freq, _F64, inv_freq.shape, dev)
+    n = 2 * inv_freq.shape[0]
+    return n, inv_freq.data_ptr() if n else None
+
+
+def _layout(layout):
+    code = _LAYOUTS.get(layout)
+    if code is None:
+        raise ValueError(f"layout {layout!r}, expected 'half' or 'interleaved'")
+    return code
+
+
+def kda_rotary(q, k, positions, inv_freq, *, layout: str = "half", rotary_scale: float = 1.0, inverse: bool = False,
+               q_out=None, k_out=None, stream=None):
+    """Rotary positions of queries and keys; returns (q_out, k_out).
+
+    q [T, H_q, d], k [T, H_kv, d] or None (bf16 or f32; slices of a fused projection will do), positions [T] int32,
+    inv_freq [rotary_dim / 2] f64: radians a position, for the pairs (x_i, x_{i + rotary_dim / 2}) (layout "half")
+    or (x_2i, x_{2i + 1}) ("interleaved") of every head; the rest of a head is copied.  rotary_scale multiplies
+    the rotated part (stretched contexts).  inverse=True turns back with the same scale: the gradient of q, k from
+    those of the outputs.  q_out, k_out may be q and k.
+    """
+    dev = _cuda_index("q", q)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, kda_rotary, q, k, positions, inv_freq, layout=layout, rotary_scale=rotary_scale,
+                      inverse=inverse, q_out=q_out, k_out=k_out)
+    if q.dim() != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [T, H_q, d]")
+    T, d, dt = q.shape[0], q.shape[2], q.dtype
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    Hq, qs = _heads("q", q, T, d, dt, dev)
+    _check_at("positions", positions, _I32, (T,), dev)
+    rot, freq = _frequencies(inv_freq, dev)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+    if q_out.shape != q.shape:
+        raise ValueError(f"q_out: shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+    qos = _heads("q_out", q_out, T, d, dt, dev)[1]
+    Hkv = ks = kos = 0
+    if k is not None:
+        Hkv, ks = _heads("k", k, T, d, dt, dev)
+        if k_out is None:
+            k_out = torch.empty((T, Hkv, d), dtype=dt, device=q.device)
+        if k_out.shape != k.shape:
+            raise ValueError(f"k_out: shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
+        kos = _heads("k_out", k_out, T, d, dt, dev)[1]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    rc = (_LIB or load()).kda_rotary(q.data_ptr(), None if k is None else k.data_ptr(), positions.data_ptr(), freq, T, Hq,
+                                     Hkv, d, rot, qs, ks, code, _layout(layout), rotary_scale, int(inverse),
+                                     q_out.data_ptr(), qos, None if k is None else k_out.data_ptr(), kos,
+                                     _current_raw_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_rotary", rc)
+    return q_out, k_out
+
+
+def kda_cache_append(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, *, q=None, inv_freq=None,
+                     layout: str = "half", rotary_scale: float = 1.0, q_out=None, stream=None):
+    """Stores a packed batch's new keys and values in their pages; returns q_out (None without q).
+
+    k, v [T, H_kv, d] (bf16 or f32; slices of a fused projection will do): the tokens cu_seqlens[b] .. cu_seqlens[b + 1]
+    - 1 go to positions seq_lens[b] - n_b .. seq_lens[b] - 1 of row b of block_table [B, M] (pools as for
+    kda_attention_decode; seq_lens with the new tokens, as kda_cache_fork returns it).  With inv_freq (see kda_rotary)
+    keys, and queries q [T, H_q, d], are rotated by those positions; q_out may be q.
+    """
+    dev = _cuda_index("k", k)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, kda_cache_append, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, q=q,
+                      inv_freq=inv_freq, layout=layout, rotary_scale=rotary_scale, q_out=q_out)
+    if k.dim() != 3:
+        raise ValueError(f"k: shape {tuple(k.shape)}, expected [T, H_kv, d]")
+    T, d, dt = k.shape[0], k.shape[2], k.dtype
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    Hkv, ks = _heads("k", k, T, d, dt, dev)
+    if v.shape != k.shape:
+        raise ValueError(f"v: shape {tuple(v.shape)}, expected {tuple(k.shape)}")
+    vs = _heads("v", v, T, d, dt, dev)[1]
+    if k_pages.dim() != 4:
+        raise ValueError(f"k_pages: shape {tuple(k_pages.shape)}, expected [P, H_kv, page_size, d]")
+    P, _, ps, _ = k_pages.shape
+    shape = (P, Hkv, ps, d)
+    kps = _page_stride("k_pages", k_pages, shape, dt, dev)
+    vps = _page_stride("v_pages", v_pages, shape, dt, dev)
+    B, M = block_table.shape
+    _check_at("block_table", block_table, _I32, (B, M), dev)
+    _check_at("seq_lens", seq_lens, _I32, (B,), dev)
+    _check_at("cu_seqlens", cu_seqlens, _I32, (B + 1,), dev)
+    rot, freq = _frequencies(inv_freq, dev)
+    Hq = qs = qos = 0
+    if q is not None:
+        Hq, qs = _heads("q", q, T, d, dt, dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+        if q_out.shape != q.shape:
+            raise ValueError(f"q_out: shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+        qos = _heads("q_out", q_out, T, d, dt, dev)[1]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rc = (_LIB or load()).kda_cache_append(
+        None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), freq, B, T, Hq, Hkv, d, rot, qs, ks, vs, P, ps,
+        M, kps, vps, code, _layout(layout), rotary_scale, None if q is None else q_out.data_ptr(), qos,
+        _current_raw_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_cache_append", rc)
+    return q_out
+
+
+def kda_attention_prefill_workspace_size(B: int, T: int, H_q: int, H_kv: int, d: int,
+                                         dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(load().kda_attention_prefill_workspace_size(B, T, H_q, H_kv, d, _dt(dtype)))
+
+
+def kda_attention_prefill(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, *, scale: float = 1.0, window: int = 0,
+                          sinks: int = 0, o=None, lse=None, workspace=None, stream=None):
+    """Attention of a packed batch's new tokens over a paged cache that holds them already; returns o [T, H_q, d].
+
+    q [T, H_q, d] (bf16 or f32), tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of row b at positions seq_lens[b] - n_b ..
+    seq_lens[b] - 1: whole prompts, chunks behind what the cache holds, single tokens.  Each sees the tokens up to
+    itself; with window > 0 only the last `window` of them and the first `sinks`.  Pools and table as for
+    kda_attention_decode.  lse [T, H_q] f32, if given, receives the log of the softmax's sum.  Tokens behind
+    cu_seqlens[B] are left as they were.
+    """
+    dev = _cuda_index("q", q)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, kda_attention_prefill, q, k_pages, v_pages, block_table, seq_lens, cu_seqlens,
+                      scale=scale, window=window, sinks=sinks, o=o, lse=lse, workspace=workspace)
+    L = _LIB or load()
+    if q.dim() != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [T, H_q, d]")
+    if k_pages.dim() != 4:
+        raise ValueError(f"k_pages: shape {tuple(k_pages.shape)}, expected [P, H_kv, page_size, d]")
+    T, Hq, d = q.shape
+    shape = P, Hkv, ps, _ = k_pages.shape
+    dt = q.dtype
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    if d != shape[3]:
+        raise ValueError(f"k_pages: shape {tuple(shape)}, expected a last dimension of {d}")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    ks = _page_stride("k_pages", k_pages, shape, dt, dev)
+    vs = _page_stride("v_pages", v_pages, shape, dt, dev)
+    B, M = block_table.shape
+    _check_at("block_table", block_table, _I32, (B, M), dev)
+    _check_at("seq_lens", seq_lens, _I32, (B,), dev)
+    _check_at("cu_seqlens", cu_seqlens, _I32, (B + 1,), dev)
+    out_lse = None
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _check_at("o", o, dt, (T, Hq, d), dev)
+    if lse is not None:
+        _check_at("lse", lse, _F32, (T, Hq), dev)
+        out_lse = lse.data_ptr()
+    if workspace is None:
+        workspace = _new_workspace(L.kda_attention_prefill_workspace_size(B, T, Hq, Hkv, d, code), dev)
+    wbytes = _workspace(workspace, dev)
+    rc = L.kda_attention_prefill(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                                 seq_lens.data_ptr(), cu_seqlens.data_ptr(), B, T, Hq, Hkv, d, P, ps, M, ks, vs, code,
+                                 scale, window, sinks, o.data_ptr(), out_lse, workspace.data_ptr(), wbytes,
+                                 _current_raw_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_attention_prefill", rc)
+    return o
+
+
+class TokenLogprobs(NamedTuple):
+    """What kda_token_logprobs returns."""
+    logp: torch.Tensor                        # [T] f32
+    lse: torch.Tensor                         # [T] f32
+    entropy: Optional[torch.Tensor]           # [T] f32, or None
+    top_logp: torch.Tensor                    # [T, top] f32
+    top_token: torch.Tensor                   # [T, top] int32
+
+
+def _rows(name, t, dev):
+    """A matrix [T, V] with contiguous rows: (T, V, elements a row)."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, V]")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected CUDA device {dev}")
+    T, V = t.shape
+    step, inner = t.stride()
+    if inner != 1 and V > 1 or step < V and T > 1:
+        raise ValueError(f"{name}: a row must be contiguous")
+    return T, V, max(step, V)
+
+
+def kda_token_logprobs(logits, tokens, *, top: int = 0, entropy: bool = False, stream=None) -> TokenLogprobs:
+    """Log probabilities of given tokens under rows of logits; returns a TokenLogprobs.
+
+    logits [T, V] (bf16 or f32; rows may lie further apart than V), tokens [T] int32, -1: none, which gives 0.  lse is the
+    log of a row's sum, entropy (if asked for) that of its distribution, top_logp and top_token its `top` likeliest words
+    (at most 32), best first, the lowest word first among equal logits.
+    """
+    dev = _cuda_index("logits", logits)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, kda_token_logprobs, logits, tokens, top=top, entropy=entropy)
+    T, V, step = _rows("logits", logits, dev)
+    code = _DTYPES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {logits.dtype}")
+    _check_at("tokens", tokens, _I32, (T,), dev)
+    on = dict(dtype=_F32, device=logits.device)
+    out = torch.empty((3 if entropy else 2, T), **on)
+    logp, lse, H = out[0], out[1], out[2] if entropy else None
+    best = torch.empty((T, max(top, 0)), **on)
+    word = torch.empty((T, max(top, 0)), dtype=_I32, device=logits.device)
+    rc = (_LIB or load()).kda_token_logprobs(logits.data_ptr(), step, tokens.data_ptr(), T, V, code, top, logp.data_ptr(),
+                                             lse.data_ptr(), H.data_ptr() if entropy else None,
+                                             best.data_ptr() if top else None, word.data_ptr() if top else None,
+                                             _current_raw_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_token_logprobs", rc)
+    return TokenLogprobs(logp, lse, H, best, word)
+
+
+def kda_token_logprobs_backward(logits, tokens, lse, grad_logp, *, entropy=None, grad_entropy=None, grad=None,
+                                stream=None):
+    """The gradient of kda_token_logprobs with regard to the logits; returns grad [T, V] of the logits' type.
+
+    lse [T] f32 as kda_token_logprobs gave it, grad_logp [T] f32; entropy and grad_entropy [T] f32 go together.  grad may
+    be logits (in their place).
+    """
+    dev = _cuda_index("logits", logits)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, kda_token_logprobs_backward, logits, tokens, lse, grad_logp, entropy=entropy,
+                      grad_entropy=grad_entropy, grad=grad)
+    T, V, step = _rows("logits", logits, dev)
+    code = _DTYPES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {logits.dtype}")
+    _check_at("tokens", tokens, _I32, (T,), dev)
+    _check_at("lse", lse, _F32, (T,), dev)
+    _check_at("grad_logp", grad_logp, _F32, (T,), dev)
+    if (entropy is None) != (grad_entropy is None):
+        raise ValueError("entropy and grad_entropy go together")
+    if entropy is not None:
+        _check_at("entropy", entropy, _F32, (T,), dev)
+        _check_at("grad_entropy", grad_entropy, _F32, (T,), dev)
+    if grad is None:
+        grad = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+    if grad.dtype is not logits.dtype:
+        raise TypeError(f"grad: dtype {grad.dtype}, expected {logits.dtype}")
+    if grad.shape != logits.shape:
+        raise ValueError(f"grad: shape {tuple(grad.shape)}, expected {tuple(logits.shape)}")
+    gstep = _rows("grad", grad, dev)[2]
+    rc = (_LIB or load()).kda_token_logprobs_backward(
+        logits.data_ptr(), step, tokens.data_ptr(), lse.data_ptr(), None if entropy is None else entropy.data_ptr(),
+        grad_logp.data_ptr(), None if entropy is None else grad_entropy.data_ptr(), T, V, code, grad.data_ptr(), gstep,
+        _current_raw_stream(dev))
+    if rc != KDA_OK:
+        raise KdaError("kda_token_logprobs_backward", rc)
+    return grad
 
 
 def kda_get_device_error(stream=None) -> int:

@@ -1,0 +1,297 @@
+// How the work of attention over chunks of new tokens is cut into shares, for its kernels.
+//
+// The G = H_q / H_kv query heads of a key-value head read the same keys, so the rows of a product are (token, head)
+// pairs: row r of a sequence's key-value head is token r / G with head r % G.  BM of them are a unit; its work is the
+// tiles of BN tokens of the cache that any of its rows sees.  All units' tiles, numbered one after the other (all units
+// of a head, then the next head), are cut into equal shares, one per CTA, so that one long prompt, many short ones
+// and a few tokens behind a long context fill the GPU alike.  Every CTA works its own share out from cu_seqlens and
+// seq_lens on the device: a few microseconds at the most, nothing launched for it, nothing for the host to know.
+// A unit that a border between shares cuts leaves pieces (maximum, sum and unscaled outputs), which a second
+// kernel joins in the order of the CTAs: no atomics, the same bits on every call.
+#pragma once
+
+#include "kda_prompt.cuh"
+
+namespace kda {
+namespace {
+
+// t / page_size for 0 <= t < 2^31, as a multiplication.
+struct PageDiv {
+    uint32_t magic;
+    int32_t shift;
+};
+inline PageDiv page_div(int32_t page_size) {
+    PageDiv d{0u, 0};
+    while ((2ll << d.shift) < page_size) ++d.shift;
+    if (page_size > 1) d.magic = (uint32_t)((1ull << (32 + d.shift)) / page_size + 1);
+    return d;
+}
+__device__ __forceinline__ int page_of(const PageDiv& d, int t) {
+    return d.magic ? (int)(__umulhi((uint32_t)t, d.magic) >> d.shift) : t;
+}
+
+struct ChunkPlan {
+    int32_t group;               // query heads of a key-value head
+    int32_t BM;                  // rows of a unit
+    int32_t BN;                  // tokens of a tile
+    int32_t whole;               // CTA i does unit i, and nothing is left to join
+    PageDiv div;
+};
+
+// One sequence of the batch: its new tokens and its length, 0 where they are not valid.
+struct Seq {
+    int32_t start, n, len;
+    bool bad_cu, bad_len;
+};
+__device__ __forceinline__ Seq seq_of(const ChunkParams& p, int b) {
+    const int a = __ldg(p.cu + b), e = __ldg(p.cu + b + 1), len = __ldg(p.lens + b);
+    Seq s;
+    s.bad_cu = a < 0 || e < a || e > p.T || (b == 0 && a != 0);
+    s.bad_len = len < 0 || (int64_t)len > (int64_t)p.max_pages * p.page_size;
+    s.start = a;
+    s.n = s.bad_cu ? 0 : e - a;
+    s.len = s.bad_len ? 0 : len;
+    s.bad_len = s.bad_len || s.n > s.len;     // new tokens before the first place: they see nothing
+    return s;
+}
+__device__ __forceinline__ int units_of(const ChunkPlan& f, const Seq& s) {
+    return (int)(((int64_t)s.n * f.group + f.BM - 1) / f.BM);
+}
+
+// A unit's rows and tiles.  Tile i < near covers tokens from i * BN, a later one from (i + skip) * BN.
+struct Unit {
+    int32_t rows;                // of BM
+    int32_t pos0;                // position of the first row's token
+    int32_t end;                 // tokens that any row sees end here
+    int32_t near, skip, tiles;   // at least one tile, also where no row sees anything
+};
+__device__ __forceinline__ Unit unit_of(const ChunkParams& p, const ChunkPlan& f, const Seq& s, int m) {
+    Unit u;
+    const int64_t row0 = (int64_t)m * f.BM, all = (int64_t)s.n * f.group;
+    u.rows = (int)(all - row0 < f.BM ? all - row0 : f.BM);
+    const int t0 = (int)(row0 / f.group), t1 = (int)((row0 + u.rows - 1) / f.group);
+    u.pos0 = s.len - s.n + t0;
+    const int last = s.len - s.n + t1;
+    u.end = last < 0 ? 0 : last + 1;
+    const int all_tiles = (u.end + f.BN - 1) / f.BN;
+    u.near = 0, u.skip = 0;
+    if (p.window > 0) {
+        const int first = u.pos0 >= p.window ? u.pos0 + 1 - p.window : 0;      // of the window of the first row
+        const int w0 = first / f.BN;
+        const int sinks = p.sinks < u.end ? p.sinks : u.end;
+        u.near = sinks > 0 ? (sinks - 1) / f.BN + 1 : 0;
+        if (u.near > w0) u.near = w0;
+        u.skip = w0 - u.near;
+    }
+    u.tiles = all_tiles - u.skip;
+    if (u.tiles < 1) u.tiles = 1;
+    return u;
+}
+__device__ __forceinline__ int tile_start(const ChunkPlan& f, const Unit& u, int i) {
+    return (i < u.near ? i : i + u.skip) * f.BN;
+}
+__device__ __forceinline__ int64_t cost_of(const ChunkParams& p, const ChunkPlan& f, const Seq& s, int m) {
+    return f.whole ? 1 : unit_of(p, f, s, m).tiles;
+}
+
+// What a CTA does: `left` flat tiles, from tile `tile` of unit m of sequence b and key-value head h on.
+struct Share {
+    int64_t left;                // tiles; with whole shares, 1
+    int64_t start;               // flat number of the first
+    int64_t all;                 // tiles of all shares
+    int32_t ctas;                // shares
+    int32_t h, b, m, tile;
+};
+
+constexpr int MIN_SHARE = 2;                  // tiles: pieces of one would cost more to join than they save
+
+// Works the CTA's share out; all its NW warps.  `sums` holds NW numbers, `out` the result, both in shared memory.
+template <int NW>
+__device__ __forceinline__ void plan_share(const ChunkParams& p, const ChunkPlan& f, int64_t* sums, Share* out, int cta, int grid) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned all = 0xFFFFFFFFu;
+    const int b0 = (int)((int64_t)p.B * warp / NW), b1 = (int)((int64_t)p.B * (warp + 1) / NW);
+    auto add = [&](int64_t x) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(all, x, o);
+        return x;
+    };
+    // 32 sequences at a time: a lane sums a sequence's units where they are few, the warp one sequence after the other else
+    int64_t mine = 0;
+    for (int g = b0; g < b1; g += 32) {
+        Seq s{0, 0, 0, false, false};
+        if (g + lane < b1) s = seq_of(p, g + lane);
+        if (cta == 0 && (s.bad_cu || s.bad_len))
+            atomicOr(p.err, (s.bad_cu ? KDA_DEVERR_CU_SEQLENS : 0u) | (s.bad_len ? KDA_DEVERR_PAGES : 0u));
+        const int units = units_of(f, s);
+        if (!__any_sync(all, units > 32)) {
+            for (int m = 0; m < units; ++m) mine += cost_of(p, f, s, m);
+        } else {
+            for (int i = 0; i < 32 && g + i < b1; ++i) {
+                Seq x{__shfl_sync(all, s.start, i), __shfl_sync(all, s.n, i), __shfl_sync(all, s.len, i), false, false};
+                const int n = units_of(f, x);
+                for (int m = lane; m < n; m += 32) mine += cost_of(p, f, x, m);
+            }
+        }
+    }
+    mine = add(mine);
+    if (lane == 0) sums[warp] = mine;
+    if (tid == 0) out->left = 0;
+    __syncthreads();
+    int64_t head = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) before += sums[w];
+        head += sums[w];
+    }
+    const int64_t total = head * p.Hkv;
+    const int64_t most = f.whole ? total : (total + MIN_SHARE - 1) / MIN_SHARE;
+    const int ctas = (int)(most < grid ? most : grid);
+    if (cta >= ctas) {                        // (no work at all: ctas = 0)
+        __syncthreads();
+        return;
+    }
+    const int64_t x0 = total * cta / ctas, x1 = total * (cta + 1) / ctas;
+    const int h = (int)(x0 / head);
+    int64_t at = x0 - h * head - before;      // tiles of this warp's sequences before the share
+    if (at >= 0 && at < sums[warp]) {
+        bool found = false;
+        for (int g = b0; g < b1 && !found; g += 32) {
+            Seq s{0, 0, 0, false, false};
+            if (g + lane < b1) s = seq_of(p, g + lane);
+            for (int i = 0; i < 32 && g + i < b1 && !found; ++i) {
+                Seq x{__shfl_sync(all, s.start, i), __shfl_sync(all, s.n, i), __shfl_sync(all, s.len, i), false, false};
+                const int n = units_of(f, x);
+                for (int m = 0; m < n && !found; m += 32) {
+                    const int64_t c = m + lane < n ? cost_of(p, f, x, m + lane) : 0;
+                    int64_t to = c;           // tiles up to and with this lane's unit
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int64_t y = __shfl_up_sync(all, to, o);
+                        if (lane >= o) to += y;
+                    }
+                    const int64_t batch = __shfl_sync(all, to, 31);
+                    if (at < batch) {
+                        found = true;
+                        if (at >= to - c && at < to)
+                            *out = Share{x1 - x0, x0, total, ctas, h, g + i, m + lane, f.whole ? 0 : (int)(at - (to - c))};
+                    } else {
+                        at -= batch;
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// Steps through the units of a share; every warp that takes part has its own.
+struct Walk {
+    int32_t h, b, m;
+    Seq s;
+    Unit u;
+    __device__ __forceinline__ void begin(const ChunkParams& p, const ChunkPlan& f, const Share& share) {
+        h = share.h, b = share.b, m = share.m;
+        s = seq_of(p, b);
+        u = unit_of(p, f, s, m);
+    }
+    __device__ __forceinline__ void next(const ChunkParams& p, const ChunkPlan& f) {
+        if (++m >= units_of(f, s)) {
+            m = 0;
+            do {
+                if (++b == p.B) b = 0, ++h;
+                s = seq_of(p, b);
+            } while (units_of(f, s) == 0);
+        }
+        u = unit_of(p, f, s, m);
+    }
+};
+
+// A unit whose first tiles are in CTA `first`'s share and whose last ones in `last`'s; b = -1: none.
+struct ChunkRecord {
+    int32_t b, m, h, first, last, slot, pad[2];
+};
+// The share that flat tile x - 1 lies in.
+__device__ __forceinline__ int cta_before(const Share& s, int64_t x) { return (int)((x * s.ctas - 1) / s.all); }
+
+template <int D>
+__host__ __device__ constexpr int64_t piece_floats(int BM) { return (int64_t)BM * (D + 2); }
+
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr int JOIN_WARPS = 4;
+
+// Joins the pieces of a unit: a warp per row.  A piece is [BM][D] sums, then [BM] maxima (base 2) and [BM] sums.
+template <typename T, int D>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) kda_chunk_join_kernel(ChunkParams p, ChunkPlan f, int max_ctas) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const ChunkRecord r = reinterpret_cast<const ChunkRecord*>(p.workspace)[blockIdx.x];
+    if (r.b < 0) return;
+    const int lane = threadIdx.x & 31, row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5);
+    const Seq s = seq_of(p, r.b);
+    const int64_t flat = (int64_t)r.m * f.BM + row;
+    if (flat >= (int64_t)s.n * f.group) return;
+    const int64_t size = piece_floats<D>(f.BM);
+    const float* pieces = reinterpret_cast<const float*>(p.workspace + max_ctas * sizeof(ChunkRecord));
+    const int n = r.last - r.first + 1;
+    auto piece = [&](int i) { return pieces + ((int64_t)(r.first + i) * 2 + (i == 0 ? r.slot : 0)) * size; };
+    float top = -INFINITY;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, piece(i)[(int64_t)f.BM * D + row]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+    constexpr int PER = D >= 128 ? 4 : D / 32 > 0 ? D / 32 : 1;           // columns of a lane
+    float sum = 0.f, o[PER] = {};
+    for (int i = 0; i < n; ++i) {
+        const float* x = piece(i);
+        const float w = ex2_approx(x[(int64_t)f.BM * D + row] - base);
+        sum += w * x[(int64_t)f.BM * (D + 1) + row];
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+            if (lane + 32 * c < D) {
+                const float v = x[(int64_t)row * D + lane + 32 * c];
+                o[c] = fmaf(w, v, o[c]);
+            }
+    }
+    const int t = (int)(flat / f.group), head = r.h * f.group + (int)(flat - (int64_t)t * f.group);
+    const int64_t at = (int64_t)(s.start + t) * p.Hq + head;
+#pragma unroll
+    for (int c = 0; c < PER; ++c)
+        if (lane + 32 * c < D) put(static_cast<T*>(p.o) + at * D + lane + 32 * c, sum == 0.f ? 0.f : o[c] / sum);
+    if (p.lse && lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <typename T, int D>
+cudaError_t launch_join(const ChunkParams& p, const ChunkPlan& f, int grid, int max_ctas, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(grid, f.BM / JOIN_WARPS);
+    cfg.blockDim = dim3(JOIN_WARPS * 32);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kda_chunk_join_kernel<T, D>, p, f, max_ctas);
+}
+
+// Tiles of a unit, whatever the lengths: as many as its table's pages hold, or as the window and the first tokens touch.
+inline int64_t most_tiles(const ChunkParams& p, const ChunkPlan& f) {
+    const int64_t all = ((int64_t)p.max_pages * p.page_size + f.BN - 1) / f.BN;
+    if (p.window == 0) return all > 1 ? all : 1;
+    const int64_t seen = ((int64_t)p.sinks + f.BN - 1) / f.BN + ((int64_t)p.window + (f.BM - 1) / f.group + f.BN - 1) / f.BN + 1;
+    return seen < all ? seen : all > 1 ? all : 1;
+}
+inline int64_t most_units(const ChunkParams& p, const ChunkPlan& f) {
+    return ((int64_t)p.T * f.group / f.BM + (p.B < p.T ? p.B : p.T)) * p.Hkv;
+}
+
+}  // namespace
+}  // namespace kda

@@ -1,0 +1,439 @@
+// Log probabilities of given tokens, with entropy and top alternatives, and their gradient.
+//
+//   m = max x_j,  r = sum over the others of exp(x_j - m):   lse = m + log1p(r),  log p_y = (x_y - m) - log1p(r)
+//   H = -sum p_j log p_j = log1p(r) - sum exp(x_j - m) (x_j - m) / (1 + r)
+//   d / dx_j = g (1[j = y] - p_j) - h p_j (log p_j + H)      for g = d log p_y, h = dH
+//
+// The largest logit stays out of the sum r at every level (lane, warp, CTA, cluster), so that a word with nearly all
+// the probability keeps its small -log p to fp32's relative precision: 1 + r would round it to 6e-8.
+//
+// One pass over the logits.  A row, or its parts on the CTAs of a cluster where there are few rows, streams through
+// registers in chunks, the next one under way while one is summed; a warp's lanes share their maximum, so that a rescale
+// is a branch that all of them take or none.  The best words are gathered on the way: the first chunk's k-th best thread
+// maximum bounds which of its words can be among the best (at most k threads hold any), and from then on only words
+// above the k-th best so far are written down, a few hundred a row.  Rows that rise (more than the list holds) are gone
+// through once more with the bound brought up to date after every chunk.  Nothing depends on the order of the atomics:
+// they place candidates in a list whose entries are then ranked.
+#include <cooperative_groups.h>
+
+#include "kda_prompt.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace kda {
+namespace {
+
+constexpr int NT = 256, NW = NT / 32;
+constexpr int LOADS = 4;                      // 16-byte loads of a thread and chunk
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr int MAX_TOP = KDA_LOGPROBS_MAX_TOP, MAX_CLUSTER = 8;
+
+template <typename T>
+struct Elems {
+    static constexpr int W = 16 / sizeof(T), EPT = LOADS * W, CHUNK = NT * EPT;
+    static constexpr int LIST = MAX_TOP + MAX_TOP * EPT;      // kept ones, and all words of `top` threads
+};
+
+__device__ __forceinline__ void unpack(const uint4& r, float* x, __nv_bfloat16) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const uint4& r, float* x, float) {
+    x[0] = __uint_as_float(r.x), x[1] = __uint_as_float(r.y), x[2] = __uint_as_float(r.z), x[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float value(const float* p) { return *p; }
+__device__ __forceinline__ uint32_t bits16(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
+
+// Vector v of a row that begins `off` elements into its first 16 bytes; what lies outside the row reads as `fill` bits.
+__device__ __forceinline__ uint4 load_vec(const __nv_bfloat16* row, int64_t e0, int V) {
+    if (e0 >= 0 && e0 + 8 <= V) return __ldcs(reinterpret_cast<const uint4*>(row + e0));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t a = e0 + 2 * i, b = a + 1;
+        const uint32_t lo = a >= 0 && a < V ? bits16(row[a]) : 0xFF80u, hi = b >= 0 && b < V ? bits16(row[b]) : 0xFF80u;
+        w[i] = lo | hi << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 load_vec(const float* row, int64_t e0, int V) {
+    if (e0 >= 0 && e0 + 4 <= V) return __ldcs(reinterpret_cast<const uint4*>(row + e0));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = e0 + i >= 0 && e0 + i < V ? __float_as_uint(row[e0 + i]) : 0xFF800000u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// A word's place in the order: larger values first, then lower words.  A value that is not a number counts as -inf.
+__device__ __forceinline__ unsigned long long key_of(float x, int word) {
+    x = x != x ? -INFINITY : x + 0.f;
+    const uint32_t b = __float_as_uint(x), o = b & 0x80000000u ? ~b : b | 0x80000000u;
+    return (unsigned long long)o << 32 | (0xFFFFFFFFu - (uint32_t)word);
+}
+__device__ __forceinline__ float key_value(unsigned long long k) {
+    const uint32_t o = (uint32_t)(k >> 32);
+    return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ int key_word(unsigned long long k) { return (int)(0xFFFFFFFFu - (uint32_t)k); }
+
+// Sums of a set of words: reference m, r without one word that has it, and sum exp(x - m) (x - m) log2 e.
+struct Sums {
+    float m, r, t;
+};
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
+    const Sums &hi = a.m >= b.m ? a : b, &lo = a.m >= b.m ? b : a;
+    if (lo.m == -INFINITY) return Sums{hi.m, hi.r + lo.r, hi.t};           // nothing there, or a NaN to hand on
+    const float d = (lo.m - hi.m) * LOG2E, f = exp2_approx(d), all = 1.f + lo.r;
+    return Sums{hi.m, hi.r + all * f, hi.t + (f > 0.f ? f * (lo.t + all * d) : 0.f)};
+}
+
+template <int LIST>
+struct Shared {
+    unsigned long long list[LIST];
+    unsigned long long best[NT];              // thread maxima; at the end the best of all CTAs
+    unsigned long long out[MAX_TOP];
+    unsigned long long tau, bound;            // bound: key of the k-th best so far, 0 with fewer
+    Sums sums[NW];
+    Sums cta;
+    int count, overflow, found;
+};
+
+// Ranks the list and keeps its best `top` in out, in order; all threads.
+template <int LIST>
+__device__ __forceinline__ void rank_list(Shared<LIST>& sm, int top, int tid) {
+    const int n = sm.count;
+    for (int e = tid; e < n; e += NT) {
+        const unsigned long long k = sm.list[e];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += sm.list[j] > k;
+        if (rank < top) sm.out[rank] = k;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        sm.found = n < top ? n : top;
+        sm.bound = n >= top ? sm.out[top - 1] : 0ull;
+    }
+    __syncthreads();
+}
+
+// Takes a chunk's words into the list, whatever they are, and leaves the best `top` so far in list and out; all threads.
+template <int EPT, int W, int LIST>
+__device__ __forceinline__ void absorb(Shared<LIST>& sm, const float (&x)[EPT], int64_t e0, int V, int top, int tid) {
+    const unsigned long long bound = sm.bound;
+    unsigned long long best = 0;
+    auto key = [&](int i) -> unsigned long long {
+        const int64_t word = e0 + (int64_t)(i / W) * NT * W + i % W;
+        return word >= 0 && word < V ? key_of(x[i], (int)word) : 0ull;
+    };
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+        const unsigned long long k = key(i);
+        if (k > bound && k > best) best = k;
+    }
+    sm.best[tid] = best;
+    if (tid == 0) sm.tau = 1;
+    __syncthreads();
+    if (best) {
+        int rank = 0;
+        for (int j = 0; j < NT; ++j) rank += sm.best[j] > best;
+        if (rank == top - 1) sm.tau = best;
+    }
+    __syncthreads();
+    const unsigned long long tau = sm.tau;
+    if (best >= tau) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            const unsigned long long k = key(i);
+            if (k >= tau && k > bound) sm.list[atomicAdd(&sm.count, 1)] = k;
+        }
+    }
+    __syncthreads();
+    rank_list(sm, top, tid);
+    if (tid < sm.found) sm.list[tid] = sm.out[tid];
+    if (tid == 0) sm.count = sm.found;
+    __syncthreads();
+}
+
+template <typename T, bool TOP, bool ENTROPY>
+__global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, int cluster) {
+    using E = Elems<T>;
+    constexpr int W = E::W, EPT = E::EPT, CHUNK = E::CHUNK;
+    __shared__ Shared<TOP ? E::LIST : 1> sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x / cluster;
+    const int part = blockIdx.x % cluster;
+    const T* x0 = static_cast<const T*>(p.logits) + row * p.row_stride;
+    const int off = (int)(reinterpret_cast<uintptr_t>(x0) / sizeof(T) % W);
+    const int chunks = (int)(((int64_t)p.V + off + CHUNK - 1) / CHUNK);
+    const int c0 = (int)((int64_t)chunks * part / cluster), c1 = (int)((int64_t)chunks * (part + 1) / cluster);
+    if (tid == 0) sm.count = 0, sm.overflow = 0, sm.found = 0, sm.bound = 0;
+    __syncthreads();
+
+    uint4 raw[LOADS];
+    auto first = [&](int c) { return (int64_t)c * CHUNK + tid * W - off; };
+    auto load = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) raw[j] = load_vec(x0, first(c) + j * (NT * W), p.V);
+    };
+    float m = -INFINITY, r = 0.f, t = 0.f, least = 0.f;
+    bool own = false;                         // this lane holds the word that has m and stays out of r
+    if (c0 < c1) load(c0);
+    for (int c = c0; c < c1; ++c) {
+        float x[EPT];
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) unpack(raw[j], x + j * W, T());
+        if (c + 1 < c1) load(c + 1);
+        float top_x = x[0];
+#pragma unroll
+        for (int i = 1; i < EPT; ++i) top_x = fmaxf(top_x, x[i]);
+        if constexpr (TOP) {
+            if (c == c0) {
+                absorb<EPT, W>(sm, x, first(c), p.V, p.top, tid);
+                least = sm.bound ? key_value(sm.bound) : -INFINITY;
+            } else if (top_x > least) {       // a later word that equals the k-th best is behind it
+#pragma unroll
+                for (int i = 0; i < EPT; ++i)
+                    if (x[i] > least) {
+                        const int at = atomicAdd(&sm.count, 1);
+                        if (at < E::LIST)
+                            sm.list[at] = key_of(x[i], (int)(first(c) + (int64_t)(i / W) * NT * W + i % W));
+                        else
+                            sm.overflow = 1;
+                    }
+            }
+        }
+        if (__any_sync(0xFFFFFFFFu, top_x > m)) {
+            float all = top_x;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xFFFFFFFFu, all, o));
+            if (m != -INFINITY) {
+                const float d = (m - all) * LOG2E, f = exp2_approx(d), sum = r + (own ? 1.f : 0.f);
+                if constexpr (ENTROPY) t = f > 0.f ? f * (t + sum * d) : 0.f;
+                r = sum * f;
+            }
+            m = all;
+            own = lane == __ffs(__ballot_sync(0xFFFFFFFFu, top_x == all)) - 1;
+            if (own) {
+                bool out = false;
+#pragma unroll
+                for (int i = 0; i < EPT; ++i)
+                    if (!out && x[i] == all) {
+                        x[i] = -INFINITY;
+                        out = true;
+                    }
+            }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        float ra = 0.f, rb = 0.f, ta = 0.f, tb = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPT; i += 2) {
+            float ya = (x[i] - base) * LOG2E, yb = (x[i + 1] - base) * LOG2E;
+            if constexpr (ENTROPY) ya = max_nan(ya, -1000.f), yb = max_nan(yb, -1000.f);
+            const float ea = exp2_approx(ya), eb = exp2_approx(yb);
+            ra += ea, rb += eb;
+            if constexpr (ENTROPY) ta = fmaf(ea, ya, ta), tb = fmaf(eb, yb, tb);
+        }
+        r += ra + rb;
+        if constexpr (ENTROPY) t += ta + tb;
+    }
+
+    // ---- the warp's sums (its lanes have one m), the CTA's ----
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
+        if constexpr (ENTROPY) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    }
+    if (lane == 0) sm.sums[warp] = Sums{m, r, t};
+    __syncthreads();
+    if constexpr (TOP) {
+        if (sm.overflow) {                    // once more, with the bound brought up to date after every chunk
+            __syncthreads();
+            if (tid == 0) sm.count = 0, sm.found = 0, sm.bound = 0;
+            __syncthreads();
+            for (int c = c0; c < c1; ++c) {
+                float x[EPT];
+                load(c);
+#pragma unroll
+                for (int j = 0; j < LOADS; ++j) unpack(raw[j], x + j * W, T());
+                absorb<EPT, W>(sm, x, first(c), p.V, p.top, tid);
+            }
+        } else if (c1 > c0 + 1) {
+            rank_list(sm, p.top, tid);
+        }
+    }
+    if (tid == 0) {
+        Sums s = sm.sums[0];
+        for (int w = 1; w < NW; ++w) s = join(s, sm.sums[w]);
+        sm.cta = s;
+    }
+    __syncthreads();
+
+    // ---- the row's ----
+    Sums s = sm.cta;
+    if (cluster > 1) {
+        cg::cluster_group group = cg::this_cluster();
+        group.sync();
+        if (part == 0) {
+            for (int i = 1; i < cluster; ++i) s = join(s, *group.map_shared_rank(&sm.cta, i));
+            if constexpr (TOP) {
+                const int i = tid / MAX_TOP, e = tid % MAX_TOP;           // MAX_CLUSTER * MAX_TOP keys: one a thread
+                unsigned long long k = 0;
+                if (i < cluster && e < *group.map_shared_rank(&sm.found, i)) k = group.map_shared_rank(sm.out, i)[e];
+                sm.best[tid] = k;
+                __syncthreads();
+                int rank = 0;
+                for (int j = 0; j < NT; ++j) rank += sm.best[j] > k;
+                if (k && rank < p.top) sm.list[rank] = k;
+                __syncthreads();
+                if (tid < p.top) sm.out[tid] = sm.list[tid];
+                __syncthreads();
+            }
+        }
+        group.sync();
+        if (part) return;
+    }
+    const float log_r = log1pf(s.r);
+    const bool bad = s.r != s.r || s.m == INFINITY, empty = s.m == -INFINITY && !bad;
+    const float nan = __int_as_float(0x7FC00000);
+    auto log_p = [&](float x) { return bad ? nan : empty ? -INFINITY : (x - s.m) - log_r; };
+    if (tid == 0) {
+        const int y = p.tokens[row];
+        if (y < -1 || y >= p.V) atomicOr(p.err, KDA_DEVERR_TOKEN);
+        p.logp[row] = y >= 0 && y < p.V ? log_p(value(x0 + y)) : 0.f;
+        if (p.lse) p.lse[row] = bad ? nan : empty ? -INFINITY : s.m + log_r;
+        if constexpr (ENTROPY) p.entropy[row] = bad ? nan : empty ? 0.f : log_r - LN2 * s.t / (1.f + s.r);
+    }
+    if constexpr (TOP) {
+        if (tid < p.top) {
+            const unsigned long long k = sm.out[tid];
+            p.top_logp[row * p.top + tid] = log_p(key_value(k));
+            p.top_token[row * p.top + tid] = key_word(k);
+        }
+    }
+}
+
+template <typename T, bool TOP, bool ENTROPY>
+cudaError_t launch_forward(const LogprobParams& p, cudaStream_t s) {
+    using E = Elems<T>;
+    static DeviceSetup done;
+    int sms = 0;
+    const void* kernel = reinterpret_cast<const void*>(kda_logprobs_kernel<T, TOP, ENTROPY>);
+    cudaError_t e = device_setup(done, kernel, 0, &sms);
+    if (e != cudaSuccess) return e;
+    // A row's parts go to a cluster where the rows alone would leave SMs idle and a part still has a chunk.
+    int cluster = 1;
+    while (cluster < MAX_CLUSTER && (int64_t)p.T * cluster * 2 <= 2 * sms && (int64_t)E::CHUNK * cluster < p.V) cluster *= 2;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)(p.T * cluster));
+    cfg.blockDim = dim3(NT);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kda_logprobs_kernel<T, TOP, ENTROPY>, p, cluster);
+}
+
+template <typename T>
+cudaError_t launch_any(const LogprobParams& p, cudaStream_t s) {
+    if (p.top > 0) return p.entropy ? launch_forward<T, true, true>(p, s) : launch_forward<T, true, false>(p, s);
+    return p.entropy ? launch_forward<T, false, true>(p, s) : launch_forward<T, false, false>(p, s);
+}
+
+// ------------------------------------------------------------------------------------------------
+// the gradient
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ void store(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ uint4 pack(const float* x, __nv_bfloat16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack(const float* x, float) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+
+// LOADS vectors a thread; a CTA does `rows` whole rows of one chunk each, or one chunk of a row.  Each vector is read
+// before it is written, by the same thread, so the gradient may take the logits' place.
+template <typename T>
+__global__ void __launch_bounds__(NT) kda_logprobs_backward_kernel(LogprobGradParams p, int chunks) {
+    using E = Elems<T>;
+    constexpr int W = E::W;
+    const int64_t row = blockIdx.x / chunks;
+    const int c = blockIdx.x % chunks;
+    const T* x0 = static_cast<const T*>(p.logits) + row * p.row_stride;
+    T* g0 = static_cast<T*>(p.grad) + row * p.grad_stride;
+    const int off = (int)(reinterpret_cast<uintptr_t>(x0) / sizeof(T) % W);
+    const bool together = reinterpret_cast<uintptr_t>(x0) % 16 == reinterpret_cast<uintptr_t>(g0) % 16;
+    const int64_t e0 = (int64_t)c * E::CHUNK + threadIdx.x * W - off;
+    uint4 raw[LOADS];
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) raw[j] = load_vec(x0, e0 + j * (NT * W), p.V);
+    const int y0 = __ldg(p.tokens + row), y = y0 >= 0 && y0 < p.V ? y0 : -1;
+    const float lse = __ldg(p.lse + row), g = y >= 0 ? __ldg(p.grad_logp + row) : 0.f;
+    const float h = p.grad_entropy ? __ldg(p.grad_entropy + row) : 0.f, H = p.grad_entropy ? __ldg(p.entropy + row) : 0.f;
+    const bool empty = lse == -INFINITY;      // nothing above -inf: no word has a gradient
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+        const int64_t e = e0 + j * (NT * W);
+        if (e >= p.V) break;
+        float x[W];
+        unpack(raw[j], x, T());
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float lp = x[i] - lse, q = exp2_approx(lp * LOG2E);
+            float v = q == 0.f ? 0.f : -q * fmaf(h, lp + H, g);
+            if (e + i == y) v += g;
+            x[i] = empty ? 0.f : v;
+        }
+        if (together && e >= 0 && e + W <= p.V) {
+            __stcs(reinterpret_cast<uint4*>(g0 + e), pack(x, T()));
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                if (e + i >= 0 && e + i < p.V) store(g0 + e + i, x[i]);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_backward(const LogprobGradParams& p, cudaStream_t s) {
+    const int64_t chunks = ((int64_t)p.V + Elems<T>::W - 1 + Elems<T>::CHUNK - 1) / Elems<T>::CHUNK;
+    kda_logprobs_backward_kernel<T><<<(unsigned)(p.T * chunks), NT, 0, s>>>(p, (int)chunks);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(const LogprobParams& p, kda_dtype dt, cudaStream_t s) {
+    return dt == KDA_DTYPE_BF16 ? launch_any<__nv_bfloat16>(p, s) : launch_any<float>(p, s);
+}
+
+cudaError_t launch_token_logprobs_backward(const LogprobGradParams& p, kda_dtype dt, cudaStream_t s) {
+    return dt == KDA_DTYPE_BF16 ? launch_backward<__nv_bfloat16>(p, s) : launch_backward<float>(p, s);
+}
+
+}  // namespace kda

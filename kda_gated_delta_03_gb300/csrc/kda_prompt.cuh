@@ -1,0 +1,85 @@
+// Internal interfaces of the operators that bring prompts into a hybrid stack and score their tokens (rotary positions,
+// new tokens into cache pages, attention of chunks over a paged cache, token log probabilities) between their C-ABI
+// host code and their kernels.
+#pragma once
+
+#include "kda_serve.cuh"
+
+namespace kda {
+
+// Rotary positions, and tokens into cache pages.  Without `append` a token's position is positions[t] and keys go
+// to k_out; with it, a packed batch's tokens go to their places in the pages.  Strides in elements.
+struct RotaryParams {
+    const void* q;               // token t at q + t * q_stride, [Hq, d]; nullptr with Hq = 0
+    const void* k;
+    const void* v;               // append only
+    const int32_t* positions;    // [T]; rotary only
+    const double* inv_freq;      // [rot / 2]
+    void* q_out;                 // may be q
+    void* k_out;                 // rotary only; may be k
+    void* k_pages;               // append only
+    void* v_pages;
+    const int32_t* table;        // [B, max_pages]; append only
+    const int32_t* lens;         // [B], new tokens included
+    const int32_t* cu;           // [B + 1]
+    unsigned* err;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride, k_page_stride, v_page_stride;
+    int32_t B, T, Hq, Hkv, d, rot;
+    int32_t num_pages, page_size, max_pages;
+    int32_t interleaved;
+    int32_t append;              // tokens of a packed batch, into pages
+    float scale;                 // of the rotated part
+    float sign;                  // -1: turned back (the gradient)
+};
+cudaError_t launch_rotary(const RotaryParams& p, kda_dtype dt, cudaStream_t s);
+
+// Attention of chunks of new tokens, already in their pages.
+struct ChunkParams {
+    const void* q;               // [T, Hq, d]
+    const void* k_pages;         // page p at k_pages + p * k_stride elements, [Hkv, page_size, d]
+    const void* v_pages;
+    const int32_t* table;        // [B, max_pages]
+    const int32_t* lens;         // [B], new tokens included
+    const int32_t* cu;           // [B + 1]
+    void* o;                     // [T, Hq, d]
+    float* lse;                  // [T, Hq], or nullptr
+    unsigned char* workspace;
+    unsigned* err;
+    int64_t k_stride, v_stride;
+    int32_t B, T, Hq, Hkv, d;
+    int32_t num_pages, page_size, max_pages;
+    int32_t window;              // 0: every token up to the query's own
+    int32_t sinks;
+    float scale;
+};
+size_t chunk_workspace(int32_t d, kda_dtype dt);
+cudaError_t launch_attention_prefill(const ChunkParams& p, kda_dtype dt, cudaStream_t s);
+
+struct LogprobParams {
+    const void* logits;          // row r at logits + r * row_stride elements
+    const int32_t* tokens;       // [T], -1: none
+    float* logp;                 // [T]
+    float* lse;                  // [T], or nullptr
+    float* entropy;              // [T], or nullptr
+    float* top_logp;             // [T, top], or nullptr with top = 0
+    int32_t* top_token;          // [T, top]
+    unsigned* err;
+    int64_t row_stride;
+    int32_t T, V, top;
+};
+cudaError_t launch_token_logprobs(const LogprobParams& p, kda_dtype dt, cudaStream_t s);
+
+struct LogprobGradParams {
+    const void* logits;
+    const int32_t* tokens;
+    const float* lse;            // [T]
+    const float* entropy;        // [T], or nullptr
+    const float* grad_logp;      // [T]
+    const float* grad_entropy;   // [T], or nullptr
+    void* grad;                  // row r at grad + r * grad_stride elements; may be logits
+    int64_t row_stride, grad_stride;
+    int32_t T, V;
+};
+cudaError_t launch_token_logprobs_backward(const LogprobGradParams& p, kda_dtype dt, cudaStream_t s);
+
+}  // namespace kda
