@@ -234,21 +234,21 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
 
 }  // namespace
 
-size_t chunk_workspace(int32_t d, kda_dtype) {
-    return MAX_CTAS * (sizeof(ChunkRecord) + 2 * (size_t)BM * (d + 2) * sizeof(float));
+size_t chunk_workspace(int32_t d, kda_dtype dt) {
+    const size_t cores = MAX_CTAS * (sizeof(ChunkRecord) + 2 * (size_t)BM * (d + 2) * sizeof(float));
+    const size_t tensor = dt == KDA_DTYPE_BF16 && d >= 64 ? chunk_tc_workspace(d) : 0;
+    return cores > tensor ? cores : tensor;
 }
 
-namespace {
-template <typename T>
-cudaError_t launch_d(const ChunkParams& p, cudaStream_t s) {
-    if (p.d == 16) return launch<T, 16>(p, s);
-    if (p.d == 64) return launch<T, 64>(p, s);
-    return launch<T, 128>(p, s);
-}
-}  // namespace
-
+// fp32 stays here: TF32's 11 bits would not keep its precision.  So do bf16 heads of 16, whose rows of 32 bytes leave a
+// TMA box of an odd number of tokens off the 128-byte places it has to start at, and tables without a page.
 cudaError_t launch_attention_prefill(const ChunkParams& p, kda_dtype dt, cudaStream_t s) {
-    return dt == KDA_DTYPE_BF16 ? launch_d<__nv_bfloat16>(p, s) : launch_d<float>(p, s);
+    if (dt == KDA_DTYPE_BF16)
+        return p.d >= 64 && p.max_pages > 0 ? launch_attention_prefill_tc(p, s)
+               : p.d == 16                  ? launch<__nv_bfloat16, 16>(p, s)
+               : p.d == 64                  ? launch<__nv_bfloat16, 64>(p, s)
+                                            : launch<__nv_bfloat16, 128>(p, s);
+    return p.d == 16 ? launch<float, 16>(p, s) : p.d == 64 ? launch<float, 64>(p, s) : launch<float, 128>(p, s);
 }
 
 }  // namespace kda

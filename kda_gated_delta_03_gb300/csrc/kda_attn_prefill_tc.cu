@@ -1,0 +1,629 @@
+// Attention of chunks of new tokens over a paged key-value cache, on the tensor cores (bf16, d = 64 and 128).
+//
+//   s_tj = scale * q_t . k_j over the visible j,   o_t = sum_j exp(s_tj - m_t) v_j / sum_j exp(s_tj - m_t)
+//
+// One persistent CTA per SM.  A unit is 256 (token, head) rows of a sequence and key-value head, as two blocks of 128: the
+// rows of tcgen05 products S = Q K^T (operands in shared memory) and O += P V (P in tensor memory, where S was).  Two
+// groups of four warps hold a row a thread: while one group takes the exponentials of its block, the tensor core works for
+// the other.  One warp issues the products, one brings the pages in by TMA (boxes of the largest run of tokens that divides
+// a page and fits the tile, through a table lookup each), and one looks after tiles that some row sees in part.
+//
+// Exponents are in base 2.  The reference that they are taken against only moves when a row's maximum has grown by
+// more than 2^8, which rescales O in tensor memory; weights up to 256 lose nothing in bf16.  Weights are rounded to bf16
+// for the second product: half a step of 2^-8 each, independent of each other, so n equal weights bring an error of
+// 1.1e-3 / sqrt(n) of a value, below the output's own rounding.  The row's sum is taken before that, in fp32: it gives lse.
+//
+// What is masked must not be multiplied: its weight is 0, and 0 * inf would be a NaN.  In tiles that are not open to every
+// row the helper warp clears the values behind the last token, and takes values that are not finite out of the tile; the
+// rows that see them add them when the unit is done, one by one.
+//
+// Every wait is bounded (KDA_DEVERR_TIMEOUT on expiry).
+#include "kda_tc_util.cuh"
+
+#include "kda_chunk_plan.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int TILE = 128;                     // rows of a block and of a tile
+constexpr int UNIT = 2 * TILE;
+constexpr int WARPS = 12, THREADS = WARPS * 32;               // the last one only makes the third group whole
+constexpr int MMA_WARP = 8, LOAD_WARP = 9, HELP_WARP = 10;
+constexpr int TC_MAX_CTAS = 160;              // of the main kernel, whatever the GPU (bounds the workspace)
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float SLACK = 8.f;                  // the reference moves when the maximum has grown by 2^SLACK
+
+template <int D>
+struct TcLayout {
+    static constexpr int HALVES = D / 64;                      // 128-byte columns of a tile
+    static constexpr int HALF = TILE * 128;                    // bytes of one
+    static constexpr int BLOCK = HALVES * HALF;                // bytes of a block of Q, K or V
+    static constexpr int STAGES = D == 128 ? 4 : 8;            // K and V in turn
+    static constexpr int Q = 0, KV = 2 * BLOCK, BYTES = KV + STAGES * BLOCK;
+    static constexpr int DYNAMIC = BYTES + 1024;               // aligned to 1 KiB inside
+    static constexpr uint32_t S = 0, O = 2 * TILE;             // columns of tensor memory: S0, S1, O0, O1
+};
+
+// Tokens of a tile whose value is not finite, taken out of it.  A unit of 256 rows has at most 14 tiles that
+// some row sees in part: tiles hold 65 tokens or more, the rows' own tokens touch 5 of them, the lower borders of their
+// windows 5, the border of the first tokens 1.
+constexpr int MAX_ODD = 16;
+struct OddTiles {
+    int32_t n;
+    int32_t start[MAX_ODD];
+    uint32_t rows[MAX_ODD][4];
+};
+
+struct Barriers {
+    uint64_t full[8], empty[8];               // of stages
+    uint64_t fixed[4];                        // a V stage's partly seen tile is ready for the product
+    uint64_t q[2];                            // of row blocks: queries in shared memory
+    uint64_t s[2], p[2], pv[2];               // scores, weights, a tile's product done
+    uint64_t run;                             // a run's products done
+    uint64_t done;                            // all products done
+};
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(mbar)
+        : "memory");
+}
+// The product with its A operand in tensor memory.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+// Descriptor of 16 tokens (K) by D columns (N) of a V tile: N contiguous, 128-byte swizzle, 64 columns HALF bytes from the
+// next ones, 8 tokens 1 KiB from the next ones.
+__device__ __forceinline__ uint64_t desc_v(uint32_t addr, uint32_t half) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((half >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+// 32 columns of this thread's lane of tensor memory, on their way until tmem_wait32 has been called for them.
+__device__ __forceinline__ void tmem_fetch32(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait32(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]),
+                   "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]),
+                   "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 x) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
+    return x;
+}
+
+// Whether every row of the unit sees every token of the tile.
+__device__ __forceinline__ bool open_tile(const ChunkParams& p, const ChunkPlan& f, const Unit& u, int last, int j0) {
+    const int64_t end = (int64_t)j0 + f.BN;
+    return end - 1 <= u.pos0 && (p.window == 0 || (int64_t)j0 > (int64_t)last - p.window || end <= p.sinks);
+}
+__device__ __forceinline__ int last_pos(const ChunkPlan& f, const Walk& w) {
+    return w.s.len - w.s.n + (int)(((int64_t)w.m * f.BM + w.u.rows - 1) / f.group);
+}
+
+// The weight of token j for a row, against the row's reference: for the few tokens taken out of a tile.
+template <int D>
+__device__ __noinline__ float weight_of(const ChunkParams& p, const __nv_bfloat16* q, const __nv_bfloat16* k, float scale2, float base) {
+    float s = 0.f;
+    for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), s);
+    return ex2_approx(s * scale2 - base);
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using L = TcLayout<D>;
+    extern __shared__ unsigned char raw[];
+    __shared__ Barriers bar;
+    __shared__ OddTiles odd[4];
+    __shared__ int64_t sums[WARPS];
+    __shared__ Share share;
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int abort_flag;
+    unsigned char* sm = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
+    const uint32_t sm_q = saddr(sm) + L::Q, sm_kv = saddr(sm) + L::KV;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x, grid = gridDim.x;
+    ChunkRecord* records = reinterpret_cast<ChunkRecord*>(p.workspace);
+
+    if (tid == 0) {
+        auto init = [](uint64_t* b, int n) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(n) : "memory"); };
+        for (int i = 0; i < L::STAGES; ++i) init(&bar.full[i], 1), init(&bar.empty[i], i % 2 ? 2 : 1);
+        for (int i = 0; i < 4; ++i) init(&bar.fixed[i], 1);
+        for (int i = 0; i < 2; ++i) init(&bar.q[i], 4), init(&bar.s[i], 1), init(&bar.p[i], 4), init(&bar.pv[i], 1);
+        init(&bar.run, 1), init(&bar.done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        abort_flag = 0;
+        if (!f.whole) records[cta].b = -1;
+    }
+    if (warp == MMA_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_base)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (f.BN < TILE) {                        // rows that no copy ever fills
+        for (int i = tid; i < L::STAGES * (L::BLOCK / 16); i += THREADS) st_shared16(sm_kv + i * 16, make_uint4(0, 0, 0, 0));
+        fence_async_smem();
+    }
+    plan_share<WARPS>(p, f, sums, &share, cta, grid);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    auto fail = [&]() {
+        atomicOr(p.err, KDA_DEVERR_TIMEOUT);
+        abort_flag = 1;
+    };
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+        if (!mbar_wait(saddr(b), parity & 1u)) fail();
+        return abort_flag == 0;
+    };
+    const bool work = share.left > 0;
+    // A run: the share's tiles of one unit.  Every role steps through the same ones.
+    Walk w{};
+    int64_t left = share.left;
+    int tile = share.tile, run = 0;
+    auto tiles_here = [&]() { return f.whole ? w.u.tiles : (int)(left < w.u.tiles - tile ? left : w.u.tiles - tile); };
+    auto step = [&](int count) {              // to the next run, if there is one
+        left -= f.whole ? 1 : count;
+        ++run;
+        tile = 0;
+        if (left > 0) w.next(p, f);
+        return left > 0;
+    };
+    if (work) w.begin(p, f, share);
+    // Registers go from the warps that move data to those that hold rows: 2 x 208 + 88 = 3 x 168, what the launch has.
+    if (warp < MMA_WARP) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if (work) {
+        // ---------------- softmax: a row a thread ----------------
+        const int blk = warp >> 2, r = tid;   // rows 0..127 and 128..255 of the unit
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+        const uint32_t t_s = tmem + lanes + L::S + blk * TILE, t_o = tmem + lanes + L::O + blk * D;
+        const float scale2 = fmaxf(fabsf(p.scale) * LOG2E, 1e-37f);       // positive: 0 * -inf must not be met
+        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;            // the sign goes into the queries
+        float* pieces = f.whole ? nullptr : reinterpret_cast<float*>(p.workspace + TC_MAX_CTAS * sizeof(ChunkRecord));
+        uint32_t ns = 0;                      // tiles of this block so far
+        bool ok = true, first_unit = true;
+        do {
+            const int count = tiles_here(), last = last_pos(f, w);
+            const bool mine = r < w.u.rows, active = blk * TILE < w.u.rows;
+            const int64_t flat = (int64_t)w.m * UNIT + r;
+            const int t = (int)(flat / f.group), head = w.h * f.group + (int)(flat - (int64_t)t * f.group);
+            const int64_t at = ((int64_t)w.s.start + t) * p.Hq + head;
+            const int pos = mine ? max(w.s.len - w.s.n + t, -1) : -1;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + at * D;
+            if (active) {
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (mine) {
+                        x = __ldg(reinterpret_cast<const uint4*>(q) + c);
+                        x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
+                    }
+                    const int row = r & (TILE - 1);
+                    st_shared16(sm_q + blk * L::BLOCK + (c >> 3) * L::HALF + row * 128 + (((c & 7) ^ (row & 7)) << 4), x);
+                }
+                fence_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) arrive(&bar.q[blk]);
+            float m = -INFINITY, ref = -INFINITY, l = 0.f;
+            bool part = false;                // the helper has looked at a tile of this run
+            if (active) {
+                for (int it = tile; it < tile + count && ok; ++it, ++ns) {
+                    const int j0 = tile_start(f, w.u, it);
+                    ok = wait(&bar.s[blk], ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    __syncwarp();
+                    // Two passes over S, 32 columns at a time with the next ones on their way: the whole row would
+                    // take 128 registers.
+                    const bool open = open_tile(p, f, w.u, last, j0), masked = f.BN < TILE || !open;
+                    part = part || !open;
+                    const int hi = min(pos - j0, f.BN - 1);
+                    const int lo = p.window ? max(pos - p.window, j0 - 1) - j0 : -1;
+                    const int near = p.window ? p.sinks - j0 : 0;
+                    float s[2][32];
+                    auto hide = [&](int c, float (&x)[32]) {
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] = c + i <= hi && (c + i > lo || c + i < near) ? x[i] : -INFINITY;
+                        }
+                    };
+                    tmem_fetch32(t_s, s[0]);
+                    float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < TILE; c += 32) {
+                        float (&x)[32] = s[c / 32 & 1];
+                        tmem_wait32(x);
+                        tmem_fetch32(t_s + (c + 32) % TILE, s[(c / 32 + 1) & 1]);
+                        hide(c, x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+                    }
+                    m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    const bool move = (m - ref) * scale2 > SLACK;          // (NaN with nothing seen so far: no)
+                    if (__any_sync(0xFFFFFFFFu, move)) {
+                        const float to = move ? m : ref;
+                        const float by = !move ? 1.f : ref == -INFINITY ? 0.f : ex2_approx((ref - to) * scale2);
+                        l *= by;
+                        if (it > tile) {
+                            ok = wait(&bar.pv[blk], ns - 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            __syncwarp();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                float o[32];
+                                tmem_ld32(t_o + c, o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] *= by;
+                                tmem_st32(t_o + c, o);
+                            }
+                        }
+                        ref = to;
+                    }
+                    const float base = ref == -INFINITY ? 0.f : ref * scale2;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < TILE; c += 32) {
+                        float (&x)[32] = s[c / 32 & 1];
+                        tmem_wait32(x);
+                        if (c + 32 < TILE) tmem_fetch32(t_s + c + 32, s[(c / 32 + 1) & 1]);
+                        hide(c, x);
+                        float w2[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float a = ex2_approx(fmaf(x[2 * i], scale2, -base)), b = ex2_approx(fmaf(x[2 * i + 1], scale2, -base));
+                            w2[i] = __uint_as_float(pack_bf16x2(a, b));
+                            sum[2 * (i & 1)] += a;
+                            sum[2 * (i & 1) + 1] += b;
+                        }
+                        tmem_st16(t_s + c / 2, w2);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(&bar.p[blk]);
+                }
+            }
+            // The second block waits for the whole run also where it has no rows, so that neither group gets ahead of the
+            // products by more than a run (a barrier's phases are told apart by one bit).
+            if (ok) ok = blk == 0 ? wait(&bar.pv[0], ns - 1) : wait(&bar.run, run);
+            if (!ok) break;
+            // ---- outputs, or a piece of them ----
+            const bool starts = tile == 0, ends = tile + count == w.u.tiles, complete = starts && ends;
+            if (active) {
+                tc_fence_after();
+                __syncwarp();
+                const OddTiles& list = odd[run & 3];
+                const float inv = l == 0.f ? 0.f : 1.f / l, base = ref == -INFINITY ? 0.f : ref * scale2;
+                float* piece = complete ? nullptr : pieces + ((int64_t)cta * 2 + (first_unit ? 0 : 1)) * piece_floats<D>(UNIT);
+                const int odd_tiles = part ? *const_cast<const volatile int32_t*>(&list.n) : 0;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(t_o + c, o);
+                    for (int e = 0; e < odd_tiles; ++e)        // rare: values that are not finite
+                        for (int x = 0; x < TILE; ++x) {
+                            const int j = list.start[e] + x;
+                            if (!(list.rows[e][x >> 5] >> (x & 31) & 1u) || j > pos || (p.window && j <= pos - p.window && j >= p.sinks)) continue;
+                            const int slot = page_of(f.div, j), page = __ldg(p.table + (int64_t)w.b * p.max_pages + slot);
+                            const int64_t off = ((int64_t)w.h * p.page_size + (j - slot * p.page_size)) * D;
+                            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k_pages) + page * p.k_stride + off;
+                            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_pages) + page * p.v_stride + off;
+                            const float y = weight_of<D>(p, q, k, p.scale < 0.f ? -scale2 : scale2, base);
+                            for (int i = 0; i < 32; ++i) o[i] = fmaf(y, __bfloat162float(v[c + i]), o[i]);
+                        }
+                    if (!mine) continue;
+                    if (complete) {
+                        uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + c);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            auto two = [&](int k) { return l == 0.f ? 0u : pack_bf16x2(o[i + k] * inv, o[i + k + 1] * inv); };
+                            to[i / 8] = make_uint4(two(0), two(2), two(4), two(6));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4*>(piece + r * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                }
+                if (mine) {
+                    if (!complete)
+                        piece[UNIT * D + r] = ref == -INFINITY ? -INFINITY : base, piece[UNIT * (D + 1) + r] = l;
+                    else if (p.lse)
+                        p.lse[at] = l == 0.f ? -INFINITY : (base + log2f(l)) * LN2;
+                }
+                tc_fence_before();            // the next unit's products overwrite O
+            }
+            if (tid == 0 && starts && !ends) {
+                const int64_t x = share.start + share.left - left + w.u.tiles;     // flat tiles up to the unit's last
+                records[cta] = ChunkRecord{w.b, w.m, w.h, cta, cta_before(share, x), first_unit ? 0 : 1, {0, 0}};
+            }
+            first_unit = false;
+            if (!step(count)) break;
+        } while (true);
+    }
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == LOAD_WARP && work) {
+        // ---------------- pages ----------------
+        uint32_t n = 0;                       // stages filled
+        const int boxes = f.BN / box;
+        bool ok = true;
+        do {
+            const int count = tiles_here();
+            const int32_t* table = p.table + (int64_t)w.b * p.max_pages;
+            for (int it = tile; it < tile + count && ok; ++it) {
+                const int j0 = tile_start(f, w.u, it);
+                int page[4], row[4], found = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = lane + 32 * i, j = j0 + x * box;
+                    page[i] = -2;
+                    if (x < boxes && j < w.u.end) {
+                        const int slot = page_of(f.div, j);
+                        row[i] = j - slot * p.page_size;
+                        page[i] = __ldg(table + slot);
+                        if (page[i] < 0 || page[i] >= p.num_pages) {
+                            page[i] = -1;
+                            atomicOr(p.err, KDA_DEVERR_PAGES);
+                        }
+                    }
+                    found += __popc(__ballot_sync(0xFFFFFFFFu, page[i] >= 0));
+                }
+                for (int v = 0; v < 2 && ok; ++v, ++n) {
+                    const int st = n % L::STAGES;
+                    ok = wait(&bar.empty[st], n / L::STAGES + 1);
+                    if (!ok) break;
+                    const uint32_t to = sm_kv + st * L::BLOCK;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (page[i] == -1)    // no such page: zeros
+                            for (int h = 0; h < L::HALVES; ++h)
+                                for (int y = 0; y < box * 8; ++y)
+                                    st_shared16(to + h * L::HALF + (lane + 32 * i) * box * 128 + y * 16, make_uint4(0, 0, 0, 0));
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_expect_tx(saddr(&bar.full[st]), (uint32_t)(found * box * D * 2));
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (page[i] >= 0)
+#pragma unroll
+                            for (int h = 0; h < L::HALVES; ++h)
+                                tma_load_4d(to + h * L::HALF + (lane + 32 * i) * box * 128, v ? &v_map : &k_map, h * 64, row[i], w.h,
+                                            page[i], saddr(&bar.full[st]));
+                }
+            }
+            if (!ok || !step(count)) break;
+        } while (true);
+        // no copy is left in flight
+        for (uint32_t i = n > L::STAGES ? n - L::STAGES : 0; i < n; ++i) mbar_wait(saddr(&bar.full[i % L::STAGES]), (i / L::STAGES) & 1u);
+    } else if (warp == HELP_WARP && work) {
+        // ---------------- tiles that some row sees in part ----------------
+        uint32_t n = 1;                       // V's stages are the odd ones
+        bool ok = true;
+        do {
+            const int count = tiles_here(), last = last_pos(f, w);
+            OddTiles& list = odd[run & 3];
+            if (lane == 0) list.n = 0;
+            __syncwarp();
+            for (int it = tile; it < tile + count && ok; ++it, n += 2) {
+                const int st = n % L::STAGES, j0 = tile_start(f, w.u, it);
+                ok = wait(&bar.full[st], n / L::STAGES);
+                if (!ok) break;
+                if (!open_tile(p, f, w.u, last, j0)) {
+                    const uint32_t at = sm_kv + st * L::BLOCK;
+                    const int real = w.u.end - j0 < f.BN ? w.u.end - j0 : f.BN;     // may be less than 1: nothing is seen
+                    uint32_t bad[4] = {0, 0, 0, 0};
+                    // eight lanes a row; swizzling moves a row's chunks around in it, which is all the same here
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll 4
+                        for (int y = 0; y < 8; ++y) {
+                            const int r = 32 * g + 4 * y + (lane >> 3);
+                            bool hit = false;
+#pragma unroll
+                            for (int h = 0; h < L::HALVES; ++h) {
+                                const uint4 x = ld_shared16(at + h * L::HALF + r * 128 + (lane & 7) * 16);
+                                auto odd_pair = [](uint32_t v) { return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u; };
+                                hit = hit || odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w);
+                            }
+                            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, hit);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (votes >> (8 * i) & 0xFFu) bad[g] |= 1u << (4 * y + i);
+                        }
+                    // clear them, and what lies behind the end; only visible tokens are written down
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int n_real = real - 32 * g;
+                        const uint32_t in = n_real >= 32 ? 0xFFFFFFFFu : n_real <= 0 ? 0u : (1u << n_real) - 1u;
+                        uint32_t clear = bad[g] | ~in;
+                        bad[g] &= in;
+                        any |= bad[g];
+                        while (clear) {
+                            const int r = 32 * g + __ffs(clear) - 1;
+                            clear &= clear - 1;
+                            if (lane < 8 * L::HALVES) st_shared16(at + (lane >> 3) * L::HALF + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
+                        }
+                    }
+                    if (any && lane == 0 && list.n < MAX_ODD) {
+                        list.start[list.n] = j0;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) list.rows[list.n][g] = bad[g];
+                        ++list.n;
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive(&bar.fixed[st / 2]);
+                }
+                if (lane == 0) arrive(&bar.empty[st]);
+            }
+            if (!ok || !step(count)) break;
+        } while (true);
+    } else if (warp == MMA_WARP && work) {
+        // ---------------- products ----------------
+        const uint32_t id_s = idesc_bf16(TILE, TILE), id_o = idesc_bf16(TILE, D) | (1u << 16);      // V's columns are contiguous
+        uint32_t nk = 0, np[2] = {0, 0}, fixed[4] = {0, 0, 0, 0};
+        bool ok = true;
+        auto scores = [&](int i, int st) {    // S_i = Q_i K^T
+            if (elect_one()) {
+                const uint32_t a = sm_q + i * L::BLOCK, b = sm_kv + st * L::BLOCK;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t o = (ks / 4) * L::HALF + (ks % 4) * 32;
+                    umma_bf16_1(tmem + L::S + i * TILE, desc_sw128(a + o), desc_sw128(b + o), id_s, ks > 0);
+                }
+                umma_commit(saddr(&bar.s[i]));
+            }
+            __syncwarp();
+        };
+        do {
+            const int count = tiles_here(), last = last_pos(f, w), blocks = w.u.rows > TILE ? 2 : 1;
+            ok = ok && wait(&bar.q[0], run) && wait(&bar.q[1], run) && wait(&bar.full[nk % L::STAGES], nk / L::STAGES);
+            if (!ok) break;
+            tc_fence_after();
+            for (int i = 0; i < blocks; ++i) scores(i, nk % L::STAGES);
+            if (elect_one()) umma_commit(saddr(&bar.empty[nk % L::STAGES]));
+            __syncwarp();
+            for (int it = tile; it < tile + count && ok; ++it, nk += 2) {
+                const uint32_t nv = nk + 1, nn = nk + 2;
+                const int sv = nv % L::STAGES, sk = nn % L::STAGES;
+                const bool more = it + 1 < tile + count;
+                ok = wait(&bar.full[sv], nv / L::STAGES);
+                if (ok && !open_tile(p, f, w.u, last, tile_start(f, w.u, it))) {
+                    uint32_t phase = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i == sv / 2) phase = fixed[i]++;
+                    ok = wait(&bar.fixed[sv / 2], phase);
+                }
+                for (int i = 0; i < blocks && ok; ++i) {
+                    ok = wait(&bar.p[i], np[i]++);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t b = sm_kv + sv * L::BLOCK;
+#pragma unroll
+                        for (int ks = 0; ks < TILE / 16; ++ks)
+                            umma_bf16_ts(tmem + L::O + i * D, tmem + L::S + i * TILE + ks * 8, desc_v(b + ks * 2048, L::HALF), id_o,
+                                         it > tile || ks > 0);
+                        umma_commit(saddr(&bar.pv[i]));
+                    }
+                    __syncwarp();
+                    if (more) {
+                        if (i == 0) ok = wait(&bar.full[sk], nn / L::STAGES);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(i, sk);
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    umma_commit(saddr(&bar.empty[sv]));
+                    if (more) umma_commit(saddr(&bar.empty[sk]));
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (elect_one()) umma_commit(saddr(&bar.run));
+            __syncwarp();
+            if (!step(count)) break;
+        } while (true);
+        if (elect_one()) umma_commit(saddr(&bar.done));
+        __syncwarp();
+        mbar_wait(saddr(&bar.done), 0);       // no product is left in flight
+    }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+// Tokens of a TMA box: the largest run that divides a page, fits a tile and fills three quarters of it, or else the
+// one that fills it best.
+int box_of(int page_size) {
+    int best = 1, fill = 0;
+    for (int x = page_size < TILE ? page_size : TILE; x >= 1; --x) {
+        if (page_size % x) continue;
+        const int n = TILE / x * x;
+        if (4 * n >= 3 * TILE) return x;
+        if (n > fill) best = x, fill = n;
+    }
+    return best;
+}
+
+bool encode_pages(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const ChunkParams& p, const void* base, int64_t stride, int box) {
+    const int64_t page = (int64_t)p.Hkv * p.page_size * p.d;
+    const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.page_size, (cuuint64_t)p.Hkv, (cuuint64_t)p.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.page_size * p.d * 2, (cuuint64_t)(p.num_pages > 1 ? stride : page) * 2};
+    const cuuint32_t boxes[4] = {64u, (cuuint32_t)box, 1u, 1u}, ones[4] = {1u, 1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_tc(const ChunkParams& p, cudaStream_t s) {
+    static DeviceSetup done;
+    int sms = 0;
+    cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_chunk_tc_kernel<D>), TcLayout<D>::DYNAMIC, &sms);
+    if (e != cudaSuccess) return e;
+    const auto enc = tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const int box = box_of(p.page_size);
+    CUtensorMap k_map, v_map;
+    if (!encode_pages(enc, &k_map, p, p.k_pages, p.k_stride, box) || !encode_pages(enc, &v_map, p, p.v_pages, p.v_stride, box))
+        return cudaErrorInvalidValue;
+    ChunkPlan f{p.Hq / p.Hkv, UNIT, TILE / box * box, 0, page_div(p.page_size)};
+    int grid = sms < TC_MAX_CTAS ? sms : TC_MAX_CTAS;
+    const int64_t units = most_units(p, f);
+    // Where a unit has few tiles, whatever the lengths, pieces and a second kernel would cost more than they bring.
+    f.whole = units <= 3 * (int64_t)grid && most_tiles(p, f) <= 2 * MIN_SHARE;
+    if (f.whole) grid = (int)units;
+    kda_chunk_tc_kernel<D><<<grid, THREADS, TcLayout<D>::DYNAMIC, s>>>(p, f, box, k_map, v_map);
+    e = cudaGetLastError();
+    return e != cudaSuccess || f.whole ? e : launch_join<__nv_bfloat16, D>(p, f, grid, TC_MAX_CTAS, s);
+}
+
+}  // namespace
+
+size_t chunk_tc_workspace(int32_t d) { return TC_MAX_CTAS * (sizeof(ChunkRecord) + 2 * (size_t)UNIT * (d + 2) * sizeof(float)); }
+
+cudaError_t launch_attention_prefill_tc(const ChunkParams& p, cudaStream_t s) {
+    return p.d == 64 ? launch_tc<64>(p, s) : launch_tc<128>(p, s);
+}
+
+}  // namespace kda

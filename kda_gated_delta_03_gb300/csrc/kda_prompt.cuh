@@ -54,6 +54,8 @@ struct ChunkParams {
 };
 size_t chunk_workspace(int32_t d, kda_dtype dt);
 cudaError_t launch_attention_prefill(const ChunkParams& p, kda_dtype dt, cudaStream_t s);
+size_t chunk_tc_workspace(int32_t d);                                       // its tensor-core path
+cudaError_t launch_attention_prefill_tc(const ChunkParams& p, cudaStream_t s);
 
 struct LogprobParams {
     const void* logits;          // row r at logits + r * row_stride elements
