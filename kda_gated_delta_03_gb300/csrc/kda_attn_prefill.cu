@@ -54,15 +54,15 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
     bool first_unit = true;
     while (true) {
         const Unit& u = w.u;
-        const int64_t row0 = (int64_t)w.m * BM;
+        const int row0 = w.m * BM;
         const int count = f.whole ? u.tiles : (int)(left < u.tiles - tile ? left : u.tiles - tile);
         // ---- the unit's queries ----
         for (int i = tid; i < BM * (D / 4); i += NT) {
             const int r = i / (D / 4), c = i % (D / 4) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < u.rows) {
-                const int64_t t = (row0 + r) / f.group, h = (row0 + r) - t * f.group;
-                x = load4(static_cast<const T*>(p.q) + ((w.s.start + t) * p.Hq + w.h * f.group + h) * D + c);
+                const int t = over(row0 + r, f.by_group), h = row0 + r - t * f.group;
+                x = load4(static_cast<const T*>(p.q) + ((int64_t)(w.s.start + t) * p.Hq + w.h * f.group + h) * D + c);
             }
             *reinterpret_cast<float4*>(Qs + r * L::LD + c) = x;
         }
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = ty * 4 + i;
-            pos[i] = r < u.rows ? (int)(w.s.len - w.s.n + (row0 + r) / f.group) : -1;
+            pos[i] = r < u.rows ? w.s.len - w.s.n + over(row0 + r, f.by_group) : -1;
             m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
             for (int c = 0; c < GO * CO; ++c) o[i][c] = 0.f;
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
                 const int r = i / (D / 4), c = i % (D / 4) * 4, j = j0 + r;
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (j < u.end) {
-                    const int slot = page_of(f.div, j), page = __ldg(table + slot);
+                    const int slot = over(j, f.by_page), page = __ldg(table + slot);
                     if (page >= 0 && page < p.num_pages)
                         x = load4(static_cast<const T*>(pages) + page * stride +
                                   ((int64_t)w.h * p.page_size + (j - slot * p.page_size)) * D + c);
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
                         s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
             }
             // every row of the unit sees every token of the tile: the first row's position bounds it from above, the last one's window from below
-            const int last = w.s.len - w.s.n + (int)((row0 + u.rows - 1) / f.group);
+            const int last = w.s.len - w.s.n + over(row0 + u.rows - 1, f.by_group);
             const bool open = j0 + BN - 1 <= u.pos0 && (p.window == 0 || j0 > last - p.window || j0 + BN <= p.sinks);
             float grow[4];
 #pragma unroll
@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
             const int r = ty * 4 + i;
             if (r >= u.rows) continue;
             if (complete) {
-                const int64_t t = (row0 + r) / f.group;
-                const int64_t at = (w.s.start + t) * p.Hq + w.h * f.group + (row0 + r - t * f.group);
+                const int t = over(row0 + r, f.by_group);
+                const int64_t at = (int64_t)(w.s.start + t) * p.Hq + w.h * f.group + (row0 + r - t * f.group);
                 const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
                 for (int g = 0; g < GO; ++g)
@@ -221,7 +221,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
     int sms = 0;
     cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_chunk_kernel<T, D>), Layout<D>::BYTES, &sms);
     if (e != cudaSuccess) return e;
-    ChunkPlan f{p.Hq / p.Hkv, BM, BN, 0, page_div(p.page_size)};
+    ChunkPlan f = chunk_plan(p, BM, BN);
     int grid = 2 * sms < MAX_CTAS ? 2 * sms : MAX_CTAS;
     const int64_t units = most_units(p, f);
     // Where a unit has few tiles, whatever the lengths, pieces and a second kernel would cost more than they bring.
@@ -241,10 +241,11 @@ size_t chunk_workspace(int32_t d, kda_dtype dt) {
 }
 
 // fp32 stays here: TF32's 11 bits would not keep its precision.  So do bf16 heads of 16, whose rows of 32 bytes leave a
-// TMA box of an odd number of tokens off the 128-byte places it has to start at, and tables without a page.
+// TMA box of an odd number of tokens off the 128-byte places it has to start at, tables without a page, and scales below
+// zero, where the largest score is the smallest product.
 cudaError_t launch_attention_prefill(const ChunkParams& p, kda_dtype dt, cudaStream_t s) {
     if (dt == KDA_DTYPE_BF16)
-        return p.d >= 64 && p.max_pages > 0 ? launch_attention_prefill_tc(p, s)
+        return p.d >= 64 && p.max_pages > 0 && p.scale >= 0.f ? launch_attention_prefill_tc(p, s)
                : p.d == 16                  ? launch<__nv_bfloat16, 16>(p, s)
                : p.d == 64                  ? launch<__nv_bfloat16, 64>(p, s)
                                             : launch<__nv_bfloat16, 128>(p, s);

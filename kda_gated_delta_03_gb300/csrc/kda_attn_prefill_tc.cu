@@ -27,8 +27,8 @@ namespace {
 
 constexpr int TILE = 128;                     // rows of a block and of a tile
 constexpr int UNIT = 2 * TILE;
-constexpr int WARPS = 12, THREADS = WARPS * 32;               // the last one only makes the third group whole
-constexpr int MMA_WARP = 8, LOAD_WARP = 9, HELP_WARP = 10;
+constexpr int WARPS = 12, THREADS = WARPS * 32;
+constexpr int MMA_WARP = 8, LOAD_WARP = 9, HELP_WARP = 10, QUERY_WARP = 11;
 constexpr int TC_MAX_CTAS = 160;              // of the main kernel, whatever the GPU (bounds the workspace)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float SLACK = 8.f;                  // the reference moves when the maximum has grown by 2^SLACK
@@ -54,12 +54,14 @@ struct OddTiles {
     uint32_t rows[MAX_ODD][4];
 };
 
+constexpr int RING = 8;                       // runs whose lists are kept: the helper is at most 6 ahead of a reader
+
 struct Barriers {
     uint64_t full[8], empty[8];               // of stages
     uint64_t fixed[4];                        // a V stage's partly seen tile is ready for the product
-    uint64_t q[2];                            // of row blocks: queries in shared memory
-    uint64_t s[2], p[2], pv[2];               // scores, weights, a tile's product done
-    uint64_t run;                             // a run's products done
+    uint64_t q, q_empty;                      // a run's queries in shared memory, and read for the last time
+    uint64_t s[2], p[2], pv[2];               // of row blocks: scores, weights, a tile's product done
+    uint64_t run, ack;                        // a run's products done, and the second block's group has seen that
     uint64_t done;                            // all products done
 };
 
@@ -124,16 +126,94 @@ __device__ __forceinline__ bool open_tile(const ChunkParams& p, const ChunkPlan&
     return end - 1 <= u.pos0 && (p.window == 0 || (int64_t)j0 > (int64_t)last - p.window || end <= p.sinks);
 }
 __device__ __forceinline__ int last_pos(const ChunkPlan& f, const Walk& w) {
-    return w.s.len - w.s.n + (int)(((int64_t)w.m * f.BM + w.u.rows - 1) / f.group);
+    return w.s.len - w.s.n + over(w.m * UNIT + w.u.rows - 1, f.by_group);
 }
 
-// The weight of token j for a row, against the row's reference: for the few tokens taken out of a tile.
-template <int D>
-__device__ __noinline__ float weight_of(const ChunkParams& p, const __nv_bfloat16* q, const __nv_bfloat16* k, float scale2, float base) {
-    float s = 0.f;
-    for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), s);
-    return ex2_approx(s * scale2 - base);
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\nfma.rn.f32x2 x, x, y, z;\n"
+        "mov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// 64 bytes of a row: whole 32-byte sectors at a time where the address allows it, since each lane has a row of its own.
+__device__ __forceinline__ void store64(void* to, const uint32_t (&x)[16], bool wide) {
+    uint32_t* p = static_cast<uint32_t*>(to);
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + i), "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]),
+                         "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4*>(p + i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    }
+}
+
+// Adds the tokens that were taken out of a run's tiles to a row that sees them; a whole warp.
+template <int D>
+__device__ __noinline__ void add_odd(const ChunkParams& p, const ChunkPlan& f, const OddTiles& list, int b, int h, int pos,
+                                     const __nv_bfloat16* q, uint32_t t_o, float scale2, float base) {
+    for (int e = 0; e < list.n; ++e)
+        for (int x = 0; x < TILE; ++x) {
+            if (!(list.rows[e][x >> 5] >> (x & 31) & 1u)) continue;
+            const int j = list.start[e] + x, slot = over(j, f.by_page), page = __ldg(p.table + (int64_t)b * p.max_pages + slot);
+            const int64_t off = ((int64_t)h * p.page_size + (j - slot * p.page_size)) * D;
+            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k_pages) + page * p.k_stride + off;
+            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_pages) + page * p.v_stride + off;
+            const bool seen = j <= pos && (p.window == 0 || j > pos - p.window || j < p.sinks);
+            float s = 0.f;
+            for (int c = 0; seen && c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), s);
+            const float y = ex2_approx(s * scale2 - base);
+            for (int c = 0; c < D; c += 16) {
+                float o[16];
+                __syncwarp();
+                tmem_ld16(t_o + c, o);
+                for (int i = 0; i < 16; ++i)
+                    if (seen) o[i] = fmaf(y, __bfloat162float(v[c + i]), o[i]);
+                tmem_st16(t_o + c, o);
+                tmem_wait_st();
+            }
+        }
+}
+
+// A run: the share's tiles of one unit.  Every role steps through the same ones.
+struct Runs {
+    Walk w;
+    int64_t left;
+    int32_t tile, count, run;    // of the run: its first tile and how many; its number
+    __device__ __forceinline__ Runs(const ChunkParams& p, const ChunkPlan& f, const Share& share) : left(share.left), tile(share.tile), run(0) {
+        w.begin(p, f, share);
+        measure(f);
+    }
+    __device__ __forceinline__ void measure(const ChunkPlan& f) {
+        count = f.whole ? w.u.tiles : (int)(left < w.u.tiles - tile ? left : w.u.tiles - tile);
+    }
+    __device__ __forceinline__ bool next(const ChunkParams& p, const ChunkPlan& f) {
+        left -= f.whole ? 1 : count;
+        if (left <= 0) return false;
+        ++run;
+        tile = 0;
+        w.next(p, f);
+        measure(f);
+        return true;
+    }
+};
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -141,7 +221,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
     using L = TcLayout<D>;
     extern __shared__ unsigned char raw[];
     __shared__ Barriers bar;
-    __shared__ OddTiles odd[4];
+    __shared__ OddTiles odd[RING];
     __shared__ int64_t sums[WARPS];
     __shared__ Share share;
     __shared__ uint32_t tmem_base;
@@ -155,8 +235,8 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
         auto init = [](uint64_t* b, int n) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(n) : "memory"); };
         for (int i = 0; i < L::STAGES; ++i) init(&bar.full[i], 1), init(&bar.empty[i], i % 2 ? 2 : 1);
         for (int i = 0; i < 4; ++i) init(&bar.fixed[i], 1);
-        for (int i = 0; i < 2; ++i) init(&bar.q[i], 4), init(&bar.s[i], 1), init(&bar.p[i], 4), init(&bar.pv[i], 1);
-        init(&bar.run, 1), init(&bar.done, 1);
+        for (int i = 0; i < 2; ++i) init(&bar.s[i], 1), init(&bar.p[i], 4), init(&bar.pv[i], 1);
+        init(&bar.q, 1), init(&bar.q_empty, 1), init(&bar.run, 1), init(&bar.ack, 4), init(&bar.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         abort_flag = 0;
         if (!f.whole) records[cta].b = -1;
@@ -183,90 +263,61 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
         return abort_flag == 0;
     };
     const bool work = share.left > 0;
-    // A run: the share's tiles of one unit.  Every role steps through the same ones.
-    Walk w{};
-    int64_t left = share.left;
-    int tile = share.tile, run = 0;
-    auto tiles_here = [&]() { return f.whole ? w.u.tiles : (int)(left < w.u.tiles - tile ? left : w.u.tiles - tile); };
-    auto step = [&](int count) {              // to the next run, if there is one
-        left -= f.whole ? 1 : count;
-        ++run;
-        tile = 0;
-        if (left > 0) w.next(p, f);
-        return left > 0;
-    };
-    if (work) w.begin(p, f, share);
     // Registers go from the warps that move data to those that hold rows: 2 x 208 + 88 = 3 x 168, what the launch has.
     if (warp < MMA_WARP) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    if (work) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (work) {
         // ---------------- softmax: a row a thread ----------------
         const int blk = warp >> 2, r = tid;   // rows 0..127 and 128..255 of the unit
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
         const uint32_t t_s = tmem + lanes + L::S + blk * TILE, t_o = tmem + lanes + L::O + blk * D;
-        const float scale2 = fmaxf(fabsf(p.scale) * LOG2E, 1e-37f);       // positive: 0 * -inf must not be met
-        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;            // the sign goes into the queries
-        float* pieces = f.whole ? nullptr : reinterpret_cast<float*>(p.workspace + TC_MAX_CTAS * sizeof(ChunkRecord));
+        const float scale2 = fmaxf(p.scale * LOG2E, 1e-37f);               // above 0: 0 * -inf must not be met
         uint32_t ns = 0;                      // tiles of this block so far
         bool ok = true, first_unit = true;
+        Runs runs(p, f, share);
         do {
-            const int count = tiles_here(), last = last_pos(f, w);
-            const bool mine = r < w.u.rows, active = blk * TILE < w.u.rows;
-            const int64_t flat = (int64_t)w.m * UNIT + r;
-            const int t = (int)(flat / f.group), head = w.h * f.group + (int)(flat - (int64_t)t * f.group);
-            const int64_t at = ((int64_t)w.s.start + t) * p.Hq + head;
-            const int pos = mine ? max(w.s.len - w.s.n + t, -1) : -1;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + at * D;
-            if (active) {
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (mine) {
-                        x = __ldg(reinterpret_cast<const uint4*>(q) + c);
-                        x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-                    }
-                    const int row = r & (TILE - 1);
-                    st_shared16(sm_q + blk * L::BLOCK + (c >> 3) * L::HALF + row * 128 + (((c & 7) ^ (row & 7)) << 4), x);
-                }
-                fence_async_smem();
-            }
-            __syncwarp();
-            if (lane == 0) arrive(&bar.q[blk]);
-            float m = -INFINITY, ref = -INFINITY, l = 0.f;
+            const Walk& w = runs.w;
+            const int count = runs.count, tile = runs.tile, run = runs.run;
+            const bool active = blk * TILE < w.u.rows;
+            float ref = -INFINITY, l = 0.f;
             bool part = false;                // the helper has looked at a tile of this run
             if (active) {
-                for (int it = tile; it < tile + count && ok; ++it, ++ns) {
+                const int last = last_pos(f, w);
+                const int pos = r < w.u.rows ? max(w.s.len - w.s.n + over(w.m * UNIT + r, f.by_group), -1) : -1;
+                for (int it = tile; it < tile + count; ++it, ++ns) {
                     const int j0 = tile_start(f, w.u, it);
+                    const bool open = open_tile(p, f, w.u, last, j0);
+                    part = part || !open;
                     ok = wait(&bar.s[blk], ns);
                     if (!ok) break;
                     tc_fence_after();
                     __syncwarp();
-                    // Two passes over S, 32 columns at a time with the next ones on their way: the whole row would
-                    // take 128 registers.
-                    const bool open = open_tile(p, f, w.u, last, j0), masked = f.BN < TILE || !open;
-                    part = part || !open;
-                    const int hi = min(pos - j0, f.BN - 1);
-                    const int lo = p.window ? max(pos - p.window, j0 - 1) - j0 : -1;
-                    const int near = p.window ? p.sinks - j0 : 0;
-                    float s[2][32];
-                    auto hide = [&](int c, float (&x)[32]) {
-                        if (masked) {
+                    float s[4][32];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = c + i <= hi && (c + i > lo || c + i < near) ? x[i] : -INFINITY;
+                    for (int c = 0; c < 4; ++c) tmem_fetch32(t_s + 32 * c, s[c]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_wait32(s[c]);
+                    if (!open || f.BN < TILE) {
+                        const int hi = min(pos - j0, f.BN - 1);
+                        if (p.window == 0) {
+#pragma unroll
+                            for (int c = 0; c < TILE; ++c) s[c / 32][c % 32] = c <= hi ? s[c / 32][c % 32] : -INFINITY;
+                        } else {
+                            const int lo = max(pos - p.window, j0 - 1) - j0, near = p.sinks - j0;
+#pragma unroll
+                            for (int c = 0; c < TILE; ++c)
+                                s[c / 32][c % 32] = c <= hi && (c > lo || c < near) ? s[c / 32][c % 32] : -INFINITY;
                         }
-                    };
-                    tmem_fetch32(t_s, s[0]);
-                    float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < TILE; c += 32) {
-                        float (&x)[32] = s[c / 32 & 1];
-                        tmem_wait32(x);
-                        tmem_fetch32(t_s + (c + 32) % TILE, s[(c / 32 + 1) & 1]);
-                        hide(c, x);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
                     }
-                    m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    float top[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        top[c] = max3(s[c][0], s[c][1], s[c][2]);
+#pragma unroll
+                        for (int i = 3; i < 31; i += 2) top[c] = max3(top[c], s[c][i], s[c][i + 1]);
+                        top[c] = fmaxf(top[c], s[c][31]);
+                    }
+                    const float m = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     const bool move = (m - ref) * scale2 > SLACK;          // (NaN with nothing seen so far: no)
                     if (__any_sync(0xFFFFFFFFu, move)) {
                         const float to = move ? m : ref;
@@ -278,97 +329,92 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
                             tc_fence_after();
                             __syncwarp();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                float o[32];
-                                tmem_ld32(t_o + c, o);
+                            for (int c = 0; c < D; c += 16) {
+                                float o[16];
+                                tmem_ld16(t_o + c, o);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= by;
-                                tmem_st32(t_o + c, o);
+                                for (int i = 0; i < 16; ++i) o[i] *= by;
+                                tmem_st16(t_o + c, o);
                             }
                         }
                         ref = to;
                     }
                     const float base = ref == -INFINITY ? 0.f : ref * scale2;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 by2 = make_float2(scale2, scale2), minus = make_float2(-base, -base);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int c = 0; c < TILE; c += 32) {
-                        float (&x)[32] = s[c / 32 & 1];
-                        tmem_wait32(x);
-                        if (c + 32 < TILE) tmem_fetch32(t_s + c + 32, s[(c / 32 + 1) & 1]);
-                        hide(c, x);
-                        float w2[16];
+                    for (int c = 0; c < 4; ++c) {
+                        float x[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float a = ex2_approx(fmaf(x[2 * i], scale2, -base)), b = ex2_approx(fmaf(x[2 * i + 1], scale2, -base));
-                            w2[i] = __uint_as_float(pack_bf16x2(a, b));
-                            sum[2 * (i & 1)] += a;
-                            sum[2 * (i & 1) + 1] += b;
+                            const float2 y = fma2(make_float2(s[c][2 * i], s[c][2 * i + 1]), by2, minus);
+                            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                            x[i] = __uint_as_float(pack_bf16x2(e.x, e.y));
+                            sum[i & 1] = add2(sum[i & 1], e);
                         }
-                        tmem_st16(t_s + c / 2, w2);
+                        tmem_st16(t_s + 16 * c, x);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) arrive(&bar.p[blk]);
                 }
             }
-            // The second block waits for the whole run also where it has no rows, so that neither group gets ahead of the
-            // products by more than a run (a barrier's phases are told apart by one bit).
+            // The second block waits for the whole run also where it has no rows, and says so, so that neither side gets
+            // ahead by more than a run (a barrier's phases are told apart by one bit).
             if (ok) ok = blk == 0 ? wait(&bar.pv[0], ns - 1) : wait(&bar.run, run);
             if (!ok) break;
+            __syncwarp();
+            if (blk == 1 && lane == 0) arrive(&bar.ack);
             // ---- outputs, or a piece of them ----
             const bool starts = tile == 0, ends = tile + count == w.u.tiles, complete = starts && ends;
             if (active) {
                 tc_fence_after();
                 __syncwarp();
-                const OddTiles& list = odd[run & 3];
-                const float inv = l == 0.f ? 0.f : 1.f / l, base = ref == -INFINITY ? 0.f : ref * scale2;
-                float* piece = complete ? nullptr : pieces + ((int64_t)cta * 2 + (first_unit ? 0 : 1)) * piece_floats<D>(UNIT);
-                const int odd_tiles = part ? *const_cast<const volatile int32_t*>(&list.n) : 0;
+                const bool mine = r < w.u.rows;
+                const int flat = w.m * UNIT + (mine ? r : 0), t = over(flat, f.by_group);
+                const int64_t at = (int64_t)(w.s.start + t) * p.Hq + w.h * f.group + flat - t * f.group;
+                const float base = ref == -INFINITY ? 0.f : ref * scale2;
+                if (part && *const_cast<const volatile int32_t*>(&odd[run % RING].n) > 0)
+                    add_odd<D>(p, f, odd[run % RING], w.b, w.h, mine ? w.s.len - w.s.n + t : -1,
+                               static_cast<const __nv_bfloat16*>(p.q) + at * D, t_o, scale2, base);
+                if (complete) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + at * D;
+                    const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    tmem_ld32(t_o + c, o);
-                    for (int e = 0; e < odd_tiles; ++e)        // rare: values that are not finite
-                        for (int x = 0; x < TILE; ++x) {
-                            const int j = list.start[e] + x;
-                            if (!(list.rows[e][x >> 5] >> (x & 31) & 1u) || j > pos || (p.window && j <= pos - p.window && j >= p.sinks)) continue;
-                            const int slot = page_of(f.div, j), page = __ldg(p.table + (int64_t)w.b * p.max_pages + slot);
-                            const int64_t off = ((int64_t)w.h * p.page_size + (j - slot * p.page_size)) * D;
-                            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k_pages) + page * p.k_stride + off;
-                            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_pages) + page * p.v_stride + off;
-                            const float y = weight_of<D>(p, q, k, p.scale < 0.f ? -scale2 : scale2, base);
-                            for (int i = 0; i < 32; ++i) o[i] = fmaf(y, __bfloat162float(v[c + i]), o[i]);
-                        }
-                    if (!mine) continue;
-                    if (complete) {
-                        uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + c);
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld32(t_o + c, o);
+                        uint32_t x[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            auto two = [&](int k) { return l == 0.f ? 0u : pack_bf16x2(o[i + k] * inv, o[i + k + 1] * inv); };
-                            to[i / 8] = make_uint4(two(0), two(2), two(4), two(6));
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4*>(piece + r * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        for (int i = 0; i < 16; ++i) x[i] = l == 0.f ? 0u : pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+                        if (mine) store64(to + c, x, wide);
                     }
+                    if (mine && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (base + log2f(l)) * LN2;
+                } else {
+                    float* piece = reinterpret_cast<float*>(p.workspace + TC_MAX_CTAS * sizeof(ChunkRecord)) +
+                                   ((int64_t)cta * 2 + (first_unit ? 0 : 1)) * piece_floats<D>(UNIT);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld32(t_o + c, o);
+                        if (mine) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 16) store64(piece + r * D + c + i, reinterpret_cast<const uint32_t(&)[16]>(o[i]), true);
+                        }
+                    }
+                    if (mine) piece[UNIT * D + r] = ref == -INFINITY ? -INFINITY : base, piece[UNIT * (D + 1) + r] = l;
                 }
-                if (mine) {
-                    if (!complete)
-                        piece[UNIT * D + r] = ref == -INFINITY ? -INFINITY : base, piece[UNIT * (D + 1) + r] = l;
-                    else if (p.lse)
-                        p.lse[at] = l == 0.f ? -INFINITY : (base + log2f(l)) * LN2;
-                }
-                tc_fence_before();            // the next unit's products overwrite O
+                tc_fence_before();            // the next run's products overwrite O
             }
             if (tid == 0 && starts && !ends) {
-                const int64_t x = share.start + share.left - left + w.u.tiles;     // flat tiles up to the unit's last
+                const int64_t x = share.start + share.left - runs.left + w.u.tiles;     // flat tiles up to the unit's last
                 records[cta] = ChunkRecord{w.b, w.m, w.h, cta, cta_before(share, x), first_unit ? 0 : 1, {0, 0}};
             }
             first_unit = false;
-            if (!step(count)) break;
+            if (!runs.next(p, f)) break;
         } while (true);
     }
     } else {
@@ -378,8 +424,10 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
         uint32_t n = 0;                       // stages filled
         const int boxes = f.BN / box;
         bool ok = true;
+        Runs runs(p, f, share);
         do {
-            const int count = tiles_here();
+            const Walk& w = runs.w;
+            const int count = runs.count, tile = runs.tile;
             const int32_t* table = p.table + (int64_t)w.b * p.max_pages;
             for (int it = tile; it < tile + count && ok; ++it) {
                 const int j0 = tile_start(f, w.u, it);
@@ -389,7 +437,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
                     const int x = lane + 32 * i, j = j0 + x * box;
                     page[i] = -2;
                     if (x < boxes && j < w.u.end) {
-                        const int slot = page_of(f.div, j);
+                        const int slot = over(j, f.by_page);
                         row[i] = j - slot * p.page_size;
                         page[i] = __ldg(table + slot);
                         if (page[i] < 0 || page[i] >= p.num_pages) {
@@ -423,17 +471,44 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
                                             page[i], saddr(&bar.full[st]));
                 }
             }
-            if (!ok || !step(count)) break;
+            if (!ok || !runs.next(p, f)) break;
         } while (true);
         // no copy is left in flight
         for (uint32_t i = n > L::STAGES ? n - L::STAGES : 0; i < n; ++i) mbar_wait(saddr(&bar.full[i % L::STAGES]), (i / L::STAGES) & 1u);
+    } else if (warp == QUERY_WARP && work) {
+        // ---------------- queries ----------------
+        bool ok = true;
+        Runs runs(p, f, share);
+        do {
+            const Walk& w = runs.w;
+            const int run = runs.run, row0 = w.m * UNIT;
+            if (run > 0) ok = wait(&bar.q_empty, run - 1);
+            if (!ok) break;
+            constexpr int PER = D / 8;        // 16-byte columns of a row
+            const int c = lane % PER;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)w.s.start * p.Hq + w.h * f.group) * D + c * 8;
+#pragma unroll 4
+            for (int r = lane / PER; r < w.u.rows; r += 32 / PER) {        // rows behind the unit's last hold anything
+                const int t = over(row0 + r, f.by_group), g = row0 + r - t * f.group;
+                const uint32_t to = sm_q + (r >> 7) * L::BLOCK + (c >> 3) * L::HALF + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(q + ((int64_t)t * p.Hq + g) * D) : "memory");
+            }
+            cp_async_commit();
+            cp_async_wait_all();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(&bar.q);
+            if (!runs.next(p, f)) break;
+        } while (true);
     } else if (warp == HELP_WARP && work) {
         // ---------------- tiles that some row sees in part ----------------
         uint32_t n = 1;                       // V's stages are the odd ones
         bool ok = true;
+        Runs runs(p, f, share);
         do {
-            const int count = tiles_here(), last = last_pos(f, w);
-            OddTiles& list = odd[run & 3];
+            const Walk& w = runs.w;
+            const int count = runs.count, tile = runs.tile, run = runs.run, last = last_pos(f, w);
+            OddTiles& list = odd[run % RING];
             if (lane == 0) list.n = 0;
             __syncwarp();
             for (int it = tile; it < tile + count && ok; ++it, n += 2) {
@@ -443,38 +518,31 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
                 if (!open_tile(p, f, w.u, last, j0)) {
                     const uint32_t at = sm_kv + st * L::BLOCK;
                     const int real = w.u.end - j0 < f.BN ? w.u.end - j0 : f.BN;     // may be less than 1: nothing is seen
-                    uint32_t bad[4] = {0, 0, 0, 0};
-                    // eight lanes a row; swizzling moves a row's chunks around in it, which is all the same here
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll 4
-                        for (int y = 0; y < 8; ++y) {
-                            const int r = 32 * g + 4 * y + (lane >> 3);
-                            bool hit = false;
-#pragma unroll
-                            for (int h = 0; h < L::HALVES; ++h) {
-                                const uint4 x = ld_shared16(at + h * L::HALF + r * 128 + (lane & 7) * 16);
-                                auto odd_pair = [](uint32_t v) { return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u; };
-                                hit = hit || odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w);
-                            }
-                            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, hit);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (votes >> (8 * i) & 0xFFu) bad[g] |= 1u << (4 * y + i);
-                        }
-                    // clear them, and what lies behind the end; only visible tokens are written down
-                    uint32_t any = 0;
+                    // Tokens up to the first row's are hidden from nobody where there is no window.  A lane has rows
+                    // 32 g + lane; eight lanes at a time read eight different 16-byte columns.
+                    const int first = p.window == 0 ? max(w.u.pos0 + 1 - j0, 0) : 0;
+                    uint32_t any = 0, bad[4];
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const int n_real = real - 32 * g;
-                        const uint32_t in = n_real >= 32 ? 0xFFFFFFFFu : n_real <= 0 ? 0u : (1u << n_real) - 1u;
-                        uint32_t clear = bad[g] | ~in;
-                        bad[g] &= in;
+                        const int r = 32 * g + lane;
+                        const uint32_t row = at + r * 128;
+                        const bool look = r >= first && r < real;
+                        uint32_t hit = 0;     // an exponent of all ones carries into the sign's place
+                        if (__any_sync(0xFFFFFFFFu, look)) {
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c) {
+                                const uint4 x = ld_shared16(row + (c >> 3) * L::HALF + (((c & 7) ^ (r & 7)) << 4));
+                                hit |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
+                                       ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
+                            }
+                        }
+                        const bool out = look && (hit & 0x80008000u);
+                        bad[g] = __ballot_sync(0xFFFFFFFFu, out);
                         any |= bad[g];
-                        while (clear) {
-                            const int r = 32 * g + __ffs(clear) - 1;
-                            clear &= clear - 1;
-                            if (lane < 8 * L::HALVES) st_shared16(at + (lane >> 3) * L::HALF + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
+                        if (out || r >= real) {
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c)
+                                st_shared16(row + (c >> 3) * L::HALF + (((c & 7) ^ (r & 7)) << 4), make_uint4(0, 0, 0, 0));
                         }
                     }
                     if (any && lane == 0 && list.n < MAX_ODD) {
@@ -489,7 +557,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
                 }
                 if (lane == 0) arrive(&bar.empty[st]);
             }
-            if (!ok || !step(count)) break;
+            if (!ok || !runs.next(p, f)) break;
         } while (true);
     } else if (warp == MMA_WARP && work) {
         // ---------------- products ----------------
@@ -508,13 +576,18 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
             }
             __syncwarp();
         };
+        Runs runs(p, f, share);
         do {
-            const int count = tiles_here(), last = last_pos(f, w), blocks = w.u.rows > TILE ? 2 : 1;
-            ok = ok && wait(&bar.q[0], run) && wait(&bar.q[1], run) && wait(&bar.full[nk % L::STAGES], nk / L::STAGES);
+            const Walk& w = runs.w;
+            const int count = runs.count, tile = runs.tile, run = runs.run, last = last_pos(f, w), blocks = w.u.rows > TILE ? 2 : 1;
+            ok = wait(&bar.q, run) && wait(&bar.full[nk % L::STAGES], nk / L::STAGES);
             if (!ok) break;
             tc_fence_after();
             for (int i = 0; i < blocks; ++i) scores(i, nk % L::STAGES);
-            if (elect_one()) umma_commit(saddr(&bar.empty[nk % L::STAGES]));
+            if (elect_one()) {
+                umma_commit(saddr(&bar.empty[nk % L::STAGES]));
+                if (count == 1) umma_commit(saddr(&bar.q_empty));
+            }
             __syncwarp();
             for (int it = tile; it < tile + count && ok; ++it, nk += 2) {
                 const uint32_t nv = nk + 1, nn = nk + 2;
@@ -552,13 +625,15 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
                 if (elect_one()) {
                     umma_commit(saddr(&bar.empty[sv]));
                     if (more) umma_commit(saddr(&bar.empty[sk]));
+                    if (it + 2 == tile + count) umma_commit(saddr(&bar.q_empty));
                 }
                 __syncwarp();
             }
+            if (ok && run > 0) ok = wait(&bar.ack, run - 1);
             if (!ok) break;
             if (elect_one()) umma_commit(saddr(&bar.run));
             __syncwarp();
-            if (!step(count)) break;
+            if (!runs.next(p, f)) break;
         } while (true);
         if (elect_one()) umma_commit(saddr(&bar.done));
         __syncwarp();
@@ -607,7 +682,7 @@ cudaError_t launch_tc(const ChunkParams& p, cudaStream_t s) {
     CUtensorMap k_map, v_map;
     if (!encode_pages(enc, &k_map, p, p.k_pages, p.k_stride, box) || !encode_pages(enc, &v_map, p, p.v_pages, p.v_stride, box))
         return cudaErrorInvalidValue;
-    ChunkPlan f{p.Hq / p.Hkv, UNIT, TILE / box * box, 0, page_div(p.page_size)};
+    ChunkPlan f = chunk_plan(p, UNIT, TILE / box * box);
     int grid = sms < TC_MAX_CTAS ? sms : TC_MAX_CTAS;
     const int64_t units = most_units(p, f);
     // Where a unit has few tiles, whatever the lengths, pieces and a second kernel would cost more than they bring.

@@ -15,28 +15,30 @@
 namespace kda {
 namespace {
 
-// t / page_size for 0 <= t < 2^31, as a multiplication.
-struct PageDiv {
+// t / n for 0 <= t < 2^31 and a divisor that the host knows, as a multiplication.
+struct Divisor {
     uint32_t magic;
     int32_t shift;
 };
-inline PageDiv page_div(int32_t page_size) {
-    PageDiv d{0u, 0};
-    while ((2ll << d.shift) < page_size) ++d.shift;
-    if (page_size > 1) d.magic = (uint32_t)((1ull << (32 + d.shift)) / page_size + 1);
+inline Divisor divisor(int32_t n) {
+    Divisor d{0u, 0};
+    while ((2ll << d.shift) < n) ++d.shift;
+    if (n > 1) d.magic = (uint32_t)((1ull << (32 + d.shift)) / n + 1);
     return d;
 }
-__device__ __forceinline__ int page_of(const PageDiv& d, int t) {
-    return d.magic ? (int)(__umulhi((uint32_t)t, d.magic) >> d.shift) : t;
-}
+__device__ __forceinline__ int over(int t, const Divisor& d) { return d.magic ? (int)(__umulhi((uint32_t)t, d.magic) >> d.shift) : t; }
 
 struct ChunkPlan {
     int32_t group;               // query heads of a key-value head
-    int32_t BM;                  // rows of a unit
+    int32_t BM;                  // rows of a unit, a power of two
     int32_t BN;                  // tokens of a tile
     int32_t whole;               // CTA i does unit i, and nothing is left to join
-    PageDiv div;
+    Divisor by_page, by_group, by_tile;
 };
+inline ChunkPlan chunk_plan(const ChunkParams& p, int32_t BM, int32_t BN) {
+    const int32_t group = p.Hq / p.Hkv;
+    return ChunkPlan{group, BM, BN, 0, divisor(p.page_size), divisor(group), divisor(BN)};
+}
 
 // One sequence of the batch: its new tokens and its length, 0 where they are not valid.
 struct Seq {
@@ -55,7 +57,7 @@ __device__ __forceinline__ Seq seq_of(const ChunkParams& p, int b) {
     return s;
 }
 __device__ __forceinline__ int units_of(const ChunkPlan& f, const Seq& s) {
-    return (int)(((int64_t)s.n * f.group + f.BM - 1) / f.BM);
+    return (int)(((unsigned)(s.n * f.group) + f.BM - 1) / f.BM);          // rows are numbered in 31 bits, BM is a power of two
 }
 
 // A unit's rows and tiles.  Tile i < near covers tokens from i * BN, a later one from (i + skip) * BN.
@@ -67,19 +69,19 @@ struct Unit {
 };
 __device__ __forceinline__ Unit unit_of(const ChunkParams& p, const ChunkPlan& f, const Seq& s, int m) {
     Unit u;
-    const int64_t row0 = (int64_t)m * f.BM, all = (int64_t)s.n * f.group;
-    u.rows = (int)(all - row0 < f.BM ? all - row0 : f.BM);
-    const int t0 = (int)(row0 / f.group), t1 = (int)((row0 + u.rows - 1) / f.group);
+    const int row0 = m * f.BM, all = s.n * f.group;
+    u.rows = all - row0 < f.BM ? all - row0 : f.BM;
+    const int t0 = over(row0, f.by_group), t1 = over(row0 + u.rows - 1, f.by_group);
     u.pos0 = s.len - s.n + t0;
     const int last = s.len - s.n + t1;
     u.end = last < 0 ? 0 : last + 1;
-    const int all_tiles = (u.end + f.BN - 1) / f.BN;
+    const int all_tiles = over(u.end + f.BN - 1, f.by_tile);
     u.near = 0, u.skip = 0;
     if (p.window > 0) {
         const int first = u.pos0 >= p.window ? u.pos0 + 1 - p.window : 0;      // of the window of the first row
-        const int w0 = first / f.BN;
+        const int w0 = over(first, f.by_tile);
         const int sinks = p.sinks < u.end ? p.sinks : u.end;
-        u.near = sinks > 0 ? (sinks - 1) / f.BN + 1 : 0;
+        u.near = sinks > 0 ? over(sinks - 1, f.by_tile) + 1 : 0;
         if (u.near > w0) u.near = w0;
         u.skip = w0 - u.near;
     }
@@ -236,8 +238,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kda_chunk_join_kernel(ChunkPa
     if (r.b < 0) return;
     const int lane = threadIdx.x & 31, row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5);
     const Seq s = seq_of(p, r.b);
-    const int64_t flat = (int64_t)r.m * f.BM + row;
-    if (flat >= (int64_t)s.n * f.group) return;
+    const int flat = r.m * f.BM + row;
+    if (flat >= s.n * f.group) return;
     const int64_t size = piece_floats<D>(f.BM);
     const float* pieces = reinterpret_cast<const float*>(p.workspace + max_ctas * sizeof(ChunkRecord));
     const int n = r.last - r.first + 1;
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kda_chunk_join_kernel(ChunkPa
                 o[c] = fmaf(w, v, o[c]);
             }
     }
-    const int t = (int)(flat / f.group), head = r.h * f.group + (int)(flat - (int64_t)t * f.group);
+    const int t = over(flat, f.by_group), head = r.h * f.group + flat - t * f.group;
     const int64_t at = (int64_t)(s.start + t) * p.Hq + head;
 #pragma unroll
     for (int c = 0; c < PER; ++c)
