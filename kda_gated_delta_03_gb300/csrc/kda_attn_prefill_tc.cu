@@ -60,13 +60,21 @@ struct Barriers {
     uint64_t full[8], empty[8];               // of stages
     uint64_t fixed[4];                        // a V stage's partly seen tile is ready for the product
     uint64_t q, q_empty;                      // a run's queries in shared memory, and read for the last time
-    uint64_t s[2], p[2], pv[2];               // of row blocks: scores, weights, a tile's product done
+    uint64_t s[2], p[2][2], pv[2];            // of row blocks: scores, the weights' two halves, a tile's product done
     uint64_t run, ack;                        // a run's products done, and the second block's group has seen that
     uint64_t done;                            // all products done
 };
 
 __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done)
+                 : "r"(mbar), "r"(parity)
+                 : "memory");
+    return done;
 }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t mbar) {
     asm volatile(
@@ -217,7 +225,8 @@ struct Runs {
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
-kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __grid_constant__ CUtensorMap q_map,
+                    const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using L = TcLayout<D>;
     extern __shared__ unsigned char raw[];
     __shared__ Barriers bar;
@@ -225,7 +234,6 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
     __shared__ int64_t sums[WARPS];
     __shared__ Share share;
     __shared__ uint32_t tmem_base;
-    __shared__ volatile int abort_flag;
     unsigned char* sm = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
     const uint32_t sm_q = saddr(sm) + L::Q, sm_kv = saddr(sm) + L::KV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x, grid = gridDim.x;
@@ -235,10 +243,9 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
         auto init = [](uint64_t* b, int n) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(n) : "memory"); };
         for (int i = 0; i < L::STAGES; ++i) init(&bar.full[i], 1), init(&bar.empty[i], i % 2 ? 2 : 1);
         for (int i = 0; i < 4; ++i) init(&bar.fixed[i], 1);
-        for (int i = 0; i < 2; ++i) init(&bar.s[i], 1), init(&bar.p[i], 4), init(&bar.pv[i], 1);
+        for (int i = 0; i < 2; ++i) init(&bar.s[i], 1), init(&bar.p[i][0], 4), init(&bar.p[i][1], 4), init(&bar.pv[i], 1);
         init(&bar.q, 1), init(&bar.q_empty, 1), init(&bar.run, 1), init(&bar.ack, 4), init(&bar.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        abort_flag = 0;
         if (!f.whole) records[cta].b = -1;
     }
     if (warp == MMA_WARP) {
@@ -254,13 +261,10 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    auto fail = [&]() {
+    auto wait = [&](uint64_t* b, uint32_t parity) {            // each role that gives up leaves the others to give up, too
+        if (mbar_test(saddr(b), parity & 1u) || mbar_wait(saddr(b), parity & 1u)) return true;
         atomicOr(p.err, KDA_DEVERR_TIMEOUT);
-        abort_flag = 1;
-    };
-    auto wait = [&](uint64_t* b, uint32_t parity) {
-        if (!mbar_wait(saddr(b), parity & 1u)) fail();
-        return abort_flag == 0;
+        return false;
     };
     const bool work = share.left > 0;
     // Registers go from the warps that move data to those that hold rows: 2 x 208 + 88 = 3 x 168, what the launch has.
@@ -292,11 +296,23 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
                     if (!ok) break;
                     tc_fence_after();
                     __syncwarp();
-                    float s[4][32];
+                    float s[4][32], top[4];
+                    auto top_of = [&](int c) {
+                        top[c] = max3(s[c][0], s[c][1], s[c][2]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_fetch32(t_s + 32 * c, s[c]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_wait32(s[c]);
+                        for (int i = 3; i < 31; i += 2) top[c] = max3(top[c], s[c][i], s[c][i + 1]);
+                        top[c] = fmaxf(top[c], s[c][31]);
+                    };
+                    tmem_fetch32(t_s, s[0]);
+                    tmem_fetch32(t_s + 32, s[1]);
+                    tmem_wait32(s[0]);
+                    tmem_wait32(s[1]);
+                    tmem_fetch32(t_s + 64, s[2]);
+                    tmem_fetch32(t_s + 96, s[3]);
+                    top_of(0);                // (in vain where something is masked)
+                    top_of(1);
+                    tmem_wait32(s[2]);
+                    tmem_wait32(s[3]);
                     if (!open || f.BN < TILE) {
                         const int hi = min(pos - j0, f.BN - 1);
                         if (p.window == 0) {
@@ -308,15 +324,11 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
                             for (int c = 0; c < TILE; ++c)
                                 s[c / 32][c % 32] = c <= hi && (c > lo || c < near) ? s[c / 32][c % 32] : -INFINITY;
                         }
+                        top_of(0);
+                        top_of(1);
                     }
-                    float top[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        top[c] = max3(s[c][0], s[c][1], s[c][2]);
-#pragma unroll
-                        for (int i = 3; i < 31; i += 2) top[c] = max3(top[c], s[c][i], s[c][i + 1]);
-                        top[c] = fmaxf(top[c], s[c][31]);
-                    }
+                    top_of(2);
+                    top_of(3);
                     const float m = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     const bool move = (m - ref) * scale2 > SLACK;          // (NaN with nothing seen so far: no)
                     if (__any_sync(0xFFFFFFFFu, move)) {
@@ -353,12 +365,14 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
                             sum[i & 1] = add2(sum[i & 1], e);
                         }
                         tmem_st16(t_s + 16 * c, x);
+                        if (c % 2 == 1) {     // half of the weights: the product may begin
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive(&bar.p[blk][c / 2]);
+                        }
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive(&bar.p[blk]);
                 }
             }
             // The second block waits for the whole run also where it has no rows, and says so, so that neither side gets
@@ -477,13 +491,29 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
         for (uint32_t i = n > L::STAGES ? n - L::STAGES : 0; i < n; ++i) mbar_wait(saddr(&bar.full[i % L::STAGES]), (i / L::STAGES) & 1u);
     } else if (warp == QUERY_WARP && work) {
         // ---------------- queries ----------------
+        // Boxes of the heads that share a key and the tokens that fill a block, where the heads divide it; else row by row.
         bool ok = true;
+        uint32_t boxed = 0;                   // runs whose queries came in boxes
         Runs runs(p, f, share);
         do {
             const Walk& w = runs.w;
             const int run = runs.run, row0 = w.m * UNIT;
             if (run > 0) ok = wait(&bar.q_empty, run - 1);
             if (!ok) break;
+            if (q_boxes) {
+                const int blocks = w.u.rows > TILE ? 2 : 1, t0 = w.s.start + over(row0, f.by_group), step = over(TILE, f.by_group);
+                if (lane == 0) {
+                    mbar_expect_tx(saddr(&bar.q), (uint32_t)(blocks * L::BLOCK));
+                    for (int i = 0; i < blocks; ++i)
+#pragma unroll
+                        for (int h = 0; h < L::HALVES; ++h)
+                            tma_load_3d(sm_q + i * L::BLOCK + h * L::HALF, &q_map, h * 64, w.h * f.group, t0 + i * step, saddr(&bar.q));
+                }
+                __syncwarp();
+                ++boxed;
+                if (!runs.next(p, f)) break;
+                continue;
+            }
             constexpr int PER = D / 8;        // 16-byte columns of a row
             const int c = lane % PER;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)w.s.start * p.Hq + w.h * f.group) * D + c * 8;
@@ -500,6 +530,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
             if (lane == 0) arrive(&bar.q);
             if (!runs.next(p, f)) break;
         } while (true);
+        if (boxed) mbar_wait(saddr(&bar.q), (boxed - 1) & 1u);  // no copy is left in flight
     } else if (warp == HELP_WARP && work) {
         // ---------------- tiles that some row sees in part ----------------
         uint32_t n = 1;                       // V's stages are the odd ones
@@ -560,82 +591,71 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, const __grid_constant__
             if (!ok || !runs.next(p, f)) break;
         } while (true);
     } else if (warp == MMA_WARP && work) {
-        // ---------------- products ----------------
-        const uint32_t id_s = idesc_bf16(TILE, TILE), id_o = idesc_bf16(TILE, D) | (1u << 16);      // V's columns are contiguous
-        uint32_t nk = 0, np[2] = {0, 0}, fixed[4] = {0, 0, 0, 0};
-        bool ok = true;
-        auto scores = [&](int i, int st) {    // S_i = Q_i K^T
-            if (elect_one()) {
-                const uint32_t a = sm_q + i * L::BLOCK, b = sm_kv + st * L::BLOCK;
+        // ---------------- products: one thread ----------------
+        if (elect_one()) {
+            const uint32_t id_s = idesc_bf16(TILE, TILE), id_o = idesc_bf16(TILE, D) | (1u << 16);  // V's columns are contiguous
+            const uint64_t dq = desc_sw128(sm_q), dk = desc_sw128(sm_kv), dv = desc_v(sm_kv, L::HALF);
+            constexpr uint32_t STEP = L::BLOCK >> 4;           // descriptors count in 16 bytes
+            uint32_t nk = 0, n0 = 0, n1 = 0, fixed[4] = {0, 0, 0, 0};
+            bool ok = true;
+            auto scores = [&](int i, uint32_t st) {            // S_i = Q_i K^T
+                const uint64_t a = dq + i * STEP, b = dk + st * STEP;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t o = (ks / 4) * L::HALF + (ks % 4) * 32;
-                    umma_bf16_1(tmem + L::S + i * TILE, desc_sw128(a + o), desc_sw128(b + o), id_s, ks > 0);
+                    const uint32_t o = ((ks / 4) * L::HALF + (ks % 4) * 32) >> 4;
+                    umma_bf16_1(tmem + L::S + i * TILE, a + o, b + o, id_s, ks > 0);
                 }
                 umma_commit(saddr(&bar.s[i]));
-            }
-            __syncwarp();
-        };
-        Runs runs(p, f, share);
-        do {
-            const Walk& w = runs.w;
-            const int count = runs.count, tile = runs.tile, run = runs.run, last = last_pos(f, w), blocks = w.u.rows > TILE ? 2 : 1;
-            ok = wait(&bar.q, run) && wait(&bar.full[nk % L::STAGES], nk / L::STAGES);
-            if (!ok) break;
-            tc_fence_after();
-            for (int i = 0; i < blocks; ++i) scores(i, nk % L::STAGES);
-            if (elect_one()) {
+            };
+            Runs runs(p, f, share);
+            do {
+                const Walk& w = runs.w;
+                const int count = runs.count, tile = runs.tile, run = runs.run, last = last_pos(f, w), blocks = w.u.rows > TILE ? 2 : 1;
+                ok = wait(&bar.q, run) && wait(&bar.full[nk % L::STAGES], nk / L::STAGES);
+                if (!ok) break;
+                tc_fence_after();
+                for (int i = 0; i < blocks; ++i) scores(i, nk % L::STAGES);
                 umma_commit(saddr(&bar.empty[nk % L::STAGES]));
                 if (count == 1) umma_commit(saddr(&bar.q_empty));
-            }
-            __syncwarp();
-            for (int it = tile; it < tile + count && ok; ++it, nk += 2) {
-                const uint32_t nv = nk + 1, nn = nk + 2;
-                const int sv = nv % L::STAGES, sk = nn % L::STAGES;
-                const bool more = it + 1 < tile + count;
-                ok = wait(&bar.full[sv], nv / L::STAGES);
-                if (ok && !open_tile(p, f, w.u, last, tile_start(f, w.u, it))) {
-                    uint32_t phase = 0;
+                for (int it = tile; it < tile + count; ++it, nk += 2) {
+                    const uint32_t nv = nk + 1, nn = nk + 2, sv = nv % L::STAGES, sk = nn % L::STAGES;
+                    const bool more = it + 1 < tile + count;
+                    ok = wait(&bar.full[sv], nv / L::STAGES) && (!more || wait(&bar.full[sk], nn / L::STAGES));
+                    if (ok && !open_tile(p, f, w.u, last, tile_start(f, w.u, it))) {
+                        uint32_t phase = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i == sv / 2) phase = fixed[i]++;
-                    ok = wait(&bar.fixed[sv / 2], phase);
-                }
-                for (int i = 0; i < blocks && ok; ++i) {
-                    ok = wait(&bar.p[i], np[i]++);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t b = sm_kv + sv * L::BLOCK;
+                        for (int i = 0; i < 4; ++i)
+                            if (i == (int)sv / 2) phase = fixed[i]++;
+                        ok = wait(&bar.fixed[sv / 2], phase);
+                    }
+                    const uint64_t b = dv + sv * STEP;
+                    auto product = [&](int i, uint32_t& n) {   // O_i += P_i V, the weights' halves as they come
 #pragma unroll
-                        for (int ks = 0; ks < TILE / 16; ++ks)
-                            umma_bf16_ts(tmem + L::O + i * D, tmem + L::S + i * TILE + ks * 8, desc_v(b + ks * 2048, L::HALF), id_o,
-                                         it > tile || ks > 0);
+                        for (int half = 0; half < 2; ++half) {
+                            ok = ok && wait(&bar.p[i][half], n);
+                            if (!ok) return;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = half * (TILE / 32); ks < (half + 1) * (TILE / 32); ++ks)
+                                umma_bf16_ts(tmem + L::O + i * D, tmem + L::S + i * TILE + ks * 8, b + ks * (2048 >> 4), id_o, it > tile || ks > 0);
+                        }
+                        ++n;
                         umma_commit(saddr(&bar.pv[i]));
-                    }
-                    __syncwarp();
-                    if (more) {
-                        if (i == 0) ok = wait(&bar.full[sk], nn / L::STAGES);
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(i, sk);
-                    }
-                }
-                if (!ok) break;
-                if (elect_one()) {
+                        if (more) scores(i, sk);
+                    };
+                    product(0, n0);
+                    if (blocks == 2) product(1, n1);
+                    if (!ok) break;
                     umma_commit(saddr(&bar.empty[sv]));
                     if (more) umma_commit(saddr(&bar.empty[sk]));
                     if (it + 2 == tile + count) umma_commit(saddr(&bar.q_empty));
                 }
-                __syncwarp();
-            }
-            if (ok && run > 0) ok = wait(&bar.ack, run - 1);
-            if (!ok) break;
-            if (elect_one()) umma_commit(saddr(&bar.run));
-            __syncwarp();
-            if (!runs.next(p, f)) break;
-        } while (true);
-        if (elect_one()) umma_commit(saddr(&bar.done));
+                if (ok && run > 0) ok = wait(&bar.ack, run - 1);
+                if (!ok) break;
+                umma_commit(saddr(&bar.run));
+            } while (runs.next(p, f));
+            umma_commit(saddr(&bar.done));
+        }
         __syncwarp();
         mbar_wait(saddr(&bar.done), 0);       // no product is left in flight
     }
@@ -670,6 +690,16 @@ bool encode_pages(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries [T, H_q, d]: boxes of the heads that share a key and as many tokens as fill a block.
+bool encode_queries(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const ChunkParams& p) {
+    const int group = p.Hq / p.Hkv;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.Hq * p.d * 2};
+    const cuuint32_t boxes[3] = {64u, (cuuint32_t)group, (cuuint32_t)(TILE / group)}, ones[3] = {1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 cudaError_t launch_tc(const ChunkParams& p, cudaStream_t s) {
     static DeviceSetup done;
@@ -679,7 +709,10 @@ cudaError_t launch_tc(const ChunkParams& p, cudaStream_t s) {
     const auto enc = tensor_map_encoder();
     if (!enc) return cudaErrorNotSupported;
     const int box = box_of(p.page_size);
-    CUtensorMap k_map, v_map;
+    const int group = p.Hq / p.Hkv;
+    const bool q_boxes = group <= TILE && TILE % group == 0;
+    CUtensorMap q_map, k_map, v_map;
+    if (q_boxes ? !encode_queries(enc, &q_map, p) : (std::memset(&q_map, 0, sizeof q_map), false)) return cudaErrorInvalidValue;
     if (!encode_pages(enc, &k_map, p, p.k_pages, p.k_stride, box) || !encode_pages(enc, &v_map, p, p.v_pages, p.v_stride, box))
         return cudaErrorInvalidValue;
     ChunkPlan f = chunk_plan(p, UNIT, TILE / box * box);
@@ -688,7 +721,7 @@ cudaError_t launch_tc(const ChunkParams& p, cudaStream_t s) {
     // Where a unit has few tiles, whatever the lengths, pieces and a second kernel would cost more than they bring.
     f.whole = units <= 3 * (int64_t)grid && most_tiles(p, f) <= 2 * MIN_SHARE;
     if (f.whole) grid = (int)units;
-    kda_chunk_tc_kernel<D><<<grid, THREADS, TcLayout<D>::DYNAMIC, s>>>(p, f, box, k_map, v_map);
+    kda_chunk_tc_kernel<D><<<grid, THREADS, TcLayout<D>::DYNAMIC, s>>>(p, f, box, q_boxes, q_map, k_map, v_map);
     e = cudaGetLastError();
     return e != cudaSuccess || f.whole ? e : launch_join<__nv_bfloat16, D>(p, f, grid, TC_MAX_CTAS, s);
 }
