@@ -9,11 +9,11 @@
 //
 // One pass over the logits.  A row, or its parts on the CTAs of a cluster where there are few rows, streams through
 // registers in chunks, the next one under way while one is summed; a warp's lanes share their maximum, so that a rescale
-// is a branch that all of them take or none.  The best words are gathered on the way: the first chunk's k-th best thread
-// maximum bounds which of its words can be among the best (at most k threads hold any), and from then on only words
-// above the k-th best so far are written down, a few hundred a row.  Rows that rise (more than the list holds) are gone
-// through once more with the bound brought up to date after every chunk.  Nothing depends on the order of the atomics:
-// they place candidates in a list whose entries are then ranked.
+// is a branch that all of them take or none.  The best words are gathered on the way: the top-th best of 64 maxima in the
+// first chunk bounds them from below, and vectors with a word above that, a hundred or so a row, are written down and
+// looked at again when the row is through.  Rows with too many (words in order, equal logits) are gone through once more with
+// the bound brought up to date after every chunk.  Nothing depends on the order of the atomics: they place candidates in a
+// list whose entries are then ranked.
 #include <cooperative_groups.h>
 
 #include "kda_prompt.cuh"
@@ -26,12 +26,14 @@ namespace {
 constexpr int NT = 256, NW = NT / 32;
 constexpr int LOADS = 4;                      // 16-byte loads of a thread and chunk
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float FAR = 1e37f;                  // logits below -FAR count as that in the sums
 constexpr int MAX_TOP = KDA_LOGPROBS_MAX_TOP, MAX_CLUSTER = 8;
 
 template <typename T>
 struct Elems {
     static constexpr int W = 16 / sizeof(T), EPT = LOADS * W, CHUNK = NT * EPT;
     static constexpr int LIST = MAX_TOP + MAX_TOP * EPT;      // kept ones, and all words of `top` threads
+    static constexpr int VECTORS = 2 * LIST;                  // the same place while it holds vectors' numbers
 };
 
 __device__ __forceinline__ void unpack(const uint4& r, float* x, __nv_bfloat16) {
@@ -80,6 +82,35 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\nfma.rn.f32x2 x, x, y, z;\n"
+        "mov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // A word's place in the order: larger values first, then lower words.  A value that is not a number counts as -inf.
 __device__ __forceinline__ unsigned long long key_of(float x, int word) {
     x = x != x ? -INFINITY : x + 0.f;
@@ -104,15 +135,32 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
 }
 
 template <int LIST>
-struct Shared {
-    unsigned long long list[LIST];
+struct alignas(16) Shared {
+    union {
+        unsigned long long list[LIST + 2];    // (two more: it is ranked in pairs)
+        int vectors[2 * LIST];
+    };
     unsigned long long best[NT];              // thread maxima; at the end the best of all CTAs
+    float most[NT / 4];                       // group maxima
     unsigned long long out[MAX_TOP];
-    unsigned long long tau, bound;            // bound: key of the k-th best so far, 0 with fewer
+    unsigned long long bound;                 // key of the k-th best so far, 0 with fewer
     Sums sums[NW];
     Sums cta;
-    int count, overflow, found;
+    int count, found;
 };
+
+// How many of n keys, in pairs from a 16-byte place, are above k; keys[n] may be anything.
+__device__ __forceinline__ int keys_above(const unsigned long long* keys, int n, unsigned long long k) {
+    int rank = 0;
+    const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(keys);
+#pragma unroll 8
+    for (int j = 0; j < n / 2; ++j) {
+        const ulonglong2 x = pairs[j];
+        rank += (x.x > k) + (x.y > k);
+    }
+    if (n & 1) rank += keys[n - 1] > k;
+    return rank;
+}
 
 // Ranks the list and keeps its best `top` in out, in order; all threads.
 template <int LIST>
@@ -120,8 +168,7 @@ __device__ __forceinline__ void rank_list(Shared<LIST>& sm, int top, int tid) {
     const int n = sm.count;
     for (int e = tid; e < n; e += NT) {
         const unsigned long long k = sm.list[e];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += sm.list[j] > k;
+        const int rank = keys_above(sm.list, n, k);
         if (rank < top) sm.out[rank] = k;
     }
     __syncthreads();
@@ -133,11 +180,12 @@ __device__ __forceinline__ void rank_list(Shared<LIST>& sm, int top, int tid) {
 }
 
 // Takes a chunk's words into the list, whatever they are, and leaves the best `top` so far in list and out; all threads.
+// The top-th best thread maximum bounds the words that can be among the best: at most `top` threads hold one.
 template <int EPT, int W, int LIST>
 __device__ __forceinline__ void absorb(Shared<LIST>& sm, const float (&x)[EPT], int64_t e0, int V, int top, int tid) {
     const unsigned long long bound = sm.bound;
     unsigned long long best = 0;
-    auto key = [&](int i) -> unsigned long long {
+    auto key = [&](int i) {
         const int64_t word = e0 + (int64_t)(i / W) * NT * W + i % W;
         return word >= 0 && word < V ? key_of(x[i], (int)word) : 0ull;
     };
@@ -147,15 +195,13 @@ __device__ __forceinline__ void absorb(Shared<LIST>& sm, const float (&x)[EPT], 
         if (k > bound && k > best) best = k;
     }
     sm.best[tid] = best;
-    if (tid == 0) sm.tau = 1;
     __syncthreads();
-    if (best) {
-        int rank = 0;
-        for (int j = 0; j < NT; ++j) rank += sm.best[j] > best;
-        if (rank == top - 1) sm.tau = best;
+    unsigned long long tau = 1;               // every warp finds it for itself
+    for (int w = 0; w < NW; ++w) {
+        const unsigned long long k = sm.best[w * 32 + (tid & 31)];
+        const unsigned mine = __ballot_sync(0xFFFFFFFFu, k && keys_above(sm.best, NT, k) == top - 1);
+        if (mine) tau = __shfl_sync(0xFFFFFFFFu, k, __ffs(mine) - 1);
     }
-    __syncthreads();
-    const unsigned long long tau = sm.tau;
     if (best >= tau) {
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
@@ -182,7 +228,7 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
     const int off = (int)(reinterpret_cast<uintptr_t>(x0) / sizeof(T) % W);
     const int chunks = (int)(((int64_t)p.V + off + CHUNK - 1) / CHUNK);
     const int c0 = (int)((int64_t)chunks * part / cluster), c1 = (int)((int64_t)chunks * (part + 1) / cluster);
-    if (tid == 0) sm.count = 0, sm.overflow = 0, sm.found = 0, sm.bound = 0;
+    if (tid == 0) sm.count = 0, sm.found = 0, sm.bound = 0;
     __syncthreads();
 
     uint4 raw[LOADS];
@@ -191,7 +237,7 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) raw[j] = load_vec(x0, first(c) + j * (NT * W), p.V);
     };
-    float m = -INFINITY, r = 0.f, t = 0.f, least = 0.f;
+    float m = -INFINITY, base = 0.f, r = 0.f, t = 0.f, least = -INFINITY;  // base: m, in reach
     bool own = false;                         // this lane holds the word that has m and stays out of r
     if (c0 < c1) load(c0);
     for (int c = c0; c < c1; ++c) {
@@ -199,22 +245,40 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) unpack(raw[j], x + j * W, T());
         if (c + 1 < c1) load(c + 1);
-        float top_x = x[0];
+        float most[LOADS];
 #pragma unroll
-        for (int i = 1; i < EPT; ++i) top_x = fmaxf(top_x, x[i]);
+        for (int j = 0; j < LOADS; ++j) {
+            most[j] = fmaxf(x[j * W], x[j * W + 1]);
+#pragma unroll
+            for (int i = 2; i < W; i += 2) most[j] = max3(most[j], x[j * W + i], x[j * W + i + 1]);
+        }
+        const float top_x = fmaxf(max3(most[0], most[1], most[2]), most[3]);
         if constexpr (TOP) {
-            if (c == c0) {
-                absorb<EPT, W>(sm, x, first(c), p.V, p.top, tid);
-                least = sm.bound ? key_value(sm.bound) : -INFINITY;
-            } else if (top_x > least) {       // a later word that equals the k-th best is behind it
+            if (c == c0) {                    // the top-th best of the maxima of 64 groups of four threads
+                float group = fmaxf(top_x, __shfl_xor_sync(0xFFFFFFFFu, top_x, 1));
+                group = fmaxf(group, __shfl_xor_sync(0xFFFFFFFFu, group, 2));
+                if (lane % 4 == 0) sm.most[tid / 4] = group;
+                __syncthreads();
+                const float a = sm.most[lane], b = sm.most[lane + 32];
+                int above_a = 0, above_b = 0;
+#pragma unroll 4
+                for (int j = 0; j < NT / 16; ++j) {
+                    const float4 y = reinterpret_cast<const float4*>(sm.most)[j];
+                    above_a += (y.x > a) + (y.y > a) + (y.z > a) + (y.w > a);
+                    above_b += (y.x > b) + (y.y > b) + (y.z > b) + (y.w > b);
+                }
+                // the smallest maximum with fewer than `top` above it
+                least = fminf(above_a < p.top ? a : INFINITY, above_b < p.top ? b : INFINITY);
 #pragma unroll
-                for (int i = 0; i < EPT; ++i)
-                    if (x[i] > least) {
+                for (int o = 16; o; o >>= 1) least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+            }
+            // (in later chunks a word that equals the bound is behind at least `top` others)
+            if (c == c0 ? !(top_x < least) : top_x > least) {  // (a NaN counts as -inf, which may be the bound)
+#pragma unroll
+                for (int j = 0; j < LOADS; ++j)
+                    if (c == c0 ? !(most[j] < least) : most[j] > least) {
                         const int at = atomicAdd(&sm.count, 1);
-                        if (at < E::LIST)
-                            sm.list[at] = key_of(x[i], (int)(first(c) + (int64_t)(i / W) * NT * W + i % W));
-                        else
-                            sm.overflow = 1;
+                        if (at < E::VECTORS) sm.vectors[at] = (c * LOADS + j) * NT + tid;
                     }
             }
         }
@@ -228,6 +292,7 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
                 r = sum * f;
             }
             m = all;
+            base = fmaxf(all, -FAR);
             own = lane == __ffs(__ballot_sync(0xFFFFFFFFu, top_x == all)) - 1;
             if (own) {
                 bool out = false;
@@ -239,18 +304,25 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
                     }
             }
         }
-        const float base = m == -INFINITY ? 0.f : m;
-        float ra = 0.f, rb = 0.f, ta = 0.f, tb = 0.f;
+        // Words without weight (-inf, the type's lowest value) get a finite place far down, so that 0 times their exponent is
+        // 0.  Where nothing better than the lowest value has come yet, those have weight and -inf has not.
+        if (m <= -FAR) {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) x[i] = x[i] == -INFINITY ? -20.f * FAR : max_nan(x[i], -FAR);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) x[i] = max_nan(x[i], -FAR);
+        }
+        float2 r2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < EPT; i += 2) {
-            float ya = (x[i] - base) * LOG2E, yb = (x[i + 1] - base) * LOG2E;
-            if constexpr (ENTROPY) ya = max_nan(ya, -1000.f), yb = max_nan(yb, -1000.f);
-            const float ea = exp2_approx(ya), eb = exp2_approx(yb);
-            ra += ea, rb += eb;
-            if constexpr (ENTROPY) ta = fmaf(ea, ya, ta), tb = fmaf(eb, yb, tb);
+            const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-base, -base)), make_float2(LOG2E, LOG2E));
+            const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+            r2 = add2(r2, e);
+            if constexpr (ENTROPY) t2 = fma2(e, y, t2);
         }
-        r += ra + rb;
-        if constexpr (ENTROPY) t += ta + tb;
+        r += r2.x + r2.y;
+        if constexpr (ENTROPY) t += t2.x + t2.y;
     }
 
     // ---- the warp's sums (its lanes have one m), the CTA's ----
@@ -262,7 +334,36 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
     if (lane == 0) sm.sums[warp] = Sums{m, r, t};
     __syncthreads();
     if constexpr (TOP) {
-        if (sm.overflow) {                    // once more, with the bound brought up to date after every chunk
+        // the vectors written down, once more: their words from the bound up
+        const int n = sm.count;
+        int mine[(E::VECTORS + NT - 1) / NT];
+#pragma unroll
+        for (int i = 0; i < (E::VECTORS + NT - 1) / NT; ++i) mine[i] = tid + i * NT < n && tid + i * NT < E::VECTORS ? sm.vectors[tid + i * NT] : -1;
+        __syncthreads();
+        if (tid == 0) sm.count = 0;
+        __syncthreads();
+        if (n <= E::VECTORS) {
+#pragma unroll 1
+            for (int i = 0; i < (E::VECTORS + NT - 1) / NT; ++i) {
+                int v = mine[0];
+#pragma unroll
+                for (int k = 1; k < (E::VECTORS + NT - 1) / NT; ++k) v = i == k ? mine[k] : v;
+                if (v < 0) continue;
+                const int64_t e = (int64_t)v * W - off;
+                float x[W];
+                unpack(load_vec(x0, e, p.V), x, T());
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    if (!(x[k] < least) && e + k >= 0 && e + k < p.V) {
+                        const int at = atomicAdd(&sm.count, 1);
+                        if (at < E::LIST) sm.list[at] = key_of(x[k], (int)(e + k));
+                    }
+            }
+        }
+        __syncthreads();
+        if (n > E::VECTORS || sm.count > E::LIST || (c0 < c1 && sm.count < p.top)) {
+            // Too many (words in order, equal logits), or NaNs where a bound was looked for: every chunk once more, the bound
+            // brought up to date after each.
             __syncthreads();
             if (tid == 0) sm.count = 0, sm.found = 0, sm.bound = 0;
             __syncthreads();
@@ -273,7 +374,7 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
                 for (int j = 0; j < LOADS; ++j) unpack(raw[j], x + j * W, T());
                 absorb<EPT, W>(sm, x, first(c), p.V, p.top, tid);
             }
-        } else if (c1 > c0 + 1) {
+        } else {
             rank_list(sm, p.top, tid);
         }
     }
@@ -297,9 +398,8 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
                 if (i < cluster && e < *group.map_shared_rank(&sm.found, i)) k = group.map_shared_rank(sm.out, i)[e];
                 sm.best[tid] = k;
                 __syncthreads();
-                int rank = 0;
-                for (int j = 0; j < NT; ++j) rank += sm.best[j] > k;
-                if (k && rank < p.top) sm.list[rank] = k;
+                const int rank = k ? keys_above(sm.best, NT, k) : MAX_TOP;
+                if (rank < p.top) sm.list[rank] = k;
                 __syncthreads();
                 if (tid < p.top) sm.out[tid] = sm.list[tid];
                 __syncthreads();
@@ -309,7 +409,7 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
         if (part) return;
     }
     const float log_r = log1pf(s.r);
-    const bool bad = s.r != s.r || s.m == INFINITY, empty = s.m == -INFINITY && !bad;
+    const bool bad = s.r != s.r || s.m > FAR, empty = s.m == -INFINITY && !bad;
     const float nan = __int_as_float(0x7FC00000);
     auto log_p = [&](float x) { return bad ? nan : empty ? -INFINITY : (x - s.m) - log_r; };
     if (tid == 0) {

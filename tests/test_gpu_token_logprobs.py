@@ -143,6 +143,31 @@ def test_rows_with_nothing_allowed_and_with_values_that_are_not_finite(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masks_of_the_types_lowest_value(dtype):
+    """Words masked by the lowest finite value, and a row of nothing else, which is a flat one."""
+    low = torch.finfo(DT[dtype]).min
+    logits, tokens = make(4, 20000, dtype)
+    logits[0, 100:] = low
+    logits[1, :19990] = low
+    logits[2] = low
+    logits[3, ::2], logits[3, 1::2] = low, -math.inf
+    tokens[:] = torch.tensor([5, 19995, 7, 8], dtype=torch.int32)
+    r = kda.kda_token_logprobs(logits, tokens, top=4, entropy=True)
+    logp, _, H, best, word = reference(logits, tokens, 4)
+    near(r.logp, logp)
+    near(r.entropy, H)
+    near(r.top_logp, best)
+    assert torch.equal(r.top_token, word) and r.top_token[2].tolist() == [0, 1, 2, 3]
+    assert float(r.lse[2]) == float(torch.tensor(low, dtype=torch.float32))
+    nans = logits.clone()
+    nans[0, 3], nans[0, 50] = math.nan, math.nan
+    nans[0, 100:] = -math.inf
+    nans[0, 8:100] = -math.inf
+    r = kda.kda_token_logprobs(nans, tokens, top=12)
+    assert r.top_token[0].tolist()[7:] == [3, 8, 9, 10, 11] and sorted(r.top_token[0].tolist()[:7]) == [0, 1, 2, 4, 5, 6, 7]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_tokens_outside_are_reported(dtype):
     logits, tokens = make(4, 100, dtype)
     tokens[1], tokens[2], tokens[3] = 100, -2, -2 ** 31
