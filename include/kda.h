@@ -610,8 +610,7 @@ KDA_API kda_status kda_attention_prefill(const void* q, const void* k_pages, con
  *
  * and the `top` likeliest words of each row, the lowest word first among equal logits (a NaN counts as -inf there).
  * A small -logp or entropy keeps its relative precision.  A row with nothing above -inf gives lse and every log
- * probability -inf and entropy 0; a row with a NaN or a logit above 10^37 gives NaNs.  Finite logits below -10^37 (a mask
- * of the type's lowest value) count as equal in the sums.
+ * probability -inf and entropy 0; a row with a NaN or +inf gives NaNs.
  *   logits    [T, V] dtype dt, row t at logits + t * row_stride (elements, >= V)
  *   tokens    [T] int32, -1: none (logp_t = 0); one outside [-1, V) counts as -1 and sets KDA_DEVERR_TOKEN
  *   logp [T];  lse [T] or NULL;  entropy [T] or NULL

@@ -137,27 +137,6 @@ __device__ __forceinline__ int last_pos(const ChunkPlan& f, const Walk& w) {
     return w.s.len - w.s.n + over(w.m * UNIT + w.u.rows - 1, f.by_group);
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\nfma.rn.f32x2 x, x, y, z;\n"
-        "mov.b64 {%0, %1}, x;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
 // 64 bytes of a row: whole 32-byte sectors at a time where the address allows it, since each lane has a row of its own.
 __device__ __forceinline__ void store64(void* to, const uint32_t (&x)[16], bool wide) {
     uint32_t* p = static_cast<uint32_t*>(to);
@@ -352,17 +331,17 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                         ref = to;
                     }
                     const float base = ref == -INFINITY ? 0.f : ref * scale2;
-                    const float2 by2 = make_float2(scale2, scale2), minus = make_float2(-base, -base);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const Pair by2 = pair_of(scale2, scale2), minus = pair_of(-base, -base);
+                    Pair sum[2] = {pair_of(0.f, 0.f), pair_of(0.f, 0.f)};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         float x[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float2 y = fma2(make_float2(s[c][2 * i], s[c][2 * i + 1]), by2, minus);
-                            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                            x[i] = __uint_as_float(pack_bf16x2(e.x, e.y));
-                            sum[i & 1] = add2(sum[i & 1], e);
+                            const float2 y = both(fma2(pair_of(s[c][2 * i], s[c][2 * i + 1]), by2, minus));
+                            const float a = ex2_approx(y.x), b = ex2_approx(y.y);
+                            x[i] = __uint_as_float(pack_bf16x2(a, b));
+                            sum[i & 1] = add2(sum[i & 1], pair_of(a, b));
                         }
                         tmem_st16(t_s + 16 * c, x);
                         if (c % 2 == 1) {     // half of the weights: the product may begin
@@ -372,7 +351,8 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                             if (lane == 0) arrive(&bar.p[blk][c / 2]);
                         }
                     }
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    const float2 sums2 = both(add2(sum[0], sum[1]));
+                    l += sums2.x + sums2.y;
                 }
             }
             // The second block waits for the whole run also where it has no rows, and says so, so that neither side gets

@@ -15,19 +15,6 @@
 namespace kda {
 namespace {
 
-// t / n for 0 <= t < 2^31 and a divisor that the host knows, as a multiplication.
-struct Divisor {
-    uint32_t magic;
-    int32_t shift;
-};
-inline Divisor divisor(int32_t n) {
-    Divisor d{0u, 0};
-    while ((2ll << d.shift) < n) ++d.shift;
-    if (n > 1) d.magic = (uint32_t)((1ull << (32 + d.shift)) / n + 1);
-    return d;
-}
-__device__ __forceinline__ int over(int t, const Divisor& d) { return d.magic ? (int)(__umulhi((uint32_t)t, d.magic) >> d.shift) : t; }
-
 struct ChunkPlan {
     int32_t group;               // query heads of a key-value head
     int32_t BM;                  // rows of a unit, a power of two

@@ -23,17 +23,17 @@ namespace cg = cooperative_groups;
 namespace kda {
 namespace {
 
-constexpr int NT = 256, NW = NT / 32;
-constexpr int LOADS = 4;                      // 16-byte loads of a thread and chunk
+constexpr int NT = 128, NW = NT / 32;
+constexpr int LOADS = 2;                      // 16-byte loads of a thread and chunk
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-constexpr float FAR = 1e37f;                  // logits below -FAR count as that in the sums
+constexpr int GROUPS = 64;                    // of threads, whose maxima give the bound: twice as many as a top may ask for
 constexpr int MAX_TOP = KDA_LOGPROBS_MAX_TOP, MAX_CLUSTER = 8;
 
 template <typename T>
 struct Elems {
     static constexpr int W = 16 / sizeof(T), EPT = LOADS * W, CHUNK = NT * EPT;
     static constexpr int LIST = MAX_TOP + MAX_TOP * EPT;      // kept ones, and all words of `top` threads
-    static constexpr int VECTORS = 2 * LIST;                  // the same place while it holds vectors' numbers
+    static constexpr int VECTORS = 2 * LIST;                  // those of a row that are looked at again
 };
 
 __device__ __forceinline__ void unpack(const uint4& r, float* x, __nv_bfloat16) {
@@ -82,35 +82,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\nfma.rn.f32x2 x, x, y, z;\n"
-        "mov.b64 {%0, %1}, x;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-
 // A word's place in the order: larger values first, then lower words.  A value that is not a number counts as -inf.
 __device__ __forceinline__ unsigned long long key_of(float x, int word) {
     x = x != x ? -INFINITY : x + 0.f;
@@ -136,12 +107,11 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
 
 template <int LIST>
 struct alignas(16) Shared {
-    union {
-        unsigned long long list[LIST + 2];    // (two more: it is ranked in pairs)
-        int vectors[2 * LIST];
-    };
-    unsigned long long best[NT];              // thread maxima; at the end the best of all CTAs
-    float most[NT / 4];                       // group maxima
+    unsigned long long list[LIST + 2];        // (two more: it is ranked in pairs)
+    int vectors[2 * LIST];
+    unsigned long long best[MAX_CLUSTER * MAX_TOP > NT ? MAX_CLUSTER * MAX_TOP : NT];      // thread maxima; at the end the best of all CTAs
+    float most[GROUPS];                       // group maxima
+    float least;
     unsigned long long out[MAX_TOP];
     unsigned long long bound;                 // key of the k-th best so far, 0 with fewer
     Sums sums[NW];
@@ -217,7 +187,7 @@ __device__ __forceinline__ void absorb(Shared<LIST>& sm, const float (&x)[EPT], 
 }
 
 template <typename T, bool TOP, bool ENTROPY>
-__global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, int cluster) {
+__global__ void __launch_bounds__(NT, 8) kda_logprobs_kernel(LogprobParams p, int cluster) {
     using E = Elems<T>;
     constexpr int W = E::W, EPT = E::EPT, CHUNK = E::CHUNK;
     __shared__ Shared<TOP ? E::LIST : 1> sm;
@@ -233,11 +203,25 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
 
     uint4 raw[LOADS];
     auto first = [&](int c) { return (int64_t)c * CHUNK + tid * W - off; };
+    // chunks that lie in the row as a whole need no look at its ends
+    const uint4* in = reinterpret_cast<const uint4*>(x0 - off) + tid;
+    const int inner = off ? 1 : 0, outer = (int)(((int64_t)p.V + off) / CHUNK);
     auto load = [&](int c) {
+        if (c >= inner && c < outer) {
 #pragma unroll
-        for (int j = 0; j < LOADS; ++j) raw[j] = load_vec(x0, first(c) + j * (NT * W), p.V);
+            for (int j = 0; j < LOADS; ++j) raw[j] = __ldcs(in + (int64_t)c * (LOADS * NT) + j * NT);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < LOADS; ++j) {
+                const uint4 v = load_vec(x0, first(c) + j * (NT * W), p.V);
+#pragma unroll
+                for (int k = 0; k < LOADS; ++k)
+                    if (k == j) raw[k] = v;
+            }
+        }
     };
-    float m = -INFINITY, base = 0.f, r = 0.f, t = 0.f, least = -INFINITY;  // base: m, in reach
+    float m = -INFINITY, r = 0.f, t = 0.f, least = -INFINITY, so_far = -INFINITY;    // m: of the warp
+    int from = c0;                            // chunk that the bound is from
     bool own = false;                         // this lane holds the word that has m and stays out of r
     if (c0 < c1) load(c0);
     for (int c = c0; c < c1; ++c) {
@@ -252,31 +236,40 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
 #pragma unroll
             for (int i = 2; i < W; i += 2) most[j] = max3(most[j], x[j * W + i], x[j * W + i + 1]);
         }
-        const float top_x = fmaxf(max3(most[0], most[1], most[2]), most[3]);
+        const float top_x = fmaxf(most[0], most[1]);
         if constexpr (TOP) {
-            if (c == c0) {                    // the top-th best of the maxima of 64 groups of four threads
-                float group = fmaxf(top_x, __shfl_xor_sync(0xFFFFFFFFu, top_x, 1));
-                group = fmaxf(group, __shfl_xor_sync(0xFFFFFFFFu, group, 2));
-                if (lane % 4 == 0) sm.most[tid / 4] = group;
-                __syncthreads();
-                const float a = sm.most[lane], b = sm.most[lane + 32];
-                int above_a = 0, above_b = 0;
-#pragma unroll 4
-                for (int j = 0; j < NT / 16; ++j) {
-                    const float4 y = reinterpret_cast<const float4*>(sm.most)[j];
-                    above_a += (y.x > a) + (y.y > a) + (y.z > a) + (y.w > a);
-                    above_b += (y.x > b) + (y.y > b) + (y.z > b) + (y.w > b);
-                }
-                // the smallest maximum with fewer than `top` above it
-                least = fminf(above_a < p.top ? a : INFINITY, above_b < p.top ? b : INFINITY);
+            // The bound: the top-th best of the maxima of 64 groups of threads, so far; anew after 1, 2, 4, 8 chunks.
+            so_far = fmaxf(so_far, top_x);
+            if (((c - c0) & (c - c0 + 1)) == 0 && c - c0 < 8) {
+                float group = so_far;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+                for (int o = 1; o < NT / GROUPS; o <<= 1) group = fmaxf(group, __shfl_xor_sync(0xFFFFFFFFu, group, o));
+                if (tid % (NT / GROUPS) == 0) sm.most[tid / (NT / GROUPS)] = group;
+                __syncthreads();
+                if (warp == 0) {              // the smallest maximum with fewer than `top` above it
+                    const float a = sm.most[lane], b = sm.most[lane + 32];
+                    int above_a = 0, above_b = 0;
+#pragma unroll 4
+                    for (int j = 0; j < GROUPS / 4; ++j) {
+                        const float4 y = reinterpret_cast<const float4*>(sm.most)[j];
+                        above_a += (y.x > a) + (y.y > a) + (y.z > a) + (y.w > a);
+                        above_b += (y.x > b) + (y.y > b) + (y.z > b) + (y.w > b);
+                    }
+                    float l = fminf(above_a < p.top ? a : INFINITY, above_b < p.top ? b : INFINITY);
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) l = fminf(l, __shfl_xor_sync(0xFFFFFFFFu, l, o));
+                    if (lane == 0) sm.least = l;
+                }
+                __syncthreads();
+                least = sm.least;
+                from = c;
             }
-            // (in later chunks a word that equals the bound is behind at least `top` others)
-            if (c == c0 ? !(top_x < least) : top_x > least) {  // (a NaN counts as -inf, which may be the bound)
+            // A word that equals the bound counts while the chunk that set it may hold it; in later chunks it is behind at
+            // least `top` others.  (A NaN counts as -inf, which may be the bound.)
+            if (c == from ? !(top_x < least) : top_x > least) {
 #pragma unroll
                 for (int j = 0; j < LOADS; ++j)
-                    if (c == c0 ? !(most[j] < least) : most[j] > least) {
+                    if (c == from ? !(most[j] < least) : most[j] > least) {
                         const int at = atomicAdd(&sm.count, 1);
                         if (at < E::VECTORS) sm.vectors[at] = (c * LOADS + j) * NT + tid;
                     }
@@ -292,7 +285,6 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
                 r = sum * f;
             }
             m = all;
-            base = fmaxf(all, -FAR);
             own = lane == __ffs(__ballot_sync(0xFFFFFFFFu, top_x == all)) - 1;
             if (own) {
                 bool out = false;
@@ -304,25 +296,23 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
                     }
             }
         }
-        // Words without weight (-inf, the type's lowest value) get a finite place far down, so that 0 times their exponent is
-        // 0.  Where nothing better than the lowest value has come yet, those have weight and -inf has not.
-        if (m <= -FAR) {
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) x[i] = x[i] == -INFINITY ? -20.f * FAR : max_nan(x[i], -FAR);
-        } else {
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) x[i] = max_nan(x[i], -FAR);
-        }
-        float2 r2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
+        const float base = m == -INFINITY ? 0.f : m;
+        Pair r2 = pair_of(0.f, 0.f), t2 = r2;
+        const Pair minus = pair_of(-base, -base), by = pair_of(LOG2E, LOG2E);
 #pragma unroll
         for (int i = 0; i < EPT; i += 2) {
-            const float2 y = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-base, -base)), make_float2(LOG2E, LOG2E));
-            const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+            Pair y = mul2(add2(pair_of(x[i], x[i + 1]), minus), by);
+            float2 v = both(y);
+            if constexpr (ENTROPY) {          // 0 * -inf must not be met
+                v = make_float2(max_nan(v.x, -1000.f), max_nan(v.y, -1000.f));
+                y = pair_of(v.x, v.y);
+            }
+            const Pair e = pair_of(exp2_approx(v.x), exp2_approx(v.y));
             r2 = add2(r2, e);
             if constexpr (ENTROPY) t2 = fma2(e, y, t2);
         }
-        r += r2.x + r2.y;
-        if constexpr (ENTROPY) t += t2.x + t2.y;
+        r += both(r2).x + both(r2).y;
+        if constexpr (ENTROPY) t += both(t2).x + both(t2).y;
     }
 
     // ---- the warp's sums (its lanes have one m), the CTA's ----
@@ -336,20 +326,13 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
     if constexpr (TOP) {
         // the vectors written down, once more: their words from the bound up
         const int n = sm.count;
-        int mine[(E::VECTORS + NT - 1) / NT];
-#pragma unroll
-        for (int i = 0; i < (E::VECTORS + NT - 1) / NT; ++i) mine[i] = tid + i * NT < n && tid + i * NT < E::VECTORS ? sm.vectors[tid + i * NT] : -1;
         __syncthreads();
         if (tid == 0) sm.count = 0;
         __syncthreads();
         if (n <= E::VECTORS) {
 #pragma unroll 1
-            for (int i = 0; i < (E::VECTORS + NT - 1) / NT; ++i) {
-                int v = mine[0];
-#pragma unroll
-                for (int k = 1; k < (E::VECTORS + NT - 1) / NT; ++k) v = i == k ? mine[k] : v;
-                if (v < 0) continue;
-                const int64_t e = (int64_t)v * W - off;
+            for (int i = tid; i < n; i += NT) {
+                const int64_t e = (int64_t)sm.vectors[i] * W - off;
                 float x[W];
                 unpack(load_vec(x0, e, p.V), x, T());
 #pragma unroll
@@ -393,13 +376,16 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
         if (part == 0) {
             for (int i = 1; i < cluster; ++i) s = join(s, *group.map_shared_rank(&sm.cta, i));
             if constexpr (TOP) {
-                const int i = tid / MAX_TOP, e = tid % MAX_TOP;           // MAX_CLUSTER * MAX_TOP keys: one a thread
-                unsigned long long k = 0;
-                if (i < cluster && e < *group.map_shared_rank(&sm.found, i)) k = group.map_shared_rank(sm.out, i)[e];
-                sm.best[tid] = k;
+                for (int x = tid; x < MAX_CLUSTER * MAX_TOP; x += NT) {
+                    const int i = x / MAX_TOP, e = x % MAX_TOP;
+                    sm.best[x] = i < cluster && e < *group.map_shared_rank(&sm.found, i) ? group.map_shared_rank(sm.out, i)[e] : 0ull;
+                }
                 __syncthreads();
-                const int rank = k ? keys_above(sm.best, NT, k) : MAX_TOP;
-                if (rank < p.top) sm.list[rank] = k;
+                for (int x = tid; x < MAX_CLUSTER * MAX_TOP; x += NT) {
+                    const unsigned long long k = sm.best[x];
+                    const int rank = k ? keys_above(sm.best, MAX_CLUSTER * MAX_TOP, k) : MAX_TOP;
+                    if (rank < p.top) sm.list[rank] = k;
+                }
                 __syncthreads();
                 if (tid < p.top) sm.out[tid] = sm.list[tid];
                 __syncthreads();
@@ -409,7 +395,7 @@ __global__ void __launch_bounds__(NT, 3) kda_logprobs_kernel(LogprobParams p, in
         if (part) return;
     }
     const float log_r = log1pf(s.r);
-    const bool bad = s.r != s.r || s.m > FAR, empty = s.m == -INFINITY && !bad;
+    const bool bad = s.r != s.r || s.m == INFINITY, empty = s.m == -INFINITY && !bad;
     const float nan = __int_as_float(0x7FC00000);
     auto log_p = [&](float x) { return bad ? nan : empty ? -INFINITY : (x - s.m) - log_r; };
     if (tid == 0) {

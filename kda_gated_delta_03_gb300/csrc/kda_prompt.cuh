@@ -7,6 +7,52 @@
 
 namespace kda {
 
+// Pairs of fp32 numbers in one 64-bit register, and their operations: two in one instruction.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+    Pair d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 both(Pair x) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(x));
+    return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// t / n for 0 <= t < 2^31 and a divisor that the host knows, as a multiplication.
+struct Divisor {
+    uint32_t magic;
+    int32_t shift;
+};
+inline Divisor divisor(int32_t n) {
+    Divisor d{0u, 0};
+    while ((2ll << d.shift) < n) ++d.shift;
+    if (n > 1) d.magic = (uint32_t)((1ull << (32 + d.shift)) / n + 1);
+    return d;
+}
+__device__ __forceinline__ int over(int t, const Divisor& d) { return d.magic ? (int)(__umulhi((uint32_t)t, d.magic) >> d.shift) : t; }
+
 // Rotary positions, and tokens into cache pages.  Without `append` a token's position is positions[t] and keys go
 // to k_out; with it, a packed batch's tokens go to their places in the pages.  Strides in elements.
 struct RotaryParams {
