@@ -17,9 +17,9 @@
 namespace kda {
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 128;
 constexpr int MAX_N = 64;                     // pairs of a head
-constexpr int MAX_TB = 4;                     // tokens of a CTA
+constexpr int MAX_TB = 2;                     // tokens of a CTA
 
 template <typename T, int VEC>
 struct alignas(sizeof(T) * VEC) Vec {
@@ -58,9 +58,16 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t, int 
     return lo;
 }
 
+// A token's work: for each head of q and k `turned` items that rotate, then copied vectors; then v's vectors, `whole` a head.
+// In the half layout an item is VEC pairs in two vectors, in the interleaved one a vector (or, one element at a time, a pair).
+struct Items {
+    int32_t turned, items, whole, total;
+    Divisor by_items, by_whole, by_total;
+};
+
 // VEC elements at a time: 16 bytes where everything is aligned to them, one element else.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(NT) kda_rotary_kernel(RotaryParams p, int TB) {
+__global__ void __launch_bounds__(NT) kda_rotary_kernel(RotaryParams p, Items g, int TB) {
     using V = Vec<T, VEC>;
     __shared__ float2 turn[MAX_TB][MAX_N];                     // cos, sin
     __shared__ int pos_s[MAX_TB];
@@ -114,23 +121,18 @@ __global__ void __launch_bounds__(NT) kda_rotary_kernel(RotaryParams p, int TB) 
         __syncthreads();
     }
 
-    // A head's work: `turned` items that rotate, then copied vectors.  In the half layout an item is VEC pairs in two
-    // vectors, in the interleaved one a vector (or, one element at a time, a pair).
-    const int per = p.interleaved ? (VEC > 1 ? VEC / 2 : 1) : VEC;         // pairs of an item
-    const int turned = n / per, copied = (p.d - 2 * n) / VEC, items = turned + copied;
-    const int whole = p.v ? p.d / VEC : 0;
-    const int total = (p.Hq + p.Hkv) * items + p.Hkv * whole;              // of a token
-    for (int j = 0; j < tokens; ++j) {
-        if (!real_s[j]) continue;
-        const int t = t0 + j;
-        const int64_t page = p.append ? page_s[j] : 0;
-        for (int w = tid; w < total; w += NT) {
+    const int heads = (p.Hq + p.Hkv) * g.items, all = tokens * g.total;
+    {
+        for (int w0 = tid; w0 < all; w0 += NT) {
+            const int j = over(w0, g.by_total), w = w0 - j * g.total;
+            if (!real_s[j]) continue;
+            const int64_t t = t0 + j, page = p.append ? page_s[j] : 0;
             const T* src;
             T* dst;
             int item;
-            if (w < (p.Hq + p.Hkv) * items) {
-                const int h = w / items;
-                item = w - h * items;
+            if (w < heads) {
+                const int h = over(w, g.by_items);
+                item = w - h * g.items;
                 if (h < p.Hq) {
                     src = static_cast<const T*>(p.q) + t * p.q_stride + h * p.d;
                     dst = static_cast<T*>(p.q_out) + t * p.q_out_stride + h * p.d;
@@ -146,14 +148,14 @@ __global__ void __launch_bounds__(NT) kda_rotary_kernel(RotaryParams p, int TB) 
                 }
             } else {
                 if (page < 0) continue;
-                const int x = w - (p.Hq + p.Hkv) * items, h = x / whole, c = (x - h * whole) * VEC;
+                const int x = w - heads, h = over(x, g.by_whole), c = (x - h * g.whole) * VEC;
                 *reinterpret_cast<V*>(static_cast<T*>(p.v_pages) + page * p.v_page_stride +
                                       ((int64_t)h * p.page_size + slot_s[j]) * p.d + c) =
                     *reinterpret_cast<const V*>(static_cast<const T*>(p.v) + t * p.v_stride + h * p.d + c);
                 continue;
             }
-            if (item >= turned) {
-                const int c = 2 * n + (item - turned) * VEC;
+            if (item >= g.turned) {
+                const int c = 2 * n + (item - g.turned) * VEC;
                 *reinterpret_cast<V*>(dst + c) = *reinterpret_cast<const V*>(src + c);
             } else if (!p.interleaved) {
                 const int c = item * VEC;
@@ -198,12 +200,27 @@ cudaError_t launch(const RotaryParams& p, cudaStream_t s) {
     const int64_t odd = p.q_stride | p.k_stride | p.v_stride | p.q_out_stride | p.k_out_stride;
     const bool wide = odd % W == 0 && on16(p.q) && on16(p.k) && on16(p.v) && on16(p.q_out) && on16(p.k_out) &&
                       (p.interleaved ? 2 * n : n) % W == 0 && (p.d - 2 * n) % W == 0;
-    const int TB = 1;
+    const int vec = wide ? W : 1, per = p.interleaved ? (wide ? W / 2 : 1) : vec;      // pairs of an item
+    Items g;
+    g.turned = n / per;
+    g.items = g.turned + (p.d - 2 * n) / vec;
+    g.whole = p.append ? p.d / vec : 0;
+    g.total = (p.Hq + p.Hkv) * g.items + p.Hkv * g.whole;
+    g.by_items = divisor(g.items);
+    g.by_whole = divisor(g.whole > 0 ? g.whole : 1);
+    g.by_total = divisor(g.total);
+    // Two tokens a CTA share the frequencies' conversion (16,384 tokens of 40 heads 56 us, with one 57, with four 59); one
+    // while the CTAs would not fill the GPU otherwise.
+    static DeviceSetup done;
+    int sms = 0;
+    const cudaError_t e = device_setup(done, nullptr, 0, &sms);
+    if (e != cudaSuccess) return e;
+    const int TB = p.T > 8 * sms ? MAX_TB : 1;
     const int grid = (int)(((int64_t)p.T + TB - 1) / TB);
     if (wide)
-        kda_rotary_kernel<T, W><<<grid, NT, 0, s>>>(p, TB);
+        kda_rotary_kernel<T, W><<<grid, NT, 0, s>>>(p, g, TB);
     else
-        kda_rotary_kernel<T, 1><<<grid, NT, 0, s>>>(p, TB);
+        kda_rotary_kernel<T, 1><<<grid, NT, 0, s>>>(p, g, TB);
     return cudaGetLastError();
 }
 
