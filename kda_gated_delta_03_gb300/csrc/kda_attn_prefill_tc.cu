@@ -246,9 +246,9 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
         return false;
     };
     const bool work = share.left > 0;
-    // Registers go from the warps that move data to those that hold rows: 2 x 208 + 88 = 3 x 168, what the launch has.
+    // Registers go from the warps that move data to those that hold rows: 2 x 192 + 120 = 3 x 168, what the launch has.
     if (warp < MMA_WARP) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         if (work) {
         // ---------------- softmax: a row a thread ----------------
         const int blk = warp >> 2, r = tid;   // rows 0..127 and 128..255 of the unit
@@ -412,7 +412,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
         } while (true);
     }
     } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     if (warp == LOAD_WARP && work) {
         // ---------------- pages ----------------
         uint32_t n = 0;                       // stages filled
