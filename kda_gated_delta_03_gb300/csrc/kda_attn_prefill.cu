@@ -14,6 +14,7 @@ namespace kda {
 namespace {
 
 constexpr int NT = 256, NW = NT / 32, BM = 64, BN = 64;
+constexpr int EXTRA = 0;                      // a unit's queries and outputs take little beside a tile
 constexpr int MAX_CTAS = 512;                 // of the main kernel, whatever the GPU (bounds the workspace)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
@@ -47,15 +48,13 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
     constexpr int CO = D / 16 < 4 ? D / 16 : 4, GO = D / 16 / CO;         // output columns of a thread: GO runs of CO
     const float scale2 = p.scale * LOG2E;
     float* pieces = f.whole ? nullptr : reinterpret_cast<float*>(p.workspace + MAX_CTAS * sizeof(ChunkRecord));
-    Walk w;
-    w.begin(p, f, share);
-    int64_t left = share.left;
-    int tile = share.tile;
+    Runs runs(p, f, share);
     bool first_unit = true;
-    while (true) {
+    if (runs.count <= 0) return;
+    do {
+        const Walk& w = runs.w;
         const Unit& u = w.u;
-        const int row0 = w.m * BM;
-        const int count = f.whole ? u.tiles : (int)(left < u.tiles - tile ? left : u.tiles - tile);
+        const int row0 = w.m * BM, tile = runs.tile, count = runs.count;
         // ---- the unit's queries ----
         for (int i = tid; i < BM * (D / 4); i += NT) {
             const int r = i / (D / 4), c = i % (D / 4) * 4;
@@ -203,16 +202,10 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
                 if (tx == 0) piece[BM * D + r] = m[i], piece[BM * (D + 1) + r] = l[i];
             }
         }
-        if (tid == 0 && starts && !ends) {
-            const int64_t x = share.start + share.left - left + u.tiles;       // flat tiles up to the unit's last
-            records[cta] = ChunkRecord{w.b, w.m, w.h, cta, cta_before(share, x), first_unit ? 0 : 1, {0, 0}};
-        }
-        left -= f.whole ? 1 : count;
-        if (left <= 0) break;
-        w.next(p, f);
-        tile = 0;
+        if (tid == 0 && starts && !ends)
+            records[cta] = ChunkRecord{w.b, w.m, w.h, cta, cta_before(share, runs.end(f, share)), first_unit ? 0 : 1, {0, 0}};
         first_unit = false;
-    }
+    } while (runs.next(p, f));
 }
 
 template <typename T, int D>
@@ -221,7 +214,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
     int sms = 0;
     cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_chunk_kernel<T, D>), Layout<D>::BYTES, &sms);
     if (e != cudaSuccess) return e;
-    ChunkPlan f = chunk_plan(p, BM, BN);
+    ChunkPlan f = chunk_plan(p, BM, BN, EXTRA);
     int grid = 2 * sms < MAX_CTAS ? 2 * sms : MAX_CTAS;
     const int64_t units = most_units(p, f);
     // Where a unit has few tiles, whatever the lengths, pieces and a second kernel would cost more than they bring.

@@ -31,6 +31,7 @@ constexpr int WARPS = 12, THREADS = WARPS * 32;
 constexpr int MMA_WARP = 8, LOAD_WARP = 9, HELP_WARP = 10, QUERY_WARP = 11;
 constexpr int TC_MAX_CTAS = 160;              // of the main kernel, whatever the GPU (bounds the workspace)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr int EXTRA = 1;                      // tiles' time that a unit's queries and outputs take
 constexpr float SLACK = 8.f;                  // the reference moves when the maximum has grown by 2^SLACK
 
 template <int D>
@@ -179,29 +180,6 @@ __device__ __noinline__ void add_odd(const ChunkParams& p, const ChunkPlan& f, c
         }
 }
 
-// A run: the share's tiles of one unit.  Every role steps through the same ones.
-struct Runs {
-    Walk w;
-    int64_t left;
-    int32_t tile, count, run;    // of the run: its first tile and how many; its number
-    __device__ __forceinline__ Runs(const ChunkParams& p, const ChunkPlan& f, const Share& share) : left(share.left), tile(share.tile), run(0) {
-        w.begin(p, f, share);
-        measure(f);
-    }
-    __device__ __forceinline__ void measure(const ChunkPlan& f) {
-        count = f.whole ? w.u.tiles : (int)(left < w.u.tiles - tile ? left : w.u.tiles - tile);
-    }
-    __device__ __forceinline__ bool next(const ChunkParams& p, const ChunkPlan& f) {
-        left -= f.whole ? 1 : count;
-        if (left <= 0) return false;
-        ++run;
-        tile = 0;
-        w.next(p, f);
-        measure(f);
-        return true;
-    }
-};
-
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
 kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __grid_constant__ CUtensorMap q_map,
@@ -245,7 +223,8 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
         atomicOr(p.err, KDA_DEVERR_TIMEOUT);
         return false;
     };
-    const bool work = share.left > 0;
+    // every role steps through the same runs
+    const bool work = share.left > 0 && Runs(p, f, share).count > 0;
     // Registers go from the warps that move data to those that hold rows: 2 x 192 + 120 = 3 x 168, what the launch has.
     if (warp < MMA_WARP) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
@@ -404,8 +383,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                 tc_fence_before();            // the next run's products overwrite O
             }
             if (tid == 0 && starts && !ends) {
-                const int64_t x = share.start + share.left - runs.left + w.u.tiles;     // flat tiles up to the unit's last
-                records[cta] = ChunkRecord{w.b, w.m, w.h, cta, cta_before(share, x), first_unit ? 0 : 1, {0, 0}};
+                records[cta] = ChunkRecord{w.b, w.m, w.h, cta, cta_before(share, runs.end(f, share)), first_unit ? 0 : 1, {0, 0}};
             }
             first_unit = false;
             if (!runs.next(p, f)) break;
@@ -695,7 +673,7 @@ cudaError_t launch_tc(const ChunkParams& p, cudaStream_t s) {
     if (q_boxes ? !encode_queries(enc, &q_map, p) : (std::memset(&q_map, 0, sizeof q_map), false)) return cudaErrorInvalidValue;
     if (!encode_pages(enc, &k_map, p, p.k_pages, p.k_stride, box) || !encode_pages(enc, &v_map, p, p.v_pages, p.v_stride, box))
         return cudaErrorInvalidValue;
-    ChunkPlan f = chunk_plan(p, UNIT, TILE / box * box);
+    ChunkPlan f = chunk_plan(p, UNIT, TILE / box * box, EXTRA);
     int grid = sms < TC_MAX_CTAS ? sms : TC_MAX_CTAS;
     const int64_t units = most_units(p, f);
     // Where a unit has few tiles, whatever the lengths, pieces and a second kernel would cost more than they bring.

@@ -5,7 +5,9 @@
 // tiles of BN tokens of the cache that any of its rows sees.  All units' tiles, numbered one after the other (all units
 // of a head, then the next head), are cut into equal shares, one per CTA, so that one long prompt, many short ones
 // and a few tokens behind a long context fill the GPU alike.  Every CTA works its own share out from cu_seqlens and
-// seq_lens on the device: a few microseconds at the most, nothing launched for it, nothing for the host to know.
+// seq_lens on the device: a few microseconds at the most, nothing launched for it, nothing for the host to know.  (A unit's
+// own cost, `extra` tiles, counts: without it the CTAs whose units are short were done 50 us after the others of a 455 us
+// prompt.)
 // A unit that a border between shares cuts leaves pieces (maximum, sum and unscaled outputs), which a second
 // kernel joins in the order of the CTAs: no atomics, the same bits on every call.
 #pragma once
@@ -19,12 +21,13 @@ struct ChunkPlan {
     int32_t group;               // query heads of a key-value head
     int32_t BM;                  // rows of a unit, a power of two
     int32_t BN;                  // tokens of a tile
+    int32_t extra;               // what a unit costs beside its tiles, in tiles
     int32_t whole;               // CTA i does unit i, and nothing is left to join
     Divisor by_page, by_group, by_tile;
 };
-inline ChunkPlan chunk_plan(const ChunkParams& p, int32_t BM, int32_t BN) {
+inline ChunkPlan chunk_plan(const ChunkParams& p, int32_t BM, int32_t BN, int32_t extra) {
     const int32_t group = p.Hq / p.Hkv;
-    return ChunkPlan{group, BM, BN, 0, divisor(p.page_size), divisor(group), divisor(BN)};
+    return ChunkPlan{group, BM, BN, extra, 0, divisor(p.page_size), divisor(group), divisor(BN)};
 }
 
 // One sequence of the batch: its new tokens and its length, 0 where they are not valid.
@@ -80,16 +83,17 @@ __device__ __forceinline__ int tile_start(const ChunkPlan& f, const Unit& u, int
     return (i < u.near ? i : i + u.skip) * f.BN;
 }
 __device__ __forceinline__ int64_t cost_of(const ChunkParams& p, const ChunkPlan& f, const Seq& s, int m) {
-    return f.whole ? 1 : unit_of(p, f, s, m).tiles;
+    return f.whole ? 1 : f.extra + unit_of(p, f, s, m).tiles;
 }
 
-// What a CTA does: `left` flat tiles, from tile `tile` of unit m of sequence b and key-value head h on.
+// What a CTA does: `left` places from place `at` of unit m of sequence b and key-value head h on.  A unit has `extra` places
+// for what it costs beside its tiles, and then one a tile (with whole shares, one in all).
 struct Share {
-    int64_t left;                // tiles; with whole shares, 1
-    int64_t start;               // flat number of the first
-    int64_t all;                 // tiles of all shares
+    int64_t left;
+    int64_t start;               // flat number of the first place
+    int64_t all;                 // places of all shares
     int32_t ctas;                // shares
-    int32_t h, b, m, tile;
+    int32_t h, b, m, at;
 };
 
 constexpr int MIN_SHARE = 2;                  // tiles: pieces of one would cost more to join than they save
@@ -134,7 +138,7 @@ __device__ __forceinline__ void plan_share(const ChunkParams& p, const ChunkPlan
         head += sums[w];
     }
     const int64_t total = head * p.Hkv;
-    const int64_t most = f.whole ? total : (total + MIN_SHARE - 1) / MIN_SHARE;
+    const int64_t least = MIN_SHARE + f.extra, most = f.whole ? total : (total + least - 1) / least;
     const int ctas = (int)(most < grid ? most : grid);
     if (cta >= ctas) {                        // (no work at all: ctas = 0)
         __syncthreads();
@@ -163,7 +167,7 @@ __device__ __forceinline__ void plan_share(const ChunkParams& p, const ChunkPlan
                     if (at < batch) {
                         found = true;
                         if (at >= to - c && at < to)
-                            *out = Share{x1 - x0, x0, total, ctas, h, g + i, m + lane, f.whole ? 0 : (int)(at - (to - c))};
+                            *out = Share{x1 - x0, x0, total, ctas, h, g + i, m + lane, (int)(at - (to - c))};
                     } else {
                         at -= batch;
                     }
@@ -196,6 +200,40 @@ struct Walk {
     }
 };
 
+// A run: the share's tiles of one unit.
+struct Runs {
+    Walk w;
+    int64_t left;                // places of the share, from the run's first on
+    int32_t at;                  // the run's first place in its unit
+    int32_t tile, count, run;    // its first tile and how many; its number
+    __device__ __forceinline__ Runs(const ChunkParams& p, const ChunkPlan& f, const Share& share) : left(share.left), at(share.at), run(0) {
+        w.begin(p, f, share);
+        measure(f);
+    }
+    __device__ __forceinline__ void measure(const ChunkPlan& f) {
+        if (f.whole) {
+            tile = 0, count = w.u.tiles;
+            return;
+        }
+        const int all = f.extra + w.u.tiles, end = left < all - at ? at + (int)left : all;
+        tile = at > f.extra ? at - f.extra : 0;
+        count = (end > f.extra ? end - f.extra : 0) - tile;
+    }
+    __device__ __forceinline__ bool next(const ChunkParams& p, const ChunkPlan& f) {
+        left -= f.whole ? 1 : f.extra + w.u.tiles - at;
+        if (left <= 0) return false;
+        ++run;
+        at = 0;
+        w.next(p, f);
+        measure(f);
+        return count > 0;        // a share may end among the places before a unit's first tile: that unit is the next one's
+    }
+    // Flat number of the unit's end.
+    __device__ __forceinline__ int64_t end(const ChunkPlan& f, const Share& share) const {
+        return share.start + share.left - left + (f.extra + w.u.tiles - at);
+    }
+};
+
 // A unit whose first tiles are in CTA `first`'s share and whose last ones in `last`'s; b = -1: none.
 struct ChunkRecord {
     int32_t b, m, h, first, last, slot, pad[2];
@@ -215,53 +253,88 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
-constexpr int JOIN_WARPS = 4;
+constexpr int JOIN_WARPS = 4, JOIN_ROWS = 2;  // of a CTA, and of a warp at a time
 
-// Joins the pieces of a unit: a warp per row.  A piece is [BM][D] sums, then [BM] maxima (base 2) and [BM] sums.
+template <int N>
+struct alignas(4 * N) Floats {
+    float x[N];
+};
+
+// Joins the pieces of a unit.  A piece is [BM][D] sums, then [BM] maxima (base 2) and [BM] sums.  A lane works out the weight
+// of one piece for each of the warp's rows; then all of them add the pieces up, a few columns each, with the next pieces'
+// loads under way.
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) kda_chunk_join_kernel(ChunkParams p, ChunkPlan f, int max_ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const ChunkRecord r = reinterpret_cast<const ChunkRecord*>(p.workspace)[blockIdx.x];
     if (r.b < 0) return;
-    const int lane = threadIdx.x & 31, row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5);
+    const unsigned all = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31, row0 = (blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5)) * JOIN_ROWS;
     const Seq s = seq_of(p, r.b);
-    const int flat = r.m * f.BM + row;
-    if (flat >= s.n * f.group) return;
+    const int flat0 = r.m * f.BM + row0, rows = s.n * f.group - flat0;    // of the unit from the warp's first on
+    if (rows <= 0) return;
     const int64_t size = piece_floats<D>(f.BM);
     const float* pieces = reinterpret_cast<const float*>(p.workspace + max_ctas * sizeof(ChunkRecord));
     const int n = r.last - r.first + 1;
     auto piece = [&](int i) { return pieces + ((int64_t)(r.first + i) * 2 + (i == 0 ? r.slot : 0)) * size; };
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, piece(i)[(int64_t)f.BM * D + row]);
+    constexpr int PER = D / 32 > 0 ? D / 32 : 1;                          // columns of a lane
+    const int col = lane * PER;
+    float top[JOIN_ROWS], sum[JOIN_ROWS];
+    Floats<PER> o[JOIN_ROWS];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float base = top == -INFINITY ? 0.f : top;
-    constexpr int PER = D >= 128 ? 4 : D / 32 > 0 ? D / 32 : 1;           // columns of a lane
-    float sum = 0.f, o[PER] = {};
-    for (int i = 0; i < n; ++i) {
-        const float* x = piece(i);
-        const float w = ex2_approx(x[(int64_t)f.BM * D + row] - base);
-        sum += w * x[(int64_t)f.BM * (D + 1) + row];
+    for (int k = 0; k < JOIN_ROWS; ++k) {
+        top[k] = -INFINITY, sum[k] = 0.f;
+        for (int i = lane; i < n; i += 32) top[k] = fmaxf(top[k], piece(i)[(int64_t)f.BM * D + row0 + k]);
 #pragma unroll
-        for (int c = 0; c < PER; ++c)
-            if (lane + 32 * c < D) {
-                const float v = x[(int64_t)row * D + lane + 32 * c];
-                o[c] = fmaf(w, v, o[c]);
-            }
+        for (int x = 16; x; x >>= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(all, top[k], x));
+#pragma unroll
+        for (int c = 0; c < PER; ++c) o[k].x[c] = 0.f;
     }
-    const int t = over(flat, f.by_group), head = r.h * f.group + flat - t * f.group;
-    const int64_t at = (int64_t)(s.start + t) * p.Hq + head;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float w[JOIN_ROWS];
 #pragma unroll
-    for (int c = 0; c < PER; ++c)
-        if (lane + 32 * c < D) put(static_cast<T*>(p.o) + at * D + lane + 32 * c, sum == 0.f ? 0.f : o[c] / sum);
-    if (p.lse && lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        for (int k = 0; k < JOIN_ROWS; ++k) {
+            w[k] = 0.f;
+            if (i0 + lane < n && k < rows) {
+                const float* x = piece(i0 + lane) + row0 + k;
+                w[k] = ex2_approx(x[(int64_t)f.BM * D] - (top[k] == -INFINITY ? 0.f : top[k]));
+                sum[k] = fmaf(w[k], x[(int64_t)f.BM * (D + 1)], sum[k]);
+            }
+        }
+        const int count = n - i0 < 32 ? n - i0 : 32;
+#pragma unroll 4
+        for (int i = 0; i < count; ++i) {
+            const float* x = piece(i0 + i) + (int64_t)row0 * D + col;
+#pragma unroll
+            for (int k = 0; k < JOIN_ROWS; ++k) {
+                const float y = __shfl_sync(all, w[k], i);
+                if (k >= rows || col >= D) continue;
+                const Floats<PER> v = *reinterpret_cast<const Floats<PER>*>(x + k * D);
+#pragma unroll
+                for (int c = 0; c < PER; ++c) o[k].x[c] = fmaf(y, v.x[c], o[k].x[c]);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < JOIN_ROWS; ++k) {
+#pragma unroll
+        for (int x = 16; x; x >>= 1) sum[k] += __shfl_xor_sync(all, sum[k], x);
+        if (k >= rows) continue;
+        const int t = over(flat0 + k, f.by_group), head = r.h * f.group + flat0 + k - t * f.group;
+        const int64_t at = (int64_t)(s.start + t) * p.Hq + head;
+        if (col < D) {
+#pragma unroll
+            for (int c = 0; c < PER; ++c) put(static_cast<T*>(p.o) + at * D + col + c, sum[k] == 0.f ? 0.f : o[k].x[c] / sum[k]);
+        }
+        if (p.lse && lane == 0) p.lse[at] = sum[k] == 0.f ? -INFINITY : (top[k] + log2f(sum[k])) * 0.6931471805599453f;
+    }
 }
 
 template <typename T, int D>
 cudaError_t launch_join(const ChunkParams& p, const ChunkPlan& f, int grid, int max_ctas, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(grid, f.BM / JOIN_WARPS);
+    cfg.gridDim = dim3(grid, f.BM / (JOIN_WARPS * JOIN_ROWS));
     cfg.blockDim = dim3(JOIN_WARPS * 32);
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
