@@ -34,21 +34,10 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int EXTRA = 1;                      // tiles' time that a unit's queries and outputs take
 constexpr float SLACK = 8.f;                  // the reference moves when the maximum has grown by 2^SLACK
 
-template <int D>
-struct TcLayout {
-    static constexpr int HALVES = D / 64;                      // 128-byte columns of a tile
-    static constexpr int HALF = TILE * 128;                    // bytes of one
-    static constexpr int BLOCK = HALVES * HALF;                // bytes of a block of Q, K or V
-    static constexpr int STAGES = D == 128 ? 4 : 8;            // K and V in turn
-    static constexpr int Q = 0, KV = 2 * BLOCK, BYTES = KV + STAGES * BLOCK;
-    static constexpr int DYNAMIC = BYTES + 1024;               // aligned to 1 KiB inside
-    static constexpr uint32_t S = 0, O = 2 * TILE;             // columns of tensor memory: S0, S1, O0, O1
-};
-
 // Tokens of a tile whose value is not finite, taken out of it.  A unit of 256 rows has at most 14 tiles that
 // some row sees in part: tiles hold 65 tokens or more, the rows' own tokens touch 5 of them, the lower borders of their
 // windows 5, the border of the first tokens 1.
-constexpr int MAX_ODD = 16;
+constexpr int MAX_ODD = 14;
 struct OddTiles {
     int32_t n;
     int32_t start[MAX_ODD];
@@ -59,11 +48,31 @@ constexpr int RING = 8;                       // runs whose lists are kept: the 
 
 struct Barriers {
     uint64_t full[8], empty[8];               // of stages
-    uint64_t fixed[4];                        // a V stage's partly seen tile is ready for the product
+    uint64_t fixed[8];                        // a stage's partly seen tile of V is ready for the product
     uint64_t q, q_empty;                      // a run's queries in shared memory, and read for the last time
     uint64_t s[2], p[2][2], pv[2];            // of row blocks: scores, the weights' two halves, a tile's product done
     uint64_t run, ack;                        // a run's products done, and the second block's group has seen that
     uint64_t done;                            // all products done
+};
+
+struct Misc {
+    Barriers bar;
+    OddTiles odd[RING];
+    int64_t sums[WARPS];
+    Share share;
+    uint32_t tmem_base;
+    uint32_t issued;                          // stages whose copies have been issued
+};
+
+template <int D>
+struct TcLayout {
+    static constexpr int HALVES = D / 64;                      // 128-byte columns of a tile
+    static constexpr int HALF = TILE * 128;                    // bytes of one
+    static constexpr int BLOCK = HALVES * HALF;                // bytes of a block of Q, K or V
+    static constexpr int STAGES = D == 128 ? 5 : 8;            // K and V in turn
+    static constexpr int Q = 0, KV = 2 * BLOCK, MISC = KV + STAGES * BLOCK, BYTES = MISC + (int)sizeof(Misc);
+    static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
+    static constexpr uint32_t S = 0, O = 2 * TILE;             // columns of tensor memory: S0, S1, O0, O1
 };
 
 __device__ __forceinline__ void arrive(uint64_t* bar) {
@@ -185,39 +194,39 @@ __global__ void __launch_bounds__(THREADS, 1)
 kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __grid_constant__ CUtensorMap q_map,
                     const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using L = TcLayout<D>;
-    extern __shared__ unsigned char raw[];
-    __shared__ Barriers bar;
-    __shared__ OddTiles odd[RING];
-    __shared__ int64_t sums[WARPS];
-    __shared__ Share share;
-    __shared__ uint32_t tmem_base;
-    unsigned char* sm = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Misc& misc = *reinterpret_cast<Misc*>(sm + L::MISC);
+    Barriers& bar = misc.bar;
+    OddTiles* const odd = misc.odd;
+    Share& share = misc.share;
+    volatile uint32_t& issued = misc.issued;
     const uint32_t sm_q = saddr(sm) + L::Q, sm_kv = saddr(sm) + L::KV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x, grid = gridDim.x;
     ChunkRecord* records = reinterpret_cast<ChunkRecord*>(p.workspace);
 
     if (tid == 0) {
         auto init = [](uint64_t* b, int n) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(n) : "memory"); };
-        for (int i = 0; i < L::STAGES; ++i) init(&bar.full[i], 1), init(&bar.empty[i], i % 2 ? 2 : 1);
-        for (int i = 0; i < 4; ++i) init(&bar.fixed[i], 1);
+        for (int i = 0; i < L::STAGES; ++i) init(&bar.full[i], 1), init(&bar.empty[i], 1);
+        for (int i = 0; i < 8; ++i) init(&bar.fixed[i], 1);
         for (int i = 0; i < 2; ++i) init(&bar.s[i], 1), init(&bar.p[i][0], 4), init(&bar.p[i][1], 4), init(&bar.pv[i], 1);
         init(&bar.q, 1), init(&bar.q_empty, 1), init(&bar.run, 1), init(&bar.ack, 4), init(&bar.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        issued = 0;
         if (!f.whole) records[cta].b = -1;
     }
     if (warp == MMA_WARP) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_base)), "r"(512) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&misc.tmem_base)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (f.BN < TILE) {                        // rows that no copy ever fills
         for (int i = tid; i < L::STAGES * (L::BLOCK / 16); i += THREADS) st_shared16(sm_kv + i * 16, make_uint4(0, 0, 0, 0));
         fence_async_smem();
     }
-    plan_share<WARPS>(p, f, sums, &share, cta, grid);
+    plan_share<WARPS>(p, f, misc.sums, &share, cta, grid);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = misc.tmem_base;
     auto wait = [&](uint64_t* b, uint32_t parity) {            // each role that gives up leaves the others to give up, too
         if (mbar_test(saddr(b), parity & 1u) || mbar_wait(saddr(b), parity & 1u)) return true;
         atomicOr(p.err, KDA_DEVERR_TIMEOUT);
@@ -441,6 +450,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                             for (int h = 0; h < L::HALVES; ++h)
                                 tma_load_4d(to + h * L::HALF + (lane + 32 * i) * box * 128, v ? &v_map : &k_map, h * 64, row[i], w.h,
                                             page[i], saddr(&bar.full[st]));
+                    if (lane == 0) issued = n + 1;
                 }
             }
             if (!ok || !runs.next(p, f)) break;
@@ -491,20 +501,26 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
         if (boxed) mbar_wait(saddr(&bar.q), (boxed - 1) & 1u);  // no copy is left in flight
     } else if (warp == HELP_WARP && work) {
         // ---------------- tiles that some row sees in part ----------------
-        uint32_t n = 1;                       // V's stages are the odd ones
         bool ok = true;
         Runs runs(p, f, share);
         do {
             const Walk& w = runs.w;
             const int count = runs.count, tile = runs.tile, run = runs.run, last = last_pos(f, w);
             OddTiles& list = odd[run % RING];
-            if (lane == 0) list.n = 0;
-            __syncwarp();
-            for (int it = tile; it < tile + count && ok; ++it, n += 2) {
-                const int st = n % L::STAGES, j0 = tile_start(f, w.u, it);
-                ok = wait(&bar.full[st], n / L::STAGES);
+            bool begun = false;
+            for (int it = tile; it < tile + count; ++it) {
+                const int j0 = tile_start(f, w.u, it);
+                if (open_tile(p, f, w.u, last, j0)) continue;
+                if (!begun && lane == 0) list.n = 0;
+                begun = true;
+                // The copy has to have been issued before its barrier's phase can be told from the one before.
+                const uint32_t n = 2 * (runs.before + it - tile) + 1, st = n % L::STAGES;
+                const long long t0 = clock64();
+                while (issued <= n && (ok = clock64() - t0 < kWaitLimit)) {}
+                ok = ok && wait(&bar.full[st], n / L::STAGES);
                 if (!ok) break;
-                if (!open_tile(p, f, w.u, last, j0)) {
+                __syncwarp();
+                {
                     const uint32_t at = sm_kv + st * L::BLOCK;
                     const int real = w.u.end - j0 < f.BN ? w.u.end - j0 : f.BN;     // may be less than 1: nothing is seen
                     // Tokens up to the first row's are hidden from nobody where there is no window.  A lane has rows
@@ -542,9 +558,8 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                     }
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) arrive(&bar.fixed[st / 2]);
+                    if (lane == 0) arrive(&bar.fixed[st]);
                 }
-                if (lane == 0) arrive(&bar.empty[st]);
             }
             if (!ok || !runs.next(p, f)) break;
         } while (true);
@@ -554,7 +569,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
             const uint32_t id_s = idesc_bf16(TILE, TILE), id_o = idesc_bf16(TILE, D) | (1u << 16);  // V's columns are contiguous
             const uint64_t dq = desc_sw128(sm_q), dk = desc_sw128(sm_kv), dv = desc_v(sm_kv, L::HALF);
             constexpr uint32_t STEP = L::BLOCK >> 4;           // descriptors count in 16 bytes
-            uint32_t nk = 0, n0 = 0, n1 = 0, fixed[4] = {0, 0, 0, 0};
+            uint32_t nk = 0, n0 = 0, n1 = 0, fixed = 0;     // (fixed: phases, a bit a stage)
             bool ok = true;
             auto scores = [&](int i, uint32_t st) {            // S_i = Q_i K^T
                 const uint64_t a = dq + i * STEP, b = dk + st * STEP;
@@ -580,11 +595,8 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                     const bool more = it + 1 < tile + count;
                     ok = wait(&bar.full[sv], nv / L::STAGES) && (!more || wait(&bar.full[sk], nn / L::STAGES));
                     if (ok && !open_tile(p, f, w.u, last, tile_start(f, w.u, it))) {
-                        uint32_t phase = 0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i == (int)sv / 2) phase = fixed[i]++;
-                        ok = wait(&bar.fixed[sv / 2], phase);
+                        ok = wait(&bar.fixed[sv], fixed >> sv);
+                        fixed ^= 1u << sv;
                     }
                     const uint64_t b = dv + sv * STEP;
                     auto product = [&](int i, uint32_t& n) {   // O_i += P_i V, the weights' halves as they come
@@ -662,7 +674,7 @@ template <int D>
 cudaError_t launch_tc(const ChunkParams& p, cudaStream_t s) {
     static DeviceSetup done;
     int sms = 0;
-    cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_chunk_tc_kernel<D>), TcLayout<D>::DYNAMIC, &sms);
+    cudaError_t e = device_setup(done, reinterpret_cast<const void*>(kda_chunk_tc_kernel<D>), TcLayout<D>::BYTES, &sms);
     if (e != cudaSuccess) return e;
     const auto enc = tensor_map_encoder();
     if (!enc) return cudaErrorNotSupported;
@@ -679,7 +691,7 @@ cudaError_t launch_tc(const ChunkParams& p, cudaStream_t s) {
     // Where a unit has few tiles, whatever the lengths, pieces and a second kernel would cost more than they bring.
     f.whole = units <= 3 * (int64_t)grid && most_tiles(p, f) <= 2 * MIN_SHARE;
     if (f.whole) grid = (int)units;
-    kda_chunk_tc_kernel<D><<<grid, THREADS, TcLayout<D>::DYNAMIC, s>>>(p, f, box, q_boxes, q_map, k_map, v_map);
+    kda_chunk_tc_kernel<D><<<grid, THREADS, TcLayout<D>::BYTES, s>>>(p, f, box, q_boxes, q_map, k_map, v_map);
     e = cudaGetLastError();
     return e != cudaSuccess || f.whole ? e : launch_join<__nv_bfloat16, D>(p, f, grid, TC_MAX_CTAS, s);
 }

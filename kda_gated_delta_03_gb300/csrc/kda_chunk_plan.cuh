@@ -206,6 +206,7 @@ struct Runs {
     int64_t left;                // places of the share, from the run's first on
     int32_t at;                  // the run's first place in its unit
     int32_t tile, count, run;    // its first tile and how many; its number
+    uint32_t before = 0;         // tiles of the runs before it
     __device__ __forceinline__ Runs(const ChunkParams& p, const ChunkPlan& f, const Share& share) : left(share.left), at(share.at), run(0) {
         w.begin(p, f, share);
         measure(f);
@@ -223,6 +224,7 @@ struct Runs {
         left -= f.whole ? 1 : f.extra + w.u.tiles - at;
         if (left <= 0) return false;
         ++run;
+        before += count;
         at = 0;
         w.next(p, f);
         measure(f);
