@@ -138,14 +138,20 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
     return x;
 }
 
-// Whether every row of the unit sees every token of the tile.
-__device__ __forceinline__ bool open_tile(const ChunkParams& p, const ChunkPlan& f, const Unit& u, int last, int j0) {
-    const int64_t end = (int64_t)j0 + f.BN;
-    return end - 1 <= u.pos0 && (p.window == 0 || (int64_t)j0 > (int64_t)last - p.window || end <= p.sinks);
-}
-__device__ __forceinline__ int last_pos(const ChunkPlan& f, const Walk& w) {
-    return w.s.len - w.s.n + over(w.m * UNIT + w.u.rows - 1, f.by_group);
-}
+// Tiles that are open: every row of the unit sees every token of them.  Among the first `near` ones (first tokens behind a
+// window) those below a, else those from b to below c.
+struct Open {
+    int32_t near, a, b, c;
+    __device__ __forceinline__ Open(const ChunkParams& p, const ChunkPlan& f, const Walk& w) {
+        const int below = max(w.u.pos0 + 1, 0);                // tokens that the first row sees end here
+        const int last = w.s.len - w.s.n + over(w.m * UNIT + w.u.rows - 1, f.by_group);
+        near = w.u.near;
+        a = over(min(p.sinks, below), f.by_tile);
+        b = p.window > 0 && last >= p.window ? over(last - p.window, f.by_tile) + 1 - w.u.skip : 0;
+        c = over(below, f.by_tile) - w.u.skip;
+    }
+    __device__ __forceinline__ bool operator()(int it) const { return it < near ? it < a : it >= b && it < c; }
+};
 
 // 64 bytes of a row: whole 32-byte sectors at a time where the address allows it, since each lane has a row of its own.
 __device__ __forceinline__ void store64(void* to, const uint32_t (&x)[16], bool wide) {
@@ -227,11 +233,12 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc.tmem_base;
-    auto wait = [&](uint64_t* b, uint32_t parity) {            // each role that gives up leaves the others to give up, too
-        if (mbar_test(saddr(b), parity & 1u) || mbar_wait(saddr(b), parity & 1u)) return true;
+    auto wait_at = [&](uint32_t b, uint32_t parity) {          // each role that gives up leaves the others to give up, too
+        if (mbar_test(b, parity & 1u) || mbar_wait(b, parity & 1u)) return true;
         atomicOr(p.err, KDA_DEVERR_TIMEOUT);
         return false;
     };
+    auto wait = [&](uint64_t* b, uint32_t parity) { return wait_at(saddr(b), parity); };
     // every role steps through the same runs
     const bool work = share.left > 0 && Runs(p, f, share).count > 0;
     // Registers go from the warps that move data to those that hold rows: 2 x 192 + 120 = 3 x 168, what the launch has.
@@ -253,11 +260,11 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
             float ref = -INFINITY, l = 0.f;
             bool part = false;                // the helper has looked at a tile of this run
             if (active) {
-                const int last = last_pos(f, w);
+                const Open is_open(p, f, w);
                 const int pos = r < w.u.rows ? max(w.s.len - w.s.n + over(w.m * UNIT + r, f.by_group), -1) : -1;
                 for (int it = tile; it < tile + count; ++it, ++ns) {
                     const int j0 = tile_start(f, w.u, it);
-                    const bool open = open_tile(p, f, w.u, last, j0);
+                    const bool open = is_open(it);
                     part = part || !open;
                     ok = wait(&bar.s[blk], ns);
                     if (!ok) break;
@@ -505,12 +512,13 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
         Runs runs(p, f, share);
         do {
             const Walk& w = runs.w;
-            const int count = runs.count, tile = runs.tile, run = runs.run, last = last_pos(f, w);
+            const int count = runs.count, tile = runs.tile, run = runs.run;
+            const Open is_open(p, f, w);
             OddTiles& list = odd[run % RING];
             bool begun = false;
             for (int it = tile; it < tile + count; ++it) {
+                if (is_open(it)) continue;
                 const int j0 = tile_start(f, w.u, it);
-                if (open_tile(p, f, w.u, last, j0)) continue;
                 if (!begun && lane == 0) list.n = 0;
                 begun = true;
                 // The copy has to have been issued before its barrier's phase can be told from the one before.
@@ -569,10 +577,18 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
             const uint32_t id_s = idesc_bf16(TILE, TILE), id_o = idesc_bf16(TILE, D) | (1u << 16);  // V's columns are contiguous
             const uint64_t dq = desc_sw128(sm_q), dk = desc_sw128(sm_kv), dv = desc_v(sm_kv, L::HALF);
             constexpr uint32_t STEP = L::BLOCK >> 4;           // descriptors count in 16 bytes
-            uint32_t nk = 0, n0 = 0, n1 = 0, fixed = 0;     // (fixed: phases, a bit a stage)
+            constexpr uint32_t S = L::STAGES;
+            // The tensor core takes few products ahead, and every hundred cycles between two batches of them beyond
+            // that stand still: what a tile needs beside its products is done between the batches before.
+            uint32_t st = 0, phase = 0, n0 = 0, n1 = 0, fixed = 0;         // next stage; tiles of each block; phases of `fixed`
             bool ok = true;
-            auto scores = [&](int i, uint32_t st) {            // S_i = Q_i K^T
-                const uint64_t a = dq + i * STEP, b = dk + st * STEP;
+            const uint32_t full = saddr(bar.full), empty = saddr(bar.empty);
+            auto filled = [&](uint32_t x, uint32_t ph) { ok = ok && wait_at(full + 8 * x, ph); };
+            auto step = [&](uint32_t& x, uint32_t& ph) {
+                if (++x == S) x = 0, ph ^= 1;
+            };
+            auto scores = [&](int i, uint32_t x) {             // S_i = Q_i K^T
+                const uint64_t a = dq + i * STEP, b = dk + x * STEP;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t o = ((ks / 4) * L::HALF + (ks % 4) * 32) >> 4;
@@ -580,47 +596,70 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                 }
                 umma_commit(saddr(&bar.s[i]));
             };
+            auto product = [&](int i, int half, uint32_t n, uint32_t x, bool first) {          // O_i += P_i V, half of the tokens
+                ok = ok && wait(&bar.p[i][half], n);
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t b = dv + x * STEP;
+#pragma unroll
+                for (int ks = half * (TILE / 32); ks < (half + 1) * (TILE / 32); ++ks)
+                    umma_bf16_ts(tmem + L::O + i * D, tmem + L::S + i * TILE + ks * 8, b + ks * (2048 >> 4), id_o, !first || ks > 0);
+                if (half == 1) umma_commit(saddr(&bar.pv[i]));
+            };
             Runs runs(p, f, share);
             do {
                 const Walk& w = runs.w;
-                const int count = runs.count, tile = runs.tile, run = runs.run, last = last_pos(f, w), blocks = w.u.rows > TILE ? 2 : 1;
-                ok = wait(&bar.q, run) && wait(&bar.full[nk % L::STAGES], nk / L::STAGES);
+                const int end = runs.tile + runs.count;
+                const bool two = w.u.rows > TILE;
+                const Open is_open(p, f, w);
+                ok = wait(&bar.q, runs.run);
+                filled(st, phase);
                 if (!ok) break;
                 tc_fence_after();
-                for (int i = 0; i < blocks; ++i) scores(i, nk % L::STAGES);
-                umma_commit(saddr(&bar.empty[nk % L::STAGES]));
-                if (count == 1) umma_commit(saddr(&bar.q_empty));
-                for (int it = tile; it < tile + count; ++it, nk += 2) {
-                    const uint32_t nv = nk + 1, nn = nk + 2, sv = nv % L::STAGES, sk = nn % L::STAGES;
-                    const bool more = it + 1 < tile + count;
-                    ok = wait(&bar.full[sv], nv / L::STAGES) && (!more || wait(&bar.full[sk], nn / L::STAGES));
-                    if (ok && !open_tile(p, f, w.u, last, tile_start(f, w.u, it))) {
+                scores(0, st);
+                if (two) scores(1, st);
+                umma_commit(empty + 8 * st);
+                if (runs.count == 1) umma_commit(saddr(&bar.q_empty));
+                step(st, phase);
+                bool open = is_open(runs.tile);
+                filled(st, phase);                             // V of the first tile
+                for (int it = runs.tile; it < end; ++it) {
+                    const bool more = it + 1 < end, first = it == runs.tile;
+                    const uint32_t sv = st;
+                    if (!open && ok) {
                         ok = wait(&bar.fixed[sv], fixed >> sv);
                         fixed ^= 1u << sv;
                     }
-                    const uint64_t b = dv + sv * STEP;
-                    auto product = [&](int i, uint32_t& n) {   // O_i += P_i V, the weights' halves as they come
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            ok = ok && wait(&bar.p[i][half], n);
-                            if (!ok) return;
-                            tc_fence_after();
-#pragma unroll
-                            for (int ks = half * (TILE / 32); ks < (half + 1) * (TILE / 32); ++ks)
-                                umma_bf16_ts(tmem + L::O + i * D, tmem + L::S + i * TILE + ks * 8, b + ks * (2048 >> 4), id_o, it > tile || ks > 0);
-                        }
-                        ++n;
-                        umma_commit(saddr(&bar.pv[i]));
-                        if (more) scores(i, sk);
-                    };
-                    product(0, n0);
-                    if (blocks == 2) product(1, n1);
+                    product(0, 0, n0, sv, first);
+                    step(st, phase);
+                    const uint32_t sk = st, k_phase = phase;   // K of the next tile
+                    if (more) filled(sk, k_phase);
+                    product(0, 1, n0, sv, first);
+                    ++n0;
                     if (!ok) break;
-                    umma_commit(saddr(&bar.empty[sv]));
-                    if (more) umma_commit(saddr(&bar.empty[sk]));
-                    if (it + 2 == tile + count) umma_commit(saddr(&bar.q_empty));
+                    if (more) {
+                        scores(0, sk);
+                        step(st, phase);
+                        open = is_open(it + 1);
+                    }
+                    if (two) {
+                        product(1, 0, n1, sv, first);
+                        if (more) filled(st, phase);           // V of the next tile
+                        product(1, 1, n1, sv, first);
+                        ++n1;
+                    }
+                    if (!ok) break;
+                    umma_commit(empty + 8 * sv);
+                    if (more) {
+                        if (two)
+                            scores(1, sk);
+                        else
+                            filled(st, phase);
+                        umma_commit(empty + 8 * sk);
+                        if (it + 2 == end) umma_commit(saddr(&bar.q_empty));
+                    }
                 }
-                if (ok && run > 0) ok = wait(&bar.ack, run - 1);
+                if (ok && runs.run > 0) ok = wait(&bar.ack, runs.run - 1);
                 if (!ok) break;
                 umma_commit(saddr(&bar.run));
             } while (runs.next(p, f));
