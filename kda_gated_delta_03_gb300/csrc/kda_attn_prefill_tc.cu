@@ -580,31 +580,22 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
             constexpr uint32_t S = L::STAGES;
             // The tensor core takes few products ahead, and every hundred cycles between two batches of them beyond
             // that stand still: what a tile needs beside its products is done between the batches before.
-            uint32_t st = 0, phase = 0, n0 = 0, n1 = 0, fixed = 0;         // next stage; tiles of each block; phases of `fixed`
+            uint32_t st = 0, phase = 0, n0 = 0, n1 = 0, fixed = 0;         // next stage; tiles of each block; phases of `fixed`, a bit a stage
             bool ok = true;
-            const uint32_t full = saddr(bar.full), empty = saddr(bar.empty);
+            const uint32_t full = saddr(bar.full), empty = saddr(bar.empty), p_full = saddr(&bar.p[0][0]), s_full = saddr(bar.s), pv = saddr(bar.pv),
+                           q_empty = saddr(&bar.q_empty);
             auto filled = [&](uint32_t x, uint32_t ph) { ok = ok && wait_at(full + 8 * x, ph); };
             auto step = [&](uint32_t& x, uint32_t& ph) {
                 if (++x == S) x = 0, ph ^= 1;
             };
-            auto scores = [&](int i, uint32_t x) {             // S_i = Q_i K^T
+            auto scores = [&](uint32_t i, uint32_t x) {        // S_i = Q_i K^T
                 const uint64_t a = dq + i * STEP, b = dk + x * STEP;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t o = ((ks / 4) * L::HALF + (ks % 4) * 32) >> 4;
                     umma_bf16_1(tmem + L::S + i * TILE, a + o, b + o, id_s, ks > 0);
                 }
-                umma_commit(saddr(&bar.s[i]));
-            };
-            auto product = [&](int i, int half, uint32_t n, uint32_t x, bool first) {          // O_i += P_i V, half of the tokens
-                ok = ok && wait(&bar.p[i][half], n);
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t b = dv + x * STEP;
-#pragma unroll
-                for (int ks = half * (TILE / 32); ks < (half + 1) * (TILE / 32); ++ks)
-                    umma_bf16_ts(tmem + L::O + i * D, tmem + L::S + i * TILE + ks * 8, b + ks * (2048 >> 4), id_o, !first || ks > 0);
-                if (half == 1) umma_commit(saddr(&bar.pv[i]));
+                umma_commit(s_full + 8 * i);
             };
             Runs runs(p, f, share);
             do {
@@ -630,33 +621,45 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                         ok = wait(&bar.fixed[sv], fixed >> sv);
                         fixed ^= 1u << sv;
                     }
-                    product(0, 0, n0, sv, first);
                     step(st, phase);
                     const uint32_t sk = st, k_phase = phase;   // K of the next tile
-                    if (more) filled(sk, k_phase);
-                    product(0, 1, n0, sv, first);
-                    ++n0;
-                    if (!ok) break;
-                    if (more) {
-                        scores(0, sk);
-                        step(st, phase);
-                        open = is_open(it + 1);
+                    if (more) step(st, phase);
+                    const uint64_t b = dv + sv * STEP;
+                    const uint32_t blocks = two ? 2 : 1;
+#pragma unroll 1
+                    for (uint32_t i = 0; i < blocks && ok; ++i) {
+                        const uint32_t o = tmem + L::O + i * D, pw = tmem + L::S + i * TILE;
+                        // O_i += P_i V.  With one block the first half of the weights starts it; with two the other block's
+                        // products cover the wait, and a pause between the halves would cost more.
+                        auto tokens = [&](int half) {
+#pragma unroll
+                            for (int ks = half * (TILE / 32); ks < (half + 1) * (TILE / 32); ++ks)
+                                umma_bf16_ts(o, pw + ks * 8, b + ks * (2048 >> 4), id_o, !first || ks > 0);
+                        };
+                        if (!two) {
+                            ok = wait_at(p_full, n0);
+                            if (!ok) break;
+                            tc_fence_after();
+                            tokens(0);
+                        }
+                        ok = wait_at(p_full + 16 * i + 8, i ? n1 : n0);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (two) tokens(0);
+                        tokens(1);
+                        umma_commit(pv + 8 * i);
+                        if (!more) continue;
+                        if (i == 0) filled(sk, k_phase);
+                        if (ok) scores(i, sk);
+                        if (i + 1 == blocks) filled(st, phase);                // V of the next tile
                     }
-                    if (two) {
-                        product(1, 0, n1, sv, first);
-                        if (more) filled(st, phase);           // V of the next tile
-                        product(1, 1, n1, sv, first);
-                        ++n1;
-                    }
+                    ++n0, n1 += two;
                     if (!ok) break;
                     umma_commit(empty + 8 * sv);
                     if (more) {
-                        if (two)
-                            scores(1, sk);
-                        else
-                            filled(st, phase);
                         umma_commit(empty + 8 * sk);
-                        if (it + 2 == end) umma_commit(saddr(&bar.q_empty));
+                        if (it + 2 == end) umma_commit(q_empty);
+                        open = is_open(it + 1);
                     }
                 }
                 if (ok && runs.run > 0) ok = wait(&bar.ack, runs.run - 1);
