@@ -50,7 +50,8 @@ struct Barriers {
     uint64_t full[8], empty[8];               // of stages
     uint64_t fixed[8];                        // a stage's partly seen tile of V is ready for the product
     uint64_t q, q_empty;                      // a run's queries in shared memory, and read for the last time
-    uint64_t s[2], p[2][2], pv[2];            // of row blocks: scores, the weights' two halves, a tile's product done
+    uint64_t s[2], p[2][2];                   // of row blocks: scores, the weights' two halves
+    uint64_t first;                           // a run's products for the first block done
     uint64_t run, ack;                        // a run's products done, and the second block's group has seen that
     uint64_t done;                            // all products done
 };
@@ -214,8 +215,8 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
         auto init = [](uint64_t* b, int n) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(n) : "memory"); };
         for (int i = 0; i < L::STAGES; ++i) init(&bar.full[i], 1), init(&bar.empty[i], 1);
         for (int i = 0; i < 8; ++i) init(&bar.fixed[i], 1);
-        for (int i = 0; i < 2; ++i) init(&bar.s[i], 1), init(&bar.p[i][0], 4), init(&bar.p[i][1], 4), init(&bar.pv[i], 1);
-        init(&bar.q, 1), init(&bar.q_empty, 1), init(&bar.run, 1), init(&bar.ack, 4), init(&bar.done, 1);
+        for (int i = 0; i < 2; ++i) init(&bar.s[i], 1), init(&bar.p[i][0], 4), init(&bar.p[i][1], 4);
+        init(&bar.q, 1), init(&bar.q_empty, 1), init(&bar.first, 1), init(&bar.run, 1), init(&bar.ack, 4), init(&bar.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         issued = 0;
         if (!f.whole) records[cta].b = -1;
@@ -257,6 +258,9 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
             const Walk& w = runs.w;
             const int count = runs.count, tile = runs.tile, run = runs.run;
             const bool active = blk * TILE < w.u.rows;
+            // The thread that tells the loader of free stages, when the scores of the last block are there: the products' thread
+            // has no time for it (a commit behind products holds it up until they are done).
+            const bool releases = lane == 0 && warp == (w.u.rows > TILE ? 4 : 0);
             float ref = -INFINITY, l = 0.f;
             bool part = false;                // the helper has looked at a tile of this run
             if (active) {
@@ -269,6 +273,11 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                     ok = wait(&bar.s[blk], ns);
                     if (!ok) break;
                     tc_fence_after();
+                    if (releases) {           // K of this tile and V of the one before have been read for the last time
+                        const uint32_t n = 2 * (runs.before + it - tile);
+                        arrive(&bar.empty[n % L::STAGES]);
+                        if (it > tile) arrive(&bar.empty[(n - 1) % L::STAGES]);
+                    }
                     __syncwarp();
                     float s[4][32], top[4];
                     auto top_of = [&](int c) {
@@ -309,11 +318,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                         const float to = move ? m : ref;
                         const float by = !move ? 1.f : ref == -INFINITY ? 0.f : ex2_approx((ref - to) * scale2);
                         l *= by;
-                        if (it > tile) {
-                            ok = wait(&bar.pv[blk], ns - 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                            __syncwarp();
+                        if (it > tile) {      // the scores' barrier tells of the products issued before them, too
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
                                 float o[16];
@@ -352,8 +357,9 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
             }
             // The second block waits for the whole run also where it has no rows, and says so, so that neither side gets
             // ahead by more than a run (a barrier's phases are told apart by one bit).
-            if (ok) ok = blk == 0 ? wait(&bar.pv[0], ns - 1) : wait(&bar.run, run);
+            if (ok) ok = blk == 0 ? wait(&bar.first, run) : wait(&bar.run, run);
             if (!ok) break;
+            if (releases) arrive(&bar.empty[(2 * (runs.before + count) - 1) % L::STAGES]);
             __syncwarp();
             if (blk == 1 && lane == 0) arrive(&bar.ack);
             // ---- outputs, or a piece of them ----
@@ -582,7 +588,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
             // that stand still: what a tile needs beside its products is done between the batches before.
             uint32_t st = 0, phase = 0, n0 = 0, n1 = 0, fixed = 0;         // next stage; tiles of each block; phases of `fixed`, a bit a stage
             bool ok = true;
-            const uint32_t full = saddr(bar.full), empty = saddr(bar.empty), p_full = saddr(&bar.p[0][0]), s_full = saddr(bar.s), pv = saddr(bar.pv),
+            const uint32_t full = saddr(bar.full), p_full = saddr(&bar.p[0][0]), s_full = saddr(bar.s),
                            q_empty = saddr(&bar.q_empty);
             auto filled = [&](uint32_t x, uint32_t ph) { ok = ok && wait_at(full + 8 * x, ph); };
             auto step = [&](uint32_t& x, uint32_t& ph) {
@@ -609,8 +615,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                 tc_fence_after();
                 scores(0, st);
                 if (two) scores(1, st);
-                umma_commit(empty + 8 * st);
-                if (runs.count == 1) umma_commit(saddr(&bar.q_empty));
+                if (runs.count == 1) umma_commit(q_empty);
                 step(st, phase);
                 bool open = is_open(runs.tile);
                 filled(st, phase);                             // V of the first tile
@@ -647,20 +652,20 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                         tc_fence_after();
                         if (two) tokens(0);
                         tokens(1);
-                        umma_commit(pv + 8 * i);
-                        if (!more) continue;
+                        if (!more) {
+                            if (i == 0) umma_commit(saddr(&bar.first));
+                            continue;
+                        }
                         if (i == 0) filled(sk, k_phase);
+                        if (i + 1 == blocks) {                                 // V of the next tile
+                            filled(st, phase);
+                            open = is_open(it + 1);
+                        }
                         if (ok) scores(i, sk);
-                        if (i + 1 == blocks) filled(st, phase);                // V of the next tile
                     }
                     ++n0, n1 += two;
                     if (!ok) break;
-                    umma_commit(empty + 8 * sv);
-                    if (more) {
-                        umma_commit(empty + 8 * sk);
-                        if (it + 2 == end) umma_commit(q_empty);
-                        open = is_open(it + 1);
-                    }
+                    if (it + 2 == end) umma_commit(q_empty);
                 }
                 if (ok && runs.run > 0) ok = wait(&bar.ack, runs.run - 1);
                 if (!ok) break;
