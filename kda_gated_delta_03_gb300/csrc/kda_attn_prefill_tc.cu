@@ -584,18 +584,17 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
             const uint64_t dq = desc_sw128(sm_q), dk = desc_sw128(sm_kv), dv = desc_v(sm_kv, L::HALF);
             constexpr uint32_t STEP = L::BLOCK >> 4;           // descriptors count in 16 bytes
             constexpr uint32_t S = L::STAGES;
-            // The tensor core takes few products ahead, and every hundred cycles between two batches of them beyond
-            // that stand still: what a tile needs beside its products is done between the batches before.
+            // The tensor core takes few products ahead, and every hundred cycles between two batches of them beyond that it
+            // stands still.  So what the next tile needs is done while the products of P V run that were issued last.
             uint32_t st = 0, phase = 0, n0 = 0, n1 = 0, fixed = 0;         // next stage; tiles of each block; phases of `fixed`, a bit a stage
             bool ok = true;
-            const uint32_t full = saddr(bar.full), p_full = saddr(&bar.p[0][0]), s_full = saddr(bar.s),
-                           q_empty = saddr(&bar.q_empty);
+            const uint32_t full = saddr(bar.full), p_full = saddr(&bar.p[0][0]), s_full = saddr(bar.s), q_empty = saddr(&bar.q_empty);
             auto filled = [&](uint32_t x, uint32_t ph) { ok = ok && wait_at(full + 8 * x, ph); };
-            auto step = [&](uint32_t& x, uint32_t& ph) {
-                if (++x == S) x = 0, ph ^= 1;
+            auto step = [&]() {
+                if (++st == S) st = 0, phase ^= 1;
             };
-            auto scores = [&](uint32_t i, uint32_t x) {        // S_i = Q_i K^T
-                const uint64_t a = dq + i * STEP, b = dk + x * STEP;
+            auto scores = [&](int i, uint64_t b) {             // S_i = Q_i K^T
+                const uint64_t a = dq + i * STEP;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t o = ((ks / 4) * L::HALF + (ks % 4) * 32) >> 4;
@@ -603,69 +602,87 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                 }
                 umma_commit(s_full + 8 * i);
             };
+            auto product = [&](int i, int half, uint64_t b, bool first) {      // O_i += P_i V, half of the tokens
+#pragma unroll
+                for (int ks = half * (TILE / 32); ks < (half + 1) * (TILE / 32); ++ks)
+                    umma_bf16_ts(tmem + L::O + i * D, tmem + L::S + i * TILE + ks * 8, b + ks * (2048 >> 4), id_o, !first || ks > 0);
+            };
+            auto weights = [&](int i, int half, uint32_t n) {
+                ok = ok && wait_at(p_full + 16 * i + 8 * half, n);
+                if (ok) tc_fence_after();
+                return ok;
+            };
+            // The next V: there, and looked after where some row sees it in part.
+            auto values = [&](bool open) {
+                filled(st, phase);
+                if (!open && ok) {
+                    ok = wait(&bar.fixed[st], fixed >> st);
+                    fixed ^= 1u << st;
+                }
+                const uint64_t b = dv + st * STEP;
+                step();
+                return b;
+            };
             Runs runs(p, f, share);
             do {
                 const Walk& w = runs.w;
-                const int end = runs.tile + runs.count;
+                int left = runs.count, it = runs.tile;         // tiles whose products are to come
                 const bool two = w.u.rows > TILE;
                 const Open is_open(p, f, w);
                 ok = wait(&bar.q, runs.run);
                 filled(st, phase);
                 if (!ok) break;
                 tc_fence_after();
-                scores(0, st);
-                if (two) scores(1, st);
-                if (runs.count == 1) umma_commit(q_empty);
-                step(st, phase);
-                bool open = is_open(runs.tile);
-                filled(st, phase);                             // V of the first tile
-                for (int it = runs.tile; it < end; ++it) {
-                    const bool more = it + 1 < end, first = it == runs.tile;
-                    const uint32_t sv = st;
-                    if (!open && ok) {
-                        ok = wait(&bar.fixed[sv], fixed >> sv);
-                        fixed ^= 1u << sv;
-                    }
-                    step(st, phase);
-                    const uint32_t sk = st, k_phase = phase;   // K of the next tile
-                    if (more) step(st, phase);
-                    const uint64_t b = dv + sv * STEP;
-                    const uint32_t blocks = two ? 2 : 1;
-#pragma unroll 1
-                    for (uint32_t i = 0; i < blocks && ok; ++i) {
-                        const uint32_t o = tmem + L::O + i * D, pw = tmem + L::S + i * TILE;
-                        // O_i += P_i V.  With one block the first half of the weights starts it; with two the other block's
-                        // products cover the wait, and a pause between the halves would cost more.
-                        auto tokens = [&](int half) {
-#pragma unroll
-                            for (int ks = half * (TILE / 32); ks < (half + 1) * (TILE / 32); ++ks)
-                                umma_bf16_ts(o, pw + ks * 8, b + ks * (2048 >> 4), id_o, !first || ks > 0);
-                        };
-                        if (!two) {
-                            ok = wait_at(p_full, n0);
-                            if (!ok) break;
-                            tc_fence_after();
-                            tokens(0);
-                        }
-                        ok = wait_at(p_full + 16 * i + 8, i ? n1 : n0);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (two) tokens(0);
-                        tokens(1);
-                        if (!more) {
-                            if (i == 0) umma_commit(saddr(&bar.first));
-                            continue;
-                        }
-                        if (i == 0) filled(sk, k_phase);
-                        if (i + 1 == blocks) {                                 // V of the next tile
+                uint64_t k = dk + st * STEP;
+                step();
+                scores(0, k);
+                if (two) scores(1, k);
+                if (left == 1) umma_commit(q_empty);
+                uint64_t v = values(is_open(it));
+                bool first = true;
+                if (two) {                                     // the other block's products cover the wait for a block's weights
+                    while (ok) {
+                        if (!weights(0, 1, n0)) break;
+                        product(0, 0, v, first);
+                        product(0, 1, v, first);
+                        if (left > 1) {
                             filled(st, phase);
-                            open = is_open(it + 1);
+                            k = dk + st * STEP;
+                            if (!ok) break;
+                            scores(0, k);
+                        } else {
+                            umma_commit(saddr(&bar.first));
                         }
-                        if (ok) scores(i, sk);
+                        if (!weights(1, 1, n1)) break;
+                        product(1, 0, v, first);
+                        product(1, 1, v, first);
+                        ++n0, ++n1;
+                        if (--left == 0) break;
+                        step();
+                        v = values(is_open(++it));
+                        first = false;
+                        if (!ok) break;
+                        scores(1, k);
+                        if (left == 1) umma_commit(q_empty);
                     }
-                    ++n0, n1 += two;
-                    if (!ok) break;
-                    if (it + 2 == end) umma_commit(q_empty);
+                } else {                                       // the first half of the weights starts the products
+                    while (ok) {
+                        if (!weights(0, 0, n0)) break;
+                        product(0, 0, v, first);
+                        if (!weights(0, 1, n0)) break;
+                        product(0, 1, v, first);
+                        ++n0;
+                        if (--left == 0) break;
+                        filled(st, phase);
+                        k = dk + st * STEP;
+                        step();
+                        if (!ok) break;
+                        scores(0, k);
+                        if (left == 1) umma_commit(q_empty);
+                        v = values(is_open(++it));
+                        first = false;
+                    }
+                    umma_commit(saddr(&bar.first));
                 }
                 if (ok && runs.run > 0) ok = wait(&bar.ack, runs.run - 1);
                 if (!ok) break;
