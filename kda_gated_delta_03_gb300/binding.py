@@ -754,6 +754,9 @@ def _there(dev, stream, call, *args, **kwargs):
 
 def _heads(name, t, T, d, dtype, dev):
     """A tensor [T, H, d] whose tokens are contiguous, as a slice of a fused projection is: (H, elements a token)."""
+    shape = t.shape
+    if len(shape) == 3 and shape[0] == T and shape[2] == d and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return shape[1], shape[1] * d
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
@@ -767,14 +770,21 @@ def _heads(name, t, T, d, dtype, dev):
     return H, max(step, H * d)
 
 
+def _out_stride(name, t, shape, dtype, dev):
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return _heads(name, t, shape[0], shape[2], dtype, dev)[1]
+
+
 def _frequencies(inv_freq, dev):
     if inv_freq is None:
         return 0, None
-    if inv_freq.dim() != 1:
-        raise ValueError(f"inv_freq: shape {tuple(inv_freq.shape)}, expected [rotary_dim / 2]")
-    _check_at("inv_freq", inv_freq, _F64, inv_freq.shape, dev)
-    n = 2 * inv_freq.shape[0]
-    return n, inv_freq.data_ptr() if n else None
+    shape = inv_freq.shape
+    if len(shape) != 1:
+        raise ValueError(f"inv_freq: shape {tuple(shape)}, expected [rotary_dim / 2]")
+    _check_at("inv_freq", inv_freq, _F64, shape, dev)
+    n = shape[0]
+    return 2 * n, inv_freq.data_ptr() if n else None
 
 
 def _layout(layout):
@@ -800,7 +810,8 @@ def kda_rotary(q, k, positions, inv_freq, *, layout: str = "half", rotary_scale:
                       inverse=inverse, q_out=q_out, k_out=k_out)
     if q.dim() != 3:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [T, H_q, d]")
-    T, d, dt = q.shape[0], q.shape[2], q.dtype
+    shape = q.shape
+    T, d, dt = shape[0], shape[2], q.dtype
     code = _DTYPES.get(dt)
     if code is None:
         raise TypeError(f"unsupported dtype {dt}")
@@ -808,18 +819,18 @@ def kda_rotary(q, k, positions, inv_freq, *, layout: str = "half", rotary_scale:
     _check_at("positions", positions, _I32, (T,), dev)
     rot, freq = _frequencies(inv_freq, dev)
     if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
-    if q_out.shape != q.shape:
-        raise ValueError(f"q_out: shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
-    qos = _heads("q_out", q_out, T, d, dt, dev)[1]
+        q_out = q.new_empty(shape)
+        qos = Hq * d
+    else:
+        qos = _out_stride("q_out", q_out, shape, dt, dev)
     Hkv = ks = kos = 0
     if k is not None:
         Hkv, ks = _heads("k", k, T, d, dt, dev)
         if k_out is None:
-            k_out = torch.empty((T, Hkv, d), dtype=dt, device=q.device)
-        if k_out.shape != k.shape:
-            raise ValueError(f"k_out: shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
-        kos = _heads("k_out", k_out, T, d, dt, dev)[1]
+            k_out = k.new_empty(k.shape)
+            kos = Hkv * d
+        else:
+            kos = _out_stride("k_out", k_out, k.shape, dt, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
     rc = (_LIB or load()).kda_rotary(q.data_ptr(), None if k is None else k.data_ptr(), positions.data_ptr(), freq, T, Hq,
@@ -869,10 +880,10 @@ def kda_cache_append(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, 
     if q is not None:
         Hq, qs = _heads("q", q, T, d, dt, dev)
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
-        if q_out.shape != q.shape:
-            raise ValueError(f"q_out: shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
-        qos = _heads("q_out", q_out, T, d, dt, dev)[1]
+            q_out = q.new_empty(q.shape)
+            qos = Hq * d
+        else:
+            qos = _out_stride("q_out", q_out, q.shape, dt, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     rc = (_LIB or load()).kda_cache_append(
@@ -956,7 +967,7 @@ class TokenLogprobs(NamedTuple):
 
 def _rows(name, t, dev):
     """A matrix [T, V] with contiguous rows: (T, V, elements a row)."""
-    if t.dim() != 2:
+    if len(t.shape) != 2:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, V]")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, expected CUDA device {dev}")
@@ -982,11 +993,10 @@ def kda_token_logprobs(logits, tokens, *, top: int = 0, entropy: bool = False, s
     if code is None:
         raise TypeError(f"unsupported dtype {logits.dtype}")
     _check_at("tokens", tokens, _I32, (T,), dev)
-    on = dict(dtype=_F32, device=logits.device)
-    out = torch.empty((3 if entropy else 2, T), **on)
-    logp, lse, H = out[0], out[1], out[2] if entropy else None
-    best = torch.empty((T, max(top, 0)), **on)
-    word = torch.empty((T, max(top, 0)), dtype=_I32, device=logits.device)
+    k, on = max(top, 0), logits.device
+    logp, lse = torch.empty((T,), dtype=_F32, device=on), torch.empty((T,), dtype=_F32, device=on)
+    H = torch.empty((T,), dtype=_F32, device=on) if entropy else None
+    best, word = torch.empty((T, k), dtype=_F32, device=on), torch.empty((T, k), dtype=_I32, device=on)
     rc = (_LIB or load()).kda_token_logprobs(logits.data_ptr(), step, tokens.data_ptr(), T, V, code, top, logp.data_ptr(),
                                              lse.data_ptr(), H.data_ptr() if entropy else None,
                                              best.data_ptr() if top else None, word.data_ptr() if top else None,

@@ -415,55 +415,69 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     if (warp == LOAD_WARP && work) {
         // ---------------- pages ----------------
-        uint32_t n = 0;                       // stages filled
+        // Lane x has the boxes x, x + 32, ..; the next tile's page numbers are on their way while this one is copied.
+        uint32_t n = 0, st = 0, turn = 1;     // stages filled; the next one, and the phase of `empty` to wait for
         const int boxes = f.BN / box;
         bool ok = true;
         Runs runs(p, f, share);
         do {
             const Walk& w = runs.w;
-            const int count = runs.count, tile = runs.tile;
+            const int end = runs.tile + runs.count;
             const int32_t* table = p.table + (int64_t)w.b * p.max_pages;
-            for (int it = tile; it < tile + count && ok; ++it) {
+            int next[4], next_row[4];
+            auto look_up = [&](int it) {
                 const int j0 = tile_start(f, w.u, it);
-                int page[4], row[4], found = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int x = lane + 32 * i, j = j0 + x * box;
-                    page[i] = -2;
-                    if (x < boxes && j < w.u.end) {
+                    next[i] = INT32_MIN;      // no box
+                    if (32 * i < boxes && x < boxes && j < w.u.end) {
                         const int slot = over(j, f.by_page);
-                        row[i] = j - slot * p.page_size;
-                        page[i] = __ldg(table + slot);
-                        if (page[i] < 0 || page[i] >= p.num_pages) {
-                            page[i] = -1;
-                            atomicOr(p.err, KDA_DEVERR_PAGES);
-                        }
+                        next_row[i] = j - slot * p.page_size;
+                        next[i] = max(__ldg(table + slot), -1);
                     }
-                    found += __popc(__ballot_sync(0xFFFFFFFFu, page[i] >= 0));
                 }
-                for (int v = 0; v < 2 && ok; ++v, ++n) {
-                    const int st = n % L::STAGES;
-                    ok = wait(&bar.empty[st], n / L::STAGES + 1);
-                    if (!ok) break;
-                    const uint32_t to = sm_kv + st * L::BLOCK;
+            };
+            look_up(runs.tile);
+            for (int it = runs.tile; it < end && ok; ++it) {
+                int page[4], row[4], found = 0;
+                bool bad = false;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (page[i] == -1)    // no such page: zeros
-                            for (int h = 0; h < L::HALVES; ++h)
-                                for (int y = 0; y < box * 8; ++y)
-                                    st_shared16(to + h * L::HALF + (lane + 32 * i) * box * 128 + y * 16, make_uint4(0, 0, 0, 0));
-                    fence_async_smem();
+                for (int i = 0; i < 4; ++i) {
+                    page[i] = next[i], row[i] = next_row[i];
+                    if (32 * i < boxes) {
+                        if (page[i] >= p.num_pages) page[i] = -1;
+                        bad = bad || page[i] == -1;
+                        found += __popc(__ballot_sync(0xFFFFFFFFu, page[i] >= 0));
+                    }
+                }
+                if (it + 1 < end) look_up(it + 1);
+                const bool zeros = __any_sync(0xFFFFFFFFu, bad);
+                if (zeros && lane == 0) atomicOr(p.err, KDA_DEVERR_PAGES);
+                for (int v = 0; v < 2; ++v, ++n) {
+                    ok = wait(&bar.empty[st], turn);
+                    if (!ok) break;
+                    const uint32_t to = sm_kv + st * L::BLOCK, full = saddr(&bar.full[st]);
+                    if (zeros) {              // no such page
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (page[i] == -1)
+                                for (int h = 0; h < L::HALVES; ++h)
+                                    for (int y = 0; y < box * 8; ++y)
+                                        st_shared16(to + h * L::HALF + (lane + 32 * i) * box * 128 + y * 16, make_uint4(0, 0, 0, 0));
+                        fence_async_smem();
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_expect_tx(saddr(&bar.full[st]), (uint32_t)(found * box * D * 2));
+                    if (lane == 0) mbar_expect_tx(full, (uint32_t)(found * box * D * 2));
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (page[i] >= 0)
 #pragma unroll
                             for (int h = 0; h < L::HALVES; ++h)
-                                tma_load_4d(to + h * L::HALF + (lane + 32 * i) * box * 128, v ? &v_map : &k_map, h * 64, row[i], w.h,
-                                            page[i], saddr(&bar.full[st]));
+                                tma_load_4d(to + h * L::HALF + (lane + 32 * i) * box * 128, v ? &v_map : &k_map, h * 64, row[i], w.h, page[i], full);
                     if (lane == 0) issued = n + 1;
+                    if (++st == L::STAGES) st = 0, turn ^= 1;
                 }
             }
             if (!ok || !runs.next(p, f)) break;
