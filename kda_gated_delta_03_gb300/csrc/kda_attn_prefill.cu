@@ -22,7 +22,10 @@ template <int D>
 struct Layout {
     static constexpr int LD = D + 4;                           // floats of a row of Q and K
     static constexpr int PLD = BN + 4;
-    static constexpr int Q = 0, KV = BM * LD, P = KV + BN * LD, BYTES = (P + BM * PLD) * 4;
+    // Two CTAs an SM: at d = 128 the weights take the keys' place, and the next keys are fetched after them.
+    static constexpr bool OWN_P = D < 128;
+    static constexpr int Q = 0, K = BM * LD, V = K + BN * LD, P = OWN_P ? V + BN * D : K, BYTES = (V + BN * D + (OWN_P ? BM * PLD : 0)) * 4;
+    static_assert((OWN_P || LD >= PLD) && BYTES <= 113 * 1024, "two CTAs an SM");
 };
 
 // Four elements from global memory, as floats.
@@ -39,7 +42,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
     extern __shared__ float smem[];
     __shared__ int64_t sums[NW];
     __shared__ Share share;
-    float *Qs = smem + L::Q, *KV = smem + L::KV, *Ps = smem + L::P;
+    float *Qs = smem + L::Q, *Ks = smem + L::K, *Vs = smem + L::V, *Ps = smem + L::P;
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16, cta = blockIdx.x, grid = gridDim.x;
     ChunkRecord* records = reinterpret_cast<ChunkRecord*>(p.workspace);
     if (!f.whole && tid == 0) records[cta].b = -1;
@@ -76,24 +79,33 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
             for (int c = 0; c < GO * CO; ++c) o[i][c] = 0.f;
         }
         const int32_t* table = p.table + (int64_t)w.b * p.max_pages;
-        auto fetch = [&](const void* pages, int64_t stride, int j0, int ld) {
+        // A tile's rows into shared memory: fp32 on its way until the copies of its group are waited for.
+        auto fetch = [&](const void* pages, int64_t stride, int j0, float* to, int ld) {
             for (int i = tid; i < BN * (D / 4); i += NT) {
                 const int r = i / (D / 4), c = i % (D / 4) * 4, j = j0 + r;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                const T* from = nullptr;
                 if (j < u.end) {
                     const int slot = over(j, f.by_page), page = __ldg(table + slot);
                     if (page >= 0 && page < p.num_pages)
-                        x = load4(static_cast<const T*>(pages) + page * stride +
-                                  ((int64_t)w.h * p.page_size + (j - slot * p.page_size)) * D + c);
+                        from = static_cast<const T*>(pages) + page * stride + ((int64_t)w.h * p.page_size + (j - slot * p.page_size)) * D + c;
                     else if (c == 0)
                         atomicOr(p.err, KDA_DEVERR_PAGES);
                 }
-                *reinterpret_cast<float4*>(KV + r * ld + c) = x;
+                if constexpr (sizeof(T) == 4) {
+                    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to + r * ld + c);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(from ? from : static_cast<const T*>(p.q)), "r"(from ? 16 : 0)
+                                 : "memory");
+                } else {
+                    *reinterpret_cast<float4*>(to + r * ld + c) = from ? load4(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
             }
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
         };
+        fetch(p.k_pages, p.k_stride, tile_start(f, u, tile), Ks, L::LD);
         for (int it = tile; it < tile + count; ++it) {
             const int j0 = tile_start(f, u, it);
-            fetch(p.k_pages, p.k_stride, j0, L::LD);
+            fetch(p.v_pages, p.v_stride, j0, Vs, D);
+            asm volatile("cp.async.wait_group 1;\n" ::: "memory");         // the keys
             __syncthreads();
             float s[4][4] = {};
 #pragma unroll 4
@@ -102,7 +114,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(Qs + (ty * 4 + i) * L::LD + k);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(KV + (tx + 16 * j) * L::LD + k);
+                for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * L::LD + k);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -112,6 +124,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
             // every row of the unit sees every token of the tile: the first row's position bounds it from above, the last one's window from below
             const int last = w.s.len - w.s.n + over(row0 + u.rows - 1, f.by_group);
             const bool open = j0 + BN - 1 <= u.pos0 && (p.window == 0 || j0 > last - p.window || j0 + BN <= p.sinks);
+            if (!L::OWN_P) __syncthreads();   // every thread has read the keys
             float grow[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -143,9 +156,10 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
 #pragma unroll
                 for (int c = 0; c < GO * CO; ++c) o[i][c] *= grow[i];
             }
+            asm volatile("cp.async.wait_group 0;\n" ::: "memory");         // the values
             __syncthreads();
-            fetch(p.v_pages, p.v_stride, j0, D);
-            __syncthreads();
+            const bool more = it + 1 < tile + count;
+            if (L::OWN_P && more) fetch(p.k_pages, p.k_stride, tile_start(f, u, it + 1), Ks, L::LD);
             auto product = [&](auto checked) {
 #pragma unroll 2
                 for (int j = 0; j < BN; j += 4) {
@@ -161,7 +175,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
                         for (int g = 0; g < GO; ++g) {
                             float v[CO];
 #pragma unroll
-                            for (int c = 0; c < CO; ++c) v[c] = KV[(j + jj) * D + g * 16 * CO + tx * CO + c];
+                            for (int c = 0; c < CO; ++c) v[c] = Vs[(j + jj) * D + g * 16 * CO + tx * CO + c];
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -176,6 +190,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
             else
                 product(std::true_type());
             __syncthreads();
+            if (!L::OWN_P && more) fetch(p.k_pages, p.k_stride, tile_start(f, u, it + 1), Ks, L::LD);
         }
         // ---- outputs, or a piece of them ----
         const bool starts = tile == 0, ends = tile + count == u.tiles, complete = starts && ends;
