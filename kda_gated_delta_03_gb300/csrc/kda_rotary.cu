@@ -86,8 +86,10 @@ __global__ void __launch_bounds__(NT) kda_rotary_kernel(RotaryParams p, Items g,
             const int t = t0 + warp, b = sequence_of(p.cu, p.B, t, lane);
             if (lane == 0) {
                 int page = -1, slot = 0, pos = 0, real = 0;
-                if (b < p.B && __ldg(p.cu + b) <= t) {
-                    const int end = __ldg(p.cu + b + 1), len = __ldg(p.lens + b);
+                const int start = b < p.B ? __ldg(p.cu + b) : 0, end = b < p.B ? __ldg(p.cu + b + 1) : 0;
+                // a sequence whose borders are not in order counts as empty: its tokens are left alone
+                if (start >= 0 && start <= t && t < end && end <= p.T && (b > 0 || start == 0)) {
+                    const int len = __ldg(p.lens + b);
                     real = 1;
                     pos = (int)((int64_t)len - ((int64_t)end - t));
                     if (len >= 0 && (int64_t)len <= (int64_t)p.max_pages * p.page_size && pos >= 0) {

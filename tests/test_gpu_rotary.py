@@ -238,6 +238,27 @@ def test_append_bad_tables_lengths_and_borders_are_reported(dtype):
         assert torch.equal(a["k_pages"][others], want["k_pages"][others])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_leaves_sequences_with_bad_borders_alone(dtype):
+    """They count as empty: nothing of theirs is stored, and their queries' outputs stay as they were."""
+    rows, ps = [(5, 30), (20, 0), (3, 3)], 16
+    for b, value, left in ((0, 4, range(0, 5)), (0, -2, range(0, 5)), (3, 29, range(25, 28)), (3, 1 << 20, range(25, 28)),
+                           (3, 24, range(25, 28))):
+        a, old = batch(rows, 2, 64, ps, dtype), batch(rows, 2, 64, ps, dtype)
+        a["cu_seqlens"][b] = value
+        q = randn(28, 4, 64, dtype=dtype)
+        out = torch.full_like(q, 7.0)
+        kda.kda_cache_append(**a, q=q, q_out=out)
+        assert kda.kda_get_device_error() == 0x1
+        t, pos, page, slot = places(rows, ps, old["block_table"])
+        bad = torch.tensor([int(i) in left for i in t], device=DEV)
+        for name in ("k", "v"):
+            pool = a[name + "_pages"][page, :, slot]
+            assert torch.equal(bits(pool[bad]), bits(old[name + "_pages"][page, :, slot][bad]))
+            assert torch.equal(pool[~bad], a[name][t[~bad]])
+        assert bool((out[t[bad]] == 7).all()) and torch.equal(out[t[~bad]], q[t[~bad]])
+
+
 def test_streams_and_graphs():
     rows = [(1, n) for n in (0, 31, 32, 500)]
     a = batch(rows, 2, 64, 16, "bf16")
