@@ -547,7 +547,7 @@ KDA_API kda_status kda_cache_compact(const int32_t* block_table, int32_t rows, i
  *     rotary_scale * (a cos - b sin, b cos + a sin),   angle = positions[t] * inv_freq[i]
  *
  * and the rest of the head is copied.  inverse != 0 turns by minus the angle, with the same scale: the gradient
- * of the outputs becomes that of the inputs.  Angles are exact to 2^-32 of a turn for every 32-bit position.
+ * of the outputs becomes that of the inputs.  Angles are exact to 2^-25 of a radian for every 32-bit position.
  *
  *   q, q_out   [T, H_q, d] dtype dt, token t at q + t * q_stride (elements); likewise k, k_out with H_kv heads.
  *              k NULL: only q.  q_out may be q and k_out may be k, with the same strides; no other overlap.

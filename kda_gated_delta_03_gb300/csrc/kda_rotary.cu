@@ -6,9 +6,11 @@
 // copied.  Turned by minus the angle it is its own gradient.
 //
 // Angles: position * inv_freq reaches 1e6 radians and more, where fp32 holds no fraction of a turn.  A frequency is
-// made a 64-bit fraction of a turn, once by each thread; its product with the position modulo 2^64 is an integer
-// multiplication, which drops whole turns exactly, and the upper 32 bits of the rest go to sincospi.  So any 32-bit
-// position is as exact as the first one, and no 64-bit sine is needed (one costs more than a head's whole traffic).
+// made a 64-bit fraction of a turn, once by each thread (fp64, the product's and the constant's lower parts included); its
+// product with the position modulo 2^64 is an integer multiplication, which drops whole turns exactly.  Quarter turns come
+// off the upper 32 bits of the rest before they become a float, so that the 24 bits are those of an eighth of a turn, and
+// sincospi takes that.  So any 32-bit position is as exact as the first one, and no 64-bit sine is needed (one costs more
+// than a head's whole traffic).
 //
 // What bounds it is DRAM: every element is read and written once.  A CTA takes TB tokens: their n angles each are
 // worked out once in shared memory and used for all heads of q and k, while the first vectors are on their way.
@@ -35,11 +37,20 @@ __device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2
 __device__ __forceinline__ float across(float a, float b, float2 cs) { return __fmaf_rn(a, cs.x, -__fmul_rn(b, cs.y)); }
 __device__ __forceinline__ float along(float a, float b, float2 cs) { return __fmaf_rn(b, cs.x, __fmul_rn(a, cs.y)); }
 
-// inv_freq (radians a position) as a fraction of a turn in 64 bits.
+// inv_freq (radians a position) as a fraction of a turn in 64 bits: f / (2 pi) in two parts, whole turns off the first one.
 __device__ __forceinline__ uint64_t turn_fraction(double f) {
-    double t = f * 0.15915494309189533577;    // 1 / (2 pi)
-    t -= floor(t);
-    return __double2ull_rz(t * 18446744073709551616.0);
+    const double c = 0.15915494309189535, c_low = -9.839338337591243e-18;  // 1 / (2 pi)
+    const double hi = __dmul_rn(f, c), lo = __fma_rn(f, c_low, __fma_rn(f, c, -hi));
+    return (uint64_t)__double2ll_rn((hi - rint(hi)) * 0x1p64) + (uint64_t)__double2ll_rn(lo * 0x1p64);
+}
+
+// cos, sin of a 64-bit fraction of a turn.
+__device__ __forceinline__ float2 cos_sin(uint64_t phase) {
+    const uint32_t x = (uint32_t)(phase >> 32), quarters = (x + (1u << 29)) >> 30;
+    float s, c;
+    sincospif((float)(int32_t)(x - (quarters << 30)) * 0x1p-31f, &s, &c);
+    const float2 y = quarters & 1u ? make_float2(-s, c) : make_float2(c, s);
+    return quarters & 2u ? make_float2(-y.x, -y.y) : y;
 }
 
 // The sequence of a packed batch that token t belongs to: the first b with cu[b + 1] > t, or B.  A warp looks at 32
@@ -114,10 +125,8 @@ __global__ void __launch_bounds__(NT) kda_rotary_kernel(RotaryParams p, Items g,
         if (i < n) {
             const uint64_t f = turn_fraction(__ldg(p.inv_freq + i));
             for (int j = tid / MAX_N; j < tokens; j += group) {
-                const uint64_t phase = (uint64_t)(int64_t)pos_s[j] * f;
-                float s, c;
-                sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-                turn[j][i] = make_float2(c * p.scale, s * p.scale * p.sign);
+                const float2 cs = cos_sin((uint64_t)(int64_t)pos_s[j] * f);
+                turn[j][i] = make_float2(cs.x * p.scale, cs.y * p.scale * p.sign);
             }
         }
         __syncthreads();
