@@ -2,10 +2,11 @@
 
 Shows the calls of a decode loop as a serving program makes them.  For N requests with K beams each, N * K rows:
 
-* ``kda_prefill`` brings the prompts' KDA states; their keys and values go into pages that ``kda_cache_fork`` hands
-  out to the (until then empty) rows;
+* ``kda_cache_fork`` hands pages out to the (until then empty) rows; in the layers ``kda_prefill`` brings the prompts'
+  KDA states, ``kda_cache_append`` their keys and values into the pages, ``kda_attention_prefill`` their attention;
 * each step, ``kda_beam_select`` chooses the beams that go on, ``kda_state_fork`` and ``kda_cache_fork`` give them
-  their states and pages, ``kda_decode_step`` and ``kda_attention_decode`` run the layers on the new tokens.
+  their states and pages, ``kda_decode_step`` and ``kda_attention_decode`` run the layers on the new tokens;
+* at the end ``kda_token_logprobs`` scores the found sequences in one pass over all of them, as prompts.
 
 Run on a GPU:  python examples/hybrid_beam_search.py
 """
@@ -54,6 +55,49 @@ class HybridStack:
                 (x @ w["v"]).view(T, self.Hkv, self.d))
 
 
+def run_prompts(model, prompts, K, k_pool, v_pool, table, lens, states=None):
+    """Prompts through the layers, packed one after the other, prompt n in row n * K of the table (the other rows stay
+    empty).  Returns the last layer's outputs and the prompts' borders; states[layer, n * K] receives their KDA states."""
+    dev, (H, d) = model.device, (model.H, model.d)
+    packed = torch.tensor([0] + [len(p) for p in prompts]).cumsum(0).int()
+    rows = torch.cat([packed[:1], packed[1:].repeat_interleave(K)]).to(dev)  # borders of all rows, empty ones among them
+    packed = packed.to(dev)
+    x = model.embed[torch.tensor([t for p in prompts for t in p], device=dev)]
+    ik = ia = 0
+    for kind, w in zip(model.kinds, model.w):
+        h = model.norm(x)
+        if kind == "k":
+            o, s = kda.kda_prefill(*(t.contiguous() for t in model.kda_inputs(w, h)), packed)
+            if states is not None:
+                states[ik, ::K] = s
+            ik += 1
+        else:
+            q, k, v = model.attention_inputs(w, h)
+            kda.kda_cache_append(k, v, k_pool[ia], v_pool[ia], table, lens, rows)
+            o = kda.kda_attention_prefill(q, k_pool[ia], v_pool[ia], table, lens, rows, scale=1 / math.sqrt(d))
+            ia += 1
+        x = x + o.reshape(-1, H * d) @ w["o"]
+    return x, packed
+
+
+def score(model, prompts, continuations, page_size=4, top=1):
+    """Log probabilities of each prompt's continuation, word by word, and the `top` likeliest words in their places: the
+    TokenLogprobs of all sequences' tokens packed one after the other (0 for the prompts' own words), and the borders."""
+    dev, n = model.device, len(prompts)
+    sequences = [list(p) + list(c) for p, c in zip(prompts, continuations)]
+    counts = [-(-len(s) // page_size) for s in sequences]
+    i32 = dict(dtype=torch.int32, device=dev)
+    k_pool = torch.zeros((model.kinds.count("a"), sum(counts), model.Hkv, page_size, model.d), device=dev)
+    v_pool = torch.zeros_like(k_pool)
+    table, lens, _ = kda.kda_cache_fork(torch.empty((0, max(counts)), **i32), torch.empty(0, **i32), torch.full((n,), -1, **i32),
+                                        torch.zeros(sum(counts), **i32), page_size,
+                                        grow=torch.tensor([len(s) for s in sequences], **i32))
+    x, packed = run_prompts(model, sequences, 1, k_pool, v_pool, table, lens)
+    # a position's logits are about the next word
+    words = [t for p, s in zip(prompts, sequences) for t in [-1] * (len(p) - 1) + s[len(p):] + [-1]]
+    return kda.kda_token_logprobs(model.norm(x) @ model.head, torch.tensor(words, **i32), top=top), packed
+
+
 def beam_search(model, prompts, K, steps, eos, page_size=4, pages=None):
     """The K best continuations of each prompt: (scores [N, K], sequences: N lists of K token lists)."""
     dev, N = model.device, len(prompts)
@@ -74,30 +118,9 @@ def beam_search(model, prompts, K, steps, eos, page_size=4, pages=None):
     lens[::K] = torch.tensor([len(p) for p in prompts], **i32)
     table, lens, ref = kda.kda_cache_fork(torch.empty((0, M), **i32), torch.empty(0, **i32), torch.full((R,), -1, **i32), ref,
                                           page_size, grow=lens)
-    cu = torch.tensor([0] + [len(p) for p in prompts]).cumsum(0)
-    x = model.embed[torch.tensor([t for p in prompts for t in p], device=dev)]
-    place = torch.cat([torch.arange(len(p)) for p in prompts]).to(dev)       # position within its prompt
-    row = torch.repeat_interleave(torch.arange(N), cu.diff()).to(dev) * K
-    page, slot = table[row, place // page_size].long(), place % page_size
-    seen = (row[:, None] == row[None, :]) & (place[None, :] <= place[:, None])
-    ik = ia = 0
-    for kind, w in zip(model.kinds, model.w):
-        h = model.norm(x)
-        if kind == "k":
-            o, s = kda.kda_prefill(*(t.contiguous() for t in model.kda_inputs(w, h)), cu.int().to(dev))
-            states[ik, ::K] = s
-            ik += 1
-        else:
-            q, k, v = model.attention_inputs(w, h)
-            k_pool[ia, page, :, slot], v_pool[ia, page, :, slot] = k, v
-            g = H // Hkv
-            a = torch.einsum("thgd,shd->hgts", q.view(-1, Hkv, g, d), k) / math.sqrt(d)
-            a = torch.softmax(a.masked_fill(~seen, float("-inf")), -1)
-            o = torch.einsum("hgts,shd->thgd", a, v)
-            ia += 1
-        x = x + o.reshape(-1, H * d) @ w["o"]
+    x, packed = run_prompts(model, prompts, K, k_pool, v_pool, table, lens, states)
     logits = torch.zeros((R, model.vocab), device=dev)
-    logits[::K] = model.norm(x[cu[1:].to(dev) - 1]) @ model.head
+    logits[::K] = model.norm(x[packed[1:].long() - 1]) @ model.head
 
     # ---- steps ----
     scores = torch.full((N, K), float("-inf"), device=dev)
@@ -138,15 +161,25 @@ def beam_search(model, prompts, K, steps, eos, page_size=4, pages=None):
     return scores, [sequences[n * K:(n + 1) * K] for n in range(N)]
 
 
+def until(beam, eos):
+    """A found sequence up to its first end."""
+    return beam[:beam.index(eos) + 1] if eos in beam else beam
+
+
 def main():
     model = HybridStack()
     g = torch.Generator().manual_seed(1)
     prompts = [torch.randint(0, model.vocab, (n,), generator=g).tolist() for n in (9, 1, 30)]
     scores, sequences = beam_search(model, prompts, K=4, steps=12, eos=5)
+    sequences = [[until(beam, 5) for beam in beams] for beams in sequences]
+    again, packed = score(model, [p for p in prompts for _ in range(4)], [beam for beams in sequences for beam in beams])
+    likeliest = [x == w for x, w in zip(again.top_logp[:, 0].tolist(), again.logp.tolist())]
+    packed = packed.tolist()
     for n, (s, beams) in enumerate(zip(scores.tolist(), sequences)):
         print(f"prompt of {len(prompts[n])} tokens")
-        for score, beam in zip(s, beams):
-            print(f"  {score:9.4f}  {beam}")
+        for i, (total, beam) in enumerate(zip(s, beams)):
+            end = packed[4 * n + i + 1] - 1
+            print(f"  {total:9.4f}  {beam}  ({sum(likeliest[end - len(beam):end])} of {len(beam)} words the likeliest)")
 
 
 if __name__ == "__main__":
