@@ -131,6 +131,10 @@ def test_backward_refuses(lib, over, code):
     assert backward(lib, **over) == code
 
 
+def test_backward_refuses_more_chunks_than_a_grid_has(lib):
+    assert backward(lib, T=1 << 20, V=1 << 22, stride=1 << 22, gstride=1 << 22, dt=0) == TOO_LARGE
+
+
 def test_binding_wants_cuda_tensors():
     i, x = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 1, 64)
     pool, table = torch.zeros(3, 1, 4, 64), torch.zeros((1, 2), dtype=torch.int32)
