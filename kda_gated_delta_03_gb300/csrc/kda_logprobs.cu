@@ -7,8 +7,8 @@
 // The largest logit stays out of the sum r at every level (lane, warp, CTA, cluster), so that a word with nearly all
 // the probability keeps its small -log p to fp32's relative precision: 1 + r would round it to 6e-8.
 //
-// One pass over the logits.  A row, or its parts on the CTAs of a cluster where there are few rows, streams through
-// registers in chunks, the next one under way while one is summed; a warp's lanes share their maximum, so that a rescale
+// One pass over the logits.  A row, or its parts on the CTAs of a cluster where there are few rows, streams through a ring
+// of chunks in shared memory, the next ones under way while one is summed; a warp's lanes share their maximum, so that a rescale
 // is a branch that all of them take or none.  The best words are gathered on the way: the top-th best of 64 maxima in the
 // first chunk bounds them from below, and vectors with a word above that, a hundred or so a row, are written down and
 // looked at again when the row is through.  Rows with too many (words in order, equal logits) are gone through once more with
@@ -25,6 +25,7 @@ namespace {
 
 constexpr int NT = 128, NW = NT / 32;
 constexpr int LOADS = 2;                      // 16-byte loads of a thread and chunk
+constexpr int STAGES = 3;                     // chunks under way (2, 3, 4: 121.5, 119.4, 119.7 us)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int GROUPS = 64;                    // of threads, whose maxima give the bound: twice as many as a top may ask for
 constexpr int MAX_TOP = KDA_LOGPROBS_MAX_TOP, MAX_CLUSTER = 8;
@@ -47,8 +48,6 @@ __device__ __forceinline__ void unpack(const uint4& r, float* x, __nv_bfloat16) 
 __device__ __forceinline__ void unpack(const uint4& r, float* x, float) {
     x[0] = __uint_as_float(r.x), x[1] = __uint_as_float(r.y), x[2] = __uint_as_float(r.z), x[3] = __uint_as_float(r.w);
 }
-__device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float value(const float* p) { return *p; }
 __device__ __forceinline__ uint32_t bits16(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
 
 // Vector v of a row that begins `off` elements into its first 16 bytes; what lies outside the row reads as `fill` bits.
@@ -186,12 +185,16 @@ __device__ __forceinline__ void absorb(Shared<LIST>& sm, const float (&x)[EPT], 
     __syncthreads();
 }
 
-template <typename T, bool TOP, bool ENTROPY>
-__global__ void __launch_bounds__(NT, 8) kda_logprobs_kernel(LogprobParams p, int cluster) {
+// CLUSTER: a row's parts lie on several CTAs.  A kernel of its own, since the code that joins them costs the loop registers where
+// nothing is joined (2,048 rows of 131,072 words 127 us against 119).
+template <typename T, bool TOP, bool ENTROPY, bool CLUSTER>
+__global__ void __launch_bounds__(NT, 8) kda_logprobs_kernel(LogprobParams p, int clusters) {
     using E = Elems<T>;
     constexpr int W = E::W, EPT = E::EPT, CHUNK = E::CHUNK;
     __shared__ Shared<TOP ? E::LIST : 1> sm;
+    __shared__ uint4 ring[STAGES][LOADS][NT];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cluster = CLUSTER ? clusters : 1;
     const int64_t row = blockIdx.x / cluster;
     const int part = blockIdx.x % cluster;
     const T* x0 = static_cast<const T*>(p.logits) + row * p.row_stride;
@@ -201,34 +204,40 @@ __global__ void __launch_bounds__(NT, 8) kda_logprobs_kernel(LogprobParams p, in
     if (tid == 0) sm.count = 0, sm.found = 0, sm.bound = 0;
     __syncthreads();
 
-    uint4 raw[LOADS];
+    // Chunks come in through a ring that is STAGES deep: every thread copies its own vectors and takes them out again, so that
+    // nobody waits for anybody.
     auto first = [&](int c) { return (int64_t)c * CHUNK + tid * W - off; };
     // chunks that lie in the row as a whole need no look at its ends
     const uint4* in = reinterpret_cast<const uint4*>(x0 - off) + tid;
-    const int inner = off ? 1 : 0, outer = (int)(((int64_t)p.V + off) / CHUNK);
-    auto load = [&](int c) {
+    const int inner = off ? 1 : 0, outer = min((int)(((int64_t)p.V + off) / CHUNK), c1);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(&ring[0][0][tid]);
+    auto load = [&](int c, int stage) {
         if (c >= inner && c < outer) {
 #pragma unroll
-            for (int j = 0; j < LOADS; ++j) raw[j] = __ldcs(in + (int64_t)c * (LOADS * NT) + j * NT);
-        } else {
+            for (int j = 0; j < LOADS; ++j)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(ring_at + (stage * LOADS + j) * (NT * 16)),
+                             "l"(in + (int64_t)c * (LOADS * NT) + j * NT)
+                             : "memory");
+        } else if (c < c1) {
 #pragma unroll 1
-            for (int j = 0; j < LOADS; ++j) {
-                const uint4 v = load_vec(x0, first(c) + j * (NT * W), p.V);
-#pragma unroll
-                for (int k = 0; k < LOADS; ++k)
-                    if (k == j) raw[k] = v;
-            }
+            for (int j = 0; j < LOADS; ++j) ring[stage][j][tid] = load_vec(x0, first(c) + j * (NT * W), p.V);
         }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    auto take = [&](float* x, int stage) {
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 1) : "memory");
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) unpack(ring[stage][j][tid], x + j * W, T());
     };
     float m = -INFINITY, r = 0.f, t = 0.f, least = -INFINITY, so_far = -INFINITY;    // m: of the warp
     int from = c0;                            // chunk that the bound is from
     bool own = false;                         // this lane holds the word that has m and stays out of r
-    if (c0 < c1) load(c0);
-    for (int c = c0; c < c1; ++c) {
-        float x[EPT];
 #pragma unroll
-        for (int j = 0; j < LOADS; ++j) unpack(raw[j], x + j * W, T());
-        if (c + 1 < c1) load(c + 1);
+    for (int i = 0; i < STAGES; ++i) load(c0 + i, i);
+    for (int c = c0, stage = 0; c < c1; ++c, stage = stage + 1 == STAGES ? 0 : stage + 1) {
+        float x[EPT];
+        take(x, stage);
+        load(c + STAGES, stage);
         float most[LOADS];
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
@@ -315,6 +324,15 @@ __global__ void __launch_bounds__(NT, 8) kda_logprobs_kernel(LogprobParams p, in
         if constexpr (ENTROPY) t += both(t2).x + both(t2).y;
     }
 
+    bool given = false;                       // the row has a word to score
+    float x_y = 0.f;
+    if (tid == 0 && part == 0) {
+        const int y = __ldg(p.tokens + row);
+        if (y < -1 || y >= p.V) atomicOr(p.err, KDA_DEVERR_TOKEN);
+        given = y >= 0 && y < p.V;
+        if (given) x_y = (float)x0[y];        // (used at the end)
+    }
+
     // ---- the warp's sums (its lanes have one m), the CTA's ----
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -352,9 +370,8 @@ __global__ void __launch_bounds__(NT, 8) kda_logprobs_kernel(LogprobParams p, in
             __syncthreads();
             for (int c = c0; c < c1; ++c) {
                 float x[EPT];
-                load(c);
 #pragma unroll
-                for (int j = 0; j < LOADS; ++j) unpack(raw[j], x + j * W, T());
+                for (int j = 0; j < LOADS; ++j) unpack(load_vec(x0, first(c) + j * (NT * W), p.V), x + j * W, T());
                 absorb<EPT, W>(sm, x, first(c), p.V, p.top, tid);
             }
         } else {
@@ -370,20 +387,24 @@ __global__ void __launch_bounds__(NT, 8) kda_logprobs_kernel(LogprobParams p, in
 
     // ---- the row's ----
     Sums s = sm.cta;
-    if (cluster > 1) {
+    if constexpr (CLUSTER) {
         cg::cluster_group group = cg::this_cluster();
         group.sync();
         if (part == 0) {
-            for (int i = 1; i < cluster; ++i) s = join(s, *group.map_shared_rank(&sm.cta, i));
+            // every warp fetches all CTAs' sums at once and joins them in their order
+            const Sums theirs = *group.map_shared_rank(&sm.cta, lane < cluster ? lane : 0);
+            for (int i = 1; i < cluster; ++i)
+                s = join(s, Sums{__shfl_sync(0xFFFFFFFFu, theirs.m, i), __shfl_sync(0xFFFFFFFFu, theirs.r, i), __shfl_sync(0xFFFFFFFFu, theirs.t, i)});
             if constexpr (TOP) {
-                for (int x = tid; x < MAX_CLUSTER * MAX_TOP; x += NT) {
-                    const int i = x / MAX_TOP, e = x % MAX_TOP;
-                    sm.best[x] = i < cluster && e < *group.map_shared_rank(&sm.found, i) ? group.map_shared_rank(sm.out, i)[e] : 0ull;
+                const int n = cluster * p.top;                // `top` places of each CTA, 0 in those that it does not fill
+                for (int x = tid; x < n; x += NT) {
+                    const int i = x / p.top, e = x - i * p.top;
+                    sm.best[x] = e < *group.map_shared_rank(&sm.found, i) ? group.map_shared_rank(sm.out, i)[e] : 0ull;
                 }
                 __syncthreads();
-                for (int x = tid; x < MAX_CLUSTER * MAX_TOP; x += NT) {
+                for (int x = tid; x < n; x += NT) {
                     const unsigned long long k = sm.best[x];
-                    const int rank = k ? keys_above(sm.best, MAX_CLUSTER * MAX_TOP, k) : MAX_TOP;
+                    const int rank = k ? keys_above(sm.best, n, k) : MAX_TOP;
                     if (rank < p.top) sm.list[rank] = k;
                 }
                 __syncthreads();
@@ -399,9 +420,7 @@ __global__ void __launch_bounds__(NT, 8) kda_logprobs_kernel(LogprobParams p, in
     const float nan = __int_as_float(0x7FC00000);
     auto log_p = [&](float x) { return bad ? nan : empty ? -INFINITY : (x - s.m) - log_r; };
     if (tid == 0) {
-        const int y = p.tokens[row];
-        if (y < -1 || y >= p.V) atomicOr(p.err, KDA_DEVERR_TOKEN);
-        p.logp[row] = y >= 0 && y < p.V ? log_p(value(x0 + y)) : 0.f;
+        p.logp[row] = given ? log_p(x_y) : 0.f;
         if (p.lse) p.lse[row] = bad ? nan : empty ? -INFINITY : s.m + log_r;
         if constexpr (ENTROPY) p.entropy[row] = bad ? nan : empty ? 0.f : log_r - LN2 * s.t / (1.f + s.r);
     }
@@ -419,12 +438,15 @@ cudaError_t launch_forward(const LogprobParams& p, cudaStream_t s) {
     using E = Elems<T>;
     static DeviceSetup done;
     int sms = 0;
-    const void* kernel = reinterpret_cast<const void*>(kda_logprobs_kernel<T, TOP, ENTROPY>);
-    cudaError_t e = device_setup(done, kernel, 0, &sms);
+    cudaError_t e = device_setup(done, nullptr, 0, &sms);
     if (e != cudaSuccess) return e;
     // A row's parts go to a cluster where the rows alone would leave SMs idle and a part still has a chunk.
     int cluster = 1;
     while (cluster < MAX_CLUSTER && (int64_t)p.T * cluster * 2 <= 2 * sms && (int64_t)E::CHUNK * cluster < p.V) cluster *= 2;
+    if (cluster == 1) {
+        kda_logprobs_kernel<T, TOP, ENTROPY, false><<<(unsigned)p.T, NT, 0, s>>>(p, 1);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)(p.T * cluster));
@@ -435,7 +457,7 @@ cudaError_t launch_forward(const LogprobParams& p, cudaStream_t s) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_logprobs_kernel<T, TOP, ENTROPY>, p, cluster);
+    return cudaLaunchKernelEx(&cfg, kda_logprobs_kernel<T, TOP, ENTROPY, true>, p, cluster);
 }
 
 template <typename T>
@@ -462,7 +484,10 @@ __device__ __forceinline__ uint4 pack(const float* x, float) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
-// LOADS vectors a thread; a CTA does `rows` whole rows of one chunk each, or one chunk of a row.  Each vector is read
+// One, two, four and eight vectors a thread: 2,048 rows of 131,072 bf16 words in 238, 187, 174 and 168 us.
+constexpr int BACK = 8;
+
+// BACK vectors a thread, one chunk of a row a CTA.  Each vector is read
 // before it is written, by the same thread, so the gradient may take the logits' place.
 template <typename T>
 __global__ void __launch_bounds__(NT) kda_logprobs_backward_kernel(LogprobGradParams p, int chunks) {
@@ -474,16 +499,16 @@ __global__ void __launch_bounds__(NT) kda_logprobs_backward_kernel(LogprobGradPa
     T* g0 = static_cast<T*>(p.grad) + row * p.grad_stride;
     const int off = (int)(reinterpret_cast<uintptr_t>(x0) / sizeof(T) % W);
     const bool together = reinterpret_cast<uintptr_t>(x0) % 16 == reinterpret_cast<uintptr_t>(g0) % 16;
-    const int64_t e0 = (int64_t)c * E::CHUNK + threadIdx.x * W - off;
-    uint4 raw[LOADS];
+    const int64_t e0 = (int64_t)c * (BACK * NT * W) + threadIdx.x * W - off;
+    uint4 raw[BACK];
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) raw[j] = load_vec(x0, e0 + j * (NT * W), p.V);
+    for (int j = 0; j < BACK; ++j) raw[j] = load_vec(x0, e0 + j * (NT * W), p.V);
     const int y0 = __ldg(p.tokens + row), y = y0 >= 0 && y0 < p.V ? y0 : -1;
     const float lse = __ldg(p.lse + row), g = y >= 0 ? __ldg(p.grad_logp + row) : 0.f;
     const float h = p.grad_entropy ? __ldg(p.grad_entropy + row) : 0.f, H = p.grad_entropy ? __ldg(p.entropy + row) : 0.f;
     const bool empty = lse == -INFINITY;      // nothing above -inf: no word has a gradient
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
+    for (int j = 0; j < BACK; ++j) {
         const int64_t e = e0 + j * (NT * W);
         if (e >= p.V) break;
         float x[W];
@@ -507,7 +532,7 @@ __global__ void __launch_bounds__(NT) kda_logprobs_backward_kernel(LogprobGradPa
 
 template <typename T>
 cudaError_t launch_backward(const LogprobGradParams& p, cudaStream_t s) {
-    const int64_t chunks = ((int64_t)p.V + Elems<T>::W - 1 + Elems<T>::CHUNK - 1) / Elems<T>::CHUNK;
+    const int64_t chunks = ((int64_t)p.V + Elems<T>::W - 2 + BACK * NT * Elems<T>::W) / (BACK * NT * Elems<T>::W);
     kda_logprobs_backward_kernel<T><<<(unsigned)(p.T * chunks), NT, 0, s>>>(p, (int)chunks);
     return cudaGetLastError();
 }
