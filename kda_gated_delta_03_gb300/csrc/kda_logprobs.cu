@@ -486,7 +486,9 @@ __device__ __forceinline__ uint4 pack(const float* x, float) {
 
 constexpr int BACK = 4;
 
-// BACK vectors a thread, one chunk of a row a CTA (2,048 rows of 131,072 bf16 words: 157 us, 6.8 TB/s, with four as with eight).  Each vector is read before it is written, by the same thread, so the gradient may take the logits' place.
+// BACK vectors a thread, one chunk of a row a CTA.  Each vector is read before it is written, by the same thread, so the
+// gradient may take the logits' place.  DRAM bounds it: 2,048 rows of 131,072 bf16 words 157 us (6.8 TB/s), with four as with eight
+// vectors.
 template <typename T>
 __global__ void __launch_bounds__(NT) kda_logprobs_backward_kernel(LogprobGradParams p, int chunks) {
     using E = Elems<T>;

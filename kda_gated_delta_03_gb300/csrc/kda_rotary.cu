@@ -12,8 +12,11 @@
 // sincospi takes that.  So any 32-bit position is as exact as the first one, and no 64-bit sine is needed (one costs more
 // than a head's whole traffic).
 //
-// What bounds it is DRAM: every element is read and written once.  A CTA takes TB tokens: their n angles each are
-// worked out once in shared memory and used for all heads of q and k, while the first vectors are on their way.
+// What bounds it is DRAM: every element is read and written once.  A CTA takes TB tokens: their n angles each are worked out
+// once in shared memory and used for all heads of q and k.  A thread has two vectors of 16 bytes under way at a time and 16
+// CTAs fit an SM: 24,000 tokens of 48 heads into pages 105 us (6.25 TB/s; with one vector 140), 16,384 tokens of 40
+// heads 56.5 us (5.9 TB/s).
+// More loads a thread were slower, since their registers cost CTAs.
 #include "kda_prompt.cuh"
 
 namespace kda {
@@ -23,15 +26,47 @@ constexpr int NT = 128;
 constexpr int MAX_N = 64;                     // pairs of a head
 constexpr int MAX_TB = 2;                     // tokens of a CTA
 
+// VEC elements as they are loaded and stored, and as floats.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Vec {
-    T x[VEC];
+struct Vec;
+template <typename T>
+struct Vec<T, 1> {
+    T x;
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = (float)x; }
+    __device__ __forceinline__ void set(const float (&f)[1]) { x = (T)f[0]; }
+};
+template <>
+struct Vec<float, 4> {
+    float4 x;
+    __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w; }
+    __device__ __forceinline__ void set(const float (&f)[4]) { x = make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Vec<__nv_bfloat16, 8> {
+    uint4 x;
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+        x = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f(float& y, float x) { y = x; }
-__device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+// Where pair i's cosine and sine lie.  A thread needs those of VEC pairs from item * VEC on, two at a time: the same two of
+// neighbouring items lie side by side, so that a warp's reads of 16 bytes meet in no bank.
+template <int VEC>
+__device__ __forceinline__ int place(int i) {
+    return VEC == 1 ? i : (i % VEC / 2) * (2 * MAX_N / VEC) + i / VEC * 2 + i % 2;
+}
+template <int VEC>
+__device__ __forceinline__ float4 two_places(const float2* turn, int item, int k) {
+    return *reinterpret_cast<const float4*>(turn + k * (2 * MAX_N / VEC) + item * 2);
+}
 
 // The rotation, with the same roundings wherever it stands: every variant gives the same bits.
 __device__ __forceinline__ float across(float a, float b, float2 cs) { return __fmaf_rn(a, cs.x, -__fmul_rn(b, cs.y)); }
@@ -69,10 +104,11 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t, int 
     return lo;
 }
 
-// A token's work: for each head of q and k `turned` items that rotate, then copied vectors; then v's vectors, `whole` a head.
-// In the half layout an item is VEC pairs in two vectors, in the interleaved one a vector (or, one element at a time, a pair).
+// A token's work: the items of each head of q and k, then v's, `whole` a head.  An item is two vectors of VEC elements, so that a
+// thread has two loads under way: those of VEC pairs in the half layout, neighbours in the interleaved one and where
+// heads are copied (the second may lie past the head there).
 struct Items {
-    int32_t turned, items, whole, total;
+    int32_t turned, items, whole, total;      // turned: items whose vectors are pairs of each other
     Divisor by_items, by_whole, by_total;
 };
 
@@ -80,7 +116,7 @@ struct Items {
 template <typename T, int VEC>
 __global__ void __launch_bounds__(NT) kda_rotary_kernel(RotaryParams p, Items g, int TB) {
     using V = Vec<T, VEC>;
-    __shared__ float2 turn[MAX_TB][MAX_N];                     // cos, sin
+    __shared__ __align__(16) float2 turn[MAX_TB][MAX_N];       // cos, sin, pair i at place(i)
     __shared__ int pos_s[MAX_TB];
     __shared__ int page_s[MAX_TB], slot_s[MAX_TB];             // page -1: not stored
     __shared__ int real_s[MAX_TB];                             // a token of some sequence
@@ -126,7 +162,7 @@ __global__ void __launch_bounds__(NT) kda_rotary_kernel(RotaryParams p, Items g,
             const uint64_t f = turn_fraction(__ldg(p.inv_freq + i));
             for (int j = tid / MAX_N; j < tokens; j += group) {
                 const float2 cs = cos_sin((uint64_t)(int64_t)pos_s[j] * f);
-                turn[j][i] = make_float2(cs.x * p.scale, cs.y * p.scale * p.sign);
+                turn[j][place<VEC>(i)] = make_float2(cs.x * p.scale, cs.y * p.scale * p.sign);
             }
         }
         __syncthreads();
@@ -140,7 +176,7 @@ __global__ void __launch_bounds__(NT) kda_rotary_kernel(RotaryParams p, Items g,
             const int64_t t = t0 + j, page = p.append ? page_s[j] : 0;
             const T* src;
             T* dst;
-            int item;
+            int item, c, apart;
             if (w < heads) {
                 const int h = over(w, g.by_items);
                 item = w - h * g.items;
@@ -157,47 +193,60 @@ __global__ void __launch_bounds__(NT) kda_rotary_kernel(RotaryParams p, Items g,
                         dst = static_cast<T*>(p.k_out) + t * p.k_out_stride + (h - p.Hq) * p.d;
                     }
                 }
+                const bool halves = item < g.turned && !p.interleaved;
+                c = halves ? item * VEC : p.interleaved ? 2 * item * VEC : 2 * n + 2 * (item - g.turned) * VEC;
+                apart = halves ? n : VEC;
             } else {
                 if (page < 0) continue;
-                const int x = w - heads, h = over(x, g.by_whole), c = (x - h * g.whole) * VEC;
-                *reinterpret_cast<V*>(static_cast<T*>(p.v_pages) + page * p.v_page_stride +
-                                      ((int64_t)h * p.page_size + slot_s[j]) * p.d + c) =
-                    *reinterpret_cast<const V*>(static_cast<const T*>(p.v) + t * p.v_stride + h * p.d + c);
-                continue;
+                const int x = w - heads, h = over(x, g.by_whole);
+                item = INT32_MAX, c = (x - h * g.whole) * 2 * VEC, apart = VEC;
+                src = static_cast<const T*>(p.v) + t * p.v_stride + h * p.d;
+                dst = static_cast<T*>(p.v_pages) + page * p.v_page_stride + ((int64_t)h * p.page_size + slot_s[j]) * p.d;
             }
-            if (item >= g.turned) {
-                const int c = 2 * n + (item - g.turned) * VEC;
-                *reinterpret_cast<V*>(dst + c) = *reinterpret_cast<const V*>(src + c);
-            } else if (!p.interleaved) {
-                const int c = item * VEC;
-                const V a = *reinterpret_cast<const V*>(src + c), b = *reinterpret_cast<const V*>(src + n + c);
-                V x, y;
+            const bool two = c + apart < p.d;
+            V a = *reinterpret_cast<const V*>(src + c), b{};
+            if (two) b = *reinterpret_cast<const V*>(src + c + apart);
+            if (item < g.turned) {
+                float x[VEC], y[VEC];
+                a.get(x), b.get(y);
+                auto turned = [&](int i, float2 cs) {
+                    const float u = x[i], v = y[i];
+                    x[i] = across(u, v, cs);
+                    y[i] = along(u, v, cs);
+                };
+                if constexpr (VEC == 1) {
+                    turned(0, turn[j][item]);
+                } else {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float2 cs = turn[j][c + i];
-                    const float u = to_f(a.x[i]), v = to_f(b.x[i]);
-                    from_f(x.x[i], across(u, v, cs));
-                    from_f(y.x[i], along(u, v, cs));
+                    for (int k = 0; k < VEC / 2; ++k) {
+                        const float4 cs = two_places<VEC>(turn[j], item, k);
+                        turned(2 * k, make_float2(cs.x, cs.y));
+                        turned(2 * k + 1, make_float2(cs.z, cs.w));
+                    }
                 }
-                *reinterpret_cast<V*>(dst + c) = x;
-                *reinterpret_cast<V*>(dst + n + c) = y;
+                a.set(x), b.set(y);
             } else if constexpr (VEC > 1) {
-                const V a = *reinterpret_cast<const V*>(src + item * VEC);
-                V x;
+                if (c < 2 * n && item != INT32_MAX) {          // pairs side by side
+                    auto turned = [&](V& vec, int second) {
+                        float x[VEC];
+                        vec.get(x);
 #pragma unroll
-                for (int i = 0; i < VEC; i += 2) {
-                    const float2 cs = turn[j][item * (VEC / 2) + i / 2];
-                    const float u = to_f(a.x[i]), v = to_f(a.x[i + 1]);
-                    from_f(x.x[i], across(u, v, cs));
-                    from_f(x.x[i + 1], along(u, v, cs));
+                        for (int k = 0; k < VEC / 4; ++k) {
+                            const float4 cs = two_places<VEC>(turn[j], item, second * (VEC / 4) + k);
+                            const float u = x[4 * k], v = x[4 * k + 1], w = x[4 * k + 2], z = x[4 * k + 3];
+                            x[4 * k] = across(u, v, make_float2(cs.x, cs.y));
+                            x[4 * k + 1] = along(u, v, make_float2(cs.x, cs.y));
+                            x[4 * k + 2] = across(w, z, make_float2(cs.z, cs.w));
+                            x[4 * k + 3] = along(w, z, make_float2(cs.z, cs.w));
+                        }
+                        vec.set(x);
+                    };
+                    turned(a, 0);
+                    if (c + VEC < 2 * n) turned(b, 1);
                 }
-                *reinterpret_cast<V*>(dst + item * VEC) = x;
-            } else {
-                const float2 cs = turn[j][item];
-                const float u = to_f(src[2 * item]), v = to_f(src[2 * item + 1]);
-                from_f(dst[2 * item], across(u, v, cs));
-                from_f(dst[2 * item + 1], along(u, v, cs));
             }
+            *reinterpret_cast<V*>(dst + c) = a;
+            if (two) *reinterpret_cast<V*>(dst + c + apart) = b;
         }
     }
 }
@@ -211,11 +260,12 @@ cudaError_t launch(const RotaryParams& p, cudaStream_t s) {
     const int64_t odd = p.q_stride | p.k_stride | p.v_stride | p.q_out_stride | p.k_out_stride;
     const bool wide = odd % W == 0 && on16(p.q) && on16(p.k) && on16(p.v) && on16(p.q_out) && on16(p.k_out) &&
                       (p.interleaved ? 2 * n : n) % W == 0 && (p.d - 2 * n) % W == 0;
-    const int vec = wide ? W : 1, per = p.interleaved ? (wide ? W / 2 : 1) : vec;      // pairs of an item
+    const int vec = wide ? W : 1;
     Items g;
-    g.turned = n / per;
-    g.items = g.turned + (p.d - 2 * n) / vec;
-    g.whole = p.append ? p.d / vec : 0;
+    g.turned = p.interleaved && wide ? 0 : n / vec;
+    const int rest = (p.interleaved && wide ? p.d : p.d - 2 * n) / vec;    // vectors outside of those items
+    g.items = g.turned + (rest + 1) / 2;
+    g.whole = p.append ? p.d / vec / 2 : 0;
     g.total = (p.Hq + p.Hkv) * g.items + p.Hkv * g.whole;
     g.by_items = divisor(g.items);
     g.by_whole = divisor(g.whole > 0 ? g.whole : 1);
