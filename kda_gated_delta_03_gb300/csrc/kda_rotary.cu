@@ -13,10 +13,9 @@
 // than a head's whole traffic).
 //
 // What bounds it is DRAM: every element is read and written once.  A CTA takes TB tokens: their n angles each are worked out
-// once in shared memory and used for all heads of q and k.  A thread has two vectors of 16 bytes under way at a time and 16
-// CTAs fit an SM: 24,000 tokens of 48 heads into pages 105 us (6.25 TB/s; with one vector 140), 16,384 tokens of 40
-// heads 56.5 us (5.9 TB/s).
-// More loads a thread were slower, since their registers cost CTAs.
+// once in shared memory and used for all heads of q and k.  A thread has two vectors of 16 bytes under way at a time, and 16
+// CTAs fit an SM: 26,814 tokens of 48 heads into pages 105 us (6.3 TB/s; with one vector 140), 16,384 tokens of 40 heads
+// 56.5 us (5.9 TB/s).  Two to four such items loaded before the first is stored were slower (76 to 110 us for the latter).
 #include "kda_prompt.cuh"
 
 namespace kda {
