@@ -755,8 +755,10 @@ def _there(dev, stream, call, *args, **kwargs):
 def _heads(name, t, T, d, dtype, dev):
     """A tensor [T, H, d] whose tokens are contiguous, as a slice of a fused projection is: (H, elements a token)."""
     shape = t.shape
-    if len(shape) == 3 and shape[0] == T and shape[2] == d and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        return shape[1], shape[1] * d
+    if len(shape) == 3 and shape[0] == T and shape[2] == d and t.dtype is dtype and t.get_device() == dev:
+        H, (step, head, inner) = shape[1], t.stride()
+        if inner == 1 and head == d and step >= H * d:
+            return H, step
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
