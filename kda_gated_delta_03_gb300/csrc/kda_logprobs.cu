@@ -10,7 +10,7 @@
 // One pass over the logits.  A row, or its parts on the CTAs of a cluster where there are few rows, streams through a ring
 // of chunks in shared memory, the next ones under way while one is summed; a warp's lanes share their maximum, so that a rescale
 // is a branch that all of them take or none.  The best words are gathered on the way: the top-th best of 64 maxima in the
-// first chunk bounds them from below, and vectors with a word above that, a hundred or so a row, are written down and
+// first chunks bounds them from below, and vectors with a word above that, some hundreds a row, are written down and
 // looked at again when the row is through.  Rows with too many (words in order, equal logits) are gone through once more with
 // the bound brought up to date after every chunk.  Nothing depends on the order of the atomics: they place candidates in a
 // list whose entries are then ranked.
@@ -30,11 +30,14 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int GROUPS = 64;                    // of threads, whose maxima give the bound: twice as many as a top may ask for
 constexpr int MAX_TOP = KDA_LOGPROBS_MAX_TOP, MAX_CLUSTER = 8;
 
+// Vectors of a row that are looked at again, for a list of that many words (1: no list).
+constexpr int vectors_of(int list) { return list == 1 ? 1 : 2 * list > 1200 ? 2 * list : 1200; }
+
 template <typename T>
 struct Elems {
     static constexpr int W = 16 / sizeof(T), EPT = LOADS * W, CHUNK = NT * EPT;
     static constexpr int LIST = MAX_TOP + MAX_TOP * EPT;      // kept ones, and all words of `top` threads
-    static constexpr int VECTORS = 2 * LIST;                  // those of a row that are looked at again
+    static constexpr int VECTORS = vectors_of(LIST);
 };
 
 __device__ __forceinline__ void unpack(const uint4& r, float* x, __nv_bfloat16) {
@@ -107,7 +110,7 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
 template <int LIST>
 struct alignas(16) Shared {
     unsigned long long list[LIST + 2];        // (two more: it is ranked in pairs)
-    int vectors[2 * LIST];
+    int vectors[vectors_of(LIST)];
     unsigned long long best[MAX_CLUSTER * MAX_TOP > NT ? MAX_CLUSTER * MAX_TOP : NT];      // thread maxima; at the end the best of all CTAs
     float most[GROUPS];                       // group maxima
     float least;
@@ -247,9 +250,13 @@ __global__ void __launch_bounds__(NT, 8) kda_logprobs_kernel(LogprobParams p, in
         }
         const float top_x = fmaxf(most[0], most[1]);
         if constexpr (TOP) {
-            // The bound: the top-th best of the maxima of 64 groups of threads, so far; anew after 1, 2, 4, 8 chunks.
+            // The bound: the top-th best of the maxima of 64 groups of threads, so far; anew after 4, 16, 64 .. chunks, so that the
+            // vectors written down grow with the logarithm of a row's length.  (All warps meet for it: 2,048 rows of 131,072
+            // words 114 us, after 1, 2, 4 and 8 118; 400 rows of 260,000 fp32 words with top 32 91 us, with no later ones 677, since the
+            // list ran over.)
             so_far = fmaxf(so_far, top_x);
-            if (((c - c0) & (c - c0 + 1)) == 0 && c - c0 < 8) {
+            const uint32_t seen = (uint32_t)(c - c0) + 1;
+            if ((seen & (seen - 1)) == 0 && (seen & 0x55555555u)) {
                 float group = so_far;
 #pragma unroll
                 for (int o = 1; o < NT / GROUPS; o <<= 1) group = fmaxf(group, __shfl_xor_sync(0xFFFFFFFFu, group, o));
