@@ -10,8 +10,10 @@
 //
 // Exponents are in base 2.  The reference that they are taken against only moves when a row's maximum has grown by
 // more than 2^8, which rescales O in tensor memory; weights up to 256 lose nothing in bf16.  Weights are rounded to bf16
-// for the second product: half a step of 2^-8 each, independent of each other, so n equal weights bring an error of
-// 1.1e-3 / sqrt(n) of a value, below the output's own rounding.  The row's sum is taken before that, in fp32: it gives lse.
+// for the second product, by half a step (2^-8 of a value) at most.  Where they differ these errors are independent of each other,
+// and n weights of a size bring 1.1e-3 / sqrt(n) of a value; where all of a row's weights are alike and the reference lags
+// behind their maximum they are one and the same, up to the size of the output's own rounding.
+// The row's sum is taken before that, in fp32: it gives lse.
 //
 // What is masked must not be multiplied: its weight is 0, and 0 * inf would be a NaN.  In tiles that are not open to every
 // row the helper warp clears the values behind the last token, and takes values that are not finite out of the tile; the
