@@ -590,7 +590,8 @@ KDA_API kda_status kda_cache_append(const void* q, const void* k, const void* v,
  *   workspace  kda_attention_prefill_workspace_size(...) bytes: partial results of units whose keys are split over
  *              several CTAs, joined in a fixed order (two calls give the same bits)
  * bf16: scores, sums and outputs are float32 until the end; at d = 64 and 128 weights are rounded to bf16 for the second
- * product.  Limits as for kda_attention_decode, and T * H_q below 2^31.
+ * product, whose outputs are divided by the sum of the rounded ones.  Limits as for kda_attention_decode, and T * H_q
+ * below 2^31.
  * A length outside [0, max_pages * page_size] counts as 0, new tokens before position 0 see nothing, and a page outside
  * [0, num_pages) reads as zeros; all set KDA_DEVERR_PAGES.
  */

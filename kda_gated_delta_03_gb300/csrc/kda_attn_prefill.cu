@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
         }
         // ---- outputs, or a piece of them ----
         const bool starts = tile == 0, ends = tile + count == u.tiles, complete = starts && ends;
-        float* piece = complete ? nullptr : pieces + ((int64_t)cta * 2 + (first_unit ? 0 : 1)) * piece_floats<D>(BM);
+        float* piece = complete ? nullptr : pieces + ((int64_t)cta * 2 + (first_unit ? 0 : 1)) * piece_floats(BM, D);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = ty * 4 + i;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
                 for (int g = 0; g < GO; ++g)
 #pragma unroll
                     for (int c = 0; c < CO; ++c) piece[r * D + g * 16 * CO + tx * CO + c] = o[i][g * CO + c];
-                if (tx == 0) piece[BM * D + r] = m[i], piece[BM * (D + 1) + r] = l[i];
+                if (tx == 0) piece[BM * D + r] = m[i], piece[BM * (D + 1) + r] = piece[BM * (D + 2) + r] = l[i];
             }
         }
         if (tid == 0 && starts && !ends)
@@ -243,7 +243,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
 }  // namespace
 
 size_t chunk_workspace(int32_t d, kda_dtype dt) {
-    const size_t cores = MAX_CTAS * (sizeof(ChunkRecord) + 2 * (size_t)BM * (d + 2) * sizeof(float));
+    const size_t cores = MAX_CTAS * (sizeof(ChunkRecord) + 2 * (size_t)piece_floats(BM, d) * sizeof(float));
     const size_t tensor = dt == KDA_DTYPE_BF16 && d >= 64 ? chunk_tc_workspace(d) : 0;
     return cores > tensor ? cores : tensor;
 }

@@ -10,10 +10,10 @@
 //
 // Exponents are in base 2.  The reference that they are taken against only moves when a row's maximum has grown by
 // more than 2^8, which rescales O in tensor memory; weights up to 256 lose nothing in bf16.  Weights are rounded to bf16
-// for the second product, by half a step (2^-8 of a value) at most.  Where they differ these errors are independent of each other,
-// and n weights of a size bring 1.1e-3 / sqrt(n) of a value; where all of a row's weights are alike and the reference lags
-// behind their maximum they are one and the same, up to the size of the output's own rounding.
-// The row's sum is taken before that, in fp32: it gives lse.
+// for the second product, by half a step (2^-8 of a value) at most, and the outputs are divided by the sum of the rounded ones,
+// so that an error that many weights share (keys of the same score) drops out and those of different ones are left: n weights of
+// a size bring 1.1e-3 / sqrt(n) of a value.  Divided by the sum of the unrounded ones, 4,000 equal keys behind a higher
+// one were off by 3.7e-3.  The sum before rounding, in fp32, gives lse.
 //
 // What is masked must not be multiplied: its weight is 0, and 0 * inf would be a NaN.  In tiles that are not open to every
 // row the helper warp clears the values behind the last token, and takes values that are not finite out of the tile; the
@@ -65,6 +65,7 @@ struct Misc {
     Share share;
     uint32_t tmem_base;
     uint32_t issued;                          // stages whose copies have been issued
+    float zero;
 };
 
 template <int D>
@@ -156,6 +157,11 @@ struct Open {
     __device__ __forceinline__ bool operator()(int it) const { return it < near ? it < a : it >= b && it < c; }
 };
 
+// Adds the two weights of a packed pair to a sum each.
+__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t x) {
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\nadd.rn.f32.bf16 %0, l, %0;\nadd.rn.f32.bf16 %1, h, %1;\n}\n" : "+f"(a), "+f"(b) : "r"(x));
+}
+
 // 64 bytes of a row: whole 32-byte sectors at a time where the address allows it, since each lane has a row of its own.
 __device__ __forceinline__ void store64(void* to, const uint32_t (&x)[16], bool wide) {
     uint32_t* p = static_cast<uint32_t*>(to);
@@ -221,6 +227,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
         init(&bar.q, 1), init(&bar.q_empty, 1), init(&bar.first, 1), init(&bar.run, 1), init(&bar.ack, 4), init(&bar.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         issued = 0;
+        misc.zero = 0.f;
         if (!f.whole) records[cta].b = -1;
     }
     if (warp == MMA_WARP) {
@@ -263,7 +270,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
             // The thread that tells the loader of free stages, when the scores of the last block are there: the products' thread
             // has no time for it (a commit behind products holds it up until they are done).
             const bool releases = lane == 0 && warp == (w.u.rows > TILE ? 4 : 0);
-            float ref = -INFINITY, l = 0.f;
+            float ref = -INFINITY, l = 0.f, lw = 0.f;      // lw: of the rounded weights
             bool part = false;                // the helper has looked at a tile of this run
             if (active) {
                 const Open is_open(p, f, w);
@@ -319,7 +326,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                     if (__any_sync(0xFFFFFFFFu, move)) {
                         const float to = move ? m : ref;
                         const float by = !move ? 1.f : ref == -INFINITY ? 0.f : ex2_approx((ref - to) * scale2);
-                        l *= by;
+                        l *= by, lw *= by;
                         if (it > tile) {      // the scores' barrier tells of the products issued before them, too
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
@@ -335,17 +342,17 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                     const float base = ref == -INFINITY ? 0.f : ref * scale2;
                     const Pair by2 = pair_of(scale2, scale2), minus = pair_of(-base, -base);
                     Pair sum[2] = {pair_of(0.f, 0.f), pair_of(0.f, 0.f)};
+                    float x[4][16];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        float x[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const float2 y = both(fma2(pair_of(s[c][2 * i], s[c][2 * i + 1]), by2, minus));
                             const float a = ex2_approx(y.x), b = ex2_approx(y.y);
-                            x[i] = __uint_as_float(pack_bf16x2(a, b));
+                            x[c][i] = __uint_as_float(pack_bf16x2(a, b));
                             sum[i & 1] = add2(sum[i & 1], pair_of(a, b));
                         }
-                        tmem_st16(t_s + 16 * c, x);
+                        tmem_st16(t_s + 16 * c, x[c]);
                         if (c % 2 == 1) {     // half of the weights: the product may begin
                             tmem_wait_st();
                             tc_fence_before();
@@ -355,6 +362,16 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                     }
                     const float2 sums2 = both(add2(sum[0], sum[1]));
                     l += sums2.x + sums2.y;
+                    // The rounded weights' sum, behind their hand-over: it begins with a zero that is read there, so that no
+                    // compiler brings it forward.  (Among the exponentials the prompt of 8,192 tokens took 452 us, here 443, without
+                    // it 383; as a product on the old matrix path 500; with the halves taken apart by shifts 508.)
+                    float zero;
+                    asm volatile("ld.volatile.shared.f32 %0, [%1];" : "=f"(zero) : "r"(saddr(&misc.zero)) : "memory");
+                    float odd_sum = zero;
+                    lw += zero;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) add_bf16x2(lw, odd_sum, __float_as_uint(x[i / 16][i % 16]));
+                    lw += odd_sum;
                 }
             }
             // The second block waits for the whole run also where it has no rows, and says so, so that neither side gets
@@ -377,7 +394,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                     add_odd<D>(p, f, odd[run % RING], w.b, w.h, mine ? w.s.len - w.s.n + t : -1,
                                static_cast<const __nv_bfloat16*>(p.q) + at * D, t_o, scale2, base);
                 if (complete) {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    const float inv = l == 0.f ? 0.f : 1.f / lw;
                     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + at * D;
                     const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
 #pragma unroll 1
@@ -392,7 +409,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                     if (mine && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (base + log2f(l)) * LN2;
                 } else {
                     float* piece = reinterpret_cast<float*>(p.workspace + TC_MAX_CTAS * sizeof(ChunkRecord)) +
-                                   ((int64_t)cta * 2 + (first_unit ? 0 : 1)) * piece_floats<D>(UNIT);
+                                   ((int64_t)cta * 2 + (first_unit ? 0 : 1)) * piece_floats(UNIT, D);
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         float o[32];
@@ -402,7 +419,7 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                             for (int i = 0; i < 32; i += 16) store64(piece + r * D + c + i, reinterpret_cast<const uint32_t(&)[16]>(o[i]), true);
                         }
                     }
-                    if (mine) piece[UNIT * D + r] = ref == -INFINITY ? -INFINITY : base, piece[UNIT * (D + 1) + r] = l;
+                    if (mine) piece[UNIT * D + r] = ref == -INFINITY ? -INFINITY : base, piece[UNIT * (D + 1) + r] = l, piece[UNIT * (D + 2) + r] = lw;
                 }
                 tc_fence_before();            // the next run's products overwrite O
             }
@@ -778,7 +795,7 @@ cudaError_t launch_tc(const ChunkParams& p, cudaStream_t s) {
 
 }  // namespace
 
-size_t chunk_tc_workspace(int32_t d) { return TC_MAX_CTAS * (sizeof(ChunkRecord) + 2 * (size_t)UNIT * (d + 2) * sizeof(float)); }
+size_t chunk_tc_workspace(int32_t d) { return TC_MAX_CTAS * (sizeof(ChunkRecord) + 2 * (size_t)piece_floats(UNIT, d) * sizeof(float)); }
 
 cudaError_t launch_attention_prefill_tc(const ChunkParams& p, cudaStream_t s) {
     return p.d == 64 ? launch_tc<64>(p, s) : launch_tc<128>(p, s);

@@ -8,7 +8,7 @@
 // seq_lens on the device: a few microseconds at the most, nothing launched for it, nothing for the host to know.  (A unit's
 // own cost, `extra` tiles, counts: without it the CTAs whose units are short were done 50 us after the others of a 455 us
 // prompt.)
-// A unit that a border between shares cuts leaves pieces (maximum, sum and unscaled outputs), which a second
+// A unit that a border between shares cuts leaves pieces (maximum, sums and unscaled outputs), which a second
 // kernel joins in the order of the CTAs: no atomics, the same bits on every call.
 #pragma once
 
@@ -243,8 +243,7 @@ struct ChunkRecord {
 // The share that flat tile x - 1 lies in.
 __device__ __forceinline__ int cta_before(const Share& s, int64_t x) { return (int)((x * s.ctas - 1) / s.all); }
 
-template <int D>
-__host__ __device__ constexpr int64_t piece_floats(int BM) { return (int64_t)BM * (D + 2); }
+__host__ __device__ constexpr int64_t piece_floats(int BM, int D) { return (int64_t)BM * (D + 3); }
 
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
@@ -262,7 +261,8 @@ struct alignas(4 * N) Floats {
     float x[N];
 };
 
-// Joins the pieces of a unit.  A piece is [BM][D] sums, then [BM] maxima (base 2) and [BM] sums.  A lane works out the weight
+// Joins the pieces of a unit.  A piece is [BM][D] sums, then [BM] maxima (base 2), [BM] sums of the weights and [BM] sums of them
+// as they were multiplied, which the outputs are divided by.  A lane works out the weight
 // of one piece for each of the warp's rows; then all of them add the pieces up, a few columns each, with the next pieces'
 // loads under way.
 template <typename T, int D>
@@ -275,17 +275,17 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kda_chunk_join_kernel(ChunkPa
     const Seq s = seq_of(p, r.b);
     const int flat0 = r.m * f.BM + row0, rows = s.n * f.group - flat0;    // of the unit from the warp's first on
     if (rows <= 0) return;
-    const int64_t size = piece_floats<D>(f.BM);
+    const int64_t size = piece_floats(f.BM, D);
     const float* pieces = reinterpret_cast<const float*>(p.workspace + max_ctas * sizeof(ChunkRecord));
     const int n = r.last - r.first + 1;
     auto piece = [&](int i) { return pieces + ((int64_t)(r.first + i) * 2 + (i == 0 ? r.slot : 0)) * size; };
     constexpr int PER = D / 32 > 0 ? D / 32 : 1;                          // columns of a lane
     const int col = lane * PER;
-    float top[JOIN_ROWS], sum[JOIN_ROWS];
+    float top[JOIN_ROWS], sum[JOIN_ROWS], by[JOIN_ROWS];
     Floats<PER> o[JOIN_ROWS];
 #pragma unroll
     for (int k = 0; k < JOIN_ROWS; ++k) {
-        top[k] = -INFINITY, sum[k] = 0.f;
+        top[k] = -INFINITY, sum[k] = by[k] = 0.f;
         for (int i = lane; i < n; i += 32) top[k] = fmaxf(top[k], piece(i)[(int64_t)f.BM * D + row0 + k]);
 #pragma unroll
         for (int x = 16; x; x >>= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(all, top[k], x));
@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kda_chunk_join_kernel(ChunkPa
                 const float* x = piece(i0 + lane) + row0 + k;
                 w[k] = ex2_approx(x[(int64_t)f.BM * D] - (top[k] == -INFINITY ? 0.f : top[k]));
                 sum[k] = fmaf(w[k], x[(int64_t)f.BM * (D + 1)], sum[k]);
+                by[k] = fmaf(w[k], x[(int64_t)f.BM * (D + 2)], by[k]);
             }
         }
         const int count = n - i0 < 32 ? n - i0 : 32;
@@ -320,13 +321,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kda_chunk_join_kernel(ChunkPa
 #pragma unroll
     for (int k = 0; k < JOIN_ROWS; ++k) {
 #pragma unroll
-        for (int x = 16; x; x >>= 1) sum[k] += __shfl_xor_sync(all, sum[k], x);
+        for (int x = 16; x; x >>= 1) sum[k] += __shfl_xor_sync(all, sum[k], x), by[k] += __shfl_xor_sync(all, by[k], x);
         if (k >= rows) continue;
         const int t = over(flat0 + k, f.by_group), head = r.h * f.group + flat0 + k - t * f.group;
         const int64_t at = (int64_t)(s.start + t) * p.Hq + head;
         if (col < D) {
 #pragma unroll
-            for (int c = 0; c < PER; ++c) put(static_cast<T*>(p.o) + at * D + col + c, sum[k] == 0.f ? 0.f : o[k].x[c] / sum[k]);
+            for (int c = 0; c < PER; ++c) put(static_cast<T*>(p.o) + at * D + col + c, sum[k] == 0.f ? 0.f : o[k].x[c] / by[k]);
         }
         if (p.lse && lane == 0) p.lse[at] = sum[k] == 0.f ? -INFINITY : (top[k] + log2f(sum[k])) * 0.6931471805599453f;
     }

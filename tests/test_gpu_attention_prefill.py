@@ -178,6 +178,50 @@ def test_scales_of_either_sign_and_zero(dtype, scale):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("others", [1, 500])
+def test_many_keys_of_one_score(dtype, d, others):
+    """A few keys of score 0 (one, or more than three tiles of them, behind whose maximum the reference then stays) and thousands
+    that share another one, whose weight is next to half a step of bf16 from its rounding, so that nearly all of a row's
+    weights have one and the same error.  Values of 1 give outputs of 1, the sums' own roundings left: 4,016 terms of one size, one
+    after the other, at most 2^-24 of what is summed so far each, 4,016 / 2 * 2^-24 = 1.2e-4 together in fp32, which is far less
+    than half a step of bf16 below 1 (2^-9).  With values a and b in the mean and weights A and B of the
+    two scores, o = (A a + B b) / (A + B) moves by AB / (A + B)^2 <= 1/4 times the difference of the two scores' errors (at most
+    2^-8 each in bf16, 2^-24 in fp32) times |a - b|.  Forty sequences of eight heads, on the same pages, so that a CTA goes through
+    whole rows; alone, too, where rows are cut into pieces."""
+    n, B, half = 16, 40, (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    for seed, (exponent, part) in enumerate([(e, x) for e in (-6, -1, 0, 2, 7) for x in (1.0038, 1.0040, 1.5)]):
+        t = make([(n, 4000)], 16, 8, d, 64, dtype, seed)
+        pages = t["block_table"][0].long()
+        size = math.log(2.0 ** exponent * part)
+        high = float(torch.tensor(size).to(DT[dtype]))
+        t["k_pages"][pages] = 0
+        for at, x in ((0, high), (1, size - high)):    # a score to 16 bits, also in bf16
+            score = torch.full((pages.numel() * 64,), x, device=DEV)
+            score[:others] = 0
+            t["k_pages"][pages, :, :, at] = score.view(-1, 1, 64).to(DT[dtype])
+        t["q"].zero_()
+        t["q"][..., :2] = 1
+        ref, ref_lse = reference(t, [(n, 4000)], 64, 1.0)
+        v = t["v_pages"][pages].double().transpose(0, 1).reshape(8, -1, d)
+        apart = (v[:, :others].mean(1) - v[:, others:4000].mean(1)).abs().repeat_interleave(2, 0)
+        # (the last 16 tokens, which not every row sees, move the mean by less than 0.1)
+        bound = half * ref.abs() + half / 2 * (apart + 0.1) + 1.2e-4 * v.nan_to_num(0, 0, 0).abs().max()
+        many = dict(t, q=t["q"].repeat(B, 1, 1), block_table=t["block_table"].repeat(B, 1), seq_lens=t["seq_lens"].repeat(B),
+                    cu_seqlens=torch.arange(0, n * B + 1, n, **i32))
+        for call in (t, many):
+            lse = torch.empty(call["q"].shape[:2], device=DEV)
+            o = kda.kda_attention_prefill(**call, lse=lse).double().view(-1, n, 16, d)
+            assert bool(((o - ref).abs() <= bound).all()), (exponent, part, float(((o - ref).abs() / bound).max()))
+            assert float((lse.double().view(-1, n, 16) - ref_lse).abs().max()) <= 1e-4
+        t["v_pages"][pages] = 1
+        for call in (t, many):
+            o = kda.kda_attention_prefill(**call)
+            assert float((o - 1).abs().max()) <= (0 if dtype == "bf16" else 1.2e-4), (exponent, part, float((o - 1).abs().max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rising_and_falling_scores(dtype):
     """Keys that grow along the sequence (the maximum moves in every tile) and that shrink."""
     for sign in (1, -1):
