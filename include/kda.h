@@ -626,7 +626,9 @@ KDA_API kda_status kda_token_logprobs(const void* logits, int64_t row_stride, co
 
 /*
  * Their gradient: grad_tv = grad_logp_t (1[v = y_t] - p_tv) - grad_entropy_t p_tv (log p_tv + entropy_t), with p from
- * the lse that kda_token_logprobs gave.  A token outside [0, V) has no grad_logp; a row whose lse is -inf no gradient.
+ * the lse that kda_token_logprobs gave, or from the row itself where float32 leaves such an lse too few bits (beyond 1,024
+ * from zero: rows masked by a type's lowest value, too).  A token outside [0, V) has no grad_logp; a row whose lse is -inf
+ * no gradient.
  *   grad  [T, V] dtype dt, row t at grad + t * grad_stride; may be logits, with the same stride
  *   entropy and grad_entropy [T] float32, or both NULL
  */

@@ -244,6 +244,45 @@ def test_gradient_against_differences():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1, 7, 1000, 40001])
+def test_gradient_of_rows_far_from_zero(dtype, V):
+    """Logits so large that lse in fp32 is off by a part of a word's probability, or by all of it: rows masked by the type's lowest
+    value and nothing else, or by a large number, and rows far from zero.  Differences of the logits are exact (or, between two
+    of a size, the logits' own), so p is as near as that of any row: its sum's and exponentials' roundings, 4e-6 of it."""
+    low = torch.finfo(DT[dtype]).min
+    j = torch.arange(V, device=DEV).float()
+    rows = [torch.full((V,), low, device=DEV), torch.where(j % 3 == 0, low, -math.inf), torch.full((V,), -1e9, device=DEV),
+            torch.where(j % 5 == 0, 1e6 + 8 * torch.sin(j), -1e9), -3e4 + 4 * torch.cos(j), 1500 + 3 * torch.sin(3 * j), -1025 - j % 7,
+            1023 + 0 * j, torch.sin(j)]
+    logits = torch.stack(rows).to(DT[dtype])
+    T = logits.shape[0]
+    tokens = ((torch.arange(T, device=DEV) * 3) % V).int()
+    tokens[2] = -1
+    g = torch.Generator(device=DEV).manual_seed(V)
+    gl, gh = (torch.randn(T, device=DEV, generator=g) for _ in range(2))
+    r = kda.kda_token_logprobs(logits, tokens, entropy=True)
+    p = torch.softmax(logits.double(), 1)
+    lse = torch.logsumexp(logits.double(), 1).abs()
+    scored = (tokens >= 0)[:, None]
+    given = torch.zeros_like(p).scatter_(1, tokens.long().clamp(min=0)[:, None], 1.0) * scored
+    entr = torch.special.entr(p)
+    for entropy in (False, True):
+        want = gl.double()[:, None] * (given - p * scored)
+        size = p * gl.abs()[:, None] + (gl.abs()[:, None] * 1e-3 if dtype == "f32" else 0)
+        if entropy:
+            want = want + gh.double()[:, None] * (entr - p * entr.sum(1, keepdim=True))
+            size = size + p * gh.abs()[:, None] * (30 + 1)
+        # within 1,024 of zero p has lse's rounding, too
+        rounding = torch.where(lse <= 1024.01, lse * 2.0 ** -24, 0.0)[:, None]
+        bound = (4e-6 + rounding) * size + torch.finfo(DT[dtype]).eps / 2 * want.abs() + 1e-30
+        extra = dict(entropy=r.entropy, grad_entropy=gh) if entropy else {}
+        for place in (None, logits.clone()):           # the last one in the logits' place
+            got = kda.kda_token_logprobs_backward(logits if place is None else place, tokens, r.lse, gl, grad=place, **extra)
+            off = ((got.double() - want).abs() / bound).amax(1)
+            assert bool((off <= 1).all()), off.tolist()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_same_bits_streams_and_graphs(dtype):
     logits, tokens = make(6, 50257, dtype)
     a = kda.kda_token_logprobs(logits, tokens, top=9, entropy=True)
