@@ -593,7 +593,8 @@ KDA_API kda_status kda_cache_append(const void* q, const void* k, const void* v,
  * product, whose outputs are divided by the sum of the rounded ones.  Limits as for kda_attention_decode, and T * H_q
  * below 2^31.
  * A length outside [0, max_pages * page_size] counts as 0, new tokens before position 0 see nothing, and a page outside
- * [0, num_pages) reads as zeros; all set KDA_DEVERR_PAGES.
+ * [0, num_pages) reads as zeros; all set KDA_DEVERR_PAGES.  A page that no token sees (behind every window) may be
+ * any number.
  */
 KDA_API size_t kda_attention_prefill_workspace_size(int32_t B, int32_t T, int32_t H_q, int32_t H_kv, int32_t d,
                                                     kda_dtype dt);

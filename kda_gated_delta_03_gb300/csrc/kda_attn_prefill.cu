@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(NT, 2) kda_chunk_kernel(ChunkParams p, ChunkPl
                     const int slot = over(j, f.by_page), page = __ldg(table + slot);
                     if (page >= 0 && page < p.num_pages)
                         from = static_cast<const T*>(pages) + page * stride + ((int64_t)w.h * p.page_size + (j - slot * p.page_size)) * D + c;
-                    else if (c == 0)
+                    else if (c == 0 && (j >= seen_from(p, u.pos0) || j < p.sinks))       // (in a tile, but seen by nobody: nothing wrong)
                         atomicOr(p.err, KDA_DEVERR_PAGES);
                 }
                 if constexpr (sizeof(T) == 4) {

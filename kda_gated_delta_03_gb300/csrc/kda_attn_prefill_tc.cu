@@ -177,6 +177,12 @@ __device__ __forceinline__ void store64(void* to, const uint32_t (&x)[16], bool 
     }
 }
 
+// Reports a lane's boxes of tokens from j, j + 32 box, .. on that have no page, if some row sees a token of one.
+__device__ __noinline__ void tell_bad_pages(const ChunkParams& p, bool a, bool b, bool c, bool d, int j, int box, int from) {
+    auto seen = [&](int x) { return x + box > from || x < p.sinks; };
+    if ((a && seen(j)) || (b && seen(j + 32 * box)) || (c && seen(j + 64 * box)) || (d && seen(j + 96 * box))) atomicOr(p.err, KDA_DEVERR_PAGES);
+}
+
 // Adds the tokens that were taken out of a run's tiles to a row that sees them; a whole warp.
 template <int D>
 __device__ __noinline__ void add_odd(const ChunkParams& p, const ChunkPlan& f, const OddTiles& list, int b, int h, int pos,
@@ -472,7 +478,10 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                 }
                 if (it + 1 < end) look_up(it + 1);
                 const bool zeros = __any_sync(0xFFFFFFFFu, bad);
-                if (zeros && lane == 0) atomicOr(p.err, KDA_DEVERR_PAGES);
+                if (zeros) {
+                    const int j = tile_start(f, w.u, it) + lane * box;
+                    tell_bad_pages(p, page[0] == -1, page[1] == -1, page[2] == -1, page[3] == -1, j, box, seen_from(p, w.u.pos0));
+                }
                 for (int v = 0; v < 2; ++v, ++n) {
                     ok = wait(&bar.empty[st], turn);
                     if (!ok) break;

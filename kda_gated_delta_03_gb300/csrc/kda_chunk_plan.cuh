@@ -57,6 +57,10 @@ struct Unit {
     int32_t end;                 // tokens that any row sees end here
     int32_t near, skip, tiles;   // at least one tile, also where no row sees anything
 };
+// The first token that any row of a unit sees, but for the first ones of all (p.sinks).
+__device__ __forceinline__ int seen_from(const ChunkParams& p, int pos0) {
+    return p.window > 0 && pos0 >= p.window ? pos0 + 1 - p.window : 0;
+}
 __device__ __forceinline__ Unit unit_of(const ChunkParams& p, const ChunkPlan& f, const Seq& s, int m) {
     Unit u;
     const int row0 = m * f.BM, all = s.n * f.group;
@@ -68,8 +72,7 @@ __device__ __forceinline__ Unit unit_of(const ChunkParams& p, const ChunkPlan& f
     const int all_tiles = over(u.end + f.BN - 1, f.by_tile);
     u.near = 0, u.skip = 0;
     if (p.window > 0) {
-        const int first = u.pos0 >= p.window ? u.pos0 + 1 - p.window : 0;      // of the window of the first row
-        const int w0 = over(first, f.by_tile);
+        const int w0 = over(seen_from(p, u.pos0), f.by_tile);
         const int sinks = p.sinks < u.end ? p.sinks : u.end;
         u.near = sinks > 0 ? over(sinks - 1, f.by_tile) + 1 : 0;
         if (u.near > w0) u.near = w0;

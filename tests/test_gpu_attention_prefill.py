@@ -329,6 +329,34 @@ def test_bad_tables_and_lengths_are_reported_not_faulted(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,ps", [(64, 16), (128, 7), (64, 64), (16, 16), (128, 200)])
+@pytest.mark.parametrize("window,sinks", [(40, 0), (100, 3), (129, 20), (1, 0)])
+def test_pages_behind_every_window_may_be_any_number(dtype, d, ps, window, sinks):
+    """A server that has given such pages back leaves -1 or a stale number in the table: nothing is reported, and the results are
+    those of the full table.  One page that some token sees is reported."""
+    rows = [(1, 700), (30, 555), (300, 900), (0, 400), (64, 0)]
+    t = make(rows, 4, 2, d, ps, dtype, window + ps)
+    want_lse, lse = (torch.empty(t["q"].shape[:2], device=DEV) for _ in range(2))
+    want = kda.kda_attention_prefill(**t, scale=0.1, window=window, sinks=sinks, lse=want_lse)
+    assert kda.kda_get_device_error() == 0
+    for number in (-1, t["k_pages"].shape[0], -2 ** 31, 2 ** 31 - 1):
+        table = t["block_table"].clone()
+        for b, (n, past) in enumerate(rows):
+            first = max(0, past + 1 - window) if n else n + past               # of the first new token's window
+            for i in range(-(-(n + past) // ps)):
+                if i * ps >= sinks and (i + 1) * ps <= first:
+                    table[b, i] = number
+        assert int((table[2] == number).sum()) >= (901 - window - sinks) // ps - 2
+        o = kda.kda_attention_prefill(**dict(t, block_table=table), scale=0.1, window=window, sinks=sinks, lse=lse)
+        assert kda.kda_get_device_error() == 0
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+        seen = max(0, 900 + 1 - window) // ps                                  # holds the first token of the third row's window
+        table[2, seen] = number
+        kda.kda_attention_prefill(**dict(t, block_table=table), scale=0.1, window=window, sinks=sinks)
+        assert kda.kda_get_device_error() == 0x20
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_bad_borders_are_reported_not_faulted(dtype):
     rows = [(50, 150), (64, 0), (20, 70)]
     t = make(rows, 8, 2, 64, 16, dtype, 8)
