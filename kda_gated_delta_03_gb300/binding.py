@@ -421,6 +421,12 @@ def _in_stream(stream, call, *args, **kwargs):
         return call(*args, **kwargs)
 
 
+def _too_large(name, *values):
+    """Raises for numbers that do not fit the C ABI's 32 bits, of which ctypes would pass the lower ones.  (Callers look at all
+    of them at once: or'ed together they are within 31 bits if each is, and the library refuses negative ones.)"""
+    raise ValueError(f"{name}: one of the sizes and numbers {values} does not fit 32 bits")
+
+
 def _workspace(workspace, dev):
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on CUDA device {dev}")
@@ -502,6 +508,8 @@ def kda_attention_decode(q, k_pages, v_pages, block_table, seq_lens, *, scale: f
     ks = _page_stride("k_pages", k_pages, shape, dt, dev)
     vs = _page_stride("v_pages", v_pages, shape, dt, dev)
     M = block_table.shape[1]
+    if (B | Hq | Hkv | P | M | ps | window | sinks) >> 31 not in (0, -1):
+        _too_large("kda_attention_decode", B, Hq, Hkv, P, M, ps, window, sinks)
     _check_at("block_table", block_table, _I32, (B, M), dev)
     _check_at("seq_lens", seq_lens, _I32, (B,), dev)
     kn = vn = out_lse = None
@@ -835,6 +843,8 @@ def kda_rotary(q, k, positions, inv_freq, *, layout: str = "half", rotary_scale:
             kos = _out_stride("k_out", k_out, k.shape, dt, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
+    if (T | Hq | Hkv | d) >> 31:
+        _too_large("kda_rotary", T, Hq, Hkv, d)
     rc = (_LIB or load()).kda_rotary(q.data_ptr(), None if k is None else k.data_ptr(), positions.data_ptr(), freq, T, Hq,
                                      Hkv, d, rot, qs, ks, code, _layout(layout), rotary_scale, int(inverse),
                                      q_out.data_ptr(), qos, None if k is None else k_out.data_ptr(), kos,
@@ -888,6 +898,8 @@ def kda_cache_append(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, 
             qos = _out_stride("q_out", q_out, q.shape, dt, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
+    if (T | B | Hq | Hkv | P | M | ps) >> 31:
+        _too_large("kda_cache_append", T, B, Hq, Hkv, P, M, ps)
     rc = (_LIB or load()).kda_cache_append(
         None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
         block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), freq, B, T, Hq, Hkv, d, rot, qs, ks, vs, P, ps,
@@ -935,6 +947,8 @@ def kda_attention_prefill(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens
     ks = _page_stride("k_pages", k_pages, shape, dt, dev)
     vs = _page_stride("v_pages", v_pages, shape, dt, dev)
     B, M = block_table.shape
+    if (T | B | Hq | Hkv | P | M | ps | window | sinks) >> 31 not in (0, -1):
+        _too_large("kda_attention_prefill", T, B, Hq, Hkv, P, M, ps, window, sinks)
     _check_at("block_table", block_table, _I32, (B, M), dev)
     _check_at("seq_lens", seq_lens, _I32, (B,), dev)
     _check_at("cu_seqlens", cu_seqlens, _I32, (B + 1,), dev)
@@ -994,6 +1008,8 @@ def kda_token_logprobs(logits, tokens, *, top: int = 0, entropy: bool = False, s
     code = _DTYPES.get(logits.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {logits.dtype}")
+    if (T | V | top) >> 31 not in (0, -1):
+        _too_large("kda_token_logprobs", T, V, top)
     _check_at("tokens", tokens, _I32, (T,), dev)
     k, on = max(top, 0), logits.device
     logp, lse = torch.empty((T,), dtype=_F32, device=on), torch.empty((T,), dtype=_F32, device=on)
@@ -1023,6 +1039,8 @@ def kda_token_logprobs_backward(logits, tokens, lse, grad_logp, *, entropy=None,
     code = _DTYPES.get(logits.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {logits.dtype}")
+    if (T | V) >> 31:
+        _too_large("kda_token_logprobs_backward", T, V)
     _check_at("tokens", tokens, _I32, (T,), dev)
     _check_at("lse", lse, _F32, (T,), dev)
     _check_at("grad_logp", grad_logp, _F32, (T,), dev)

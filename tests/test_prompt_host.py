@@ -145,3 +145,69 @@ def test_binding_wants_cuda_tensors():
                  lambda: kda.kda_token_logprobs_backward(torch.zeros(2, 8), i, f.float(), f.float())):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.fixture
+def passed(monkeypatch):
+    """The binding on tensors without data (device -1), before a library that takes any call: its calls' names."""
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: calls.append(name) or 0
+
+    monkeypatch.setattr(binding, "_LIB", Library())
+    monkeypatch.setattr(binding, "_cuda_index", lambda name, t: t.get_device())
+    monkeypatch.setattr(binding, "_elsewhere", lambda dev, stream: False)
+    monkeypatch.setattr(binding, "_current_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(binding, "_new_workspace", lambda need, dev: torch.empty(1, dtype=torch.uint8))
+    return calls
+
+
+def meta(*shape, dtype=torch.bfloat16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63, -2 ** 31 - 1, -2 ** 32])
+def test_numbers_beyond_32_bits_are_refused(passed, value):
+    """ctypes passes the lower 32 bits of a number: a window of 2^32 would be none, 2^32 first tokens none at all."""
+    i32 = dict(dtype=torch.int32)
+    pages = (meta(3, 1, 4, 64), meta(3, 1, 4, 64), meta(1, 2, **i32))
+    for over in (dict(window=value), dict(sinks=value), dict(window=5, sinks=value)):
+        with pytest.raises(ValueError):
+            kda.kda_attention_prefill(meta(2, 1, 64), *pages, meta(1, **i32), meta(2, **i32), **over)
+        with pytest.raises(ValueError):
+            kda.kda_attention_decode(meta(1, 1, 64), *pages, meta(1, **i32), **over)
+    with pytest.raises(ValueError):
+        kda.kda_token_logprobs(meta(2, 9), meta(2, **i32), top=value)
+    assert not [c for c in passed if not c.endswith("_size")]
+    kda.kda_attention_prefill(meta(2, 1, 64), *pages, meta(1, **i32), meta(2, **i32), window=2 ** 31 - 1, sinks=2 ** 31 - 1)
+    assert passed[-1] == "kda_attention_prefill"
+
+
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32, 2 ** 32 + 3])
+def test_sizes_beyond_32_bits_are_refused(passed, n):
+    i32, f32 = dict(dtype=torch.int32), dict(dtype=torch.float32)
+    pages, table, one = (meta(3, 1, 4, 16), meta(3, 1, 4, 16)), meta(1, 2, **i32), meta(1, **i32)
+    many = (meta(n, 1, 4, 16), meta(n, 1, 4, 16))
+    q, two = meta(2, 1, 16), meta(2, **i32)
+    for call in (lambda: kda.kda_rotary(meta(n, 1, 16), None, meta(n, **i32), None),
+                 lambda: kda.kda_rotary(q, meta(2, n, 16), two, None),
+                 lambda: kda.kda_cache_append(q, q, *pages, table, one, two, q=meta(2, n, 16)),
+                 lambda: kda.kda_attention_prefill(meta(2, n, 16), *pages, table, one, two),
+                 lambda: kda.kda_cache_append(meta(n, 1, 16), meta(n, 1, 16), *pages, table, one, two),
+                 lambda: kda.kda_cache_append(q, q, *many, table, one, two),
+                 lambda: kda.kda_cache_append(q, q, *pages, meta(n, 2, **i32), meta(n, **i32), meta(n + 1, **i32)),
+                 lambda: kda.kda_cache_append(q, q, *pages, meta(1, n, **i32), one, two),
+                 lambda: kda.kda_attention_prefill(meta(n, 1, 16), *pages, table, one, two),
+                 lambda: kda.kda_attention_prefill(q, *many, table, one, two),
+                 lambda: kda.kda_attention_prefill(q, *pages, meta(1, n, **i32), one, two),
+                 lambda: kda.kda_token_logprobs(meta(n, 3), meta(n, **i32)),
+                 lambda: kda.kda_token_logprobs(meta(1, n), one),
+                 lambda: kda.kda_token_logprobs_backward(meta(n, 3), meta(n, **i32), meta(n, **f32), meta(n, **f32)),
+                 lambda: kda.kda_token_logprobs_backward(meta(1, n), one, meta(1, **f32), meta(1, **f32))):
+        with pytest.raises(ValueError):
+            call()
+    assert not passed
+    kda.kda_token_logprobs_backward(meta(4, 9), meta(4, **i32), meta(4, **f32), meta(4, **f32))
+    assert passed == ["kda_token_logprobs_backward"]
