@@ -754,6 +754,8 @@ def _elsewhere(dev, stream):
 
 def _there(dev, stream, call, *args, **kwargs):
     """The call on its tensors' device and with `stream` as the current one (see _in_stream)."""
+    if stream is not None and stream.device_index != dev:                     # (it would run on some other stream)
+        raise ValueError(f"stream is on CUDA device {stream.device_index}, the tensors on {dev}")
     with torch.cuda.device(dev):
         if stream is None:
             return call(*args, **kwargs)

@@ -2,6 +2,7 @@
 every bad argument is refused before any CUDA call, so these run without a GPU.  The addresses below are never
 dereferenced."""
 
+import contextlib
 import os
 import shutil
 
@@ -211,3 +212,31 @@ def test_sizes_beyond_32_bits_are_refused(passed, n):
     assert not passed
     kda.kda_token_logprobs_backward(meta(4, 9), meta(4, **i32), meta(4, **f32), meta(4, **f32))
     assert passed == ["kda_token_logprobs_backward"]
+
+
+def test_streams_of_another_device_are_refused(monkeypatch):
+    """Such a call would find itself on the tensors' device and that device's own current stream, unordered with the given one."""
+    ran = []
+    monkeypatch.setattr(binding, "_cuda_index", lambda name, t: 0)
+    monkeypatch.setattr(binding, "_in_stream", lambda stream, call, *args, **kwargs: ran.append(call))
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+
+    class Stream:
+        cuda_stream = 0
+
+        def __init__(self, device_index):
+            self.device_index = device_index
+
+    i, x = meta(2, dtype=torch.int32), meta(2, 1, 64)
+    pool, table, f = meta(3, 1, 4, 64), meta(1, 2, dtype=torch.int32), meta(2, dtype=torch.float32)
+    calls = [lambda s: kda.kda_rotary(x, x, i, None, stream=s), lambda s: kda.kda_cache_append(x, x, pool, pool, table, i[:1], i, stream=s),
+             lambda s: kda.kda_attention_prefill(x, pool, pool, table, i[:1], i, stream=s),
+             lambda s: kda.kda_token_logprobs(meta(2, 8), i, stream=s),
+             lambda s: kda.kda_token_logprobs_backward(meta(2, 8), i, f, f, stream=s)]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call(Stream(1))
+    assert not ran
+    for call in calls:
+        call(Stream(0))
+    assert len(ran) == len(calls)
