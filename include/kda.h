@@ -632,6 +632,8 @@ KDA_API kda_status kda_token_logprobs(const void* logits, int64_t row_stride, co
  * no gradient.
  *   grad  [T, V] dtype dt, row t at grad + t * grad_stride; may be logits, with the same stride
  *   entropy and grad_entropy [T] float32, or both NULL
+ * Limits as for kda_token_logprobs, and all rows' chunks of 4,096 bf16 or 2,048 float32 words (the first one up to 7 or 3
+ * words shorter) below 2^31 (KDA_ERR_TOO_LARGE above).
  */
 KDA_API kda_status kda_token_logprobs_backward(const void* logits, int64_t row_stride, const int32_t* tokens,
                                                const float* lse, const float* entropy, const float* grad_logp,

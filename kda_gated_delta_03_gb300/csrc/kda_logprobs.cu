@@ -607,8 +607,13 @@ __global__ void __launch_bounds__(NT, 16) kda_logprobs_backward_kernel(LogprobGr
 }
 
 template <typename T>
+int64_t backward_chunks(int32_t V) {
+    return ((int64_t)V + Elems<T>::W - 2 + BACK * NT * Elems<T>::W) / (BACK * NT * Elems<T>::W);
+}
+
+template <typename T>
 cudaError_t launch_backward(const LogprobGradParams& p, cudaStream_t s) {
-    const int64_t chunks = ((int64_t)p.V + Elems<T>::W - 2 + BACK * NT * Elems<T>::W) / (BACK * NT * Elems<T>::W);
+    const int64_t chunks = backward_chunks<T>(p.V);
     kda_logprobs_backward_kernel<T><<<(unsigned)(p.T * chunks), NT, 0, s>>>(p, (int)chunks);
     return cudaGetLastError();
 }
@@ -617,6 +622,10 @@ cudaError_t launch_backward(const LogprobGradParams& p, cudaStream_t s) {
 
 cudaError_t launch_token_logprobs(const LogprobParams& p, kda_dtype dt, cudaStream_t s) {
     return dt == KDA_DTYPE_BF16 ? launch_any<__nv_bfloat16>(p, s) : launch_any<float>(p, s);
+}
+
+int64_t logprobs_backward_chunks(int32_t V, kda_dtype dt) {
+    return dt == KDA_DTYPE_BF16 ? backward_chunks<__nv_bfloat16>(V) : backward_chunks<float>(V);
 }
 
 cudaError_t launch_token_logprobs_backward(const LogprobGradParams& p, kda_dtype dt, cudaStream_t s) {

@@ -128,6 +128,7 @@ struct LogprobGradParams {
     int64_t row_stride, grad_stride;
     int32_t T, V;
 };
+int64_t logprobs_backward_chunks(int32_t V, kda_dtype dt);    // of a row, wherever it begins; all rows' are numbered in 31 bits
 cudaError_t launch_token_logprobs_backward(const LogprobGradParams& p, kda_dtype dt, cudaStream_t s);
 
 }  // namespace kda

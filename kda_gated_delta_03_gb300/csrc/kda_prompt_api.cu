@@ -160,8 +160,7 @@ kda_status kda_token_logprobs_backward(const void* logits, int64_t row_stride, c
                                        int32_t V, kda_dtype dt, void* grad, int64_t grad_stride, void* stream) {
     if (T < 0 || V <= 0 || !known(dt) || row_stride < V || grad_stride < V || (entropy == nullptr) != (grad_entropy == nullptr))
         return KDA_ERR_INVALID_ARG;
-    // a row's chunks, of 2^9 words at least, are numbered in 31 bits together with the rows
-    if (V > MOST_WORDS || T > MOST_ROWS || (int64_t)T * ((int64_t)V / (1 << 9) + 2) > INT32_MAX) return KDA_ERR_TOO_LARGE;
+    if (V > MOST_WORDS || T > MOST_ROWS || T * kda::logprobs_backward_chunks(V, dt) > INT32_MAX) return KDA_ERR_TOO_LARGE;
     if (T == 0) return KDA_OK;
     if (!logits || !aligned(logits, esize(dt)) || !table_ok(tokens) || !table_ok(lse) || !table_ok(grad_logp) ||
         (entropy && (!aligned(entropy, 4) || !aligned(grad_entropy, 4))) || !grad || !aligned(grad, esize(dt)) ||

@@ -136,6 +136,15 @@ def test_backward_refuses_more_chunks_than_a_grid_has(lib):
     assert backward(lib, T=1 << 20, V=1 << 22, stride=1 << 22, gstride=1 << 22, dt=0) == TOO_LARGE
 
 
+def test_backward_takes_as_many_chunks_as_a_grid_has(lib):
+    """Chunks of 4,096 bf16 and 2,048 fp32 words, wherever a row begins.  A call that is not too large is refused for its logits."""
+    for dt, words, short in ((1, 4096, 7), (0, 2048, 3)):
+        for V, chunks in ((9 * words - short, 9), (9 * words - short + 1, 10), (512 * words, 513), (1023 * words, 1024)):
+            rows = (2 ** 31 - 1) // chunks
+            assert backward(lib, T=rows, V=V, stride=V, gstride=V, dt=dt, x=None) == INV
+            assert backward(lib, T=rows + 1, V=V, stride=V, gstride=V, dt=dt, x=None) == TOO_LARGE
+
+
 def test_binding_wants_cuda_tensors():
     i, x = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 1, 64)
     pool, table = torch.zeros(3, 1, 4, 64), torch.zeros((1, 2), dtype=torch.int32)
