@@ -569,8 +569,9 @@ KDA_API kda_status kda_rotary(const void* q, const void* k, const int32_t* posit
  *   k_pages, v_pages, block_table [B, max_pages], seq_lens [B]  as for kda_attention_decode
  *   cu_seqlens [B + 1] int32;  inv_freq, layout, rotary_scale  as for kda_rotary
  * No two new tokens may have the same place, and k, v may not overlap the pools.  A token without a place (a length
- * outside [0, max_pages * page_size] or less than n_b, a page outside [0, num_pages)) is not stored and sets
- * KDA_DEVERR_PAGES.  Limits as for kda_rotary and kda_attention_decode.
+ * outside [0, max_pages * page_size], a position below 0 where the length is less than n_b, a page outside [0, num_pages))
+ * is not stored and sets KDA_DEVERR_PAGES; the row's other tokens are stored, and its queries rotated all the same.
+ * Limits as for kda_rotary and kda_attention_decode.
  */
 KDA_API kda_status kda_cache_append(const void* q, const void* k, const void* v, void* k_pages, void* v_pages,
                                     const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_seqlens,

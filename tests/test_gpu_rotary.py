@@ -260,6 +260,33 @@ def test_append_bad_tables_lengths_and_borders_are_reported(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_of_more_tokens_than_the_length_holds(dtype):
+    """Tokens with a position below 0 are not stored; the others of their row are, and attention lets them see each other."""
+    rows, ps = [(5, 30), (20, 0), (3, 3)], 16
+    a, old = batch(rows, 2, 64, ps, dtype), batch(rows, 2, 64, ps, dtype)
+    a["seq_lens"][1] = 13                              # the first seven of 20 lie before position 0
+    q, f = randn(28, 4, 64, dtype=dtype), frequencies(64)
+    out = kda.kda_cache_append(**a, q=q, inv_freq=f)
+    assert kda.kda_get_device_error() == 0x20
+    t, pos, page, slot = places([(5, 30), (13, 0), (3, 3)], ps, old["block_table"])
+    t = torch.where(t >= 5, t + 7, t)                  # tokens 12 .. 24 at positions 0 .. 12
+    near(a["k_pages"][page, :, slot], turned(a["k"][t], pos, f, "half"), a["k"][t], 64, "half")
+    assert torch.equal(a["v_pages"][page, :, slot], a["v"][t])
+    for name in ("k_pages", "v_pages"):
+        left = old[name].clone()
+        left[page, :, slot] = a[name][page, :, slot]
+        assert torch.equal(bits(left), bits(a[name]))
+    near(out[t], turned(q[t], pos, f, "half"), q[t], 64, "half")
+    o = kda.kda_attention_prefill(out, a["k_pages"], a["v_pages"], a["block_table"], a["seq_lens"], a["cu_seqlens"], scale=0.1)
+    assert kda.kda_get_device_error() == 0x20 and not o[5:12].any()
+    cu = torch.tensor([0, 13], dtype=torch.int32, device=DEV)
+    alone = kda.kda_attention_prefill(out[12:25].contiguous(), a["k_pages"], a["v_pages"], a["block_table"][1:2], a["seq_lens"][1:2], cu, scale=0.1)
+    assert kda.kda_get_device_error() == 0
+    # the same sums in an order that may differ: outputs twice rounded, below 3 in size
+    assert float((o[12:25].double() - alone.double()).abs().max()) <= 2 * 3 * torch.finfo(DT[dtype]).eps
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_append_leaves_sequences_with_bad_borders_alone(dtype):
     """They count as empty: nothing of theirs is stored, and their queries' outputs stay as they were."""
     rows, ps = [(5, 30), (20, 0), (3, 3)], 16
