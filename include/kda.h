@@ -534,8 +534,8 @@ KDA_API kda_status kda_cache_compact(const int32_t* block_table, int32_t rows, i
  * them, seq_lens[b] with the new ones, as kda_cache_fork returns it for grow = n_b).  A chunk may be a whole
  * prompt, a part of one behind what the cache holds already, or one token.  cu_seqlens[0] = 0; cu_seqlens[B] may be
  * less than T, and outputs of the tokens behind it are left as they were.  A sequence whose borders are not
- * 0 <= cu_seqlens[b] <= cu_seqlens[b + 1] <= T counts as empty and sets KDA_DEVERR_CU_SEQLENS (where borders fall, a
- * token may lie between those of two others: which of them has it is not defined).
+ * 0 <= cu_seqlens[b] <= cu_seqlens[b + 1] <= T counts as empty and sets KDA_DEVERR_CU_SEQLENS (where borders fall, or the
+ * first is not 0, a token that lies between those of two sequences goes to either, and tokens of others may be left out).
  * ------------------------------------------------------------------------------------------------ */
 
 #define KDA_ROTARY_HALF 0         /* pairs (x_i, x_{i + rotary_dim / 2}) */

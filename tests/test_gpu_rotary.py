@@ -259,6 +259,46 @@ def test_append_bad_tables_lengths_and_borders_are_reported(dtype):
         assert torch.equal(a["k_pages"][others], want["k_pages"][others])
 
 
+@pytest.mark.parametrize("B", [3, 40, 300])
+def test_append_with_borders_in_any_order(B):
+    """Every token is stored in the place that some sequence in order gives it, or not at all; where the first border is 0 a token
+    that lies in one sequence alone is stored there; no other place changes."""
+    gen = torch.Generator().manual_seed(B)
+    T, ps, d = 2 * B + 7, 4, 16
+    for kind in range(4):
+        cu = torch.randint(0, T + 1, (B + 1,), generator=gen)
+        if kind < 2:
+            cu = cu.sort().values
+            cu[torch.randint(0, B + 1, (2,), generator=gen)] = torch.tensor([T + 50, -3][kind])
+        elif kind == 3:
+            cu[torch.rand(B + 1, generator=gen) < 0.3] = 2 ** 31 - 1
+        if kind != 2:
+            cu[0] = 0
+        cu = cu.int()
+        lens, M = torch.full((B,), T), -(-T // ps)
+        table = torch.arange(B * M, dtype=torch.int32).view(B, M)
+        a = dict(k=randn(T, 1, d, dtype="f32", seed=kind), v=randn(T, 1, d, dtype="f32", seed=kind + 9), block_table=table.to(DEV),
+                 seq_lens=lens.int().to(DEV), cu_seqlens=cu.to(DEV))
+        pools = [torch.zeros((B * M, 1, ps, d), device=DEV) for _ in range(2)]
+        kda.kda_cache_append(a["k"], a["v"], *pools, a["block_table"], a["seq_lens"], a["cu_seqlens"])
+        falls = bool((cu[1:] < cu[:-1]).any() or (cu > T).any() or cu[0] != 0)
+        assert kda.kda_get_device_error() == (0x1 if falls else 0)
+        flat = pools[0].view(B, M * ps, d).cpu()
+        k, c, stored = a["k"][:, 0].cpu(), cu.tolist(), [0] * T
+        inside = [[b for b in range(B) if c[b] <= t < c[b + 1]] for t in range(T)]     # of any sequence, in order or not
+        for b in range(B):
+            for p in flat[b].any(1).nonzero()[:, 0].tolist():
+                t = c[b + 1] - (T - p)                 # the token that b's borders put at position p
+                assert 0 <= c[b] <= t < c[b + 1] <= T and (b > 0 or c[0] == 0) and torch.equal(flat[b, p], k[t])
+                stored[t] += 1
+        for t in range(T):
+            assert stored[t] <= 1
+            if len(inside[t]) == 1 and c[0] == 0:
+                b = inside[t][0]
+                assert stored[t] == (c[b] >= 0 and c[b + 1] <= T)
+        assert torch.equal(pools[1].any(3), pools[0].any(3))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_append_of_more_tokens_than_the_length_holds(dtype):
     """Tokens with a position below 0 are not stored; the others of their row are, and attention lets them see each other."""
