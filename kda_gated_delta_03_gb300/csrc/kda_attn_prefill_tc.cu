@@ -36,10 +36,10 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int EXTRA = 1;                      // tiles' time that a unit's queries and outputs take
 constexpr float SLACK = 8.f;                  // the reference moves when the maximum has grown by 2^SLACK
 
-// Tokens of a tile whose value is not finite, taken out of it.  A unit of 256 rows has at most 14 tiles that
-// some row sees in part: tiles hold 65 tokens or more, the rows' own tokens touch 5 of them, the lower borders of their
-// windows 5, the border of the first tokens 1.
-constexpr int MAX_ODD = 14;
+// Tokens of a tile whose value is not finite, taken out of it.  A unit of 256 rows has at most nine tiles that some row sees
+// in part: tiles hold 96 tokens or more (box_of), the rows' own tokens touch 4 of them, the lower borders of their windows 4,
+// the border of the first tokens 1.
+constexpr int MAX_ODD = 9;
 struct OddTiles {
     int32_t n;
     int32_t start[MAX_ODD];
@@ -744,17 +744,12 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
     }
 }
 
-// Tokens of a TMA box: the largest run that divides a page, fits a tile and fills three quarters of it, or else the
-// one that fills it best.
+// Tokens of a TMA box: the largest run that divides a page and of which whole ones fill three quarters of a tile (one token
+// always does).
 int box_of(int page_size) {
-    int best = 1, fill = 0;
-    for (int x = page_size < TILE ? page_size : TILE; x >= 1; --x) {
-        if (page_size % x) continue;
-        const int n = TILE / x * x;
-        if (4 * n >= 3 * TILE) return x;
-        if (n > fill) best = x, fill = n;
-    }
-    return best;
+    int x = page_size < TILE ? page_size : TILE;
+    while (page_size % x || 4 * (TILE / x * x) < 3 * TILE) --x;
+    return x;
 }
 
 bool encode_pages(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const ChunkParams& p, const void* base, int64_t stride, int box) {
