@@ -288,6 +288,34 @@ def test_what_is_masked_is_not_used_whatever_it_holds(dtype, d, bad):
                 assert bool(torch.isnan(o[~fine]).all()) and bool(torch.isnan(lse[~fine]).all())
 
 
+@pytest.mark.parametrize("d,ps", [(64, 96), (128, 96), (128, 16), (64, 100), (16, 16)])
+@pytest.mark.parametrize("window,sinks", [(500, 0), (300, 130), (0, 0)])
+def test_values_that_are_not_finite_in_every_partly_seen_tile(d, ps, window, sinks):
+    """256 rows of one token each, and in every tile that some of them see in part, and in two pages in three elsewhere among the first
+    tokens, a value that is not finite: rows that see none of them are right, the others say so."""
+    n, past = 256, 701
+    t = make([(n, past)], 2, 2, d, ps, "bf16", d + ps)
+    pos = torch.arange(past, past + n, device=DEV)
+    seen = lambda j: (pos >= j) & ((pos - j < window) | torch.tensor(j < sinks, device=DEV) if window else pos >= 0)
+    part = [j for j in range(past + n) if 0 < int(seen(j).sum()) < n]          # tokens that some rows see and others not
+    bad = part[5::50] if window else part[5::60]
+    clean = t["v_pages"].clone()
+    for i, j in enumerate(bad):
+        t["v_pages"][int(t["block_table"][0, j // ps]), i % 2, j % ps, i % d] = (math.nan, math.inf, -math.inf)[i % 3]
+    assert len(bad) >= (5 if window == 0 else 9)
+    ref, ref_lse = reference(dict(t, v_pages=clean), [(n, past)], ps, 0.1, window, sinks)
+    lse = torch.empty((n, 2), device=DEV)
+    o = kda.kda_attention_prefill(**t, scale=0.1, window=window, sinks=sinks, lse=lse)
+    assert kda.kda_get_device_error() == 0
+    hit = torch.zeros((n, 2, d), dtype=torch.bool, device=DEV)
+    for i, j in enumerate(bad):
+        hit[:, i % 2, i % d] |= seen(j)
+    assert bool(hit.any()) and not bool(hit.all())
+    assert bool(torch.isfinite(o[~hit]).all()) and not bool(torch.isfinite(o[hit]).any())
+    assert float((o[~hit].double() - ref[~hit]).norm() / ref[~hit].norm()) <= TOL["bf16"]
+    assert float((lse.double() - ref_lse).abs().max()) <= 1e-4
+
+
 def test_a_row_whose_scores_are_all_minus_infinity():
     for dtype in ("bf16", "f32"):
         t = make([(40, 0)], 2, 1, 64, 16, dtype, 11)
