@@ -36,10 +36,10 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int EXTRA = 1;                      // tiles' time that a unit's queries and outputs take
 constexpr float SLACK = 8.f;                  // the reference moves when the maximum has grown by 2^SLACK
 
-// Tokens of a tile whose value is not finite, taken out of it.  A unit of 256 rows has at most nine tiles that some row sees
-// in part: tiles hold 96 tokens or more (box_of), the rows' own tokens touch 4 of them, the lower borders of their windows 4,
+// Tokens of a tile whose value is not finite, taken out of it.  A unit of 256 rows has at most eleven tiles that some row sees
+// in part: tiles hold 65 tokens or more (box_of), the rows' own tokens touch 5 of them, the lower borders of their windows 5,
 // the border of the first tokens 1.
-constexpr int MAX_ODD = 9;
+constexpr int MAX_ODD = 11;
 struct OddTiles {
     int32_t n;
     int32_t start[MAX_ODD];
@@ -744,11 +744,16 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
     }
 }
 
-// Tokens of a TMA box: the largest run that divides a page and of which whole ones fill three quarters of a tile (one token
-// always does).
+// Tokens of a TMA box: the largest run that divides a page and of which at most 24 fill three quarters of a tile, else the
+// largest of which whole ones fill more than half (one token always does).  2,048 tokens behind 6,000 (32 / 8 heads of 128), as
+// many boxes that fill more against one that fills less: pages of 77, 11 of 11 302 us, one 360; of 66, 3 of 33 295, one 415; of 94,
+// 64 of 2 803, one 302; of 67, 128 of one token 1,437, one 409.
 int box_of(int page_size) {
-    int x = page_size < TILE ? page_size : TILE;
-    while (page_size % x || 4 * (TILE / x * x) < 3 * TILE) --x;
+    const int most = page_size < TILE ? page_size : TILE;
+    for (int x = most; TILE / x <= 24; --x)
+        if (page_size % x == 0 && 4 * (TILE / x * x) >= 3 * TILE) return x;
+    int x = most;
+    while (page_size % x || 2 * (TILE / x * x) <= TILE) --x;
     return x;
 }
 

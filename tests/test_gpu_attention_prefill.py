@@ -132,6 +132,14 @@ def test_page_sizes(dtype, ps):
     check([(140, 23)], 2, 2, 128, ps, dtype, seed=ps + 1)
 
 
+@pytest.mark.parametrize("ps", [2, 5, 9, 65, 66, 67, 71, 77, 90, 94, 127, 134, 201, 469])
+@pytest.mark.parametrize("d", [64, 128])
+def test_pages_of_few_divisors(d, ps):
+    """Tiles of less than 128 tokens, in one box or several."""
+    check([(1, 0), (99, 200), (40, 600), (256, 801)], 4, 2, d, ps, "bf16", seed=ps)
+    check([(99, 200), (300, 701), (1, 5000)], 2, 2, d, ps, "bf16", seed=ps + 1, window=150, sinks=70)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 3), (64, 0), (64, 64), (100, 4), (300, 70), (2000, 4), (129, 500),
                                           (2 ** 31 - 1, 0), (7, 2 ** 31 - 1)])
@@ -288,7 +296,7 @@ def test_what_is_masked_is_not_used_whatever_it_holds(dtype, d, bad):
                 assert bool(torch.isnan(o[~fine]).all()) and bool(torch.isnan(lse[~fine]).all())
 
 
-@pytest.mark.parametrize("d,ps", [(64, 96), (128, 96), (128, 16), (64, 100), (16, 16)])
+@pytest.mark.parametrize("d,ps", [(64, 96), (128, 96), (128, 16), (64, 100), (16, 16), (64, 67), (128, 71), (128, 134)])
 @pytest.mark.parametrize("window,sinks", [(500, 0), (300, 130), (0, 0)])
 def test_values_that_are_not_finite_in_every_partly_seen_tile(d, ps, window, sinks):
     """256 rows of one token each, and in every tile that some of them see in part, and in two pages in three elsewhere among the first
