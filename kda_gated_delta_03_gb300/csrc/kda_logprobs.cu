@@ -570,7 +570,7 @@ __device__ __noinline__ void backward_row(const T* x0, T* g0, int V, int y, floa
 // gradient may take the logits' place.  DRAM bounds it: 2,048 rows of 131,072 bf16 words 157 us (6.8 TB/s), with four as with eight
 // vectors.
 template <typename T>
-__global__ void __launch_bounds__(NT, 16) kda_logprobs_backward_kernel(LogprobGradParams p, int chunks) {
+__global__ void __launch_bounds__(NT) kda_logprobs_backward_kernel(LogprobGradParams p, int chunks) {
     using E = Elems<T>;
     constexpr int W = E::W;
     const int64_t row = blockIdx.x / chunks;
