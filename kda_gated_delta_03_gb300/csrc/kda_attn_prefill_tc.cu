@@ -794,7 +794,9 @@ cudaError_t launch_tc(const ChunkParams& p, cudaStream_t s) {
     ChunkPlan f = chunk_plan(p, UNIT, TILE / box * box, EXTRA);
     int grid = sms < TC_MAX_CTAS ? sms : TC_MAX_CTAS;
     const int64_t units = most_units(p, f);
-    // Where a unit has few tiles, whatever the lengths, pieces and a second kernel would cost more than they bring.
+    // Where a unit has few tiles, whatever the lengths, pieces and a second kernel would cost more than they bring: 16 rows of one
+    // token behind 100 and 400 (32 / 8 heads of 128) 9.9 and 15.5 us, in shares 19.0 and 21.4; 12 rows of 64 tokens behind 400 20.6
+    // and 33.9; at the limit of units, 48 rows of one token behind 400, 45.2 and 45.0.
     f.whole = units <= 3 * (int64_t)grid && most_tiles(p, f) <= 2 * MIN_SHARE;
     if (f.whole) grid = (int)units;
     kda_chunk_tc_kernel<D><<<grid, THREADS, TcLayout<D>::BYTES, s>>>(p, f, box, q_boxes, q_map, k_map, v_map);

@@ -135,6 +135,25 @@ def test_angles_at_every_position():
         assert float(off.max()) <= 3.6e-7, (float(off.max()), int(off.argmax()))
 
 
+def test_cosines_and_sines_of_angles_at_every_position():
+    """The turned unit vectors, that is the cosine and the sine themselves.  The angle is off by 2^-32 of a turn and by half a step
+    of an eighth of one in 24 bits, 16 * 2^-32 of a turn (1.5e-9 + 2.3e-8 radians, below 2^-25), either function by two units
+    of its last place, at most 2^-22 of it."""
+    pi = Fraction(31415926535897932384626433832795028841971693993751058209749446, 10 ** 61)
+    gen = torch.Generator().manual_seed(3)
+    pos = torch.cat([torch.randint(-2 ** 31, 2 ** 31, (200,), generator=gen), torch.tensor([2 ** 31 - 1, -2 ** 31, 0, 1])]).int()
+    d, f = 128, frequencies(128, 500000.0)
+    f[::7] *= 1e5
+    turns = [[float((int(p) * Fraction(x) / (2 * pi)) % 1) for x in f.tolist()] for p in pos.tolist()]
+    angle = torch.tensor(turns, dtype=torch.float64, device=DEV) * 2 * math.pi
+    unit = torch.zeros((pos.numel(), 1, d), device=DEV)
+    unit[..., :d // 2] = 1
+    got, _ = kda.kda_rotary(unit, None, pos.to(DEV), f)
+    want = torch.cat([angle.cos(), angle.sin()], -1)[:, None]
+    off = (got.double() - want).abs()
+    assert bool((off <= 2.5e-8 + 2.0 ** -22 * want.abs() + 1e-15).all()), float((off - 2.0 ** -22 * want.abs()).max())
+
+
 def test_the_inverse_is_the_gradient():
     T, H, d, rot = 7, 2, 16, 12
     f, pos = frequencies(rot), torch.arange(T, device=DEV).int() * 1000
