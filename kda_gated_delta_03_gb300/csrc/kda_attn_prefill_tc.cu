@@ -157,9 +157,9 @@ struct Open {
     __device__ __forceinline__ bool operator()(int it) const { return it < near ? it < a : it >= b && it < c; }
 };
 
-// Adds the two weights of a packed pair to a sum each.
-__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t x) {
-    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\nadd.rn.f32.bf16 %0, l, %0;\nadd.rn.f32.bf16 %1, h, %1;\n}\n" : "+f"(a), "+f"(b) : "r"(x));
+// Adds the two weights of a packed pair to their sum.
+__device__ __forceinline__ void add_bf16x2(float& sum, uint32_t x) {
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\nadd.rn.f32.bf16 %0, l, %0;\nadd.rn.f32.bf16 %0, h, %0;\n}\n" : "+f"(sum) : "r"(x));
 }
 
 // 64 bytes of a row: whole 32-byte sectors at a time where the address allows it, since each lane has a row of its own.
@@ -368,16 +368,15 @@ kda_chunk_tc_kernel(ChunkParams p, ChunkPlan f, int box, int q_boxes, const __gr
                     }
                     const float2 sums2 = both(add2(sum[0], sum[1]));
                     l += sums2.x + sums2.y;
-                    // The rounded weights' sum, behind their hand-over: it begins with a zero that is read there, so that no
-                    // compiler brings it forward.  (Among the exponentials the prompt of 8,192 tokens took 452 us, here 443, without
-                    // it 383; as a product on the old matrix path 500; with the halves taken apart by shifts 508.)
+                    // The rounded weights' sum, behind their hand-over, one at a time, so that it leaves the other block the pipes:
+                    // it begins with a zero that is read there, so that no compiler brings it forward.  (The prompt of 8,192
+                    // tokens 442 us, without it 383; two and four chains 446 and 451, among the exponentials 452, with the halves
+                    // taken apart by shifts 490 to 508, as a product on the old matrix path 500.)
                     float zero;
                     asm volatile("ld.volatile.shared.f32 %0, [%1];" : "=f"(zero) : "r"(saddr(&misc.zero)) : "memory");
-                    float odd_sum = zero;
                     lw += zero;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) add_bf16x2(lw, odd_sum, __float_as_uint(x[i / 16][i % 16]));
-                    lw += odd_sum;
+                    for (int i = 0; i < 64; ++i) add_bf16x2(lw, __float_as_uint(x[i / 16][i % 16]));
                 }
             }
             // The second block waits for the whole run also where it has no rows, and says so, so that neither side gets
